@@ -225,6 +225,169 @@ psa_status_t psa_attention_bwd_noalloc(const void *qkv_nchw, const void *out_nch
  * and 512 < N <= 2048, B*num_heads*N*32*4 rounded up to 256 (a dQ accumulator). */
 size_t psa_attention_bwd_workspace_size(psa_shape_t shape);
 
+/* ---- token sequences: positions, windows, caches -------------------------------- */
+
+/* The entry points of this section work on views: a view [B, heads, N, d] is a base
+ * pointer and the strides, in elements, of its first three dimensions; the d channels
+ * of a row are contiguous.  A projection's output [B, N, heads, d], a part of its
+ * heads, or the first rows of a longer cache are views; nothing has to be copied into
+ * a dense tensor first.  Rules (for each view): the pointer and, where a dimension
+ * has more than one entry, its stride are multiples of 16 bytes (PSA_ERR_ALIGNMENT);
+ * strides are positive and rows do not overlap: with the dimensions in order of
+ * stride, each stride is at least the extent times the stride of the one before, d
+ * for the first (PSA_ERR_INVALID_ARG).  The stride of a dimension of one entry is not
+ * read.  Outputs must not overlap inputs or one another, except where an entry point
+ * says so.  int and float arrays are dense and 4-byte aligned (cos and sin 16-byte).
+ *
+ * A workspace belongs to one call at a time: two calls, or two captured graphs, that
+ * may run at the same moment need one each.  Nothing in it has to be cleared, and
+ * nothing in it is kept from call to call. */
+typedef struct {
+    void *ptr;
+    long long stride_b, stride_h, stride_n;
+} psa_rows_t;
+
+/* Norms of queries and keys with the position rotation. */
+typedef struct {
+    int B, num_heads, num_kv_heads, N, head_dim;
+    psa_dtype_t dtype;
+    int rotary_dim;  /* leading channels that are rotated: a multiple of 16, 0 .. head_dim */
+    int interleaved; /* 0: channel i turns with i + rotary_dim / 2; 1: channel 2i with 2i + 1 */
+    int max_pos;     /* rows of the cos and sin tables */
+    float eps;
+} psa_norm_rope_t;
+
+/* For each head's row x of q [B, num_heads, N, d] and k [B, num_kv_heads, N, d]:
+ *   y = R(pos) (w o x / sqrt(mean(x^2) + eps)),
+ * where R turns the pair (a, b) of index i into (a cos - b sin, a sin + b cos) with
+ * the entries [pos, i] of the fp32 tables cos, sin [max_pos, rotary_dim / 2], and
+ * channels from rotary_dim on are not turned.  Statistics and products are fp32, the
+ * result is rounded once.  q_weight, k_weight: fp32 [d] (NULL: ones).  positions:
+ * int32 [B, N] on the device (NULL: row n is at position n, N <= max_pos); a token
+ * whose position lies outside 0 .. max_pos - 1 is padding: its rows of q_out and
+ * k_out are left as they were.  q_out may be the same view as q, k_out as k.
+ * head_dim 32, 64 or 128 (PSA_ERR_UNSUPPORTED otherwise); bf16 or fp32.  cos and sin
+ * may be NULL only when rotary_dim is 0. */
+psa_status_t psa_qk_norm_rope_fwd(psa_rows_t q, psa_rows_t k, const float *q_weight,
+                                  const float *k_weight, const float *cos, const float *sin,
+                                  const int *positions, psa_rows_t q_out, psa_rows_t k_out,
+                                  psa_norm_rope_t p, cudaStream_t stream);
+
+/* Its backward: from the forward's inputs and the gradients dq_out, dk_out of its
+ * outputs, writes the gradients dq, dk of q and k (overwritten; zeros in the rows of
+ * padding tokens, whose dq_out and dk_out are not used) and of the weights,
+ * dq_weight and dk_weight, fp32 [d] (overwritten; either may be NULL: not wanted).
+ * The weights' gradients are summed in fp32 in a fixed order: reruns are bitwise
+ * identical.  dq may be the same view as dq_out, dk as dk_out.  workspace: 16-byte
+ * aligned, at least psa_qk_norm_rope_bwd_workspace_size(p) bytes
+ * (PSA_ERR_INVALID_ARG if smaller). */
+psa_status_t psa_qk_norm_rope_bwd(psa_rows_t q, psa_rows_t k, const float *q_weight,
+                                  const float *k_weight, const float *cos, const float *sin,
+                                  const int *positions, psa_rows_t dq_out, psa_rows_t dk_out,
+                                  psa_rows_t dq, psa_rows_t dk, float *dq_weight,
+                                  float *dk_weight, void *workspace, size_t ws_bytes,
+                                  psa_norm_rope_t p, cudaStream_t stream);
+
+/* Bytes of device workspace for psa_qk_norm_rope_bwd (0 for an invalid problem). */
+size_t psa_qk_norm_rope_bwd_workspace_size(psa_norm_rope_t p);
+
+/* Attention with a sliding window and first tokens that stay visible: q
+ * [B, num_heads, n_q, d], k and v [B, num_kv_heads, n_k, d]; query head h reads
+ * key/value head h / (num_heads / num_kv_heads).  Query row i stands at position
+ * p = i + n_k - n_q, key row j at position j; the query sees the key if
+ *   j <= p + window_right  and  (j >= p - window_left  or  j < sinks),
+ * where a negative window means no limit on that side: window_right = 0 is causal,
+ * window_left = 255, window_right = 0 a window of 256 positions.  With per-sequence
+ * lengths (lens, int32 [B] on the device; NULL: n_k), positions from lens[b] on are
+ * padding: they are seen by none and see none.  A query that sees nothing has output
+ * 0 and log-sum-exp -infinity, and gets and gives no gradient.  What rows of padding
+ * hold does not matter (NaN included); values inside the lengths must be finite. */
+typedef struct {
+    int B, num_heads, num_kv_heads, n_q, n_k, head_dim;
+    psa_dtype_t dtype;
+    int window_left, window_right, sinks;
+} psa_window_t;
+
+/* Forward: o = softmax(scale q k^T) v over the visible keys (every row of o is
+ * written) and lse, the natural-log log-sum-exp of each row, fp32 [B, num_heads,
+ * n_q] (NULL: not wanted).  head_dim 64 or 128 (PSA_ERR_UNSUPPORTED otherwise); bf16
+ * (tensor cores; softmax and sums in fp32, probabilities rounded to bf16 before the
+ * product with v) or fp32 (CUDA cores, fp32 throughout).  B * num_heads up to 65535. */
+psa_status_t psa_window_attn_fwd(psa_rows_t q, psa_rows_t k, psa_rows_t v, const int *lens,
+                                 psa_rows_t o, float *lse, psa_window_t p, float scale,
+                                 cudaStream_t stream);
+
+/* Backward: from the forward's inputs, its o and lse and the gradient do_ of o, writes
+ * dq, dk, dv (every row, overwritten; a key/value head's gradient sums those of its
+ * query heads in a fixed order: reruns are bitwise identical).  workspace: 16-byte
+ * aligned, at least psa_window_attn_bwd_workspace_size(p) bytes (PSA_ERR_INVALID_ARG
+ * if smaller).  Sizes and types as in the forward; bf16: P and dS are rounded to bf16
+ * before their products. */
+psa_status_t psa_window_attn_bwd(psa_rows_t q, psa_rows_t k, psa_rows_t v, psa_rows_t o,
+                                 psa_rows_t do_, const float *lse, const int *lens, psa_rows_t dq,
+                                 psa_rows_t dk, psa_rows_t dv, void *workspace, size_t ws_bytes,
+                                 psa_window_t p, float scale, cudaStream_t stream);
+
+/* Bytes of device workspace for psa_window_attn_bwd (0 for an invalid problem). */
+size_t psa_window_attn_bwd_workspace_size(psa_window_t p);
+
+/* Single-token form over a cache: n_q is 1, k_cache and v_cache are views [B,
+ * num_kv_heads, n_k, d] of which sequence b has filled the first lens[b] rows (int32 on
+ * the device, required; values above n_k count as n_k), its query's own key included:
+ * the query stands at position lens[b] - 1 and window_right plays no part.  Only the
+ * visible rows are read.  A sequence of length 0 or less gets output 0.  bf16 (fp32:
+ * PSA_ERR_UNSUPPORTED), head_dim 64 or 128, any num_heads / num_kv_heads.  workspace:
+ * 16-byte aligned, at least psa_window_attn_decode_workspace_size(p) bytes. */
+psa_status_t psa_window_attn_decode(psa_rows_t q, psa_rows_t k_cache, psa_rows_t v_cache,
+                                    const int *lens, psa_rows_t o, void *workspace,
+                                    size_t ws_bytes, psa_window_t p, float scale,
+                                    cudaStream_t stream);
+
+/* Bytes of device workspace for psa_window_attn_decode and psa_window_attn_decode_kv4 (0
+ * for an invalid problem); they depend on the problem's sizes, not on the lengths. */
+size_t psa_window_attn_decode_workspace_size(psa_window_t p);
+
+/* Rows for a cache: row n of sequence b (n < counts[b], int32 [B] on the device; NULL:
+ * all N) goes to cache row starts[b] + n (int32 [B] on the device).  Rows that fall
+ * outside the cache's max_len rows are dropped; all other cache rows stay as they
+ * were. */
+typedef struct {
+    int B, num_kv_heads, N, max_len, head_dim;
+    psa_dtype_t dtype; /* of the rows */
+} psa_cache_t;
+
+/* Copies k, v [B, num_kv_heads, N, d] into caches of the same type, views [B,
+ * num_kv_heads, max_len, d].  head_dim 64 or 128; bf16 or fp32. */
+psa_status_t psa_kv_append(psa_rows_t k, psa_rows_t v, const int *starts, const int *counts,
+                           psa_rows_t k_cache, psa_rows_t v_cache, psa_cache_t p,
+                           cudaStream_t stream);
+
+/* A cache held in 4 bits: codes uint8 [B, num_kv_heads, max_len, d / 2] and scales bf16
+ * [B, num_kv_heads, max_len, d / 32], dense and 16-byte aligned.  Each group of 32
+ * channels of a row has one scale, its largest magnitude / 7 rounded to bf16; a code is
+ * the nearest multiple of it (ties to even, clamped to -7 .. 7; 0 where the scale is 0)
+ * plus 8, and stands for (code - 8) * scale.  The code of channel 32 g + 4 a + i is the
+ * nibble (a * (d / 32) + g) * 4 + i of its row, low nibble of a byte first.  This
+ * quantises and stores the rows of k and v; head_dim 64 or 128, rows bf16 or fp32. */
+psa_status_t psa_kv4_append(psa_rows_t k, psa_rows_t v, const int *starts, const int *counts,
+                            void *k_codes, void *k_scales, void *v_codes, void *v_scales,
+                            psa_cache_t p, cudaStream_t stream);
+
+/* The values that rows 0 .. N - 1 of every sequence's 4-bit cache stand for, into the
+ * views k and v [B, num_kv_heads, N, d], N <= max_len, rounded once to their type. */
+psa_status_t psa_kv4_read(const void *k_codes, const void *k_scales, const void *v_codes,
+                          const void *v_scales, psa_rows_t k, psa_rows_t v, psa_cache_t p,
+                          cudaStream_t stream);
+
+/* psa_window_attn_decode over a cache held in 4 bits (p.n_k rows, p.dtype that of q and
+ * o: bf16).  The codes' values enter the products exactly; scales multiply fp32 sums
+ * (keys) and probabilities (values; rounded to bf16 after it). */
+psa_status_t psa_window_attn_decode_kv4(psa_rows_t q, const void *k_codes, const void *k_scales,
+                                        const void *v_codes, const void *v_scales,
+                                        const int *lens, psa_rows_t o, void *workspace,
+                                        size_t ws_bytes, psa_window_t p, float scale,
+                                        cudaStream_t stream);
+
 /* ---- status ------------------------------------------------------------------- */
 
 /* Static description of a status code. */

@@ -1,0 +1,198 @@
+"""psa_window_attn_fwd / _bwd against their 64-bit form: masks, ragged sizes, shared heads, strides,
+padding, and rows that see nothing."""
+import math
+
+import pytest
+import torch
+
+from token_reference import window_attention, within
+from vision_transformer_attention_psapackqkv_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _inputs(Bn, nh, nkv, nq, nk, d, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    return rn(Bn, nh, nq, d), rn(Bn, nkv, nk, d), rn(Bn, nkv, nk, d), rn(Bn, nh, nq, d)
+
+
+def _seven(t):
+    return torch.full(t.shape, 7.0, dtype=t.dtype, device="cuda")
+
+
+def _fwd(q, k, v, lens, left, right, sinks, scale, stream=None):
+    win = B.window_of(q, k, left, right, sinks)
+    o, lse = _seven(q), torch.full(q.shape[:3], 7.0, device="cuda")
+    B.psa_window_attn_fwd(q, k, v, lens, o, lse, win, scale, stream)
+    return o, lse
+
+
+def _bwd(q, k, v, o, do, lse, lens, left, right, sinks, scale):
+    win = B.window_of(q, k, left, right, sinks)
+    dq, dk, dv = _seven(q), _seven(k), _seven(v)
+    ws = torch.full((B.psa_window_attn_bwd_workspace_size(win),), 0xFF, dtype=torch.uint8, device="cuda")
+    B.psa_window_attn_bwd(q, k, v, o, do, lse, lens, dq, dk, dv, ws, win, scale)
+    return dq, dk, dv
+
+
+def _check(q, k, v, do, lens, left, right, sinks, scale):
+    dtype = q.dtype
+    lens_t = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = _fwd(q, k, v, lens_t, left, right, sinks, scale)
+    dq, dk, dv = _bwd(q, k, v, o, do, lse, lens_t, left, right, sinks, scale)
+    r = window_attention(q, k, v, lens, left, right, sinks, scale, do, 2.0 ** -8 if dtype == BF16 else 2.0 ** -24,
+                         dtype == F32)
+    for name, x in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        within(x, r[name], r[name + "_tol"], name)
+    assert B.psa_get_last_device_error() == B.PSA_OK
+
+
+# n_q, n_k, left, right, sinks
+MASKS = [(1, 1, -1, 0, 0), (2, 2, 0, 0, 0), (65, 65, -1, 0, 0), (127, 127, 30, 0, 4), (128, 128, -1, -1, 0),
+         (129, 129, 63, 0, 1), (200, 200, 17, 20, 3), (257, 257, 40, 0, 130), (400, 400, 60, 60, 4),
+         (385, 385, 128, 0, 0), (1, 300, -1, 0, 0), (70, 300, 90, 0, 8), (130, 513, 1, 0, 129), (90, 40, -1, 0, 0),
+         (300, 130, 20, 5, 2), (640, 640, 255, 0, 64)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,nk,left,right,sinks", MASKS)
+def test_masks_and_sizes(nq, nk, left, right, sinks, d, dtype):
+    q, k, v, do = _inputs(2, 4, 2, nq, nk, d, dtype, nq + nk + d)
+    _check(q, k, v, do, None, left, right, sinks, d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,left,sinks,lens", [(300, -1, 0, [300, 0, 1, 129]), (260, 50, 4, [128, 127, 260, 3]),
+                                               (129, 200, 0, [129, 64, 500, -7])])
+def test_padded_batches_whose_padding_holds_nan(n, left, sinks, lens, d, dtype):
+    q, k, v, do = _inputs(4, 4, 1, n, n, d, dtype, n + d)
+    for b, m in enumerate(lens):
+        for t in (q, k, v, do):
+            t[b, :, max(0, min(m, n)):] = math.nan
+    _check(q, k, v, do, lens, left, 0, sinks, d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_chunk_behind_a_prefix_in_a_padded_batch(dtype):
+    q, k, v, do = _inputs(3, 2, 2, 100, 350, 64, dtype, 8)
+    lens = [350, 300, 240]  # the last sequence ends in front of the chunk
+    for b, m in enumerate(lens):
+        k[b, :, m:], v[b, :, m:] = math.nan, math.inf
+        q[b, :, max(0, m - 250):], do[b, :, max(0, m - 250):] = math.nan, math.nan
+    _check(q, k, v, do, lens, 100, 0, 2, 0.2)
+
+
+@pytest.mark.parametrize("nh,nkv", [(1, 1), (5, 1), (8, 8), (6, 2), (7, 7), (16, 1), (40, 8)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_shared_heads(nh, nkv, d):
+    q, k, v, do = _inputs(1, nh, nkv, 140, 140, d, BF16, nh)
+    _check(q, k, v, do, None, 77, 0, 1, 0.1)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_views(dtype):
+    """q, k, v as parts of one projection's output, the keys as the front of a longer cache."""
+    Bn, n, nh, nkv, d = 2, 150, 4, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(11)
+    packed = torch.randn(Bn, n, nh + 2 * nkv, d, generator=g, device="cuda").to(dtype).transpose(1, 2)
+    q, k, v = packed[:, :nh], packed[:, nh:nh + nkv], packed[:, nh + nkv:]
+    cache = torch.full((nkv, Bn, 200, 2 * d), math.nan, dtype=dtype, device="cuda")
+    kc = cache.transpose(0, 1)[:, :, :n, d:]
+    kc.copy_(k)
+    do = torch.randn(Bn, n, nh, d, generator=g, device="cuda").to(dtype).transpose(1, 2)
+    _check(q, kc, v, do, None, 33, 0, 2, 0.08)
+    win = B.window_of(q, kc, 33, 0, 2)
+    dense = _fwd(q.contiguous(), k.contiguous(), v.contiguous(), None, 33, 0, 2, 0.08)
+    out = torch.full((Bn, n, nh + 1, d), 7.0, dtype=dtype, device="cuda")  # a view as the output
+    B.psa_window_attn_fwd(q, kc, v, None, out.transpose(1, 2)[:, :nh], None, win, 0.08)
+    assert torch.equal(out[:, :, :nh].transpose(1, 2), dense[0]) and (out[:, :, nh] == 7.0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_growing_scores(d):
+    """Row maxima that jump by far more than 2^8 from key tile to key tile, in both directions."""
+    q, k, v, do = _inputs(1, 2, 1, 520, 520, d, BF16, 12)
+    u = torch.randn(d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    u /= u.norm()
+    ramp = torch.linspace(-20, 20, 520, device="cuda")[:, None] * u
+    k = (k.float() * 0.3 + ramp).to(BF16)
+    q = (q.float() * 0.3 + 8 * u).to(BF16)
+    for kk in (k, k.flip(2).contiguous()):
+        o, lse = _fwd(q, kk, v, None, -1, 0, 0, 0.5)
+        r = window_attention(q, kk, v, None, -1, 0, 0, 0.5)
+        within(o, r["o"], r["o_tol"], "o")
+        within(lse, r["lse"], r["lse_tol"], "lse")
+
+
+def test_a_long_sequence_s_rows():
+    """One head of 8192 positions with a window: sampled rows, whole gradients' sums."""
+    n, d, scale = 8192, 128, 128 ** -0.5
+    q, k, v, do = _inputs(1, 2, 1, n, n, d, BF16, 13)
+    o, lse = _fwd(q, k, v, None, 1023, 0, 4, scale)
+    dq, dk, dv = _bwd(q, k, v, o, do, lse, None, 1023, 0, 4, scale)
+    r = window_attention(q, k, v, None, 1023, 0, 4, scale, do)
+    for name, x in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        within(x, r[name], r[name + "_tol"], name)
+
+
+def test_reruns_are_bitwise_identical():
+    q, k, v, do = _inputs(2, 8, 2, 700, 700, 128, BF16, 14)
+    runs = []
+    for _ in range(3):
+        o, lse = _fwd(q, k, v, None, 200, 0, 4, 0.1)
+        runs.append((o, lse) + _bwd(q, k, v, o, do, lse, None, 200, 0, 4, 0.1))
+    for again in runs[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(runs[0], again))
+
+
+def test_graph_replays_on_new_inputs_and_another_stream():
+    q, k, v, do = _inputs(2, 4, 2, 333, 333, 64, BF16, 15)
+    lens = torch.tensor([333, 200], dtype=torch.int32, device="cuda")
+    win = B.window_of(q, k, 100, 0, 2)
+    o, lse = _seven(q), torch.empty(q.shape[:3], device="cuda")
+    dq, dk, dv = _seven(q), _seven(k), _seven(v)
+    ws = torch.empty(B.psa_window_attn_bwd_workspace_size(win), dtype=torch.uint8, device="cuda")
+
+    def step(stream=None):
+        B.psa_window_attn_fwd(q, k, v, lens, o, lse, win, 0.1, stream)
+        B.psa_window_attn_bwd(q, k, v, o, do, lse, lens, dq, dk, dv, ws, win, 0.1, stream)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    step(s)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    new = _inputs(2, 4, 2, 333, 333, 64, BF16, 16)
+    for t, x in zip((q, k, v, do), new):
+        t.copy_(x)
+    lens.copy_(torch.tensor([150, 333], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in (o, lse, dq, dk, dv)]
+    step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, (o, lse, dq, dk, dv)))
+
+
+def test_a_window_as_wide_as_the_sequence_is_no_window():
+    q, k, v, _ = _inputs(1, 2, 2, 200, 200, 64, BF16, 17)
+    a = _fwd(q, k, v, None, -1, 0, 0, 0.1)
+    b = _fwd(q, k, v, None, 2 ** 31 - 1, 0, 2 ** 31 - 1, 0.1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_causal_attention_next_to_flash_attn2():
+    """Without any limit the operator is the framework's own attention."""
+    q, k, v, _ = _inputs(1, 3, 3, 300, 300, 64, BF16, 18)
+    o, lse = _fwd(q, k, v, None, -1, -1, 0, 0.125)
+    o2, lse2 = torch.empty_like(q[0]), torch.empty(3, 300, device="cuda")
+    B.flash_attn2_fwd(q[0], k[0], v[0], o2, lse2, 0.125)
+    r = window_attention(q, k, v, None, -1, -1, 0, 0.125)
+    within(o[0], o2, 2 * r["o_tol"][0], "o")
+    within(lse[0], lse2, 2 * r["lse_tol"][0], "lse")

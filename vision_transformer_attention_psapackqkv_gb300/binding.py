@@ -31,11 +31,38 @@ class PsaShape(ctypes.Structure):
                 ("H", ctypes.c_int), ("W", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
+class PsaRows(ctypes.Structure):
+    """A view [B, heads, N, d]: base pointer and the strides of its first three dimensions."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
+                ("stride_n", ctypes.c_longlong)]
+
+
+class PsaNormRope(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("num_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+                ("N", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("max_pos", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
+class PsaWindow(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("num_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+                ("n_q", ctypes.c_int), ("n_k", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("window_left", ctypes.c_int), ("window_right", ctypes.c_int), ("sinks", ctypes.c_int)]
+
+
+class PsaCache(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("num_kv_heads", ctypes.c_int), ("N", ctypes.c_int),
+                ("max_len", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
 EXPORTED = (
     "psa_qkv_conv", "psa_pack_qkv", "psa_unpack_qkv", "psa_extract_v", "psa_merge_attn", "psa_unmerge_attn",
     "flash_attn2_fwd", "flash_attn2_bwd_dq", "flash_attn2_bwd_dkdv", "psa_attention_fwd",
     "psa_attention_fwd_residual", "psa_attention_bwd", "psa_attention_bwd_dq", "psa_attention_bwd_dkdv", "psa_attention_bwd_noalloc",
-    "psa_attention_bwd_workspace_size", "psa_status_string",
+    "psa_attention_bwd_workspace_size", "psa_qk_norm_rope_fwd", "psa_qk_norm_rope_bwd",
+    "psa_qk_norm_rope_bwd_workspace_size", "psa_window_attn_fwd", "psa_window_attn_bwd",
+    "psa_window_attn_bwd_workspace_size", "psa_window_attn_decode", "psa_window_attn_decode_workspace_size",
+    "psa_kv_append", "psa_kv4_append", "psa_kv4_read", "psa_window_attn_decode_kv4", "psa_status_string",
     "psa_get_last_device_error", "psa_debug_wait_timeout",
 )
 
@@ -54,6 +81,7 @@ def load(path: str | None = None):
         raise RuntimeError(f"libpsa_gb300.so is not built ({path}); run __graft_entry__.build()")
     lib = ctypes.CDLL(path)
     P, I, F, S, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, PsaShape, ctypes.c_size_t
+    R, NR, WN, CA = PsaRows, PsaNormRope, PsaWindow, PsaCache
     sigs = {
         "psa_qkv_conv": [P, P, P, P, I, I, I, I, I, P],
         "psa_pack_qkv": [P, P, S, P],
@@ -71,6 +99,18 @@ def load(path: str | None = None):
         "psa_attention_bwd_dkdv": [P, P, P, P, P, P, S, F, P],
         "psa_attention_bwd_noalloc": [P, P, P, P, P, P, S, F, P],
         "psa_attention_bwd_workspace_size": [S],
+        "psa_qk_norm_rope_fwd": [R, R, P, P, P, P, P, R, R, NR, P],
+        "psa_qk_norm_rope_bwd": [R, R, P, P, P, P, P, R, R, R, R, P, P, P, Z, NR, P],
+        "psa_qk_norm_rope_bwd_workspace_size": [NR],
+        "psa_window_attn_fwd": [R, R, R, P, R, P, WN, F, P],
+        "psa_window_attn_bwd": [R, R, R, R, R, P, P, R, R, R, P, Z, WN, F, P],
+        "psa_window_attn_bwd_workspace_size": [WN],
+        "psa_window_attn_decode": [R, R, R, P, R, P, Z, WN, F, P],
+        "psa_window_attn_decode_workspace_size": [WN],
+        "psa_kv_append": [R, R, P, P, R, R, CA, P],
+        "psa_kv4_append": [R, R, P, P, P, P, P, P, CA, P],
+        "psa_kv4_read": [P, P, P, P, R, R, CA, P],
+        "psa_window_attn_decode_kv4": [R, P, P, P, P, P, R, P, Z, WN, F, P],
         "psa_status_string": [I],
         "psa_get_last_device_error": [P],
         "psa_debug_wait_timeout": [ctypes.c_ulonglong, P],
@@ -79,7 +119,8 @@ def load(path: str | None = None):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
-    lib.psa_attention_bwd_workspace_size.restype = ctypes.c_size_t
+    for name in ("psa_attention_bwd", "psa_qk_norm_rope_bwd", "psa_window_attn_bwd", "psa_window_attn_decode"):
+        getattr(lib, name + "_workspace_size").restype = ctypes.c_size_t
     lib.psa_status_string.restype = ctypes.c_char_p
     _lib = lib
     return lib
@@ -211,6 +252,202 @@ def psa_attention_bwd_noalloc(qkv, out, dout, lse, dvres, dqkv, shape: PsaShape,
     _check("psa_attention_bwd_noalloc", load().psa_attention_bwd_noalloc(
         _ptr(qkv), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dvres), _ptr(dqkv), shape, float(scale),
         _stream(stream)))
+
+
+# ------------------------------------------------------------------ token sequences
+# Views are torch tensors [B, heads, N, d] of any strides whose channels are contiguous.
+# The calls run on the tensors' device, on its current stream unless one is given.
+def _rows(t, shape, dtype, what: str) -> PsaRows:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} is {t.dtype}, expected {dtype}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: the channels of a row must be contiguous")
+    return PsaRows(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+
+
+def _dense(t, shape, dtype, what: str):
+    """Pointer of a dense array of that shape and type; None for None."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} is {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return _ptr(t)
+
+
+def _on_device(fn: str, tensors, stream, *args):
+    """Calls entry point `fn` with its arguments on the tensors' one CUDA device."""
+    import torch
+
+    device = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{fn}: tensors on {device} and {t.device}")
+    if device.type != "cuda":
+        raise ValueError(f"{fn}: tensors must be on a CUDA device, got {device}")
+    with torch.cuda.device(device):
+        _check(fn, getattr(load(), fn)(*args, _stream(stream)))
+
+
+def _workspace(t, fn: str):
+    if t is None or not t.is_contiguous():
+        raise ValueError(f"{fn}: the workspace must be a contiguous tensor")
+    return _ptr(t), t.numel() * t.element_size()
+
+
+def norm_rope_of(q, k, cos, eps: float = 1e-6, interleaved: bool = False) -> PsaNormRope:
+    """The problem of q [B, num_heads, N, d], k [B, num_kv_heads, N, d] and a table cos
+    [max_pos, rotary_dim / 2] (None: no rotation)."""
+    B, nh, N, d = q.shape
+    rot, max_pos = (0, 2 ** 31 - 1) if cos is None else (2 * cos.shape[1], cos.shape[0])
+    return PsaNormRope(B, nh, k.shape[1], N, d, dtype_code(q), rot, int(bool(interleaved)), max_pos, float(eps))
+
+
+def _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p):
+    import torch
+
+    f32, table = torch.float32, (p.max_pos, p.rotary_dim // 2)
+    return (_rows(q, (p.B, p.num_heads, p.N, p.head_dim), q.dtype, "q"),
+            _rows(k, (p.B, p.num_kv_heads, p.N, p.head_dim), q.dtype, "k"),
+            _dense(q_weight, (p.head_dim,), f32, "q_weight"), _dense(k_weight, (p.head_dim,), f32, "k_weight"),
+            _dense(cos, table, f32, "cos"), _dense(sin, table, f32, "sin"),
+            _dense(positions, (p.B, p.N), torch.int32, "positions"))
+
+
+def psa_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, p: PsaNormRope,
+                         stream=None):
+    args = _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p)
+    _on_device("psa_qk_norm_rope_fwd", (q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out), stream,
+               *args, _rows(q_out, q.shape, q.dtype, "q_out"), _rows(k_out, k.shape, q.dtype, "k_out"), p)
+
+
+def psa_qk_norm_rope_bwd_workspace_size(p: PsaNormRope) -> int:
+    return int(load().psa_qk_norm_rope_bwd_workspace_size(p))
+
+
+def psa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk, dq_weight,
+                         dk_weight, workspace, p: PsaNormRope, stream=None):
+    import torch
+
+    args = _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p)
+    grads = [_rows(t, x.shape, q.dtype, what) for t, x, what in
+             ((dq_out, q, "dq_out"), (dk_out, k, "dk_out"), (dq, q, "dq"), (dk, k, "dk"))]
+    dw = [_dense(t, (p.head_dim,), torch.float32, what) for t, what in
+          ((dq_weight, "dq_weight"), (dk_weight, "dk_weight"))]
+    _on_device("psa_qk_norm_rope_bwd",
+               (q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk, dq_weight, dk_weight,
+                workspace), stream, *args, *grads, *dw, *_workspace(workspace, "psa_qk_norm_rope_bwd"), p)
+
+
+def window_of(q, k, window_left: int = -1, window_right: int = 0, sinks: int = 0) -> PsaWindow:
+    """The problem of q [B, num_heads, n_q, d] against keys, a cache or its codes k
+    [B, num_kv_heads, n_k, ...]; a negative window has no limit on that side."""
+    B, nh, n_q, d = q.shape
+    return PsaWindow(B, nh, k.shape[1], n_q, k.shape[2], d, dtype_code(q), int(window_left), int(window_right),
+                     int(sinks))
+
+
+def _window_views(named, dtype, win: PsaWindow):
+    shapes = {"q": (win.B, win.num_heads, win.n_q, win.head_dim), "k": (win.B, win.num_kv_heads, win.n_k, win.head_dim)}
+    return [_rows(t, shapes[side], dtype, what) for t, side, what in named]
+
+
+def _lens(lens, win: PsaWindow):
+    import torch
+
+    return _dense(lens, (win.B,), torch.int32, "lens")
+
+
+def psa_window_attn_fwd(q, k, v, lens, o, lse, win: PsaWindow, scale: float, stream=None):
+    import torch
+
+    vq, vk, vv, vo = _window_views(((q, "q", "q"), (k, "k", "k"), (v, "k", "v"), (o, "q", "o")), q.dtype, win)
+    _on_device("psa_window_attn_fwd", (q, k, v, lens, o, lse), stream, vq, vk, vv, _lens(lens, win), vo,
+               _dense(lse, (win.B, win.num_heads, win.n_q), torch.float32, "lse"), win, float(scale))
+
+
+def psa_window_attn_bwd_workspace_size(win: PsaWindow) -> int:
+    return int(load().psa_window_attn_bwd_workspace_size(win))
+
+
+def psa_window_attn_bwd(q, k, v, o, do, lse, lens, dq, dk, dv, workspace, win: PsaWindow, scale: float,
+                        stream=None):
+    import torch
+
+    ins = _window_views(((q, "q", "q"), (k, "k", "k"), (v, "k", "v"), (o, "q", "o"), (do, "q", "do")), q.dtype, win)
+    outs = _window_views(((dq, "q", "dq"), (dk, "k", "dk"), (dv, "k", "dv")), q.dtype, win)
+    _on_device("psa_window_attn_bwd", (q, k, v, o, do, lse, lens, dq, dk, dv, workspace), stream, *ins,
+               _dense(lse, (win.B, win.num_heads, win.n_q), torch.float32, "lse"), _lens(lens, win), *outs,
+               *_workspace(workspace, "psa_window_attn_bwd"), win, float(scale))
+
+
+def psa_window_attn_decode_workspace_size(win: PsaWindow) -> int:
+    return int(load().psa_window_attn_decode_workspace_size(win))
+
+
+def psa_window_attn_decode(q, k_cache, v_cache, lens, o, workspace, win: PsaWindow, scale: float, stream=None):
+    vq, vk, vv, vo = _window_views(((q, "q", "q"), (k_cache, "k", "k_cache"), (v_cache, "k", "v_cache"),
+                                    (o, "q", "o")), q.dtype, win)
+    _on_device("psa_window_attn_decode", (q, k_cache, v_cache, lens, o, workspace), stream, vq, vk, vv,
+               _lens(lens, win), vo, *_workspace(workspace, "psa_window_attn_decode"), win, float(scale))
+
+
+def cache_of(k, max_len: int) -> PsaCache:
+    """Rows k [B, num_kv_heads, N, d] next to a cache of max_len rows."""
+    B, nkv, N, d = k.shape
+    return PsaCache(B, nkv, N, int(max_len), d, dtype_code(k))
+
+
+def _cache_rows(starts, counts, p: PsaCache):
+    import torch
+
+    return (_dense(starts, (p.B,), torch.int32, "starts"), _dense(counts, (p.B,), torch.int32, "counts"))
+
+
+def _kv4(k_codes, k_scales, v_codes, v_scales, B, nkv, max_len, d):
+    import torch
+
+    codes, scales = (B, nkv, max_len, d // 2), (B, nkv, max_len, d // 32)
+    return (_dense(k_codes, codes, torch.uint8, "k_codes"), _dense(k_scales, scales, torch.bfloat16, "k_scales"),
+            _dense(v_codes, codes, torch.uint8, "v_codes"), _dense(v_scales, scales, torch.bfloat16, "v_scales"))
+
+
+def psa_kv_append(k, v, starts, counts, k_cache, v_cache, stream=None):
+    p = cache_of(k, k_cache.shape[2])
+    cache = (p.B, p.num_kv_heads, p.max_len, p.head_dim)
+    _on_device("psa_kv_append", (k, v, starts, counts, k_cache, v_cache), stream, _rows(k, k.shape, k.dtype, "k"),
+               _rows(v, k.shape, k.dtype, "v"), *_cache_rows(starts, counts, p),
+               _rows(k_cache, cache, k.dtype, "k_cache"), _rows(v_cache, cache, k.dtype, "v_cache"), p)
+
+
+def psa_kv4_append(k, v, starts, counts, k_codes, k_scales, v_codes, v_scales, stream=None):
+    p = cache_of(k, k_codes.shape[2])
+    cache = (k_codes, k_scales, v_codes, v_scales)
+    _on_device("psa_kv4_append", (k, v, starts, counts, *cache), stream, _rows(k, k.shape, k.dtype, "k"),
+               _rows(v, k.shape, k.dtype, "v"), *_cache_rows(starts, counts, p),
+               *_kv4(*cache, p.B, p.num_kv_heads, p.max_len, p.head_dim), p)
+
+
+def psa_kv4_read(k_codes, k_scales, v_codes, v_scales, k, v, stream=None):
+    """Rows 0 .. N - 1 of the cache into k and v [B, num_kv_heads, N, d]."""
+    p = cache_of(k, k_codes.shape[2])
+    cache = (k_codes, k_scales, v_codes, v_scales)
+    _on_device("psa_kv4_read", (k, v, *cache), stream, *_kv4(*cache, p.B, p.num_kv_heads, p.max_len, p.head_dim),
+               _rows(k, k.shape, k.dtype, "k"), _rows(v, k.shape, k.dtype, "v"), p)
+
+
+def psa_window_attn_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, lens, o, workspace, win: PsaWindow,
+                               scale: float, stream=None):
+    cache = (k_codes, k_scales, v_codes, v_scales)
+    vq, vo = _window_views(((q, "q", "q"), (o, "q", "o")), q.dtype, win)
+    _on_device("psa_window_attn_decode_kv4", (q, *cache, lens, o, workspace), stream, vq,
+               *_kv4(*cache, win.B, win.num_kv_heads, win.n_k, win.head_dim), _lens(lens, win), vo,
+               *_workspace(workspace, "psa_window_attn_decode_kv4"), win, float(scale))
 
 
 def psa_get_last_device_error(stream=None) -> int:

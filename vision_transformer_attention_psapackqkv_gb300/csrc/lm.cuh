@@ -91,6 +91,7 @@ struct Window {
 template <int BN>
 struct KeyTiles {
   int sink, first, count;  // sink tiles 0 .. sink - 1, then first .. ; count in all
+  KeyTiles() = default;
   __device__ __forceinline__ KeyTiles(const Window& w, int len, int p0, int p1) {
     if (p0 > p1) {
       sink = first = count = 0;
@@ -124,6 +125,8 @@ struct WindowArgs {
   float* delta;        // [B, nh, n_q]: rowsum(dO o O), in the workspace
   float scale;
 };
+// Tensor cores (window_fwd.cu).
+cudaError_t launch_window_fwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cudaStream_t st);
 // CUDA cores (window_simt.cu).
 template <typename T>
 cudaError_t launch_window_fwd_simt(const WindowArgs<T>& a, int d, cudaStream_t st);

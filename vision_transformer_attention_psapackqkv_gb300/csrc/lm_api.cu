@@ -156,7 +156,10 @@ template <typename T>
 psa_status_t run_window_fwd(psa::WindowArgs<T> a, psa_rows_t o, float* lse, int d, cudaStream_t st) {
   a.out = view<T>(o);
   a.lse = lse;
-  return from_cuda(psa::launch_window_fwd_simt(a, d, st));
+  if constexpr (sizeof(T) == 2)
+    return from_cuda(psa::launch_window_fwd_tc(a, d, st));
+  else
+    return from_cuda(psa::launch_window_fwd_simt(a, d, st));
 }
 
 template <typename T>

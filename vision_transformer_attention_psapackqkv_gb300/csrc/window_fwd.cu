@@ -1,0 +1,487 @@
+// window_fwd.cu -- attention with a sliding window and first tokens that stay visible:
+// forward on tensor cores (tcgen05, bf16).
+//
+//   S = Q K^T, P = 2^(scale log2(e) S - m), O = sum P V / sum P over the visible keys, with
+//   the running maximum m and sum of an online softmax; lse = ln(sum P) + m ln 2.
+//
+// Bound by the tensor cores at head dim 128: of a 128 x 128 tile's 2 x 512 cycles there, the
+// exponentials take 512 of the multi-function units.  So the kernel is built to keep that
+// pipe fed: a persistent CTA per SM with two slots of 128 query rows, whose softmax steps
+// run while the other slot's products do.  The two slots share the key/value tiles: two query
+// heads of one key/value head at the same rows where their number is even (equal tile
+// lists), two neighbouring row tiles of one head otherwise.
+//   warps 0-3, 4-7   softmax of slot 0, 1: one thread per row (TMEM lane), 128 columns
+//   warp 8           TMA producer: Q of both slots, K and V tiles in one ring
+//   warps 9, 10      issuer of slot 0, 1 (one thread): per key tile O += P V, then the next
+//                    tile's S = Q K^T right behind it: P lies in S's own columns of tensor
+//                    memory, and products of one thread complete in order, so neither
+//                    waits for the other in software, and s_full says that both are done
+//   warp 11          zeroes the rows of padding of V tiles (0 times NaN is NaN)
+// Only tiles that some row of the pair sees are visited: the sinks' tiles, then the
+// window's; masks are applied where a tile is not wholly visible.  O is rescaled only when a
+// row's maximum grows by more than 2^8 (O and the sum share the stale maximum, so the result
+// is the same).  P is rounded to bf16 for the product with V, as its operand; the sum is of
+// the unrounded values.
+#include <math.h>
+
+#include <algorithm>
+
+#include "window_tc.cuh"
+
+namespace psa {
+namespace {
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kThreads = 384;
+  static constexpr int kProducer = 8, kIssuer = 9, kFixer = 11;
+  // shared memory that a CTA can have, less barriers and alignment, cut into tiles
+  static constexpr int STAGES = D == 128 ? 5 : 10;
+  static constexpr uint32_t TILE = kTileBytes<D>;
+  static constexpr uint32_t OFF_KV = 2 * TILE, OFF_BAR = OFF_KV + STAGES * TILE;
+  static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  // tensor memory: S of both slots (P in its first half), O of both slots
+  static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
+};
+
+struct Bars {
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], done[2], fixed;
+  uint64_t kv_full[10], kv_empty[10];
+};
+
+struct FwdParams {
+  Window w;
+  View<__nv_bfloat16> out;
+  float* lse;
+  float sl2;       // scale * log2(e)
+  int units, row_tiles;
+  bool head_pairs;  // the slots are two heads (else two row tiles of one head)
+};
+
+// Where a slot's rows are and what they see.
+struct Slot {
+  int h, row0, p0, p1;  // positions of its rows, clipped to the visible ones (empty: p0 > p1)
+};
+
+struct Unit {
+  int b, hk, len;
+  Slot s[2];
+  __device__ __forceinline__ Unit(const FwdParams& a, int u) {
+    const Window& w = a.w;
+    const int group = w.nh / w.nkv;
+    // the last row tiles see the most keys in a causal problem: they go first
+    int tile, h;
+    if (a.head_pairs) {
+      const int pairs = w.B * w.nh / 2;
+      tile = a.row_tiles - 1 - u / pairs;
+      const int x = u % pairs;
+      b = x / (w.nh / 2);
+      h = 2 * (x % (w.nh / 2));
+    } else {
+      const int heads = w.B * w.nh;
+      tile = 2 * ((a.row_tiles + 1) / 2 - 1 - u / heads);
+      const int x = u % heads;
+      b = x / w.nh;
+      h = x % w.nh;
+    }
+    hk = h / group;
+    len = w.len(b);
+    const int off = w.nk - w.nq;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s[i].h = a.head_pairs ? h + i : h;
+      s[i].row0 = (a.head_pairs ? tile : tile + i) * kTile;
+      s[i].p0 = max(0, s[i].row0 + off);
+      s[i].p1 = min(len, min(s[i].row0 + kTile, w.nq) + off) - 1;
+    }
+  }
+};
+
+// The tiles a unit visits (those of both slots), and which of them a slot takes part in.
+struct Walk {
+  KeyTiles<kTile> all;
+  int sink[2], first[2], last[2];
+  static __device__ __forceinline__ int lo(const Unit& u) {
+    return u.s[0].p0 > u.s[0].p1 ? u.s[1].p0 : u.s[1].p0 > u.s[1].p1 ? u.s[0].p0 : min(u.s[0].p0, u.s[1].p0);
+  }
+  static __device__ __forceinline__ int hi(const Unit& u) {
+    return u.s[0].p0 > u.s[0].p1 ? u.s[1].p1 : u.s[1].p0 > u.s[1].p1 ? u.s[0].p1 : max(u.s[0].p1, u.s[1].p1);
+  }
+  __device__ __forceinline__ Walk(const Window& w, const Unit& u) : all(w, u.len, lo(u), hi(u)) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool some = u.s[i].p0 <= u.s[i].p1;
+      const int top = min(u.len - 1, u.s[i].p1 + w.right);
+      first[i] = max(0, u.s[i].p0 - w.left) / kTile;
+      last[i] = some ? top / kTile : -1;
+      sink[i] = some && w.sinks > 0 ? (min(w.sinks, top + 1) + kTile - 1) / kTile : 0;
+    }
+  }
+  __device__ __forceinline__ bool takes(int slot, int tile) const {
+    return tile < sink[slot] || (tile >= first[slot] && tile <= last[slot]);
+  }
+};
+
+// Unit of CTA c in its round i: CTA order in even rounds, reverse order in odd ones, so that
+// with units from long to short no CTA collects the long ones.
+__device__ __forceinline__ int unit_of(int i) {
+  return i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+    window_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const FwdParams a) {
+  using C = Cfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = align1024(smem_raw);
+  const uint32_t sbase = smem_addr(smem);
+  Bars& bar = *reinterpret_cast<Bars*>(smem + C::OFF_BAR);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(&bar + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_at + 1);
+  static_assert(sizeof(Bars) + 16 <= 512, "barriers");
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.q_full[i], 1);
+      mbar_init(&bar.q_empty[i], 1);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], kTile);
+      mbar_init(&bar.o_full[i], 1);
+      mbar_init(&bar.done[i], 1);
+    }
+    mbar_init(&bar.fixed, 1);
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&bar.kv_full[i], 1);
+      mbar_init(&bar.kv_empty[i], 2);  // one arrival per slot
+    }
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::kFixer) {
+    tmem_alloc(tmem_at, C::TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp >= 8) {
+    if (warp == C::kProducer) {
+      // ------------------------------------------------------------ TMA producer
+      if (lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        bool ok = true;
+        int q_count[2] = {0, 0}, kv = 0;
+        for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+          const Unit u(a, unit_of(i));
+          const Walk walk(a.w, u);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (walk.last[s] < 0 || !ok) continue;
+            const int n = q_count[s];
+            if (n >= 1 && !mbar_wait(&bar.q_empty[s], (n - 1) & 1, abort)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&bar.q_full[s], C::TILE);
+            load_tile<D>(smem + s * C::TILE, &tmQ, &bar.q_full[s], u.s[s].row0, u.s[s].h, u.b);
+            q_count[s] = n + 1;
+          }
+          for (int t = 0; ok && t < 2 * walk.all.count; ++t, ++kv) {
+            const int st = kv % C::STAGES;
+            if (kv >= C::STAGES && !mbar_wait(&bar.kv_empty[st], (kv / C::STAGES - 1) & 1, abort)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&bar.kv_full[st], C::TILE);
+            load_tile<D>(smem + C::OFF_KV + st * C::TILE, (t & 1) ? &tmV : &tmK, &bar.kv_full[st],
+                         walk.all.tile(t >> 1) * kTile, u.hk, u.b);
+          }
+        }
+        if (*abort) {
+          // let the copies in flight land before the CTA exits
+          for (int s = 0; s < 2; ++s)
+            if (q_count[s] > 0) drain_wait(&bar.q_full[s], (q_count[s] - 1) & 1);
+          for (int n = max(0, kv - C::STAGES); n < kv; ++n)
+            drain_wait(&bar.kv_full[n % C::STAGES], (n / C::STAGES) & 1);
+        }
+      }
+    } else if (warp < C::kFixer) {
+      // ------------------------------------------------------------ issuer of a slot
+      const int s = warp - C::kIssuer;
+      if (lane == 0) {
+        const uint64_t dQ = desc_rows_by_channels(sbase + s * C::TILE);
+        const uint64_t dK0 = desc_rows_by_channels(sbase + C::OFF_KV);
+        const uint64_t dV0 = desc_channels_by_rows(sbase + C::OFF_KV);
+        const uint32_t tS = tmem + C::TM_S + 128 * s, tO = tmem + C::TM_O + D * s;
+        const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t idO = idesc_bf16_f32(128, D, false, true);
+        bool ok = true;
+        int kv0 = 0, q_count = 0, steps = 0, fixes = 0;  // kv0: ring index of the unit's first K
+        auto wait_kv = [&](int n) { return mbar_wait(&bar.kv_full[n % C::STAGES], (n / C::STAGES) & 1, abort); };
+        for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+          const Unit u(a, unit_of(i));
+          const Walk walk(a.w, u);
+          const int n = walk.all.count;
+          const int edge = u.len % kTile != 0 && u.len < a.w.nk ? u.len / kTile : -1;
+          // S of the unit's entry e, or its release
+          auto issue_s = [&](int e) -> bool {
+            const int kn = kv0 + 2 * e, st = kn % C::STAGES;
+            if (!wait_kv(kn)) return false;
+            if (!walk.takes(s, walk.all.tile(e))) {
+              mbar_arrive(&bar.kv_empty[st]);
+              return true;
+            }
+            tc_fence_after();
+            const uint64_t dK = dK0 + (uint64_t)(st * C::TILE >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16(tS, dQ + kstep_channels(kk), dK + kstep_channels(kk), idS, kk > 0 ? 1u : 0u);
+            mma_commit(&bar.s_full[s]);
+            mma_commit(&bar.kv_empty[st]);
+            if (walk.all.tile(e) == walk.last[s]) mma_commit(&bar.q_empty[s]);  // the next unit's Q may come
+            return true;
+          };
+          const bool mine = walk.last[s] >= 0;
+          if (mine && n > 0) ok = mbar_wait(&bar.q_full[s], q_count & 1, abort);
+          bool first = true;
+          if (ok && n > 0) ok = issue_s(0);
+          for (int e = 0; ok && e < n; ++e) {
+            const int tile = walk.all.tile(e), vn = kv0 + 2 * e + 1, st = vn % C::STAGES;
+            if (walk.takes(s, tile)) {
+              if (!mbar_wait(&bar.p_full[s], steps & 1, abort) || !wait_kv(vn) ||
+                  (tile == edge && !mbar_wait(&bar.fixed, fixes & 1, abort))) {
+                ok = false;
+                break;
+              }
+              ++steps;
+              tc_fence_after();
+              const uint64_t dV = dV0 + (uint64_t)(st * C::TILE >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                mma_bf16_ts(tO, tS + 8 * kk, dV + kk * kKstepRows, idO, !first || kk > 0 ? 1u : 0u);
+              first = false;
+              mma_commit(&bar.kv_empty[st]);
+            } else {
+              if (!wait_kv(vn) || (tile == edge && !mbar_wait(&bar.fixed, fixes & 1, abort))) {
+                ok = false;
+                break;
+              }
+              mbar_arrive(&bar.kv_empty[st]);
+            }
+            if (tile == edge) ++fixes;
+            if (e + 1 < n && !issue_s(e + 1)) ok = false;
+          }
+          if (ok && mine) {
+            mma_commit(&bar.o_full[s]);
+            ++q_count;
+          }
+          kv0 += 2 * n;
+        }
+        mma_commit(&bar.done[s]);
+        drain_wait(&bar.done[s], 0);
+      }
+    } else {
+      // ------------------------------------------------------------ rows of padding in V
+      int kv0 = 0;
+      for (int i = 0; unit_of(i) < a.units; ++i) {
+        const Unit u(a, unit_of(i));
+        const Walk walk(a.w, u);
+        const int n = walk.all.count;
+        // rows past n_k are zero already (TMA's fill)
+        const int edge = u.len % kTile != 0 && u.len < a.w.nk ? u.len / kTile : -1;
+        if (edge >= 0 && n > 0 && walk.all.tile(n - 1) == edge) {
+          const int vn = kv0 + 2 * (n - 1) + 1, st = vn % C::STAGES;
+          if (!mbar_wait(&bar.kv_full[st], (vn / C::STAGES) & 1, abort)) break;
+          zero_rows<D>(smem + C::OFF_KV + st * C::TILE, u.len % kTile, kTile, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.fixed);
+        }
+        kv0 += 2 * n;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax of a slot
+    const int s = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + C::TM_S + 128 * s + lanes, tO = tmem + C::TM_O + D * s + lanes;
+    const int off = a.w.nk - a.w.nq;
+    int steps = 0, outs = 0;
+    bool ok = true;
+    for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+      int b, h, q, len, jhi, jlo;  // this row, and the keys it sees: none if jhi < 0
+      int whole_lo, whole_hi;      // tiles between these are seen whole by every row
+      KeyTiles<kTile> tiles;
+      {
+        const Unit u(a, unit_of(i));
+        const Slot me = s ? u.s[1] : u.s[0];
+        b = u.b;
+        h = me.h;
+        len = u.len;
+        q = me.row0 + r;
+        const int p = q + off;
+        jhi = p >= 0 && p < len && q < a.w.nq ? min(len - 1, p + a.w.right) : -1;
+        jlo = p - a.w.left;
+        tiles = KeyTiles<kTile>(a.w, len, me.p0, me.p1);
+        const bool rows = me.row0 + off >= 0 && me.row0 + off + kTile <= len && me.row0 + kTile <= a.w.nq;
+        whole_lo = me.p1 - a.w.left;
+        whole_hi = rows ? min(len, me.p0 + a.w.right + 1) : 0;
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int t = 0; t < tiles.count; ++t) {
+        const int j0 = tiles.tile(t) * kTile;
+        if (!mbar_wait(&bar.s_full[s], steps & 1, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t x[128];
+        {
+          using Chunk = uint32_t[32];
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) tmem_load32_async(tS + c, *reinterpret_cast<Chunk*>(x + c));
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) tmem_pin(*reinterpret_cast<Chunk*>(x + c));
+        }
+        if (j0 + kTile > whole_hi || (j0 < whole_lo && j0 + kTile > a.w.sinks)) {
+          const int hi = jhi - j0, lo = jlo - j0, sk = a.w.sinks - j0;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > hi || (c < lo && c >= sk)) x[c] = 0xff800000u;  // -inf
+        }
+        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+          m0 = fmax3(m0, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+          m1 = fmax3(m1, __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
+          m2 = fmax3(m2, __uint_as_float(x[c + 4]), __uint_as_float(x[c + 5]));
+          m3 = fmax3(m3, __uint_as_float(x[c + 6]), __uint_as_float(x[c + 7]));
+        }
+        const float mx = fmax3(m0, m1, fmaxf(m2, m3)) * a.sl2;
+        float alpha = 1.f;
+        if (mx > m + 8.f || t == 0) {
+          // -inf - -inf: a row that has seen nothing yet has nothing to rescale
+          alpha = m == -INFINITY ? 0.f : fast_exp2(m - mx);
+          m = mx;
+        }
+        if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // s_full says that every product issued before this S is done, O's among them
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_load32(tO + c, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= alpha;
+            tmem_store32(tO + c, o);
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        const float2 sl = make_float2(a.sl2, a.sl2), nm = make_float2(-base, -base);
+        float2 l01 = make_float2(0.f, 0.f), l23 = l01;
+#pragma unroll
+        for (int c = 0; c < 128; c += 4) {
+          const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl, nm);
+          const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sl, nm);
+          const float2 p01 = make_float2(fast_exp2(x01.x), fast_exp2(x01.y));
+          const float2 p23 = make_float2(fast_exp2(x23.x), fast_exp2(x23.y));
+          l01 = __fadd2_rn(l01, p01);
+          l23 = __fadd2_rn(l23, p23);
+          x[c / 2] = pack2(p01.x, p01.y);
+          x[c / 2 + 1] = pack2(p23.x, p23.y);
+        }
+        l = l * alpha + ((l01.x + l01.y) + (l23.x + l23.y));
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) tmem_store16_async(tS + c, x + c);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar.p_full[s]);
+        ++steps;
+      }
+      if (!ok) break;
+      // ---- the rows' results
+      const bool some = tiles.count > 0;
+      if (some) {
+        if (!mbar_wait(&bar.o_full[s], outs & 1, abort)) break;
+        ++outs;
+        tc_fence_after();
+      }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const bool in = q < a.w.nq;
+      __nv_bfloat16* dst = a.out.row(b, h, in ? q : 0);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (some) {
+          tmem_load32(tO + c, o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] *= inv;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+        }
+        if (in) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4*>(dst + c + k) =
+                make_uint4(pack2(o[k], o[k + 1]), pack2(o[k + 2], o[k + 3]), pack2(o[k + 4], o[k + 5]),
+                           pack2(o[k + 6], o[k + 7]));
+        }
+      }
+      tc_fence_before();
+      if (in && a.lse)
+        a.lse[((long long)b * a.w.nh + h) * a.w.nq + q] =
+            l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kFixer) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+template <int D>
+cudaError_t fwd(const WindowArgs<__nv_bfloat16>& x, cudaStream_t st) {
+  using C = Cfg<D>;
+  const Window& w = x.w;
+  CUtensorMap mq, mk, mv;
+  if (!map_view(&mq, x.q.p, x.q.sb, x.q.sh, x.q.sn, w.B, w.nh, w.nq, D) ||
+      !map_view(&mk, x.k.p, x.k.sb, x.k.sh, x.k.sn, w.B, w.nkv, w.nk, D) ||
+      !map_view(&mv, x.v.p, x.v.sb, x.v.sh, x.v.sn, w.B, w.nkv, w.nk, D))
+    return cudaErrorInvalidValue;
+  FwdParams a{};
+  a.w = w;
+  a.out = x.out;
+  a.lse = x.lse;
+  a.sl2 = x.scale * kLog2;
+  a.row_tiles = (w.nq + kTile - 1) / kTile;
+  a.head_pairs = (w.nh / w.nkv) % 2 == 0;
+  a.units = a.head_pairs ? w.B * w.nh / 2 * a.row_tiles : w.B * w.nh * ((a.row_tiles + 1) / 2);
+  auto kern = window_fwd_tc_kernel<D>;
+  const cudaError_t e = set_max_dynamic_smem((const void*)kern, C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(std::min(a.units, device_sm_count())), dim3(C::kThreads), C::SMEM, st,
+                    mq, mk, mv, a);
+}
+
+}  // namespace
+
+cudaError_t launch_window_fwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cudaStream_t st) {
+  return d == 64 ? fwd<64>(a, st) : fwd<128>(a, st);
+}
+
+}  // namespace psa

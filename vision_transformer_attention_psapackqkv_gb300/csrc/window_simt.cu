@@ -380,7 +380,6 @@ cudaError_t launch_window_bwd_simt(const WindowArgs<T>& a, int d, cudaStream_t s
   return d == 64 ? bwd<T, 64>(a, st) : bwd<T, 128>(a, st);
 }
 template cudaError_t launch_window_fwd_simt(const WindowArgs<float>&, int, cudaStream_t);
-template cudaError_t launch_window_fwd_simt(const WindowArgs<__nv_bfloat16>&, int, cudaStream_t);
 template cudaError_t launch_window_bwd_simt(const WindowArgs<float>&, int, cudaStream_t);
 template cudaError_t launch_window_bwd_simt(const WindowArgs<__nv_bfloat16>&, int, cudaStream_t);
 

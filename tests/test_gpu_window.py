@@ -86,6 +86,19 @@ def test_chunk_behind_a_prefix_in_a_padded_batch(dtype):
     _check(q, k, v, do, lens, 100, 0, 2, 0.2)
 
 
+@pytest.mark.parametrize("nh,nkv", [(8, 8), (8, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_short_sequences_in_a_padded_batch(nh, nkv, d):
+    """Several units per CTA, each of one or two tiles that a sequence ends in."""
+    Bn, n = 90, 140
+    q, k, v, do = _inputs(Bn, nh, nkv, n, n, d, BF16, 19)
+    lens = [(37 * b) % (n + 1) for b in range(Bn)]
+    for b, m in enumerate(lens):
+        for t in (q, k, v, do):
+            t[b, :, m:] = math.nan
+    _check(q, k, v, do, lens, 100, 0, 3, 0.1)
+
+
 @pytest.mark.parametrize("nh,nkv", [(1, 1), (5, 1), (8, 8), (6, 2), (7, 7), (16, 1), (40, 8)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_shared_heads(nh, nkv, d):

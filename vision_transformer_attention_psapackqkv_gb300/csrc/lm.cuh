@@ -122,11 +122,13 @@ struct WindowArgs {
   View<const T> q, k, v, o, dO;
   View<T> out, dq, dk, dv;
   float* lse;          // [B, nh, n_q]; forward: written (or null), backward: read
-  float* delta;        // [B, nh, n_q]: rowsum(dO o O), in the workspace
+  float* delta;        // the backward's workspace; CUDA cores: rowsum(dO o O), [B, nh, n_q]
   float scale;
 };
-// Tensor cores (window_fwd.cu).
+// Tensor cores (window_fwd.cu, window_bwd.cu); delta points at the backward's workspace.
 cudaError_t launch_window_fwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cudaStream_t st);
+cudaError_t launch_window_bwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cudaStream_t st);
+size_t window_bwd_tc_ws_bytes(const Window& w);
 // CUDA cores (window_simt.cu).
 template <typename T>
 cudaError_t launch_window_fwd_simt(const WindowArgs<T>& a, int d, cudaStream_t st);

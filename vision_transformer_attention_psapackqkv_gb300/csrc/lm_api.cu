@@ -173,7 +173,10 @@ psa_status_t run_window_bwd(psa::WindowArgs<T> a, psa_rows_t o, psa_rows_t dO, c
   a.dq = view<T>(dq);
   a.dk = view<T>(dk);
   a.dv = view<T>(dv);
-  return from_cuda(psa::launch_window_bwd_simt(a, d, st));
+  if constexpr (sizeof(T) == 2)
+    return from_cuda(psa::launch_window_bwd_tc(a, d, st));
+  else
+    return from_cuda(psa::launch_window_bwd_simt(a, d, st));
 }
 
 // ---------------------------------------------------------------- caches
@@ -290,7 +293,9 @@ psa_status_t psa_window_attn_fwd(psa_rows_t q, psa_rows_t k, psa_rows_t v, const
 }
 
 size_t psa_window_attn_bwd_workspace_size(psa_window_t p) {
-  return check_window(p) == PSA_OK ? round256((size_t)p.B * p.num_heads * p.n_q * 4) : 0;
+  if (check_window(p) != PSA_OK) return 0;
+  return round256(p.dtype == PSA_DTYPE_BF16 ? psa::window_bwd_tc_ws_bytes(window(p, nullptr))
+                                            : (size_t)p.B * p.num_heads * p.n_q * 4);
 }
 
 psa_status_t psa_window_attn_bwd(psa_rows_t q, psa_rows_t k, psa_rows_t v, psa_rows_t o,

@@ -1,0 +1,794 @@
+// window_bwd.cu -- attention with a sliding window and first tokens that stay visible:
+// backward on tensor cores (tcgen05, bf16), a kernel for dQ and one for dK and dV.
+//
+//   P = 2^(scale log2(e) S - lse log2(e)), S = Q K^T over the visible keys,
+//   dP = dO V^T, dS = P o (dP - delta), delta = rowsum(dO o O),
+//   dQ = scale dS K;  dV = P^T dO, dK = scale dS^T Q.
+//
+// Bound by the tensor cores: 3 products per tile pair for dQ and 4 for dK and dV, where five
+// would do if dQ were added up across the CTAs that own the keys.  That sum would need atomics,
+// whose order changes results, or a partial dQ per key tile; two kernels need neither, and
+// each gradient is summed by one CTA in a fixed order, over the query heads that share a
+// key/value head too.
+//
+// Both kernels: a persistent CTA per SM, 256 row threads (two per row of tensor memory, each
+// 64 of the 128 columns), a TMA producer, two issuing threads, and a warp that zeroes the
+// rows of padding where they are an operand (0 times NaN is NaN).  bf16 operands made by the
+// row threads stay in tensor memory: each thread writes them over the columns that it read.
+// Products that must follow one another on the same columns are issued by one thread, whose
+// products complete in order:
+//   dQ kernel     issuer 0: S into two buffers; issuer 1: dP, then behind it dQ += dS K, whose
+//                 dS lies in dP's columns
+//   dK/dV kernel  S^T = K Q^T and dP^T = V dO^T have keys as rows; issuer 0: S^T, dV += P^T dO;
+//                 issuer 1: dP^T, dK += dS^T Q.  While the row threads turn S^T into P^T, the
+//                 products of dP^T's side run, and the other way round.
+// delta and lse come from a small kernel in front, per row as (lse log2(e), delta), in rows
+// padded to whole tiles, so that a tile's 1024 bytes are one bulk copy.
+#include <math.h>
+
+#include <algorithm>
+
+#include "window_tc.cuh"
+
+namespace psa {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kProducer = 8, kIssuer = 9, kFixer = 11;
+
+struct BwdParams {
+  Window w;
+  View<__nv_bfloat16> dq, dk, dv;
+  const float2* stat;  // [B, nh, row_tiles * 128] (lse log2(e), delta)
+  float scale, sl2;
+  int units, row_tiles, key_tiles;
+};
+
+// Unit of this CTA in its round i (from long to short: CTA order, then reverse order).
+__device__ __forceinline__ int unit_of(int i) {
+  return i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// (lse log2(e), delta) of every row; rows that see nothing, and those behind n_q, get (0, 0):
+// their scores are masked.  One row per LANES lanes.
+template <int D>
+__global__ void __launch_bounds__(256)
+    window_stat_kernel(const WindowArgs<__nv_bfloat16> a, float2* stat, int padded) {
+  constexpr int LANES = D / 8;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lr = threadIdx.x % LANES, i = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const int b = blockIdx.y / a.w.nh, h = blockIdx.y % a.w.nh;
+  const int p = i + a.w.nk - a.w.nq;
+  const bool live = i < a.w.nq && p >= 0 && p < a.w.len(b);
+  float s = 0.f, lse = 0.f;
+  if (live) {
+    float x[8], y[8];
+    unpack_vec(*reinterpret_cast<const uint4*>(a.dO.row(b, h, i) + 8 * lr), x);
+    unpack_vec(*reinterpret_cast<const uint4*>(a.o.row(b, h, i) + 8 * lr), y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += x[e] * y[e];
+    lse = a.lse[(long long)blockIdx.y * a.w.nq + i];
+  }
+#pragma unroll
+  for (int m = LANES / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+  if (lr == 0 && i < padded) stat[(long long)blockIdx.y * padded + i] = make_float2(lse * kLog2, s);
+}
+
+// ---------------------------------------------------------------- dQ
+template <int D>
+struct DqCfg {
+  static constexpr uint32_t TILE = kTileBytes<D>;
+  static constexpr int KST = D == 128 ? 3 : 4, VST = D == 128 ? 2 : 4;
+  static constexpr uint32_t OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KST * TILE;
+  static constexpr uint32_t OFF_BAR = OFF_V + VST * TILE, SMEM = OFF_BAR + 512 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static constexpr uint32_t TM_S = 0, TM_DP = 256, TM_DQ = 384;  // S: two buffers
+};
+struct DqBars {
+  uint64_t q_full, q_empty, do_full, do_empty, k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t k_fixed[4], s_full[2], s_free[2], dp_full, ds_full, dq_full, done[2];
+};
+
+// A unit of the dQ kernel: 128 query rows of a head.
+struct DqUnit {
+  int b, h, hk, row0, len, edge;
+  KeyTiles<kTile> tiles;
+  int p0, p1;
+  __device__ __forceinline__ DqUnit(const BwdParams& a, int u) {
+    const Window& w = a.w;
+    const int heads = w.B * w.nh, x = u % heads;
+    b = x / w.nh;
+    h = x % w.nh;
+    hk = h / (w.nh / w.nkv);
+    row0 = (a.row_tiles - 1 - u / heads) * kTile;
+    len = w.len(b);
+    const int off = w.nk - w.nq;
+    p0 = max(0, row0 + off);
+    p1 = min(len, min(row0 + kTile, w.nq) + off) - 1;
+    tiles = KeyTiles<kTile>(w, len, p0, p1);
+    // the key tile with rows of padding, always the last one if it is visited
+    edge = len % kTile != 0 && len < w.nk ? len / kTile : -1;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
+                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const BwdParams a) {
+  using C = DqCfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = align1024(smem_raw);
+  const uint32_t sbase = smem_addr(smem);
+  DqBars& bar = *reinterpret_cast<DqBars*>(smem + C::OFF_BAR);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(&bar + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_at + 1);
+  static_assert(sizeof(DqBars) + 16 <= 512, "barriers");
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bar.q_full, 1);
+    mbar_init(&bar.q_empty, 1);
+    mbar_init(&bar.do_full, 1);
+    mbar_init(&bar.do_empty, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar.k_full[i], 1);
+      mbar_init(&bar.k_empty[i], 2);  // S and dQ read it
+      mbar_init(&bar.k_fixed[i], 1);
+      mbar_init(&bar.v_full[i], 1);
+      mbar_init(&bar.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.s_free[i], 256);
+      mbar_init(&bar.done[i], 1);
+    }
+    mbar_init(&bar.dp_full, 1);
+    mbar_init(&bar.ds_full, 256);
+    mbar_init(&bar.dq_full, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kFixer) {
+    tmem_alloc(tmem_at, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == kProducer) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      bool ok = true;
+      int uc = 0, kc = 0;  // units with tiles, tiles
+      for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+        const DqUnit u(a, unit_of(i));
+        for (int t = 0; ok && t < u.tiles.count; ++t, ++kc) {
+          const int j0 = u.tiles.tile(t) * kTile, ks = kc % C::KST, vs = kc % C::VST;
+          if (kc >= C::KST && !mbar_wait(&bar.k_empty[ks], (kc / C::KST - 1) & 1, abort)) ok = false;
+          if (!ok) break;
+          if (t == 0) {
+            if (uc >= 1 && !mbar_wait(&bar.q_empty, (uc - 1) & 1, abort)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&bar.q_full, C::TILE);
+            load_tile<D>(smem, &tmQ, &bar.q_full, u.row0, u.h, u.b);
+          }
+          mbar_arrive_expect_tx(&bar.k_full[ks], C::TILE);
+          load_tile<D>(smem + C::OFF_K + ks * C::TILE, &tmK, &bar.k_full[ks], j0, u.hk, u.b);
+          if (t == 0) {
+            if (uc >= 1 && !mbar_wait(&bar.do_empty, (uc - 1) & 1, abort)) {
+              ++kc;
+              ++uc;
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&bar.do_full, C::TILE);
+            load_tile<D>(smem + C::OFF_DO, &tmDO, &bar.do_full, u.row0, u.h, u.b);
+            ++uc;
+          }
+          if (kc >= C::VST && !mbar_wait(&bar.v_empty[vs], (kc / C::VST - 1) & 1, abort)) {
+            ++kc;
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&bar.v_full[vs], C::TILE);
+          load_tile<D>(smem + C::OFF_V + vs * C::TILE, &tmV, &bar.v_full[vs], j0, u.hk, u.b);
+        }
+      }
+      if (*abort) {
+        // let the copies in flight land before the CTA exits (a wait for one that was not
+        // issued any more runs into its time limit)
+        if (uc > 0) {
+          drain_wait(&bar.q_full, (uc - 1) & 1);
+          drain_wait(&bar.do_full, (uc - 1) & 1);
+        }
+        for (int n = max(0, kc - C::KST); n < kc; ++n) drain_wait(&bar.k_full[n % C::KST], (n / C::KST) & 1);
+        for (int n = max(0, kc - C::VST); n < kc; ++n) drain_wait(&bar.v_full[n % C::VST], (n / C::VST) & 1);
+      }
+    }
+  } else if (warp == kIssuer || warp == kIssuer + 1) {
+    // ------------------------------------------------------------ issuers
+    if (lane == 0) {
+      const bool s_role = warp == kIssuer;
+      const uint64_t dQ = desc_rows_by_channels(sbase), dDO = desc_rows_by_channels(sbase + C::OFF_DO);
+      const uint64_t dK = desc_rows_by_channels(sbase + C::OFF_K), dV = desc_rows_by_channels(sbase + C::OFF_V);
+      const uint64_t dKb = desc_channels_by_rows(sbase + C::OFF_K);
+      const uint32_t idS = idesc_bf16_f32(128, 128, false, false), idQ = idesc_bf16_f32(128, D, false, true);
+      bool ok = true;
+      int kc = 0, uc = 0;
+      for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+        const DqUnit u(a, unit_of(i));
+        const int n = u.tiles.count;
+        if (n == 0) continue;
+        if (s_role) {
+          ok = mbar_wait(&bar.q_full, uc & 1, abort);
+          for (int t = 0; ok && t < n; ++t, ++kc) {
+            const int st = kc % C::KST, sb = kc & 1;
+            if (!mbar_wait(&bar.k_full[st], (kc / C::KST) & 1, abort) ||
+                (kc >= 2 && !mbar_wait(&bar.s_free[sb], (kc / 2 - 1) & 1, abort))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t dKs = dK + (uint64_t)(st * C::TILE >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16(tmem + C::TM_S + 128 * sb, dQ + kstep_channels(kk), dKs + kstep_channels(kk), idS,
+                       kk > 0 ? 1u : 0u);
+            mma_commit(&bar.s_full[sb]);
+            mma_commit(&bar.k_empty[st]);
+          }
+          if (ok) mma_commit(&bar.q_empty);
+        } else {
+          auto issue_dp = [&](int t) -> bool {
+            const int vc = kc + t, st = vc % C::VST;
+            if (!mbar_wait(&bar.v_full[st], (vc / C::VST) & 1, abort)) return false;
+            tc_fence_after();
+            const uint64_t dVs = dV + (uint64_t)(st * C::TILE >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16(tmem + C::TM_DP, dDO + kstep_channels(kk), dVs + kstep_channels(kk), idS, kk > 0 ? 1u : 0u);
+            mma_commit(&bar.dp_full);
+            mma_commit(&bar.v_empty[st]);
+            if (t == n - 1) mma_commit(&bar.do_empty);
+            return true;
+          };
+          ok = mbar_wait(&bar.do_full, uc & 1, abort) && issue_dp(0);
+          for (int t = 0; ok && t < n; ++t) {
+            const int kn = kc + t, st = kn % C::KST;
+            if (!mbar_wait(&bar.ds_full, kn & 1, abort) ||
+                !mbar_wait(&bar.k_fixed[st], (kn / C::KST) & 1, abort)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t dKs = dKb + (uint64_t)(st * C::TILE >> 4);
+            // 16 keys' dS are 8 columns; those of keys 64 .. 127 start at column 64
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ts(tmem + C::TM_DQ, tmem + C::TM_DP + 64 * (kk / 4) + 8 * (kk % 4), dKs + kk * kKstepRows,
+                          idQ, t > 0 || kk > 0 ? 1u : 0u);
+            mma_commit(&bar.k_empty[st]);
+            if (t == n - 1) mma_commit(&bar.dq_full);
+            else ok = issue_dp(t + 1);
+          }
+          kc += n;
+        }
+        ++uc;
+      }
+      mma_commit(&bar.done[warp - kIssuer]);
+      drain_wait(&bar.done[warp - kIssuer], 0);
+    }
+  } else if (warp == kFixer) {
+    // ------------------------------------------------------------ rows of padding in K
+    // Every tile passes through this warp, so that k_fixed's phases keep step with the ring.
+    int kc = 0;
+    bool ok = true;
+    for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+      const DqUnit u(a, unit_of(i));
+      for (int t = 0; t < u.tiles.count; ++t, ++kc) {
+        const int st = kc % C::KST;
+        if (!mbar_wait(&bar.k_full[st], (kc / C::KST) & 1, abort)) {
+          ok = false;
+          break;
+        }
+        if (u.tiles.tile(t) == u.edge) zero_rows<D>(smem + C::OFF_K + st * C::TILE, u.len % kTile, kTile, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.k_fixed[st]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ row threads
+    const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + C::TM_S + 64 * half + lanes, tP = tmem + C::TM_DP + 64 * half + lanes;
+    const uint32_t tQ = tmem + C::TM_DQ + lanes;
+    const int off = a.w.nk - a.w.nq;
+    int kc = 0, uc = 0;
+    bool ok = true;
+    for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+      const DqUnit u(a, unit_of(i));
+      const int q = u.row0 + r, p = q + off;
+      const int jhi = p >= 0 && p < u.len && q < a.w.nq ? min(u.len - 1, p + a.w.right) : -1;
+      const int jlo = p - a.w.left;
+      const bool rows = u.row0 + off >= 0 && u.row0 + off + kTile <= u.len && u.row0 + kTile <= a.w.nq;
+      const int whole_lo = u.p1 - a.w.left, whole_hi = rows ? min(u.len, u.p0 + a.w.right + 1) : 0;
+      const float2 st = a.stat[(long long)(u.b * a.w.nh + u.h) * a.row_tiles * kTile + q];
+      for (int t = 0; t < u.tiles.count; ++t, ++kc) {
+        const int tile0 = u.tiles.tile(t) * kTile, j0 = tile0 + 64 * half, sb = kc & 1;
+        if (!mbar_wait(&bar.s_full[sb], (kc / 2) & 1, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t x[64];
+        load_cols64(tS + 128 * sb, x);
+        tc_fence_before();
+        mbar_arrive(&bar.s_free[sb]);
+        if (tile0 + kTile > whole_hi || (tile0 < whole_lo && tile0 + kTile > a.w.sinks)) {
+          const int hi = jhi - j0, lo = jlo - j0, sk = a.w.sinks - j0;
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c > hi || (c < lo && c >= sk)) x[c] = 0xff800000u;  // -inf: P = 0
+        }
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          x[c] = __float_as_uint(fast_exp2(fmaf(__uint_as_float(x[c]), a.sl2, -st.x)));
+        if (!mbar_wait(&bar.dp_full, kc & 1, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t y[64];
+        load_cols64(tP, y);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          // a masked key's dP may be NaN (padding in V): its dS is 0 by selection
+          const float p0 = __uint_as_float(x[c]), p1 = __uint_as_float(x[c + 1]);
+          const float d0 = p0 == 0.f ? 0.f : p0 * (__uint_as_float(y[c]) - st.y);
+          const float d1 = p1 == 0.f ? 0.f : p1 * (__uint_as_float(y[c + 1]) - st.y);
+          y[c / 2] = pack2(d0, d1);
+        }
+        tmem_store16_async(tP, y);
+        tmem_store16_async(tP + 16, y + 16);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar.ds_full);
+      }
+      if (!ok) break;
+      // ---- dQ of this row: half of its channels per thread
+      const bool some = u.tiles.count > 0;
+      if (some) {
+        if (!mbar_wait(&bar.dq_full, uc & 1, abort)) break;
+        ++uc;
+        tc_fence_after();
+      }
+      const bool in = q < a.w.nq;
+      __nv_bfloat16* dst = a.dq.row(u.b, u.h, in ? q : 0) + half * (D / 2);
+#pragma unroll 1
+      for (int c = 0; c < D / 2; c += 32) {
+        float o[32];
+        if (some) {
+          tmem_load32(tQ + half * (D / 2) + c, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+        }
+        if (in) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4*>(dst + c + k) =
+                make_uint4(pack2(o[k] * a.scale, o[k + 1] * a.scale), pack2(o[k + 2] * a.scale, o[k + 3] * a.scale),
+                           pack2(o[k + 4] * a.scale, o[k + 5] * a.scale), pack2(o[k + 6] * a.scale, o[k + 7] * a.scale));
+        }
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kFixer) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- dK and dV
+template <int D>
+struct DkvCfg {
+  static constexpr uint32_t TILE = kTileBytes<D>;
+  static constexpr int ST = D == 128 ? 2 : 4;
+  static constexpr uint32_t OFF_V = TILE, OFF_Q = 2 * TILE, OFF_DO = OFF_Q + ST * TILE;
+  static constexpr uint32_t OFF_STAT = OFF_DO + ST * TILE, STAT = kTile * 8;
+  static constexpr uint32_t OFF_BAR = OFF_STAT + ST * STAT, SMEM = OFF_BAR + 512 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 384;
+};
+struct DkvBars {
+  uint64_t kv_full, kv_empty, q_full[4], q_empty[4], do_full[4], do_empty[4];
+  uint64_t q_fixed[4], do_fixed[4], s_full, p_full, dp_full, ds_full, acc_full, done[2];
+};
+
+// A unit of the dK/dV kernel: 128 key rows of a key/value head.  Its steps are the query
+// tiles that see them, for each query head of the group.
+struct DkvUnit {
+  int b, hk, k0, len, group;
+  int i0, i1;        // query rows that see a key of the tile
+  int tile0, tiles;  // the tiles of 128 they lie in
+  __device__ __forceinline__ DkvUnit(const BwdParams& a, int u) {
+    const Window& w = a.w;
+    const int heads = w.B * w.nkv, x = u % heads;
+    b = x / w.nkv;
+    hk = x % w.nkv;
+    group = w.nh / w.nkv;
+    k0 = (u / heads) * kTile;  // the first keys are seen by the most queries
+    len = w.len(b);
+    int n;
+    query_range(w, len, k0, min(k0 + kTile, w.nk) - 1, i0, n);
+    i1 = i0 + n;
+    tile0 = i0 / kTile;
+    tiles = n > 0 ? (i1 - 1) / kTile - tile0 + 1 : 0;
+  }
+  __device__ __forceinline__ int steps() const { return group * tiles; }
+  // a tile that holds rows that see nothing: rows of padding, or in front of position 0
+  __device__ __forceinline__ void valid(const Window& w, int row0, int& lo, int& hi) const {
+    const int off = w.nk - w.nq;
+    lo = max(0, -off - row0);
+    hi = min(kTile, len - off - row0);
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
+                          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                          const BwdParams a) {
+  using C = DkvCfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = align1024(smem_raw);
+  const uint32_t sbase = smem_addr(smem);
+  DkvBars& bar = *reinterpret_cast<DkvBars*>(smem + C::OFF_BAR);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(&bar + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_at + 1);
+  static_assert(sizeof(DkvBars) + 16 <= 512, "barriers");
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bar.kv_full, 1);
+    mbar_init(&bar.kv_empty, 2);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar.q_full[i], 1);
+      mbar_init(&bar.q_empty[i], 2);  // S^T and dK read Q
+      mbar_init(&bar.do_full[i], 1);
+      mbar_init(&bar.do_empty[i], 2);  // dP^T and dV read dO
+      mbar_init(&bar.q_fixed[i], 1);
+      mbar_init(&bar.do_fixed[i], 1);
+    }
+    mbar_init(&bar.s_full, 1);
+    mbar_init(&bar.p_full, 256);
+    mbar_init(&bar.dp_full, 1);
+    mbar_init(&bar.ds_full, 256);
+    mbar_init(&bar.acc_full, 2);
+    mbar_init(&bar.done[0], 1);
+    mbar_init(&bar.done[1], 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kFixer) {
+    tmem_alloc(tmem_at, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == kProducer) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      bool ok = true;
+      int uc = 0, qc = 0;
+      for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+        const DkvUnit u(a, unit_of(i));
+        const int n = u.steps();
+        if (n == 0) continue;
+        if (uc >= 1 && !mbar_wait(&bar.kv_empty, (uc - 1) & 1, abort)) break;
+        mbar_arrive_expect_tx(&bar.kv_full, 2 * C::TILE);
+        load_tile<D>(smem, &tmK, &bar.kv_full, u.k0, u.hk, u.b);
+        load_tile<D>(smem + C::OFF_V, &tmV, &bar.kv_full, u.k0, u.hk, u.b);
+        ++uc;
+        int h = u.hk * u.group, tile = u.tile0;
+        for (int t = 0; t < n; ++t, ++qc) {
+          const int st = qc % C::ST, par = (qc / C::ST - 1) & 1;
+          if (qc >= C::ST && (!mbar_wait(&bar.q_empty[st], par, abort) || !mbar_wait(&bar.do_empty[st], par, abort))) {
+            ok = false;
+            break;
+          }
+          // lse and delta travel with Q: S^T is the first to need them
+          mbar_arrive_expect_tx(&bar.q_full[st], C::TILE + C::STAT);
+          load_tile<D>(smem + C::OFF_Q + st * C::TILE, &tmQ, &bar.q_full[st], tile * kTile, h, u.b);
+          bulk_load(smem + C::OFF_STAT + st * C::STAT,
+                    a.stat + ((long long)(u.b * a.w.nh + h) * a.row_tiles + tile) * kTile, C::STAT, &bar.q_full[st]);
+          mbar_arrive_expect_tx(&bar.do_full[st], C::TILE);
+          load_tile<D>(smem + C::OFF_DO + st * C::TILE, &tmDO, &bar.do_full[st], tile * kTile, h, u.b);
+          if (++tile == u.tile0 + u.tiles) {
+            tile = u.tile0;
+            ++h;
+          }
+        }
+      }
+      if (*abort) {
+        if (uc > 0) drain_wait(&bar.kv_full, (uc - 1) & 1);
+        for (int n = max(0, qc - C::ST); n < qc; ++n) {
+          drain_wait(&bar.q_full[n % C::ST], (n / C::ST) & 1);
+          drain_wait(&bar.do_full[n % C::ST], (n / C::ST) & 1);
+        }
+      }
+    }
+  } else if (warp == kIssuer || warp == kIssuer + 1) {
+    // ------------------------------------------------------------ issuers
+    // Role 0: S^T = K Q^T and dV += P^T dO.  Role 1: dP^T = V dO^T and dK += dS^T Q.
+    if (lane == 0) {
+      const int role = warp - kIssuer;
+      const uint64_t dA = desc_rows_by_channels(sbase + (role ? C::OFF_V : 0));
+      const uint64_t dB = desc_rows_by_channels(sbase + (role ? C::OFF_DO : C::OFF_Q));
+      const uint64_t dG = desc_channels_by_rows(sbase + (role ? C::OFF_Q : C::OFF_DO));
+      uint64_t* first_full = role ? bar.do_full : bar.q_full;    // operand of the scores
+      uint64_t* first_empty = role ? bar.do_empty : bar.q_empty;
+      uint64_t* second_full = role ? bar.q_fixed : bar.do_fixed;  // operand of the gradient
+      uint64_t* second_empty = role ? bar.q_empty : bar.do_empty;
+      uint64_t* scores = role ? &bar.dp_full : &bar.s_full;
+      uint64_t* ready = role ? &bar.ds_full : &bar.p_full;
+      const uint32_t tX = tmem + (role ? C::TM_DP : C::TM_S), tG = tmem + (role ? C::TM_DK : C::TM_DV);
+      const uint32_t idS = idesc_bf16_f32(128, 128, false, false), idG = idesc_bf16_f32(128, D, false, true);
+      bool ok = true;
+      int qc = 0, uc = 0;
+      for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+        const DkvUnit u(a, unit_of(i));
+        const int n = u.steps();
+        if (n == 0) continue;
+        auto issue_scores = [&](int t) -> bool {
+          const int c = qc + t, st = c % C::ST;
+          if (!mbar_wait(&first_full[st], (c / C::ST) & 1, abort)) return false;
+          tc_fence_after();
+          const uint64_t d = dB + (uint64_t)(st * C::TILE >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16(tX, dA + kstep_channels(kk), d + kstep_channels(kk), idS, kk > 0 ? 1u : 0u);
+          mma_commit(scores);
+          mma_commit(&first_empty[st]);
+          if (t == n - 1) mma_commit(&bar.kv_empty);
+          return true;
+        };
+        ok = mbar_wait(&bar.kv_full, uc & 1, abort) && issue_scores(0);
+        for (int t = 0; ok && t < n; ++t) {
+          const int c = qc + t, st = c % C::ST;
+          if (!mbar_wait(ready, c & 1, abort) || !mbar_wait(&second_full[st], (c / C::ST) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t d = dG + (uint64_t)(st * C::TILE >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(tG, tX + 64 * (kk / 4) + 8 * (kk % 4), d + kk * kKstepRows, idG, t > 0 || kk > 0 ? 1u : 0u);
+          mma_commit(&second_empty[st]);
+          if (t == n - 1) mma_commit(&bar.acc_full);
+          else ok = issue_scores(t + 1);
+        }
+        qc += n;
+        ++uc;
+      }
+      mma_commit(&bar.done[role]);
+      drain_wait(&bar.done[role], 0);
+    }
+  } else if (warp == kFixer) {
+    // ------------------------------------------------------------ rows that see nothing
+    // Every tile passes through this warp, so that the barriers' phases keep step with the
+    // ring's.
+    int qc = 0;
+    bool ok = true;
+    for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+      const DkvUnit u(a, unit_of(i));
+      const int n = u.steps();
+      int tile = u.tile0;
+      for (int t = 0; t < n; ++t, ++qc) {
+        const int st = qc % C::ST, par = (qc / C::ST) & 1;
+        int lo, hi;
+        u.valid(a.w, tile * kTile, lo, hi);
+        unsigned char *dO = smem + C::OFF_DO + st * C::TILE, *Q = smem + C::OFF_Q + st * C::TILE;
+        if (!mbar_wait(&bar.do_full[st], par, abort)) {
+          ok = false;
+          break;
+        }
+        zero_rows<D>(dO, 0, lo, lane);
+        zero_rows<D>(dO, hi, kTile, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.do_fixed[st]);
+        if (!mbar_wait(&bar.q_full[st], par, abort)) {
+          ok = false;
+          break;
+        }
+        zero_rows<D>(Q, 0, lo, lane);
+        zero_rows<D>(Q, hi, kTile, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.q_fixed[st]);
+        if (++tile == u.tile0 + u.tiles) tile = u.tile0;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ row threads
+    const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + C::TM_S + 64 * half + lanes, tP = tmem + C::TM_DP + 64 * half + lanes;
+    const uint32_t tG = tmem + (half ? C::TM_DK : C::TM_DV) + lanes;
+    const int off = a.w.nk - a.w.nq;
+    int qc = 0, uc = 0;
+    bool ok = true;
+    for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+      const DkvUnit u(a, unit_of(i));
+      const int n = u.steps(), j = u.k0 + r;
+      // the queries (row numbers) that see this key: i0 <= q < i1, from the diagonal on, and
+      // within the window unless the key is a sink
+      const int qlo = max(u.i0, j - a.w.right - off);
+      const int qhi = j >= u.len ? -1 : min(u.i1 - 1, j < a.w.sinks ? u.i1 - 1 : j + a.w.left - off);
+      // tiles between these see every key of the unit
+      const int whole_lo = u.k0 + kTile <= u.len ? max(u.i0, u.k0 + kTile - 1 - a.w.right - off) : 1 << 30;
+      const int whole_hi = min(u.i1 - 1, u.k0 + kTile <= a.w.sinks ? u.i1 - 1 : u.k0 + a.w.left - off);
+      int tile = u.tile0;
+      for (int t = 0; t < n; ++t, ++qc) {
+        const int st = qc % C::ST, q0 = tile * kTile;
+        const float4* stat = reinterpret_cast<const float4*>(smem + C::OFF_STAT + st * C::STAT) + 32 * half;
+        // (lse, delta) came with Q, which S^T has read: visible to who waits for Q's barrier
+        if (!mbar_wait(&bar.q_full[st], (qc / C::ST) & 1, abort) || !mbar_wait(&bar.s_full, qc & 1, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t x[64];
+        load_cols64(tS, x);
+        if (q0 < whole_lo || q0 + kTile - 1 > whole_hi) {
+          const int lo = qlo - q0 - 64 * half, hi = qhi - q0 - 64 * half;
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c < lo || c > hi) x[c] = 0xff800000u;  // -inf: P = 0
+        }
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float4 s2 = stat[c / 2];
+          const float p0 = fast_exp2(fmaf(__uint_as_float(x[c]), a.sl2, -s2.x));
+          const float p1 = fast_exp2(fmaf(__uint_as_float(x[c + 1]), a.sl2, -s2.z));
+          x[c] = __float_as_uint(p0);
+          x[c + 1] = __float_as_uint(p1);
+          pk[c / 2] = pack2(p0, p1);
+        }
+        tmem_store16_async(tS, pk);
+        tmem_store16_async(tS + 16, pk + 16);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar.p_full);
+        if (!mbar_wait(&bar.dp_full, qc & 1, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t y[64];
+        load_cols64(tP, y);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float4 s2 = stat[c / 2];
+          const float p0 = __uint_as_float(x[c]), p1 = __uint_as_float(x[c + 1]);
+          // a masked pair's dP may be NaN (padding): its dS is 0 by selection
+          y[c / 2] = pack2(p0 == 0.f ? 0.f : p0 * (__uint_as_float(y[c]) - s2.y),
+                           p1 == 0.f ? 0.f : p1 * (__uint_as_float(y[c + 1]) - s2.w));
+        }
+        tmem_store16_async(tP, y);
+        tmem_store16_async(tP + 16, y + 16);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar.ds_full);
+        if (++tile == u.tile0 + u.tiles) tile = u.tile0;
+      }
+      if (!ok) break;
+      // ---- the first 128 threads write dV's rows, the others dK's
+      if (n > 0) {
+        if (!mbar_wait(&bar.acc_full, uc & 1, abort)) break;
+        ++uc;
+        tc_fence_after();
+      }
+      const bool in = j < a.w.nk;
+      const View<__nv_bfloat16>& out = half ? a.dk : a.dv;
+      __nv_bfloat16* dst = out.row(u.b, u.hk, in ? j : 0);
+      const float f = half ? a.scale : 1.f;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (n > 0) {
+          tmem_load32(tG + c, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+        }
+        if (in) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4*>(dst + c + k) =
+                make_uint4(pack2(o[k] * f, o[k + 1] * f), pack2(o[k + 2] * f, o[k + 3] * f),
+                           pack2(o[k + 4] * f, o[k + 5] * f), pack2(o[k + 6] * f, o[k + 7] * f));
+        }
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kFixer) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+int padded_rows(const Window& w) { return (w.nq + kTile - 1) / kTile * kTile; }
+
+template <int D>
+cudaError_t bwd(const WindowArgs<__nv_bfloat16>& x, cudaStream_t st) {
+  const Window& w = x.w;
+  CUtensorMap mq, mdo, mk, mv;
+  if (!map_view(&mq, x.q.p, x.q.sb, x.q.sh, x.q.sn, w.B, w.nh, w.nq, D) ||
+      !map_view(&mdo, x.dO.p, x.dO.sb, x.dO.sh, x.dO.sn, w.B, w.nh, w.nq, D) ||
+      !map_view(&mk, x.k.p, x.k.sb, x.k.sh, x.k.sn, w.B, w.nkv, w.nk, D) ||
+      !map_view(&mv, x.v.p, x.v.sb, x.v.sh, x.v.sn, w.B, w.nkv, w.nk, D))
+    return cudaErrorInvalidValue;
+  BwdParams a{};
+  a.w = w;
+  a.dq = x.dq;
+  a.dk = x.dk;
+  a.dv = x.dv;
+  float2* stat = reinterpret_cast<float2*>(x.delta);
+  a.stat = stat;
+  a.scale = x.scale;
+  a.sl2 = x.scale * kLog2;
+  a.row_tiles = (w.nq + kTile - 1) / kTile;
+  a.key_tiles = (w.nk + kTile - 1) / kTile;
+  auto dq = window_dq_tc_kernel<D>;
+  auto dkdv = window_dkdv_tc_kernel<D>;
+  cudaError_t e = set_max_dynamic_smem((const void*)dq, DqCfg<D>::SMEM);
+  if (e == cudaSuccess) e = set_max_dynamic_smem((const void*)dkdv, DkvCfg<D>::SMEM);
+  const int rows = 256 / (D / 8), padded = padded_rows(w);
+  if (e == cudaSuccess)
+    e = launch_pdl(window_stat_kernel<D>, dim3((padded + rows - 1) / rows, w.B * w.nh), dim3(256), 0, st, x, stat,
+                   padded);
+  if (e == cudaSuccess) {
+    a.units = w.B * w.nkv * a.key_tiles;
+    e = launch_pdl(dkdv, dim3(std::min(a.units, device_sm_count())), dim3(kThreads), DkvCfg<D>::SMEM, st, mq, mdo, mk,
+                   mv, a);
+  }
+  if (e == cudaSuccess) {
+    a.units = w.B * w.nh * a.row_tiles;
+    e = launch_pdl(dq, dim3(std::min(a.units, device_sm_count())), dim3(kThreads), DqCfg<D>::SMEM, st, mq, mdo, mk, mv,
+                   a);
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t window_bwd_tc_ws_bytes(const Window& w) { return (size_t)w.B * w.nh * padded_rows(w) * sizeof(float2); }
+
+cudaError_t launch_window_bwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cudaStream_t st) {
+  return d == 64 ? bwd<64>(a, st) : bwd<128>(a, st);
+}
+
+}  // namespace psa

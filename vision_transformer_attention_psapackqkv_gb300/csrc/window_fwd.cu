@@ -11,7 +11,7 @@
 // heads of one key/value head at the same rows where their number is even (equal tile
 // lists), two neighbouring row tiles of one head otherwise.
 //   warps 0-3, 4-7   softmax of slot 0, 1: one thread per row (TMEM lane), 128 columns
-//   warp 8           TMA producer: Q of both slots, K and V tiles in one ring
+//   warp 8           TMA producer: Q of both slots, a ring of K tiles and one of V tiles
 //   warps 9, 10      issuer of slot 0, 1 (one thread): per key tile O += P V, then the next
 //                    tile's S = Q K^T right behind it: P lies in S's own columns of tensor
 //                    memory, and products of one thread complete in order, so neither
@@ -38,9 +38,9 @@ struct Cfg {
   static constexpr int kThreads = 384;
   static constexpr int kProducer = 8, kIssuer = 9, kFixer = 11;
   // shared memory that a CTA can have, less barriers and alignment, cut into tiles
-  static constexpr int STAGES = D == 128 ? 5 : 10;
+  static constexpr int KST = D == 128 ? 3 : 5, VST = D == 128 ? 2 : 5;
   static constexpr uint32_t TILE = kTileBytes<D>;
-  static constexpr uint32_t OFF_KV = 2 * TILE, OFF_BAR = OFF_KV + STAGES * TILE;
+  static constexpr uint32_t OFF_K = 2 * TILE, OFF_V = OFF_K + KST * TILE, OFF_BAR = OFF_V + VST * TILE;
   static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   // tensor memory: S of both slots (P in its first half), O of both slots
@@ -48,8 +48,8 @@ struct Cfg {
 };
 
 struct Bars {
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], done[2], fixed;
-  uint64_t kv_full[10], kv_empty[10];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], done[2];
+  uint64_t k_full[5], k_empty[5], v_full[5], v_fixed[5], v_empty[5];
 };
 
 struct FwdParams {
@@ -155,10 +155,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       mbar_init(&bar.o_full[i], 1);
       mbar_init(&bar.done[i], 1);
     }
-    mbar_init(&bar.fixed, 1);
-    for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&bar.kv_full[i], 1);
-      mbar_init(&bar.kv_empty[i], 2);  // one arrival per slot
+    for (int i = 0; i < 5; ++i) {
+      mbar_init(&bar.k_full[i], 1);
+      mbar_init(&bar.k_empty[i], 2);  // one arrival per slot
+      mbar_init(&bar.v_full[i], 1);
+      mbar_init(&bar.v_fixed[i], 1);
+      mbar_init(&bar.v_empty[i], 2);
     }
     *abort = 0;
     fence_mbar_init();
@@ -198,23 +200,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             load_tile<D>(smem + s * C::TILE, &tmQ, &bar.q_full[s], u.s[s].row0, u.s[s].h, u.b);
             q_count[s] = n + 1;
           }
-          for (int t = 0; ok && t < 2 * walk.all.count; ++t, ++kv) {
-            const int st = kv % C::STAGES;
-            if (kv >= C::STAGES && !mbar_wait(&bar.kv_empty[st], (kv / C::STAGES - 1) & 1, abort)) {
+          for (int t = 0; ok && t < walk.all.count; ++t, ++kv) {
+            const int ks = kv % C::KST, vs = kv % C::VST, row = walk.all.tile(t) * kTile;
+            if (kv >= C::KST && !mbar_wait(&bar.k_empty[ks], (kv / C::KST - 1) & 1, abort)) {
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(&bar.kv_full[st], C::TILE);
-            load_tile<D>(smem + C::OFF_KV + st * C::TILE, (t & 1) ? &tmV : &tmK, &bar.kv_full[st],
-                         walk.all.tile(t >> 1) * kTile, u.hk, u.b);
+            mbar_arrive_expect_tx(&bar.k_full[ks], C::TILE);
+            load_tile<D>(smem + C::OFF_K + ks * C::TILE, &tmK, &bar.k_full[ks], row, u.hk, u.b);
+            if (kv >= C::VST && !mbar_wait(&bar.v_empty[vs], (kv / C::VST - 1) & 1, abort)) {
+              ++kv;
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&bar.v_full[vs], C::TILE);
+            load_tile<D>(smem + C::OFF_V + vs * C::TILE, &tmV, &bar.v_full[vs], row, u.hk, u.b);
           }
         }
         if (*abort) {
-          // let the copies in flight land before the CTA exits
+          // let the copies in flight land before the CTA exits (a wait for one that was not
+          // issued any more runs into its time limit)
           for (int s = 0; s < 2; ++s)
             if (q_count[s] > 0) drain_wait(&bar.q_full[s], (q_count[s] - 1) & 1);
-          for (int n = max(0, kv - C::STAGES); n < kv; ++n)
-            drain_wait(&bar.kv_full[n % C::STAGES], (n / C::STAGES) & 1);
+          for (int n = max(0, kv - C::KST); n < kv; ++n) drain_wait(&bar.k_full[n % C::KST], (n / C::KST) & 1);
+          for (int n = max(0, kv - C::VST); n < kv; ++n) drain_wait(&bar.v_full[n % C::VST], (n / C::VST) & 1);
         }
       }
     } else if (warp < C::kFixer) {
@@ -222,25 +231,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const int s = warp - C::kIssuer;
       if (lane == 0) {
         const uint64_t dQ = desc_rows_by_channels(sbase + s * C::TILE);
-        const uint64_t dK0 = desc_rows_by_channels(sbase + C::OFF_KV);
-        const uint64_t dV0 = desc_channels_by_rows(sbase + C::OFF_KV);
+        const uint64_t dK0 = desc_rows_by_channels(sbase + C::OFF_K);
+        const uint64_t dV0 = desc_channels_by_rows(sbase + C::OFF_V);
         const uint32_t tS = tmem + C::TM_S + 128 * s, tO = tmem + C::TM_O + D * s;
         const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
         const uint32_t idO = idesc_bf16_f32(128, D, false, true);
         bool ok = true;
-        int kv0 = 0, q_count = 0, steps = 0, fixes = 0;  // kv0: ring index of the unit's first K
-        auto wait_kv = [&](int n) { return mbar_wait(&bar.kv_full[n % C::STAGES], (n / C::STAGES) & 1, abort); };
+        int kv0 = 0, q_count = 0, steps = 0;  // kv0: ring index of the unit's first tile
         for (int i = 0; ok && unit_of(i) < a.units; ++i) {
           const Unit u(a, unit_of(i));
           const Walk walk(a.w, u);
           const int n = walk.all.count;
-          const int edge = u.len % kTile != 0 && u.len < a.w.nk ? u.len / kTile : -1;
           // S of the unit's entry e, or its release
           auto issue_s = [&](int e) -> bool {
-            const int kn = kv0 + 2 * e, st = kn % C::STAGES;
-            if (!wait_kv(kn)) return false;
+            const int kn = kv0 + e, st = kn % C::KST;
+            if (!mbar_wait(&bar.k_full[st], (kn / C::KST) & 1, abort)) return false;
             if (!walk.takes(s, walk.all.tile(e))) {
-              mbar_arrive(&bar.kv_empty[st]);
+              mbar_arrive(&bar.k_empty[st]);
               return true;
             }
             tc_fence_after();
@@ -249,7 +256,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             for (int kk = 0; kk < D / 16; ++kk)
               mma_bf16(tS, dQ + kstep_channels(kk), dK + kstep_channels(kk), idS, kk > 0 ? 1u : 0u);
             mma_commit(&bar.s_full[s]);
-            mma_commit(&bar.kv_empty[st]);
+            mma_commit(&bar.k_empty[st]);
             if (walk.all.tile(e) == walk.last[s]) mma_commit(&bar.q_empty[s]);  // the next unit's Q may come
             return true;
           };
@@ -258,10 +265,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           bool first = true;
           if (ok && n > 0) ok = issue_s(0);
           for (int e = 0; ok && e < n; ++e) {
-            const int tile = walk.all.tile(e), vn = kv0 + 2 * e + 1, st = vn % C::STAGES;
-            if (walk.takes(s, tile)) {
-              if (!mbar_wait(&bar.p_full[s], steps & 1, abort) || !wait_kv(vn) ||
-                  (tile == edge && !mbar_wait(&bar.fixed, fixes & 1, abort))) {
+            const int vn = kv0 + e, st = vn % C::VST, par = (vn / C::VST) & 1;
+            if (walk.takes(s, walk.all.tile(e))) {
+              if (!mbar_wait(&bar.p_full[s], steps & 1, abort) || !mbar_wait(&bar.v_fixed[st], par, abort)) {
                 ok = false;
                 break;
               }
@@ -272,43 +278,45 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
               for (int kk = 0; kk < kTile / 16; ++kk)
                 mma_bf16_ts(tO, tS + 8 * kk, dV + kk * kKstepRows, idO, !first || kk > 0 ? 1u : 0u);
               first = false;
-              mma_commit(&bar.kv_empty[st]);
+              mma_commit(&bar.v_empty[st]);
             } else {
-              if (!wait_kv(vn) || (tile == edge && !mbar_wait(&bar.fixed, fixes & 1, abort))) {
+              if (!mbar_wait(&bar.v_fixed[st], par, abort)) {
                 ok = false;
                 break;
               }
-              mbar_arrive(&bar.kv_empty[st]);
+              mbar_arrive(&bar.v_empty[st]);
             }
-            if (tile == edge) ++fixes;
             if (e + 1 < n && !issue_s(e + 1)) ok = false;
           }
           if (ok && mine) {
             mma_commit(&bar.o_full[s]);
             ++q_count;
           }
-          kv0 += 2 * n;
+          kv0 += n;
         }
         mma_commit(&bar.done[s]);
         drain_wait(&bar.done[s], 0);
       }
     } else {
       // ------------------------------------------------------------ rows of padding in V
-      int kv0 = 0;
-      for (int i = 0; unit_of(i) < a.units; ++i) {
+      // Every tile passes through this warp, so that v_fixed's phases keep step with the ring.
+      int kv = 0;
+      bool ok = true;
+      for (int i = 0; ok && unit_of(i) < a.units; ++i) {
         const Unit u(a, unit_of(i));
         const Walk walk(a.w, u);
-        const int n = walk.all.count;
-        // rows past n_k are zero already (TMA's fill)
+        // the tile that sequence b ends in (rows past n_k are zero already: TMA's fill)
         const int edge = u.len % kTile != 0 && u.len < a.w.nk ? u.len / kTile : -1;
-        if (edge >= 0 && n > 0 && walk.all.tile(n - 1) == edge) {
-          const int vn = kv0 + 2 * (n - 1) + 1, st = vn % C::STAGES;
-          if (!mbar_wait(&bar.kv_full[st], (vn / C::STAGES) & 1, abort)) break;
-          zero_rows<D>(smem + C::OFF_KV + st * C::TILE, u.len % kTile, kTile, lane);
+        for (int t = 0; t < walk.all.count; ++t, ++kv) {
+          const int st = kv % C::VST;
+          if (!mbar_wait(&bar.v_full[st], (kv / C::VST) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          if (walk.all.tile(t) == edge) zero_rows<D>(smem + C::OFF_V + st * C::TILE, u.len % kTile, kTile, lane);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.fixed);
+          if (lane == 0) mbar_arrive(&bar.v_fixed[st]);
         }
-        kv0 += 2 * n;
       }
     }
   } else {

@@ -381,6 +381,5 @@ cudaError_t launch_window_bwd_simt(const WindowArgs<T>& a, int d, cudaStream_t s
 }
 template cudaError_t launch_window_fwd_simt(const WindowArgs<float>&, int, cudaStream_t);
 template cudaError_t launch_window_bwd_simt(const WindowArgs<float>&, int, cudaStream_t);
-template cudaError_t launch_window_bwd_simt(const WindowArgs<__nv_bfloat16>&, int, cudaStream_t);
 
 }  // namespace psa

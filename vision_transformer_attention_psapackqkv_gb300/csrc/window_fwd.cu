@@ -48,7 +48,7 @@ struct Cfg {
 };
 
 struct Bars {
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], done[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], done;
   uint64_t k_full[5], k_empty[5], v_full[5], v_fixed[5], v_empty[5];
 };
 
@@ -153,8 +153,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.p_full[i], kTile);
       mbar_init(&bar.o_full[i], 1);
-      mbar_init(&bar.done[i], 1);
     }
+    mbar_init(&bar.done, 1);
     for (int i = 0; i < 5; ++i) {
       mbar_init(&bar.k_full[i], 1);
       mbar_init(&bar.k_empty[i], 2);  // one arrival per slot
@@ -226,78 +226,81 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           for (int n = max(0, kv - C::VST); n < kv; ++n) drain_wait(&bar.v_full[n % C::VST], (n / C::VST) & 1);
         }
       }
-    } else if (warp < C::kFixer) {
-      // ------------------------------------------------------------ issuer of a slot
-      const int s = warp - C::kIssuer;
-      if (lane == 0) {
-        const uint64_t dQ = desc_rows_by_channels(sbase + s * C::TILE);
-        const uint64_t dK0 = desc_rows_by_channels(sbase + C::OFF_K);
-        const uint64_t dV0 = desc_channels_by_rows(sbase + C::OFF_V);
-        const uint32_t tS = tmem + C::TM_S + 128 * s, tO = tmem + C::TM_O + D * s;
-        const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
-        const uint32_t idO = idesc_bf16_f32(128, D, false, true);
-        bool ok = true;
-        int kv0 = 0, q_count = 0, steps = 0;  // kv0: ring index of the unit's first tile
-        for (int i = 0; ok && unit_of(i) < a.units; ++i) {
-          const Unit u(a, unit_of(i));
-          const Walk walk(a.w, u);
-          const int n = walk.all.count;
-          // S of the unit's entry e, or its release
-          auto issue_s = [&](int e) -> bool {
-            const int kn = kv0 + e, st = kn % C::KST;
-            if (!mbar_wait(&bar.k_full[st], (kn / C::KST) & 1, abort)) return false;
-            if (!walk.takes(s, walk.all.tile(e))) {
-              mbar_arrive(&bar.k_empty[st]);
-              return true;
-            }
-            tc_fence_after();
-            const uint64_t dK = dK0 + (uint64_t)(st * C::TILE >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16(tS, dQ + kstep_channels(kk), dK + kstep_channels(kk), idS, kk > 0 ? 1u : 0u);
-            mma_commit(&bar.s_full[s]);
-            mma_commit(&bar.k_empty[st]);
-            if (walk.all.tile(e) == walk.last[s]) mma_commit(&bar.q_empty[s]);  // the next unit's Q may come
+    } else if (warp == C::kIssuer) {
+      // ------------------------------------------------------------ issuer (converged warp)
+      const uint64_t dQ0 = desc_rows_by_channels(sbase);
+      const uint64_t dK0 = desc_rows_by_channels(sbase + C::OFF_K);
+      const uint64_t dV0 = desc_channels_by_rows(sbase + C::OFF_V);
+      const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
+      const uint32_t idO = idesc_bf16_f32(128, D, false, true);
+      bool ok = true;
+      int kv0 = 0, q_count[2] = {0, 0}, steps[2] = {0, 0};  // kv0: ring index of the unit's first tile
+      for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+        const Unit u(a, unit_of(i));
+        const Walk walk(a.w, u);
+        const int n = walk.all.count;
+        bool first[2] = {true, true};
+        // S of slot s and the unit's entry e, or the tile's release
+        auto issue_s = [&](int s, int e) -> bool {
+          const int kn = kv0 + e, st = kn % C::KST, tile = walk.all.tile(e);
+          if (!mbar_wait(&bar.k_full[st], (kn / C::KST) & 1, abort)) return false;
+          if (!walk.takes(s, tile)) {
+            if (lane == 0) mbar_arrive(&bar.k_empty[st]);
+            __syncwarp();
             return true;
-          };
-          const bool mine = walk.last[s] >= 0;
-          if (mine && n > 0) ok = mbar_wait(&bar.q_full[s], q_count & 1, abort);
-          bool first = true;
-          if (ok && n > 0) ok = issue_s(0);
-          for (int e = 0; ok && e < n; ++e) {
-            const int vn = kv0 + e, st = vn % C::VST, par = (vn / C::VST) & 1;
-            if (walk.takes(s, walk.all.tile(e))) {
-              if (!mbar_wait(&bar.p_full[s], steps & 1, abort) || !mbar_wait(&bar.v_fixed[st], par, abort)) {
-                ok = false;
-                break;
-              }
-              ++steps;
+          }
+          tc_fence_after();
+          const uint64_t dQ = dQ0 + (uint64_t)(s * C::TILE >> 4), dK = dK0 + (uint64_t)(st * C::TILE >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16_warp(tmem + C::TM_S + 128 * s, dQ + kstep_channels(kk), dK + kstep_channels(kk), idS,
+                          kk > 0 ? 1u : 0u);
+          mma_commit_warp(&bar.s_full[s]);
+          mma_commit_warp(&bar.k_empty[st]);
+          if (tile == walk.last[s]) mma_commit_warp(&bar.q_empty[s]);  // the next unit's Q may come
+          return true;
+        };
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (ok && walk.last[s] >= 0) ok = mbar_wait(&bar.q_full[s], q_count[s] & 1, abort);
+          if (ok && n > 0) ok = issue_s(s, 0);
+        }
+        for (int e = 0; ok && e < n; ++e) {
+          const int vn = kv0 + e, st = vn % C::VST, par = (vn / C::VST) & 1;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (!ok) break;
+            const bool mine = walk.takes(s, walk.all.tile(e));
+            if ((mine && !mbar_wait(&bar.p_full[s], steps[s] & 1, abort)) ||
+                !mbar_wait(&bar.v_fixed[st], par, abort)) {
+              ok = false;
+              break;
+            }
+            if (mine) {
+              ++steps[s];
               tc_fence_after();
               const uint64_t dV = dV0 + (uint64_t)(st * C::TILE >> 4);
+              const uint32_t tO = tmem + C::TM_O + D * s, tP = tmem + C::TM_S + 128 * s;
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk)
-                mma_bf16_ts(tO, tS + 8 * kk, dV + kk * kKstepRows, idO, !first || kk > 0 ? 1u : 0u);
-              first = false;
-              mma_commit(&bar.v_empty[st]);
+                mma_bf16_ts_warp(tO, tP + 8 * kk, dV + kk * kKstepRows, idO, !first[s] || kk > 0 ? 1u : 0u);
+              first[s] = false;
+              mma_commit_warp(&bar.v_empty[st]);
             } else {
-              if (!mbar_wait(&bar.v_fixed[st], par, abort)) {
-                ok = false;
-                break;
-              }
-              mbar_arrive(&bar.v_empty[st]);
+              if (lane == 0) mbar_arrive(&bar.v_empty[st]);
+              __syncwarp();
             }
-            if (e + 1 < n && !issue_s(e + 1)) ok = false;
+            if (e + 1 < n) ok = issue_s(s, e + 1);
+            else if (walk.last[s] >= 0) mma_commit_warp(&bar.o_full[s]);
           }
-          if (ok && mine) {
-            mma_commit(&bar.o_full[s]);
-            ++q_count;
-          }
-          kv0 += n;
         }
-        mma_commit(&bar.done[s]);
-        drain_wait(&bar.done[s], 0);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) q_count[s] += walk.last[s] >= 0;
+        kv0 += n;
       }
-    } else {
+      mma_commit_warp(&bar.done);
+      drain_wait(&bar.done, 0);
+    } else if (warp == C::kFixer) {
       // ------------------------------------------------------------ rows of padding in V
       // Every tile passes through this warp, so that v_fixed's phases keep step with the ring.
       int kv = 0;

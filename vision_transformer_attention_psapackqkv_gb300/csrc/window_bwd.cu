@@ -12,16 +12,15 @@
 // key/value head too.
 //
 // Both kernels: a persistent CTA per SM, 256 row threads (two per row of tensor memory, each
-// 64 of the 128 columns), a TMA producer, two issuing threads, and a warp that zeroes the
-// rows of padding where they are an operand (0 times NaN is NaN).  bf16 operands made by the
-// row threads stay in tensor memory: each thread writes them over the columns that it read.
-// Products that must follow one another on the same columns are issued by one thread, whose
-// products complete in order:
-//   dQ kernel     issuer 0: S into two buffers; issuer 1: dP, then behind it dQ += dS K, whose
-//                 dS lies in dP's columns
-//   dK/dV kernel  S^T = K Q^T and dP^T = V dO^T have keys as rows; issuer 0: S^T, dV += P^T dO;
-//                 issuer 1: dP^T, dK += dS^T Q.  While the row threads turn S^T into P^T, the
-//                 products of dP^T's side run, and the other way round.
+// 64 of the 128 columns), a TMA producer, a warp that issues the products, and one that
+// zeroes the rows of padding where they are an operand (0 times NaN is NaN).  bf16 operands
+// made by the row threads stay in tensor memory: each thread writes them over the columns
+// that it read.  All products come from one warp and complete in the order they are issued:
+//   dQ kernel     dQ += dS K (dS in dP's columns), then the next tile's dP behind it, then S of
+//                 the tile after (two buffers), so the row threads always find S
+//   dK/dV kernel  S^T = K Q^T and dP^T = V dO^T have keys as rows: dV += P^T dO and the next
+//                 S^T behind it, while the row threads make dS^T; dK += dS^T Q and the next
+//                 dP^T, while they make P^T.
 // delta and lse come from a small kernel in front, per row as (lse log2(e), delta), in rows
 // padded to whole tiles, so that a tile's 1024 bytes are one bulk copy.
 #include <math.h>
@@ -34,7 +33,7 @@ namespace psa {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kProducer = 8, kIssuer = 9, kFixer = 11;
+constexpr int kProducer = 8, kIssuer = 9, kFixer = 11;  // warp 10 idles
 
 struct BwdParams {
   Window w;
@@ -87,7 +86,7 @@ struct DqCfg {
 };
 struct DqBars {
   uint64_t q_full, q_empty, do_full, do_empty, k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t k_fixed[4], s_full[2], s_free[2], dp_full, ds_full, dq_full, done[2];
+  uint64_t k_fixed[4], s_full[2], s_free[2], dp_full, ds_full, dq_full, done;
 };
 
 // A unit of the dQ kernel: 128 query rows of a head.
@@ -134,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar.do_empty, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bar.k_full[i], 1);
-      mbar_init(&bar.k_empty[i], 2);  // S and dQ read it
+      mbar_init(&bar.k_empty[i], 1);
       mbar_init(&bar.k_fixed[i], 1);
       mbar_init(&bar.v_full[i], 1);
       mbar_init(&bar.v_empty[i], 1);
@@ -142,11 +141,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.s_free[i], 256);
-      mbar_init(&bar.done[i], 1);
     }
     mbar_init(&bar.dp_full, 1);
     mbar_init(&bar.ds_full, 256);
     mbar_init(&bar.dq_full, 1);
+    mbar_init(&bar.done, 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -213,79 +212,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = max(0, kc - C::VST); n < kc; ++n) drain_wait(&bar.v_full[n % C::VST], (n / C::VST) & 1);
       }
     }
-  } else if (warp == kIssuer || warp == kIssuer + 1) {
-    // ------------------------------------------------------------ issuers
-    if (lane == 0) {
-      const bool s_role = warp == kIssuer;
-      const uint64_t dQ = desc_rows_by_channels(sbase), dDO = desc_rows_by_channels(sbase + C::OFF_DO);
-      const uint64_t dK = desc_rows_by_channels(sbase + C::OFF_K), dV = desc_rows_by_channels(sbase + C::OFF_V);
-      const uint64_t dKb = desc_channels_by_rows(sbase + C::OFF_K);
-      const uint32_t idS = idesc_bf16_f32(128, 128, false, false), idQ = idesc_bf16_f32(128, D, false, true);
-      bool ok = true;
-      int kc = 0, uc = 0;
-      for (int i = 0; ok && unit_of(i) < a.units; ++i) {
-        const DqUnit u(a, unit_of(i));
-        const int n = u.tiles.count;
-        if (n == 0) continue;
-        if (s_role) {
-          ok = mbar_wait(&bar.q_full, uc & 1, abort);
-          for (int t = 0; ok && t < n; ++t, ++kc) {
-            const int st = kc % C::KST, sb = kc & 1;
-            if (!mbar_wait(&bar.k_full[st], (kc / C::KST) & 1, abort) ||
-                (kc >= 2 && !mbar_wait(&bar.s_free[sb], (kc / 2 - 1) & 1, abort))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t dKs = dK + (uint64_t)(st * C::TILE >> 4);
+  } else if (warp == kIssuer) {
+    // ------------------------------------------------------------ issuer (converged warp)
+    const uint64_t dQ = desc_rows_by_channels(sbase), dDO = desc_rows_by_channels(sbase + C::OFF_DO);
+    const uint64_t dK = desc_rows_by_channels(sbase + C::OFF_K), dV = desc_rows_by_channels(sbase + C::OFF_V);
+    const uint64_t dKb = desc_channels_by_rows(sbase + C::OFF_K);
+    const uint32_t idS = idesc_bf16_f32(128, 128, false, false), idQ = idesc_bf16_f32(128, D, false, true);
+    bool ok = true;
+    int kc = 0, uc = 0;
+    for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+      const DqUnit u(a, unit_of(i));
+      const int n = u.tiles.count;
+      if (n == 0) continue;
+      auto issue_s = [&](int t) -> bool {
+        const int c = kc + t, st = c % C::KST, sb = c & 1;
+        if (!mbar_wait(&bar.k_full[st], (c / C::KST) & 1, abort) ||
+            (c >= 2 && !mbar_wait(&bar.s_free[sb], (c / 2 - 1) & 1, abort)))
+          return false;
+        tc_fence_after();
+        const uint64_t d = dK + (uint64_t)(st * C::TILE >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16(tmem + C::TM_S + 128 * sb, dQ + kstep_channels(kk), dKs + kstep_channels(kk), idS,
-                       kk > 0 ? 1u : 0u);
-            mma_commit(&bar.s_full[sb]);
-            mma_commit(&bar.k_empty[st]);
-          }
-          if (ok) mma_commit(&bar.q_empty);
-        } else {
-          auto issue_dp = [&](int t) -> bool {
-            const int vc = kc + t, st = vc % C::VST;
-            if (!mbar_wait(&bar.v_full[st], (vc / C::VST) & 1, abort)) return false;
-            tc_fence_after();
-            const uint64_t dVs = dV + (uint64_t)(st * C::TILE >> 4);
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16_warp(tmem + C::TM_S + 128 * sb, dQ + kstep_channels(kk), d + kstep_channels(kk), idS,
+                        kk > 0 ? 1u : 0u);
+        mma_commit_warp(&bar.s_full[sb]);
+        if (t == n - 1) mma_commit_warp(&bar.q_empty);
+        return true;
+      };
+      auto issue_dp = [&](int t) -> bool {
+        const int c = kc + t, st = c % C::VST;
+        if (!mbar_wait(&bar.v_full[st], (c / C::VST) & 1, abort)) return false;
+        tc_fence_after();
+        const uint64_t d = dV + (uint64_t)(st * C::TILE >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16(tmem + C::TM_DP, dDO + kstep_channels(kk), dVs + kstep_channels(kk), idS, kk > 0 ? 1u : 0u);
-            mma_commit(&bar.dp_full);
-            mma_commit(&bar.v_empty[st]);
-            if (t == n - 1) mma_commit(&bar.do_empty);
-            return true;
-          };
-          ok = mbar_wait(&bar.do_full, uc & 1, abort) && issue_dp(0);
-          for (int t = 0; ok && t < n; ++t) {
-            const int kn = kc + t, st = kn % C::KST;
-            if (!mbar_wait(&bar.ds_full, kn & 1, abort) ||
-                !mbar_wait(&bar.k_fixed[st], (kn / C::KST) & 1, abort)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t dKs = dKb + (uint64_t)(st * C::TILE >> 4);
-            // 16 keys' dS are 8 columns; those of keys 64 .. 127 start at column 64
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ts(tmem + C::TM_DQ, tmem + C::TM_DP + 64 * (kk / 4) + 8 * (kk % 4), dKs + kk * kKstepRows,
-                          idQ, t > 0 || kk > 0 ? 1u : 0u);
-            mma_commit(&bar.k_empty[st]);
-            if (t == n - 1) mma_commit(&bar.dq_full);
-            else ok = issue_dp(t + 1);
-          }
-          kc += n;
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16_warp(tmem + C::TM_DP, dDO + kstep_channels(kk), d + kstep_channels(kk), idS, kk > 0 ? 1u : 0u);
+        mma_commit_warp(&bar.dp_full);
+        mma_commit_warp(&bar.v_empty[st]);
+        if (t == n - 1) mma_commit_warp(&bar.do_empty);
+        return true;
+      };
+      ok = mbar_wait(&bar.q_full, uc & 1, abort) && issue_s(0) && mbar_wait(&bar.do_full, uc & 1, abort) &&
+           issue_dp(0) && (n == 1 || issue_s(1));
+      for (int t = 0; ok && t < n; ++t) {
+        const int c = kc + t, st = c % C::KST;
+        if (!mbar_wait(&bar.ds_full, c & 1, abort) || !mbar_wait(&bar.k_fixed[st], (c / C::KST) & 1, abort)) {
+          ok = false;
+          break;
         }
-        ++uc;
+        tc_fence_after();
+        const uint64_t d = dKb + (uint64_t)(st * C::TILE >> 4);
+        // 16 keys' dS are 8 columns; those of keys 64 .. 127 start at column 64
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_ts_warp(tmem + C::TM_DQ, tmem + C::TM_DP + 64 * (kk / 4) + 8 * (kk % 4), d + kk * kKstepRows, idQ,
+                           t > 0 || kk > 0 ? 1u : 0u);
+        mma_commit_warp(&bar.k_empty[st]);
+        if (t == n - 1) mma_commit_warp(&bar.dq_full);
+        else ok = issue_dp(t + 1) && (t + 2 >= n || issue_s(t + 2));
       }
-      mma_commit(&bar.done[warp - kIssuer]);
-      drain_wait(&bar.done[warp - kIssuer], 0);
+      kc += n;
+      ++uc;
     }
+    mma_commit_warp(&bar.done);
+    drain_wait(&bar.done, 0);
   } else if (warp == kFixer) {
     // ------------------------------------------------------------ rows of padding in K
     // Every tile passes through this warp, so that k_fixed's phases keep step with the ring.
@@ -304,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar.k_fixed[st]);
       }
     }
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ row threads
     const int half = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -414,7 +404,7 @@ struct DkvCfg {
 };
 struct DkvBars {
   uint64_t kv_full, kv_empty, q_full[4], q_empty[4], do_full[4], do_empty[4];
-  uint64_t q_fixed[4], do_fixed[4], s_full, p_full, dp_full, ds_full, acc_full, done[2];
+  uint64_t q_fixed[4], do_fixed[4], s_full, p_full, dp_full, ds_full, acc_full, done;
 };
 
 // A unit of the dK/dV kernel: 128 key rows of a key/value head.  Its steps are the query
@@ -463,12 +453,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&bar.kv_full, 1);
-    mbar_init(&bar.kv_empty, 2);
+    mbar_init(&bar.kv_empty, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bar.q_full[i], 1);
-      mbar_init(&bar.q_empty[i], 2);  // S^T and dK read Q
+      mbar_init(&bar.q_empty[i], 1);
       mbar_init(&bar.do_full[i], 1);
-      mbar_init(&bar.do_empty[i], 2);  // dP^T and dV read dO
+      mbar_init(&bar.do_empty[i], 1);
       mbar_init(&bar.q_fixed[i], 1);
       mbar_init(&bar.do_fixed[i], 1);
     }
@@ -476,9 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar.p_full, 256);
     mbar_init(&bar.dp_full, 1);
     mbar_init(&bar.ds_full, 256);
-    mbar_init(&bar.acc_full, 2);
-    mbar_init(&bar.done[0], 1);
-    mbar_init(&bar.done[1], 1);
+    mbar_init(&bar.acc_full, 1);
+    mbar_init(&bar.done, 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -535,63 +524,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == kIssuer || warp == kIssuer + 1) {
-    // ------------------------------------------------------------ issuers
-    // Role 0: S^T = K Q^T and dV += P^T dO.  Role 1: dP^T = V dO^T and dK += dS^T Q.
-    if (lane == 0) {
-      const int role = warp - kIssuer;
-      const uint64_t dA = desc_rows_by_channels(sbase + (role ? C::OFF_V : 0));
-      const uint64_t dB = desc_rows_by_channels(sbase + (role ? C::OFF_DO : C::OFF_Q));
-      const uint64_t dG = desc_channels_by_rows(sbase + (role ? C::OFF_Q : C::OFF_DO));
-      uint64_t* first_full = role ? bar.do_full : bar.q_full;    // operand of the scores
-      uint64_t* first_empty = role ? bar.do_empty : bar.q_empty;
-      uint64_t* second_full = role ? bar.q_fixed : bar.do_fixed;  // operand of the gradient
-      uint64_t* second_empty = role ? bar.q_empty : bar.do_empty;
-      uint64_t* scores = role ? &bar.dp_full : &bar.s_full;
-      uint64_t* ready = role ? &bar.ds_full : &bar.p_full;
-      const uint32_t tX = tmem + (role ? C::TM_DP : C::TM_S), tG = tmem + (role ? C::TM_DK : C::TM_DV);
-      const uint32_t idS = idesc_bf16_f32(128, 128, false, false), idG = idesc_bf16_f32(128, D, false, true);
-      bool ok = true;
-      int qc = 0, uc = 0;
-      for (int i = 0; ok && unit_of(i) < a.units; ++i) {
-        const DkvUnit u(a, unit_of(i));
-        const int n = u.steps();
-        if (n == 0) continue;
-        auto issue_scores = [&](int t) -> bool {
-          const int c = qc + t, st = c % C::ST;
-          if (!mbar_wait(&first_full[st], (c / C::ST) & 1, abort)) return false;
-          tc_fence_after();
-          const uint64_t d = dB + (uint64_t)(st * C::TILE >> 4);
+  } else if (warp == kIssuer) {
+    // ------------------------------------------------------------ issuer (converged warp)
+    const uint64_t dK = desc_rows_by_channels(sbase), dV = desc_rows_by_channels(sbase + C::OFF_V);
+    const uint64_t dQ = desc_rows_by_channels(sbase + C::OFF_Q), dDO = desc_rows_by_channels(sbase + C::OFF_DO);
+    const uint64_t dQb = desc_channels_by_rows(sbase + C::OFF_Q), dDOb = desc_channels_by_rows(sbase + C::OFF_DO);
+    const uint32_t idS = idesc_bf16_f32(128, 128, false, false), idG = idesc_bf16_f32(128, D, false, true);
+    // rows of the unit (dA) by those of a stage's tile (d0) into tX
+    auto scores = [&](uint32_t tX, uint64_t dA, uint64_t d0, int st) {
+      const uint64_t d = d0 + (uint64_t)(st * C::TILE >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16(tX, dA + kstep_channels(kk), d + kstep_channels(kk), idS, kk > 0 ? 1u : 0u);
-          mma_commit(scores);
-          mma_commit(&first_empty[st]);
-          if (t == n - 1) mma_commit(&bar.kv_empty);
-          return true;
-        };
-        ok = mbar_wait(&bar.kv_full, uc & 1, abort) && issue_scores(0);
-        for (int t = 0; ok && t < n; ++t) {
-          const int c = qc + t, st = c % C::ST;
-          if (!mbar_wait(ready, c & 1, abort) || !mbar_wait(&second_full[st], (c / C::ST) & 1, abort)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t d = dG + (uint64_t)(st * C::TILE >> 4);
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_bf16_warp(tX, dA + kstep_channels(kk), d + kstep_channels(kk), idS, kk > 0 ? 1u : 0u);
+    };
+    // tG += tX (bf16, 8 columns for 16 queries; those of queries 64 .. 127 from column 64 on)
+    // by a stage's tile
+    auto gradient = [&](uint32_t tG, uint32_t tX, uint64_t d0, int st, bool first) {
+      const uint64_t d = d0 + (uint64_t)(st * C::TILE >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tG, tX + 64 * (kk / 4) + 8 * (kk % 4), d + kk * kKstepRows, idG, t > 0 || kk > 0 ? 1u : 0u);
-          mma_commit(&second_empty[st]);
-          if (t == n - 1) mma_commit(&bar.acc_full);
-          else ok = issue_scores(t + 1);
+      for (int kk = 0; kk < 8; ++kk)
+        mma_bf16_ts_warp(tG, tX + 64 * (kk / 4) + 8 * (kk % 4), d + kk * kKstepRows, idG, !first || kk > 0 ? 1u : 0u);
+    };
+    bool ok = true;
+    int qc = 0, uc = 0;
+    for (int i = 0; ok && unit_of(i) < a.units; ++i) {
+      const DkvUnit u(a, unit_of(i));
+      const int n = u.steps();
+      if (n == 0) continue;
+      auto issue_s = [&](int t) -> bool {
+        const int c = qc + t, st = c % C::ST;
+        if (!mbar_wait(&bar.q_full[st], (c / C::ST) & 1, abort)) return false;
+        tc_fence_after();
+        scores(tmem + C::TM_S, dK, dQ, st);
+        mma_commit_warp(&bar.s_full);
+        return true;
+      };
+      auto issue_dp = [&](int t) -> bool {
+        const int c = qc + t, st = c % C::ST;
+        if (!mbar_wait(&bar.do_full[st], (c / C::ST) & 1, abort)) return false;
+        tc_fence_after();
+        scores(tmem + C::TM_DP, dV, dDO, st);
+        mma_commit_warp(&bar.dp_full);
+        if (t == n - 1) mma_commit_warp(&bar.kv_empty);
+        return true;
+      };
+      ok = mbar_wait(&bar.kv_full, uc & 1, abort) && issue_s(0) && issue_dp(0);
+      for (int t = 0; ok && t < n; ++t) {
+        const int c = qc + t, st = c % C::ST, par = (c / C::ST) & 1;
+        if (!mbar_wait(&bar.p_full, c & 1, abort) || !mbar_wait(&bar.do_fixed[st], par, abort)) {
+          ok = false;
+          break;
         }
-        qc += n;
-        ++uc;
+        tc_fence_after();
+        gradient(tmem + C::TM_DV, tmem + C::TM_S, dDOb, st, t == 0);
+        mma_commit_warp(&bar.do_empty[st]);
+        if (t + 1 < n && !issue_s(t + 1)) ok = false;
+        if (!ok || !mbar_wait(&bar.ds_full, c & 1, abort) || !mbar_wait(&bar.q_fixed[st], par, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        gradient(tmem + C::TM_DK, tmem + C::TM_DP, dQb, st, t == 0);
+        mma_commit_warp(&bar.q_empty[st]);
+        if (t + 1 < n) ok = issue_dp(t + 1);
+        else mma_commit_warp(&bar.acc_full);
       }
-      mma_commit(&bar.done[role]);
-      drain_wait(&bar.done[role], 0);
+      qc += n;
+      ++uc;
     }
+    mma_commit_warp(&bar.done);
+    drain_wait(&bar.done, 0);
   } else if (warp == kFixer) {
     // ------------------------------------------------------------ rows that see nothing
     // Every tile passes through this warp, so that the barriers' phases keep step with the
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++tile == u.tile0 + u.tiles) tile = u.tile0;
       }
     }
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ row threads
     const int half = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;

@@ -106,14 +106,16 @@ struct KeyTiles {
 };
 
 // The query rows (first, count) that see a key among k0 .. k1, clipped to n_q rows.
-__device__ __forceinline__ void query_range(const Window& w, int len, int k0, int k1, int& i0,
-                                            int& n) {
-  const int off = w.nk - w.nq;
-  k1 = min(k1, len - 1);
-  const int p0 = max(max(0, off), k0 - w.right);
-  const int p1 = k0 < w.sinks ? len - 1 : min(len - 1, k1 + w.left);
+__host__ __device__ __forceinline__ void query_range(const Window& w, int len, int k0, int k1,
+                                                     int& i0, int& n) {
+  const int off = w.nk - w.nq, from = k0 - w.right;
+  if (k1 > len - 1) k1 = len - 1;
+  int p0 = off > 0 ? off : 0;
+  if (p0 < from) p0 = from;
+  int p1 = len - 1;
+  if (k0 >= w.sinks && k1 + w.left < p1) p1 = k1 + w.left;
   i0 = p0 - off;
-  n = k0 <= k1 ? max(0, p1 - p0 + 1) : 0;
+  n = k0 <= k1 && p1 >= p0 ? p1 - p0 + 1 : 0;
 }
 
 template <typename T>
@@ -128,7 +130,7 @@ struct WindowArgs {
 // Tensor cores (window_fwd.cu, window_bwd.cu); delta points at the backward's workspace.
 cudaError_t launch_window_fwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cudaStream_t st);
 cudaError_t launch_window_bwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cudaStream_t st);
-size_t window_bwd_tc_ws_bytes(const Window& w);
+size_t window_bwd_tc_ws_bytes(const Window& w, int d);
 // CUDA cores (window_simt.cu).
 template <typename T>
 cudaError_t launch_window_fwd_simt(const WindowArgs<T>& a, int d, cudaStream_t st);

@@ -294,7 +294,7 @@ psa_status_t psa_window_attn_fwd(psa_rows_t q, psa_rows_t k, psa_rows_t v, const
 
 size_t psa_window_attn_bwd_workspace_size(psa_window_t p) {
   if (check_window(p) != PSA_OK) return 0;
-  return round256(p.dtype == PSA_DTYPE_BF16 ? psa::window_bwd_tc_ws_bytes(window(p, nullptr))
+  return round256(p.dtype == PSA_DTYPE_BF16 ? psa::window_bwd_tc_ws_bytes(window(p, nullptr), p.head_dim)
                                             : (size_t)p.B * p.num_heads * p.n_q * 4);
 }
 

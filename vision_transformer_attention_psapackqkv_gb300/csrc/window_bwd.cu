@@ -35,12 +35,31 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kProducer = 8, kIssuer = 9, kFixer = 11;  // warp 10 idles
 
+// How the dK/dV kernel's work is cut.  A key tile's steps are the query tiles that see it,
+// for each query head of its group: from a window's few to every query there is (sinks, or no
+// window).  Tiles with more than `steps` of them are cut into parts of that many, whose
+// fp32 results a small kernel adds in order; part p has the first tiles[p] key tiles.
+constexpr int kMaxParts = 32;
+struct Cut {
+  int parts, steps;
+  int tiles[kMaxParts];
+  int units;  // over all parts, batch items and key/value heads
+  // partial results in front of part p's (part 0: of the key tiles that have a part 1)
+  __host__ __device__ __forceinline__ int slot0(int p) const {
+    int n = 0;
+    for (int i = 1; i <= p; ++i) n += tiles[i == 1 ? 1 : i - 1];
+    return n;
+  }
+};
+
 struct BwdParams {
   Window w;
   View<__nv_bfloat16> dq, dk, dv;
   const float2* stat;  // [B, nh, row_tiles * 128] (lse log2(e), delta)
+  float* partial;      // [slots, B * nkv, 2 (dV, dK), 128, D]
   float scale, sl2;
   int units, row_tiles, key_tiles;
+  Cut cut;
 };
 
 // Unit of this CTA in its round i (from long to short: CTA order, then reverse order).
@@ -407,19 +426,19 @@ struct DkvBars {
   uint64_t q_fixed[4], do_fixed[4], s_full, p_full, dp_full, ds_full, acc_full, done;
 };
 
-// A unit of the dK/dV kernel: 128 key rows of a key/value head.  Its steps are the query
-// tiles that see them, for each query head of the group.
+// A key tile of a key/value head, and the steps of one part of it.
 struct DkvUnit {
-  int b, hk, k0, len, group;
+  int b, hk, k0, len, group, part;
   int i0, i1;        // query rows that see a key of the tile
   int tile0, tiles;  // the tiles of 128 they lie in
-  __device__ __forceinline__ DkvUnit(const BwdParams& a, int u) {
+  int from, steps;   // this part's
+  int slot;          // its partial result's place, -1: the tile has one part
+  __device__ __forceinline__ void find(const BwdParams& a, int x, int kt) {
     const Window& w = a.w;
-    const int heads = w.B * w.nkv, x = u % heads;
     b = x / w.nkv;
     hk = x % w.nkv;
     group = w.nh / w.nkv;
-    k0 = (u / heads) * kTile;  // the first keys are seen by the most queries
+    k0 = kt * kTile;
     len = w.len(b);
     int n;
     query_range(w, len, k0, min(k0 + kTile, w.nk) - 1, i0, n);
@@ -427,7 +446,17 @@ struct DkvUnit {
     tile0 = i0 / kTile;
     tiles = n > 0 ? (i1 - 1) / kTile - tile0 + 1 : 0;
   }
-  __device__ __forceinline__ int steps() const { return group * tiles; }
+  __device__ __forceinline__ DkvUnit(const BwdParams& a, int u) {
+    const int heads = a.w.B * a.w.nkv;
+    // the last parts first, the last key tiles (which the fewest see) of part 0 at the end
+    part = a.cut.parts - 1;
+    int t = u / heads;
+    while (part > 0 && t >= a.cut.tiles[part]) t -= a.cut.tiles[part--];
+    find(a, u % heads, t);
+    from = part * a.cut.steps;
+    steps = max(0, min(group * tiles - from, a.cut.steps));
+    slot = group * tiles > a.cut.steps ? (a.cut.slot0(part) + t) * heads + u % heads : -1;
+  }
   // a tile that holds rows that see nothing: rows of padding, or in front of position 0
   __device__ __forceinline__ void valid(const Window& w, int row0, int& lo, int& hi) const {
     const int off = w.nk - w.nq;
@@ -489,14 +518,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       int uc = 0, qc = 0;
       for (int i = 0; ok && unit_of(i) < a.units; ++i) {
         const DkvUnit u(a, unit_of(i));
-        const int n = u.steps();
+        const int n = u.steps;
         if (n == 0) continue;
         if (uc >= 1 && !mbar_wait(&bar.kv_empty, (uc - 1) & 1, abort)) break;
         mbar_arrive_expect_tx(&bar.kv_full, 2 * C::TILE);
         load_tile<D>(smem, &tmK, &bar.kv_full, u.k0, u.hk, u.b);
         load_tile<D>(smem + C::OFF_V, &tmV, &bar.kv_full, u.k0, u.hk, u.b);
         ++uc;
-        int h = u.hk * u.group, tile = u.tile0;
+        int h = u.hk * u.group + u.from / u.tiles, tile = u.tile0 + u.from % u.tiles;
         for (int t = 0; t < n; ++t, ++qc) {
           const int st = qc % C::ST, par = (qc / C::ST - 1) & 1;
           if (qc >= C::ST && (!mbar_wait(&bar.q_empty[st], par, abort) || !mbar_wait(&bar.do_empty[st], par, abort))) {
@@ -549,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int qc = 0, uc = 0;
     for (int i = 0; ok && unit_of(i) < a.units; ++i) {
       const DkvUnit u(a, unit_of(i));
-      const int n = u.steps();
+      const int n = u.steps;
       if (n == 0) continue;
       auto issue_s = [&](int t) -> bool {
         const int c = qc + t, st = c % C::ST;
@@ -602,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int i = 0; ok && unit_of(i) < a.units; ++i) {
       const DkvUnit u(a, unit_of(i));
-      const int n = u.steps();
-      int tile = u.tile0;
+      const int n = u.steps;
+      int tile = n > 0 ? u.tile0 + u.from % u.tiles : 0;
       for (int t = 0; t < n; ++t, ++qc) {
         const int st = qc % C::ST, par = (qc / C::ST) & 1;
         int lo, hi;
@@ -639,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int i = 0; ok && unit_of(i) < a.units; ++i) {
       const DkvUnit u(a, unit_of(i));
-      const int n = u.steps(), j = u.k0 + r;
+      const int n = u.steps, j = u.k0 + r;
       // the queries (row numbers) that see this key: i0 <= q < i1, from the diagonal on, and
       // within the window unless the key is a sink
       const int qlo = max(u.i0, j - a.w.right - off);
@@ -647,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // tiles between these see every key of the unit
       const int whole_lo = u.k0 + kTile <= u.len ? max(u.i0, u.k0 + kTile - 1 - a.w.right - off) : 1 << 30;
       const int whole_hi = min(u.i1 - 1, u.k0 + kTile <= a.w.sinks ? u.i1 - 1 : u.k0 + a.w.left - off);
-      int tile = u.tile0;
+      int tile = n > 0 ? u.tile0 + u.from % u.tiles : 0;
       for (int t = 0; t < n; ++t, ++qc) {
         const int st = qc % C::ST, q0 = tile * kTile;
         const float4* stat = reinterpret_cast<const float4*>(smem + C::OFF_STAT + st * C::STAT) + 32 * half;
@@ -709,6 +738,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++uc;
         tc_fence_after();
       }
+      if (u.slot >= 0) {
+        // a part of a tile's sums (parts behind the sequence's last have none)
+        if (n == 0) continue;
+        float4* dst = reinterpret_cast<float4*>(a.partial + ((long long)(2 * u.slot + half) * kTile + r) * D);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_load32(tG + c, o);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) dst[(c + k) / 4] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        }
+        tc_fence_before();
+        continue;
+      }
+      if (u.part > 0) continue;
       const bool in = j < a.w.nk;
       const View<__nv_bfloat16>& out = half ? a.dk : a.dv;
       __nv_bfloat16* dst = out.row(u.b, u.hk, in ? j : 0);
@@ -742,7 +786,81 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Adds the parts of one key tile, in order: 8 channels of dV or dK per thread.
+template <int D>
+__global__ void __launch_bounds__(256) window_parts_kernel(const BwdParams a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int heads = a.w.B * a.w.nkv, x = blockIdx.x % heads, kt = blockIdx.x / heads;
+  DkvUnit u(a, (a.cut.units / heads - a.cut.tiles[0] + kt) * heads + x);  // the tile's part 0
+  if (u.slot < 0) return;
+  const int parts = (u.group * u.tiles + a.cut.steps - 1) / a.cut.steps;
+  const bool is_k = blockIdx.z;
+  const int row = blockIdx.y * (256 / (D / 8)) + threadIdx.x / (D / 8), c = threadIdx.x % (D / 8) * 8;
+  if (u.k0 + row >= a.w.nk) return;
+  float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < parts; ++p) {
+    const long long slot = (long long)(a.cut.slot0(p) + kt) * heads + x;
+    const float4* src = reinterpret_cast<const float4*>(a.partial + ((2 * slot + is_k) * kTile + row) * D + c);
+    const float4 v = src[0], w = src[1];
+    o[0] += v.x; o[1] += v.y; o[2] += v.z; o[3] += v.w;
+    o[4] += w.x; o[5] += w.y; o[6] += w.z; o[7] += w.w;
+  }
+  const float f = is_k ? a.scale : 1.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) o[k] *= f;
+  const View<__nv_bfloat16>& out = is_k ? a.dk : a.dv;
+  *reinterpret_cast<uint4*>(out.row(u.b, u.hk, u.k0 + row) + c) = pack_vec(o);
+}
+
 int padded_rows(const Window& w) { return (w.nq + kTile - 1) / kTile * kTile; }
+size_t stat_bytes(const Window& w) { return (size_t)w.B * w.nh * padded_rows(w) * sizeof(float2); }
+
+// By the sizes alone (full lengths, 152 SMs).  A tile is cut only where one of them would
+// take much longer than an SM's share of all: sinks behind a window (window_train's first
+// tile has 128 steps, the others 36 to 40), or a long causal triangle of few heads.  Parts
+// are half an SM's share, but no smaller than what a tile of the window has anyway: each
+// costs a tile of fp32 sums written and read.
+Cut cut_of(const Window& w) {
+  constexpr int kSms = 152;
+  const int key_tiles = (w.nk + kTile - 1) / kTile, group = w.nh / w.nkv;
+  auto steps = [&](int kt) -> long long {
+    int i0, n;
+    query_range(w, w.nk, kt * kTile, std::min((kt + 1) * kTile, w.nk) - 1, i0, n);
+    return n > 0 ? (long long)group * ((i0 + n - 1) / kTile - i0 / kTile + 1) : 0;
+  };
+  long long total = 0, most = 0, plain = 0;  // plain: of the tiles without sinks
+  for (int kt = 0; kt < key_tiles; ++kt) {
+    const long long s = steps(kt);
+    total += s;
+    most = std::max(most, s);
+    if (kt * kTile >= w.sinks) plain = std::max(plain, s);
+  }
+  const long long share = (total * w.B * w.nkv + kSms - 1) / kSms;
+  Cut c{};
+  c.parts = 1;
+  c.steps = (int)std::max(most, 1LL);
+  c.tiles[0] = key_tiles;
+  if (most > share + share / 4) {
+    long long part = std::max<long long>((share + 1) / 2, 8);
+    if (plain <= share) part = std::max(part, plain);
+    c.steps = (int)std::max(part, (most + kMaxParts - 1) / kMaxParts);
+    c.parts = (int)((most + c.steps - 1) / c.steps);
+    for (int p = 1; p < c.parts; ++p) {
+      int n = c.tiles[p - 1];
+      while (n > 0 && steps(n - 1) <= (long long)p * c.steps) --n;
+      c.tiles[p] = n;
+    }
+  }
+  int units = 0;
+  for (int p = 0; p < c.parts; ++p) units += c.tiles[p];
+  c.units = units * w.B * w.nkv;
+  return c;
+}
+
+int cut_slots(const Cut& c, const Window& w) {
+  return c.parts == 1 ? 0 : (c.slot0(c.parts - 1) + c.tiles[c.parts - 1]) * w.B * w.nkv;
+}
 
 template <int D>
 cudaError_t bwd(const WindowArgs<__nv_bfloat16>& x, cudaStream_t st) {
@@ -772,11 +890,16 @@ cudaError_t bwd(const WindowArgs<__nv_bfloat16>& x, cudaStream_t st) {
   if (e == cudaSuccess)
     e = launch_pdl(window_stat_kernel<D>, dim3((padded + rows - 1) / rows, w.B * w.nh), dim3(256), 0, st, x, stat,
                    padded);
+  a.cut = cut_of(w);
+  a.partial = reinterpret_cast<float*>(reinterpret_cast<char*>(x.delta) + stat_bytes(w));
   if (e == cudaSuccess) {
-    a.units = w.B * w.nkv * a.key_tiles;
+    a.units = a.cut.units;
     e = launch_pdl(dkdv, dim3(std::min(a.units, device_sm_count())), dim3(kThreads), DkvCfg<D>::SMEM, st, mq, mdo, mk,
                    mv, a);
   }
+  if (e == cudaSuccess && a.cut.parts > 1)
+    e = launch_pdl(window_parts_kernel<D>, dim3(a.cut.tiles[1] * w.B * w.nkv, kTile / (256 / (D / 8)), 2), dim3(256),
+                   0, st, a);
   if (e == cudaSuccess) {
     a.units = w.B * w.nh * a.row_tiles;
     e = launch_pdl(dq, dim3(std::min(a.units, device_sm_count())), dim3(kThreads), DqCfg<D>::SMEM, st, mq, mdo, mk, mv,
@@ -787,7 +910,9 @@ cudaError_t bwd(const WindowArgs<__nv_bfloat16>& x, cudaStream_t st) {
 
 }  // namespace
 
-size_t window_bwd_tc_ws_bytes(const Window& w) { return (size_t)w.B * w.nh * padded_rows(w) * sizeof(float2); }
+size_t window_bwd_tc_ws_bytes(const Window& w, int d) {
+  return stat_bytes(w) + (size_t)cut_slots(cut_of(w), w) * 2 * kTile * d * sizeof(float);
+}
 
 cudaError_t launch_window_bwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cudaStream_t st) {
   return d == 64 ? bwd<64>(a, st) : bwd<128>(a, st);

@@ -21,8 +21,9 @@
 //   dK/dV kernel  S^T = K Q^T and dP^T = V dO^T have keys as rows: dV += P^T dO and the next
 //                 S^T behind it, while the row threads make dS^T; dK += dS^T Q and the next
 //                 dP^T, while they make P^T.
-// delta and lse come from a small kernel in front, per row as (lse log2(e), delta), in rows
-// padded to whole tiles, so that a tile's 1024 bytes are one bulk copy.
+// delta and lse come from a small kernel in front: for each tile of 128 rows (the last one
+// padded) 128 values of -lse log2(e), then 128 of -delta, so that a tile's 1024 bytes are one
+// bulk copy and two neighbouring columns' values one operand of a paired instruction.
 #include <math.h>
 
 #include <algorithm>
@@ -55,7 +56,7 @@ struct Cut {
 struct BwdParams {
   Window w;
   View<__nv_bfloat16> dq, dk, dv;
-  const float2* stat;  // [B, nh, row_tiles * 128] (lse log2(e), delta)
+  const float* stat;   // [B, nh, row_tiles, 2, 128]: -lse log2(e), -delta
   float* partial;      // [slots, B * nkv, 2 (dV, dK), 128, D]
   float scale, sl2;
   int units, row_tiles, key_tiles;
@@ -67,11 +68,11 @@ __device__ __forceinline__ int unit_of(int i) {
   return i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
-// (lse log2(e), delta) of every row; rows that see nothing, and those behind n_q, get (0, 0):
+// -lse log2(e) and -delta of every row; rows that see nothing, and those behind n_q, get 0:
 // their scores are masked.  One row per LANES lanes.
 template <int D>
 __global__ void __launch_bounds__(256)
-    window_stat_kernel(const WindowArgs<__nv_bfloat16> a, float2* stat, int padded) {
+    window_stat_kernel(const WindowArgs<__nv_bfloat16> a, float* stat, int padded) {
   constexpr int LANES = D / 8;
   pdl_launch_dependents();
   pdl_wait();
@@ -90,7 +91,21 @@ __global__ void __launch_bounds__(256)
   }
 #pragma unroll
   for (int m = LANES / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-  if (lr == 0 && i < padded) stat[(long long)blockIdx.y * padded + i] = make_float2(lse * kLog2, s);
+  if (lr == 0 && i < padded) {
+    float* at = stat + 2 * ((long long)blockIdx.y * padded + i / kTile * kTile) + i % kTile;
+    at[0] = -lse * kLog2;
+    at[kTile] = -s;
+  }
+}
+
+__device__ __forceinline__ float2 pair(const uint32_t* x) {
+  return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+}
+// A masked pair's dP may be NaN (padding); its P is 0, and so must its dS be.
+__device__ __forceinline__ void drop_masked(const uint32_t (&p)[64], uint32_t (&dp)[64]) {
+#pragma unroll
+  for (int c = 0; c < 64; ++c)
+    if (p[c] == 0u) dp[c] = 0u;
 }
 
 // ---------------------------------------------------------------- dQ
@@ -329,7 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int jlo = p - a.w.left;
       const bool rows = u.row0 + off >= 0 && u.row0 + off + kTile <= u.len && u.row0 + kTile <= a.w.nq;
       const int whole_lo = u.p1 - a.w.left, whole_hi = rows ? min(u.len, u.p0 + a.w.right + 1) : 0;
-      const float2 st = a.stat[(long long)(u.b * a.w.nh + u.h) * a.row_tiles * kTile + q];
+      const float* stat = a.stat + 2 * ((long long)(u.b * a.w.nh + u.h) * a.row_tiles * kTile + u.row0) + r;
+      const float2 nlse = make_float2(stat[0], stat[0]), ndelta = make_float2(stat[kTile], stat[kTile]);
+      const float2 sl = make_float2(a.sl2, a.sl2);
       for (int t = 0; t < u.tiles.count; ++t, ++kc) {
         const int tile0 = u.tiles.tile(t) * kTile, j0 = tile0 + 64 * half, sb = kc & 1;
         if (!mbar_wait(&bar.s_full[sb], (kc / 2) & 1, abort)) {
@@ -341,15 +358,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_cols64(tS + 128 * sb, x);
         tc_fence_before();
         mbar_arrive(&bar.s_free[sb]);
-        if (tile0 + kTile > whole_hi || (tile0 < whole_lo && tile0 + kTile > a.w.sinks)) {
+        const bool whole = tile0 + kTile <= whole_hi && (tile0 >= whole_lo || tile0 + kTile <= a.w.sinks);
+        if (!whole) {
           const int hi = jhi - j0, lo = jlo - j0, sk = a.w.sinks - j0;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c > hi || (c < lo && c >= sk)) x[c] = 0xff800000u;  // -inf: P = 0
         }
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          x[c] = __float_as_uint(fast_exp2(fmaf(__uint_as_float(x[c]), a.sl2, -st.x)));
+        for (int c = 0; c < 64; c += 2) {
+          const float2 e = __ffma2_rn(pair(x + c), sl, nlse);
+          x[c] = __float_as_uint(fast_exp2(e.x));
+          x[c + 1] = __float_as_uint(fast_exp2(e.y));
+        }
         if (!mbar_wait(&bar.dp_full, kc & 1, abort)) {
           ok = false;
           break;
@@ -357,13 +378,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         uint32_t y[64];
         load_cols64(tP, y);
+        if (!whole) drop_masked(x, y);
 #pragma unroll
         for (int c = 0; c < 64; c += 2) {
-          // a masked key's dP may be NaN (padding in V): its dS is 0 by selection
-          const float p0 = __uint_as_float(x[c]), p1 = __uint_as_float(x[c + 1]);
-          const float d0 = p0 == 0.f ? 0.f : p0 * (__uint_as_float(y[c]) - st.y);
-          const float d1 = p1 == 0.f ? 0.f : p1 * (__uint_as_float(y[c + 1]) - st.y);
-          y[c / 2] = pack2(d0, d1);
+          const float2 d = __fmul2_rn(pair(x + c), __fadd2_rn(pair(y + c), ndelta));
+          y[c / 2] = pack2(d.x, d.y);
         }
         tmem_store16_async(tP, y);
         tmem_store16_async(tP + 16, y + 16);
@@ -536,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&bar.q_full[st], C::TILE + C::STAT);
           load_tile<D>(smem + C::OFF_Q + st * C::TILE, &tmQ, &bar.q_full[st], tile * kTile, h, u.b);
           bulk_load(smem + C::OFF_STAT + st * C::STAT,
-                    a.stat + ((long long)(u.b * a.w.nh + h) * a.row_tiles + tile) * kTile, C::STAT, &bar.q_full[st]);
+                    a.stat + ((long long)(u.b * a.w.nh + h) * a.row_tiles + tile) * (2 * kTile), C::STAT, &bar.q_full[st]);
           mbar_arrive_expect_tx(&bar.do_full[st], C::TILE);
           load_tile<D>(smem + C::OFF_DO + st * C::TILE, &tmDO, &bar.do_full[st], tile * kTile, h, u.b);
           if (++tile == u.tile0 + u.tiles) {
@@ -663,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + C::TM_S + 64 * half + lanes, tP = tmem + C::TM_DP + 64 * half + lanes;
     const uint32_t tG = tmem + (half ? C::TM_DK : C::TM_DV) + lanes;
+    const float2 sl = make_float2(a.sl2, a.sl2);
     const int off = a.w.nk - a.w.nq;
     int qc = 0, uc = 0;
     bool ok = true;
@@ -679,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tile = n > 0 ? u.tile0 + u.from % u.tiles : 0;
       for (int t = 0; t < n; ++t, ++qc) {
         const int st = qc % C::ST, q0 = tile * kTile;
-        const float4* stat = reinterpret_cast<const float4*>(smem + C::OFF_STAT + st * C::STAT) + 32 * half;
+        const float4* stat = reinterpret_cast<const float4*>(smem + C::OFF_STAT + st * C::STAT) + 16 * half;
         // (lse, delta) came with Q, which S^T has read: visible to who waits for Q's barrier
         if (!mbar_wait(&bar.q_full[st], (qc / C::ST) & 1, abort) || !mbar_wait(&bar.s_full, qc & 1, abort)) {
           ok = false;
@@ -688,7 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         uint32_t x[64];
         load_cols64(tS, x);
-        if (q0 < whole_lo || q0 + kTile - 1 > whole_hi) {
+        const bool whole = q0 >= whole_lo && q0 + kTile - 1 <= whole_hi;
+        if (!whole) {
           const int lo = qlo - q0 - 64 * half, hi = qhi - q0 - 64 * half;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
@@ -696,13 +717,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint32_t pk[32];
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          const float4 s2 = stat[c / 2];
-          const float p0 = fast_exp2(fmaf(__uint_as_float(x[c]), a.sl2, -s2.x));
-          const float p1 = fast_exp2(fmaf(__uint_as_float(x[c + 1]), a.sl2, -s2.z));
+        for (int c = 0; c < 64; c += 4) {
+          const float4 nlse = stat[c / 4];
+          const float2 e0 = __ffma2_rn(pair(x + c), sl, make_float2(nlse.x, nlse.y));
+          const float2 e1 = __ffma2_rn(pair(x + c + 2), sl, make_float2(nlse.z, nlse.w));
+          const float p0 = fast_exp2(e0.x), p1 = fast_exp2(e0.y), p2 = fast_exp2(e1.x), p3 = fast_exp2(e1.y);
           x[c] = __float_as_uint(p0);
           x[c + 1] = __float_as_uint(p1);
+          x[c + 2] = __float_as_uint(p2);
+          x[c + 3] = __float_as_uint(p3);
           pk[c / 2] = pack2(p0, p1);
+          pk[c / 2 + 1] = pack2(p2, p3);
         }
         tmem_store16_async(tS, pk);
         tmem_store16_async(tS + 16, pk + 16);
@@ -716,13 +741,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         uint32_t y[64];
         load_cols64(tP, y);
+        if (!whole) drop_masked(x, y);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          const float4 s2 = stat[c / 2];
-          const float p0 = __uint_as_float(x[c]), p1 = __uint_as_float(x[c + 1]);
-          // a masked pair's dP may be NaN (padding): its dS is 0 by selection
-          y[c / 2] = pack2(p0 == 0.f ? 0.f : p0 * (__uint_as_float(y[c]) - s2.y),
-                           p1 == 0.f ? 0.f : p1 * (__uint_as_float(y[c + 1]) - s2.w));
+        for (int c = 0; c < 64; c += 4) {
+          const float4 nd = stat[32 + c / 4];
+          const float2 d0 = __fmul2_rn(pair(x + c), __fadd2_rn(pair(y + c), make_float2(nd.x, nd.y)));
+          const float2 d1 = __fmul2_rn(pair(x + c + 2), __fadd2_rn(pair(y + c + 2), make_float2(nd.z, nd.w)));
+          y[c / 2] = pack2(d0.x, d0.y);
+          y[c / 2 + 1] = pack2(d1.x, d1.y);
         }
         tmem_store16_async(tP, y);
         tmem_store16_async(tP + 16, y + 16);
@@ -876,7 +902,7 @@ cudaError_t bwd(const WindowArgs<__nv_bfloat16>& x, cudaStream_t st) {
   a.dq = x.dq;
   a.dk = x.dk;
   a.dv = x.dv;
-  float2* stat = reinterpret_cast<float2*>(x.delta);
+  float* stat = x.delta;
   a.stat = stat;
   a.scale = x.scale;
   a.sl2 = x.scale * kLog2;

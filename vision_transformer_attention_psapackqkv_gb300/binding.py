@@ -257,47 +257,65 @@ def psa_attention_bwd_noalloc(qkv, out, dout, lse, dvres, dqkv, shape: PsaShape,
 # ------------------------------------------------------------------ token sequences
 # Views are torch tensors [B, heads, N, d] of any strides whose channels are contiguous.
 # The calls run on the tensors' device, on its current stream unless one is given.
-def _rows(t, shape, dtype, what: str) -> PsaRows:
+# A decoding step's calls are as long on the host as on the device, so their checks go over
+# plain tuples and integers.
+def _wrong(t, shape, dtype, what: str):
+    """Raises what is wrong with an argument that failed its check."""
+    if t is None:
+        raise ValueError(f"{what} is required")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{what} is {t.dtype}, expected {dtype}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    raise ValueError(f"{what} must be contiguous")
+
+
+def _rows(t, shape, dtype, what: str) -> PsaRows:
+    if t is None or t.shape != shape or t.dtype != dtype:
+        _wrong(t, shape, dtype, what)
+    sb, sh, sn, sc = t.stride()
+    if sc != 1 and shape[3] != 1:
         raise ValueError(f"{what}: the channels of a row must be contiguous")
-    return PsaRows(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    return PsaRows(t.data_ptr(), sb, sh, sn)
 
 
 def _dense(t, shape, dtype, what: str):
-    """Pointer of a dense array of that shape and type; None for None."""
+    """Address of a dense array of that shape and type; None for None."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{what} is {t.dtype}, expected {dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return _ptr(t)
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        _wrong(t, shape, dtype, what)
+    return t.data_ptr()
 
 
 def _on_device(fn: str, tensors, stream, *args):
     """Calls entry point `fn` with its arguments on the tensors' one CUDA device."""
     import torch
 
-    device = tensors[0].device
+    index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{fn}: tensors on {device} and {t.device}")
-    if device.type != "cuda":
-        raise ValueError(f"{fn}: tensors must be on a CUDA device, got {device}")
-    with torch.cuda.device(device):
-        _check(fn, getattr(load(), fn)(*args, _stream(stream)))
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{fn}: tensors on {tensors[0].device} and {t.device}")
+    if index < 0:
+        raise ValueError(f"{fn}: tensors must be on a CUDA device, got {tensors[0].device}")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    call = getattr(_lib or load(), fn)
+    if torch._C._cuda_getDevice() == index:
+        status = call(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, raw)
+    if status != PSA_OK:
+        _check(fn, status)
 
 
 def _workspace(t, fn: str):
     if t is None or not t.is_contiguous():
         raise ValueError(f"{fn}: the workspace must be a contiguous tensor")
-    return _ptr(t), t.numel() * t.element_size()
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def norm_rope_of(q, k, cos, eps: float = 1e-6, interleaved: bool = False) -> PsaNormRope:
@@ -311,19 +329,18 @@ def norm_rope_of(q, k, cos, eps: float = 1e-6, interleaved: bool = False) -> Psa
 def _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p):
     import torch
 
-    f32, table = torch.float32, (p.max_pos, p.rotary_dim // 2)
-    return (_rows(q, (p.B, p.num_heads, p.N, p.head_dim), q.dtype, "q"),
-            _rows(k, (p.B, p.num_kv_heads, p.N, p.head_dim), q.dtype, "k"),
-            _dense(q_weight, (p.head_dim,), f32, "q_weight"), _dense(k_weight, (p.head_dim,), f32, "k_weight"),
-            _dense(cos, table, f32, "cos"), _dense(sin, table, f32, "sin"),
-            _dense(positions, (p.B, p.N), torch.int32, "positions"))
+    B, N, d, f32, t = p.B, p.N, p.head_dim, torch.float32, q.dtype
+    table, by_q, by_k = (p.max_pos, p.rotary_dim // 2), (B, p.num_heads, N, d), (B, p.num_kv_heads, N, d)
+    return by_q, by_k, (_rows(q, by_q, t, "q"), _rows(k, by_k, t, "k"), _dense(q_weight, (d,), f32, "q_weight"),
+                        _dense(k_weight, (d,), f32, "k_weight"), _dense(cos, table, f32, "cos"),
+                        _dense(sin, table, f32, "sin"), _dense(positions, (B, N), torch.int32, "positions"))
 
 
 def psa_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, p: PsaNormRope,
                          stream=None):
-    args = _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p)
+    by_q, by_k, args = _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p)
     _on_device("psa_qk_norm_rope_fwd", (q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out), stream,
-               *args, _rows(q_out, q.shape, q.dtype, "q_out"), _rows(k_out, k.shape, q.dtype, "k_out"), p)
+               *args, _rows(q_out, by_q, q.dtype, "q_out"), _rows(k_out, by_k, q.dtype, "k_out"), p)
 
 
 def psa_qk_norm_rope_bwd_workspace_size(p: PsaNormRope) -> int:
@@ -334,14 +351,13 @@ def psa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, 
                          dk_weight, workspace, p: PsaNormRope, stream=None):
     import torch
 
-    args = _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p)
-    grads = [_rows(t, x.shape, q.dtype, what) for t, x, what in
-             ((dq_out, q, "dq_out"), (dk_out, k, "dk_out"), (dq, q, "dq"), (dk, k, "dk"))]
-    dw = [_dense(t, (p.head_dim,), torch.float32, what) for t, what in
-          ((dq_weight, "dq_weight"), (dk_weight, "dk_weight"))]
+    by_q, by_k, args = _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p)
+    t, d = q.dtype, (p.head_dim,)
     _on_device("psa_qk_norm_rope_bwd",
                (q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk, dq_weight, dk_weight,
-                workspace), stream, *args, *grads, *dw, *_workspace(workspace, "psa_qk_norm_rope_bwd"), p)
+                workspace), stream, *args, _rows(dq_out, by_q, t, "dq_out"), _rows(dk_out, by_k, t, "dk_out"),
+               _rows(dq, by_q, t, "dq"), _rows(dk, by_k, t, "dk"), _dense(dq_weight, d, torch.float32, "dq_weight"),
+               _dense(dk_weight, d, torch.float32, "dk_weight"), *_workspace(workspace, "psa_qk_norm_rope_bwd"), p)
 
 
 def window_of(q, k, window_left: int = -1, window_right: int = 0, sinks: int = 0) -> PsaWindow:
@@ -352,9 +368,10 @@ def window_of(q, k, window_left: int = -1, window_right: int = 0, sinks: int = 0
                      int(sinks))
 
 
-def _window_views(named, dtype, win: PsaWindow):
-    shapes = {"q": (win.B, win.num_heads, win.n_q, win.head_dim), "k": (win.B, win.num_kv_heads, win.n_k, win.head_dim)}
-    return [_rows(t, shapes[side], dtype, what) for t, side, what in named]
+def _window_shapes(win: PsaWindow):
+    """Shapes of what goes by the queries, and by the keys."""
+    B, d = win.B, win.head_dim
+    return (B, win.num_heads, win.n_q, d), (B, win.num_kv_heads, win.n_k, d)
 
 
 def _lens(lens, win: PsaWindow):
@@ -366,9 +383,11 @@ def _lens(lens, win: PsaWindow):
 def psa_window_attn_fwd(q, k, v, lens, o, lse, win: PsaWindow, scale: float, stream=None):
     import torch
 
-    vq, vk, vv, vo = _window_views(((q, "q", "q"), (k, "k", "k"), (v, "k", "v"), (o, "q", "o")), q.dtype, win)
-    _on_device("psa_window_attn_fwd", (q, k, v, lens, o, lse), stream, vq, vk, vv, _lens(lens, win), vo,
-               _dense(lse, (win.B, win.num_heads, win.n_q), torch.float32, "lse"), win, float(scale))
+    by_q, by_k = _window_shapes(win)
+    t = q.dtype
+    _on_device("psa_window_attn_fwd", (q, k, v, lens, o, lse), stream, _rows(q, by_q, t, "q"), _rows(k, by_k, t, "k"),
+               _rows(v, by_k, t, "v"), _lens(lens, win), _rows(o, by_q, t, "o"),
+               _dense(lse, by_q[:3], torch.float32, "lse"), win, scale)
 
 
 def psa_window_attn_bwd_workspace_size(win: PsaWindow) -> int:
@@ -379,11 +398,13 @@ def psa_window_attn_bwd(q, k, v, o, do, lse, lens, dq, dk, dv, workspace, win: P
                         stream=None):
     import torch
 
-    ins = _window_views(((q, "q", "q"), (k, "k", "k"), (v, "k", "v"), (o, "q", "o"), (do, "q", "do")), q.dtype, win)
-    outs = _window_views(((dq, "q", "dq"), (dk, "k", "dk"), (dv, "k", "dv")), q.dtype, win)
-    _on_device("psa_window_attn_bwd", (q, k, v, o, do, lse, lens, dq, dk, dv, workspace), stream, *ins,
-               _dense(lse, (win.B, win.num_heads, win.n_q), torch.float32, "lse"), _lens(lens, win), *outs,
-               *_workspace(workspace, "psa_window_attn_bwd"), win, float(scale))
+    by_q, by_k = _window_shapes(win)
+    t = q.dtype
+    _on_device("psa_window_attn_bwd", (q, k, v, o, do, lse, lens, dq, dk, dv, workspace), stream,
+               _rows(q, by_q, t, "q"), _rows(k, by_k, t, "k"), _rows(v, by_k, t, "v"), _rows(o, by_q, t, "o"),
+               _rows(do, by_q, t, "do"), _dense(lse, by_q[:3], torch.float32, "lse"), _lens(lens, win),
+               _rows(dq, by_q, t, "dq"), _rows(dk, by_k, t, "dk"), _rows(dv, by_k, t, "dv"),
+               *_workspace(workspace, "psa_window_attn_bwd"), win, scale)
 
 
 def psa_window_attn_decode_workspace_size(win: PsaWindow) -> int:
@@ -391,10 +412,11 @@ def psa_window_attn_decode_workspace_size(win: PsaWindow) -> int:
 
 
 def psa_window_attn_decode(q, k_cache, v_cache, lens, o, workspace, win: PsaWindow, scale: float, stream=None):
-    vq, vk, vv, vo = _window_views(((q, "q", "q"), (k_cache, "k", "k_cache"), (v_cache, "k", "v_cache"),
-                                    (o, "q", "o")), q.dtype, win)
-    _on_device("psa_window_attn_decode", (q, k_cache, v_cache, lens, o, workspace), stream, vq, vk, vv,
-               _lens(lens, win), vo, *_workspace(workspace, "psa_window_attn_decode"), win, float(scale))
+    by_q, by_k = _window_shapes(win)
+    t = q.dtype
+    _on_device("psa_window_attn_decode", (q, k_cache, v_cache, lens, o, workspace), stream, _rows(q, by_q, t, "q"),
+               _rows(k_cache, by_k, t, "k_cache"), _rows(v_cache, by_k, t, "v_cache"), _lens(lens, win),
+               _rows(o, by_q, t, "o"), *_workspace(workspace, "psa_window_attn_decode"), win, scale)
 
 
 def cache_of(k, max_len: int) -> PsaCache:
@@ -444,10 +466,10 @@ def psa_kv4_read(k_codes, k_scales, v_codes, v_scales, k, v, stream=None):
 def psa_window_attn_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, lens, o, workspace, win: PsaWindow,
                                scale: float, stream=None):
     cache = (k_codes, k_scales, v_codes, v_scales)
-    vq, vo = _window_views(((q, "q", "q"), (o, "q", "o")), q.dtype, win)
-    _on_device("psa_window_attn_decode_kv4", (q, *cache, lens, o, workspace), stream, vq,
-               *_kv4(*cache, win.B, win.num_kv_heads, win.n_k, win.head_dim), _lens(lens, win), vo,
-               *_workspace(workspace, "psa_window_attn_decode_kv4"), win, float(scale))
+    by_q, (B, nkv, max_len, d) = _window_shapes(win)
+    _on_device("psa_window_attn_decode_kv4", (q, *cache, lens, o, workspace), stream, _rows(q, by_q, q.dtype, "q"),
+               *_kv4(*cache, B, nkv, max_len, d), _lens(lens, win), _rows(o, by_q, q.dtype, "o"),
+               *_workspace(workspace, "psa_window_attn_decode_kv4"), win, scale)
 
 
 def psa_get_last_device_error(stream=None) -> int:

@@ -5,26 +5,31 @@
 //   o_h = sum_j softmax_j(scale q_h . k_j) v_j over the visible rows j of the cache
 //
 // Bound by memory: every visible row of K and V is read once, for all query heads that
-// share it.  So the heads of a group are the 16 rows of a tensor-core tile (m16n8k16; the
-// work is at most a fifth of what those units can do at this rate, and there is nothing a
-// larger instruction could fill), and the cache goes from memory straight into registers as
-// the B operand of the products, without shared memory or a barrier between a load and its
-// use.  That works because the order of the inner index of Q K^T (channels), and the column
-// order of P V (channels), are free: each lane takes 16 neighbouring bytes of a row and
-// Q's fragment (the output's columns) is permuted to match.  For P V the two keys of a
-// pair sit in two registers of one lane, and one byte permute per product register puts
-// them side by side.
+// share it.  The products run on m16n8k16 tensor instructions (a fifth of their rate is
+// enough here, and nothing could fill a larger one): 16 keys by 8 query heads for S^T = K Q^T,
+// 16 channels by 8 heads for O^T = V^T P^T, so the cache is the A operand and goes from memory
+// straight into registers, without shared memory or a barrier between a load and its use.
+// That works because the order of the inner index of K Q^T (channels) and the row order of
+// V^T P^T (channels) are free: each lane takes 16 neighbouring bytes of a row, and Q's fragment
+// (the output's channels) is permuted to match.  For V the two keys of a pair sit in two
+// registers of one lane, and a byte permute puts them side by side; P, whose rows are keys,
+// becomes the B operand by an 8 x 8 transposition inside the warp.
 //
 // Keys are cut into blocks of 16; the visible blocks (the sinks', then the window's) are
 // dealt to gridDim.x CTAs in contiguous parts and inside a CTA to its warps in turn.  Every
-// warp keeps its own running maximum, sum and output; they are joined in shared memory, and
-// the parts of a sequence by a second small kernel from fp32 partial results.  The number
-// of parts goes by the problem's sizes alone: enough CTAs for every SM.
+// warp keeps its own running maximum, sum and output; the maximum moves only when a score
+// exceeds it by more than 2^8 (output and sum share the stale one, so the result is the
+// same), and only then do lanes exchange anything.  The warps' results are joined in shared
+// memory, and the parts of a sequence by a second small kernel from fp32 partial results.
+// The number of parts goes by the problem's sizes alone: enough CTAs for every SM.
 //
-// 4 bits: a code n becomes the bf16 number 128 + n by setting the exponent bits around it
-// (0x4300 | n), and 136 is subtracted: two values in two instructions, exact.  A key's
-// scale multiplies its fp32 partial score of each group of 32 channels (two products); a
-// value's scale multiplies the probability before it is rounded to bf16.
+// 4 bits: a code n becomes the bf16 number 128 + n by setting the bits around it
+// (0x4300 | n).  For V 136 is subtracted, exactly: three instructions for two values.  For K
+// the sums start at -136 times the query's sum over the group instead: fp32 partial scores
+// lose 5 of their 24 bits by that, far below what rounding P to bf16 costs.  (V's sums run
+// over all keys, where the same would leave nothing.)  A key's scale multiplies its fp32
+// partial score of each group of 32 channels; a value's scale multiplies the probability
+// before it is rounded to bf16.
 #include <algorithm>
 
 #include "lm.cuh"
@@ -35,22 +40,31 @@ namespace {
 
 constexpr int kWarps = 4;        // per CTA
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 16;        // query heads of a tile
 constexpr int kBlock = 16;       // keys of a block
 constexpr float kLog2eD = 1.4426950408889634074f;
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// (128 + n, 128 + n') - 136 for the nibbles n, n' at bits i4 and i4 + 16
+// An 8 x 8 matrix of 16-bit values, two neighbours of a row per lane, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// (128 + n, 128 + n') for the nibbles n, n' at bits i4 and i4 + 16
+__device__ __forceinline__ uint32_t nibbles_plus128(uint32_t x, int i4) {
+  return ((x >> i4) & 0x000F000Fu) | 0x43004300u;
+}
 __device__ __forceinline__ uint32_t nibbles_bf16(uint32_t x, int i4) {
-  const uint32_t u = ((x >> i4) & 0x000F000Fu) | 0x43004300u;
+  const uint32_t u = nibbles_plus128(x, i4);
   const uint32_t k136 = 0x43084308u;
   const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
                                    *reinterpret_cast<const __nv_bfloat162*>(&k136));
@@ -91,35 +105,44 @@ struct Blocks {
   __device__ __forceinline__ int block(int t) const { return t < sink ? t : first + t - sink; }
 };
 
-// One lane's part of a block of 16 keys of K (lane = 4 key + t of an 8-key half) and of V
-// (lane = 4 a + t: keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9; channels by a).
-template <int D, bool kKv4>
+// One lane's part of a block of 16 keys, lane = 4 g + t: of K the keys g and g + 8, every
+// fourth 16 bytes of their channels by t; of V the keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9,
+// channels by g.  HT: tiles of 8 query heads.
+template <int D, int HT, bool kKv4>
 struct Cache;
 
-template <int D>
-struct Cache<D, false> {
-  static constexpr int NT = D / 8;  // column tiles of the output
+template <int D, int HT>
+struct Cache<D, HT, false> {
+  const __nv_bfloat16 *kp, *vp;
+  long long kn, vn;
+  int last;
   uint4 k[2][D / 32], v[4][D / 64];
 
-  __device__ __forceinline__ void load_k(const DecodeArgs& a, int b, int h, int j0, int lane) {
+  __device__ __forceinline__ Cache(const DecodeArgs& a, int b, int h, int lane) {
+    kp = a.k.row(b, h, 0) + 8 * (lane & 3);
+    vp = a.v.row(b, h, 0) + 8 * (lane >> 2);
+    kn = a.k.sn;
+    vn = a.v.sn;
+    last = a.w.nk - 1;
+  }
+  __device__ __forceinline__ void prepare(const uint32_t (&)[HT][D / 8], int) {}
+  __device__ __forceinline__ void load_k(int j0, int lane) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int j = min(j0 + 8 * half + (lane >> 2), a.w.nk - 1);
-      const __nv_bfloat16* p = a.k.row(b, h, j) + 8 * (lane & 3);
+    for (int x = 0; x < 2; ++x) {
+      const __nv_bfloat16* p = kp + min(j0 + 8 * x + (lane >> 2), last) * kn;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) k[half][i] = load16(p + 32 * i);
+      for (int i = 0; i < D / 32; ++i) k[x][i] = load16(p + 32 * i);
     }
   }
-  __device__ __forceinline__ void load_v(const DecodeArgs& a, int b, int h, int j0, int lane) {
+  __device__ __forceinline__ void load_v(int j0, int lane) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int j = min(j0 + 2 * (lane & 3) + (x & 1) + 8 * (x >> 1), a.w.nk - 1);
-      const __nv_bfloat16* p = a.v.row(b, h, j) + 8 * (lane >> 2);
+      const __nv_bfloat16* p = vp + min(j0 + 2 * (lane & 3) + (x & 1) + 8 * (x >> 1), last) * vn;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) v[x][i] = load16(p + 64 * i);
     }
   }
-  // channels 32 i + 8 t + 2 s', + 1 are the lane's pair s' of products 2 i and 2 i + 1
+  // channels 32 i + 8 t + 2 s, + 1 are the lane's pair s of products 2 i and 2 i + 1
   static __device__ __forceinline__ void load_q(const __nv_bfloat16* row, int t, uint32_t (&q)[D / 8]) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -130,29 +153,37 @@ struct Cache<D, false> {
       q[4 * i + 3] = u.w;
     }
   }
-  __device__ __forceinline__ void scores(const uint32_t (&q0)[D / 8], const uint32_t (&q1)[D / 8],
-                                         float (&s)[2][4]) const {
+  __device__ __forceinline__ void scores(const uint32_t (&q)[HT][D / 8], float (&s)[HT][4]) const {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      s[half][0] = s[half][1] = s[half][2] = s[half][3] = 0.f;
+    for (int ht = 0; ht < HT; ++ht) {
+      // two chains of products, added at the end
+      float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint4 u = k[half][i];
-        const uint32_t a0[4] = {q0[4 * i], q1[4 * i], q0[4 * i + 1], q1[4 * i + 1]};
-        const uint32_t a1[4] = {q0[4 * i + 2], q1[4 * i + 2], q0[4 * i + 3], q1[4 * i + 3]};
-        mma16816(s[half], a0, u.x, u.y);
-        mma16816(s[half], a1, u.z, u.w);
+        const uint4 u = k[0][i], w = k[1][i];
+        mma16816(c[0], u.x, w.x, u.y, w.y, q[ht][4 * i], q[ht][4 * i + 1]);
+        mma16816(c[1], u.z, w.z, u.w, w.w, q[ht][4 * i + 2], q[ht][4 * i + 3]);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[ht][e] = c[0][e] + c[1][e];
     }
   }
   // rows that are not visible may hold anything (NaN times a probability of 0)
-  __device__ __forceinline__ void drop_v(int x) {
+  __device__ __forceinline__ void drop_v(const bool (&see)[4]) {
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) v[x][i] = make_uint4(0, 0, 0, 0);
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        if (!see[x]) v[x][i] = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void mix(const float (&p)[2][4], float (&o)[NT][4]) const {
-    const uint32_t a[4] = {pack2(p[0][0], p[0][1]), pack2(p[0][2], p[0][3]), pack2(p[1][0], p[1][1]),
-                           pack2(p[1][2], p[1][3])};
+  __device__ __forceinline__ void drop_scales(const bool (&)[2]) {}
+  __device__ __forceinline__ void mix(const float (&p)[HT][4], float (&o)[HT][D / 16][4]) const {
+    uint32_t b0[HT], b1[HT];
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht) {
+      b0[ht] = transpose8x8(pack2(p[ht][0], p[ht][1]));
+      b1[ht] = transpose8x8(pack2(p[ht][2], p[ht][3]));
+    }
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
       const uint32_t w[4][4] = {{v[0][i].x, v[0][i].y, v[0][i].z, v[0][i].w},
@@ -160,73 +191,89 @@ struct Cache<D, false> {
                                 {v[2][i].x, v[2][i].y, v[2][i].z, v[2][i].w},
                                 {v[3][i].x, v[3][i].y, v[3][i].z, v[3][i].w}};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t sel = (e & 1) ? 0x7632 : 0x5410;
-        mma16816(o[8 * i + e], a, __byte_perm(w[0][e / 2], w[1][e / 2], sel),
-                 __byte_perm(w[2][e / 2], w[3][e / 2], sel));
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t a0 = __byte_perm(w[0][e], w[1][e], 0x5410), a1 = __byte_perm(w[0][e], w[1][e], 0x7632);
+        const uint32_t a2 = __byte_perm(w[2][e], w[3][e], 0x5410), a3 = __byte_perm(w[2][e], w[3][e], 0x7632);
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht) mma16816(o[ht][4 * i + e], a0, a1, a2, a3, b0[ht], b1[ht]);
       }
     }
   }
-  // channel of column tile nt, column `col`
-  static __device__ __forceinline__ int channel(int nt, int col) {
-    return 64 * (nt / 8) + 8 * col + nt % 8;
+  // channel of output tile m, row g (low) or g + 8 (high)
+  static __device__ __forceinline__ int channel(int m, int g, int high) {
+    return 64 * (m / 4) + 8 * g + 2 * (m % 4) + high;
   }
 };
 
-template <int D>
-struct Cache<D, true> {
-  static constexpr int NT = D / 8, G = D / 32;
-  uint32_t k[2][G], v[4][G / 2];  // codes
-  uint32_t ks[2][2][G / 2];       // scales of keys 8 half + 2 t, + 1: two bf16 in each word
-  uint32_t vs[4][G / 2];
+template <int D, int HT>
+struct Cache<D, HT, true> {
+  static constexpr int G = D / 32, W = G / 2;  // groups, and words that hold a value for each
+  const char *kp, *vp, *ksp, *vsp;
+  int last;
+  uint32_t k[2][G], v[4][W], ks[2][W], vs[2][W];  // codes; scales of keys g and g + 8
+  float q0[HT][G][2];                             // -136 times the sums of heads 2 t and 2 t + 1
 
-  static __device__ __forceinline__ void load_scales(const void* scales, long long row,
-                                                     uint32_t (&s)[G / 2]) {
-    const char* p = static_cast<const char*>(scales) + row * (2 * G);
-    if constexpr (G == 4) {
+  __device__ __forceinline__ Cache(const DecodeArgs& a, int b, int h, int lane) {
+    const long long base = ((long long)b * a.w.nkv + h) * a.w.nk;
+    kp = static_cast<const char*>(a.kcodes) + base * (D / 2) + (D / 8) * (lane & 3);
+    vp = static_cast<const char*>(a.vcodes) + base * (D / 2) + (D / 16) * (lane >> 2);
+    ksp = static_cast<const char*>(a.kscales) + base * (2 * G);
+    vsp = static_cast<const char*>(a.vscales) + base * (2 * G);
+    last = a.w.nk - 1;
+  }
+  __device__ __forceinline__ void prepare(const uint32_t (&q)[HT][D / 8], int lane) {
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float s = 0.f;  // this lane's 8 channels of head lane / 4, then its four lanes'
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          s += __uint_as_float(q[ht][4 * g + i] << 16) + __uint_as_float(q[ht][4 * g + i] & 0xffff0000u);
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        q0[ht][g][0] = -136.f * __shfl_sync(0xffffffffu, s, 8 * (lane & 3));
+        q0[ht][g][1] = -136.f * __shfl_sync(0xffffffffu, s, 8 * (lane & 3) + 4);
+      }
+  }
+  static __device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[W]) {
+    if constexpr (W == 2) {
       const uint2 u = load8(p);
-      s[0] = u.x;
-      s[1] = u.y;
+      w[0] = u.x;
+      w[1] = u.y;
     } else {
-      s[0] = load4(p);
+      w[0] = load4(p);
     }
   }
-  __device__ __forceinline__ void load_k(const DecodeArgs& a, int b, int h, int j0, int lane) {
-    const long long base = ((long long)b * a.w.nkv + h) * a.w.nk;
+  __device__ __forceinline__ void load_k(int j0, int lane) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int j = min(j0 + 8 * half + (lane >> 2), a.w.nk - 1);
-      const char* p = static_cast<const char*>(a.kcodes) + (base + j) * (D / 2) + (D / 8) * (lane & 3);
+    for (int x = 0; x < 2; ++x) {
+      const long long j = min(j0 + 8 * x + (lane >> 2), last);
+      const char* p = kp + j * (D / 2);
       if constexpr (G == 4) {
         const uint4 u = load16(p);
-        k[half][0] = u.x;
-        k[half][1] = u.y;
-        k[half][2] = u.z;
-        k[half][3] = u.w;
+        k[x][0] = u.x;
+        k[x][1] = u.y;
+        k[x][2] = u.z;
+        k[x][3] = u.w;
       } else {
         const uint2 u = load8(p);
-        k[half][0] = u.x;
-        k[half][1] = u.y;
+        k[x][0] = u.x;
+        k[x][1] = u.y;
       }
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        load_scales(a.kscales, base + min(j0 + 8 * half + 2 * (lane & 3) + x, a.w.nk - 1), ks[half][x]);
+      load_words(ksp + j * (2 * G), ks[x]);
     }
   }
-  __device__ __forceinline__ void load_v(const DecodeArgs& a, int b, int h, int j0, int lane) {
-    const long long base = ((long long)b * a.w.nkv + h) * a.w.nk;
+  __device__ __forceinline__ void load_v(int j0, int lane) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int j = min(j0 + 2 * (lane & 3) + (x & 1) + 8 * (x >> 1), a.w.nk - 1);
-      const char* p = static_cast<const char*>(a.vcodes) + (base + j) * (D / 2) + (D / 16) * (lane >> 2);
-      if constexpr (G == 4) {
-        const uint2 u = load8(p);
-        v[x][0] = u.x;
-        v[x][1] = u.y;
-      } else {
-        v[x][0] = load4(p);
-      }
-      load_scales(a.vscales, base + j, vs[x]);
+      const long long j = min(j0 + 2 * (lane & 3) + (x & 1) + 8 * (x >> 1), last);
+      load_words(vp + j * (D / 2), v[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const long long j = min(j0 + 8 * x + (lane >> 2), last);
+      load_words(vsp + j * (2 * G), vs[x]);
     }
   }
   // channels 32 g + 8 t + i and 32 g + 8 t + 4 + i are pair i of group g
@@ -240,192 +287,226 @@ struct Cache<D, true> {
       q[4 * g + 3] = __byte_perm(u.y, u.w, 0x7632);
     }
   }
-  static __device__ __forceinline__ float scale_of(const uint32_t (&s)[G / 2], int g) {
+  static __device__ __forceinline__ float scale_of(const uint32_t (&s)[W], int g) {
     return __uint_as_float((g & 1) ? s[g / 2] & 0xffff0000u : s[g / 2] << 16);
   }
-  __device__ __forceinline__ void scores(const uint32_t (&q0)[D / 8], const uint32_t (&q1)[D / 8],
-                                         float (&s)[2][4]) const {
+  __device__ __forceinline__ void scores(const uint32_t (&q)[HT][D / 8], float (&s)[HT][4]) const {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      s[half][0] = s[half][1] = s[half][2] = s[half][3] = 0.f;
+    for (int ht = 0; ht < HT; ++ht) s[ht][0] = s[ht][1] = s[ht][2] = s[ht][3] = 0.f;
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        // words of a = 2 t come first, those of a = 2 t + 1 after them
-        const uint32_t x = __byte_perm(k[half][g / 2], k[half][G / 2 + g / 2], (g & 1) ? 0x7632 : 0x5410);
-        const uint32_t a0[4] = {q0[4 * g], q1[4 * g], q0[4 * g + 1], q1[4 * g + 1]};
-        const uint32_t a1[4] = {q0[4 * g + 2], q1[4 * g + 2], q0[4 * g + 3], q1[4 * g + 3]};
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816(c, a0, nibbles_bf16(x, 0), nibbles_bf16(x, 4));
-        mma16816(c, a1, nibbles_bf16(x, 8), nibbles_bf16(x, 12));
-        const float s0 = scale_of(ks[half][0], g), s1 = scale_of(ks[half][1], g);
-        s[half][0] += c[0] * s0;
-        s[half][1] += c[1] * s1;
-        s[half][2] += c[2] * s0;
-        s[half][3] += c[3] * s1;
+    for (int g = 0; g < G; ++g) {
+      // words of a = 2 t come first, those of a = 2 t + 1 after them
+      const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;
+      const uint32_t x = __byte_perm(k[0][g / 2], k[0][W + g / 2], sel);
+      const uint32_t y = __byte_perm(k[1][g / 2], k[1][W + g / 2], sel);
+      uint32_t a[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[2 * i] = nibbles_plus128(x, 4 * i);
+        a[2 * i + 1] = nibbles_plus128(y, 4 * i);
+      }
+      const float s0 = scale_of(ks[0], g), s1 = scale_of(ks[1], g);
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht) {
+        float c[4] = {q0[ht][g][0], q0[ht][g][1], q0[ht][g][0], q0[ht][g][1]};
+        mma16816(c, a[0], a[1], a[2], a[3], q[ht][4 * g], q[ht][4 * g + 1]);
+        mma16816(c, a[4], a[5], a[6], a[7], q[ht][4 * g + 2], q[ht][4 * g + 3]);
+        s[ht][0] += c[0] * s0;
+        s[ht][1] += c[1] * s0;
+        s[ht][2] += c[2] * s1;
+        s[ht][3] += c[3] * s1;
       }
     }
   }
-  __device__ __forceinline__ void drop_v(int x) {
+  // codes are finite whatever they are: only the scales of hidden keys may be NaN
+  __device__ __forceinline__ void drop_v(const bool (&)[4]) {}
+  __device__ __forceinline__ void drop_scales(const bool (&see)[2]) {
 #pragma unroll
-    for (int i = 0; i < G / 2; ++i) vs[x][i] = 0;
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (!see[x]) vs[x][i] = 0;
   }
-  __device__ __forceinline__ void mix(const float (&p)[2][4], float (&o)[NT][4]) const {
+  __device__ __forceinline__ void mix(const float (&p)[HT][4], float (&o)[HT][D / 16][4]) const {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const float s0 = scale_of(vs[0], g), s1 = scale_of(vs[1], g), s2 = scale_of(vs[2], g),
-                  s3 = scale_of(vs[3], g);
-      const uint32_t a[4] = {pack2(p[0][0] * s0, p[0][1] * s1), pack2(p[0][2] * s0, p[0][3] * s1),
-                             pack2(p[1][0] * s2, p[1][1] * s3), pack2(p[1][2] * s2, p[1][3] * s3)};
+      const float s0 = scale_of(vs[0], g), s1 = scale_of(vs[1], g);
+      uint32_t b0[HT], b1[HT];
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht) {
+        b0[ht] = transpose8x8(pack2(p[ht][0] * s0, p[ht][1] * s0));
+        b1[ht] = transpose8x8(pack2(p[ht][2] * s1, p[ht][3] * s1));
+      }
       const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;
       const uint32_t x = __byte_perm(v[0][g / 2], v[1][g / 2], sel);
       const uint32_t y = __byte_perm(v[2][g / 2], v[3][g / 2], sel);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        mma16816(o[4 * g + i], a, nibbles_bf16(x, 4 * i), nibbles_bf16(y, 4 * i));
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t a0 = nibbles_bf16(x, 8 * i), a1 = nibbles_bf16(x, 8 * i + 4);
+        const uint32_t a2 = nibbles_bf16(y, 8 * i), a3 = nibbles_bf16(y, 8 * i + 4);
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht) mma16816(o[ht][2 * g + i], a0, a1, a2, a3, b0[ht], b1[ht]);
+      }
     }
   }
-  static __device__ __forceinline__ int channel(int nt, int col) {
-    return 32 * (nt / 4) + 4 * col + nt % 4;
+  static __device__ __forceinline__ int channel(int m, int g, int high) {
+    return 32 * (m / 2) + 4 * g + 2 * (m % 2) + high;
   }
 };
 
-template <int D, bool kKv4>
-__global__ void __launch_bounds__(kThreads) window_decode_kernel(const DecodeArgs a) {
-  using C = Cache<D, kKv4>;
-  constexpr int NT = C::NT;
-  __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
-  __shared__ float sm_o[kRows][D + 4];
+template <int D, int HT, bool kKv4>
+__global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 ? 3 : 4)
+    window_decode_kernel(const DecodeArgs a) {
+  using C = Cache<D, HT, kKv4>;
+  constexpr int MT = D / 16, kHeads = 8 * HT;
+  __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
+  __shared__ float sm_o[kHeads][D + 4];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3, r = lane >> 2;
-  const int group = a.w.nh / a.w.nkv, tiles = (group + kRows - 1) / kRows;
-  const int b = blockIdx.z, h = blockIdx.y / tiles, g0 = (blockIdx.y % tiles) * kRows;
-  const int heads = min(kRows, group - g0), h0 = h * group + g0;
+  const int group = a.w.nh / a.w.nkv, tiles = (group + kHeads - 1) / kHeads;
+  const int b = blockIdx.z, h = blockIdx.y / tiles, g0 = (blockIdx.y % tiles) * kHeads;
+  const int heads = min(kHeads, group - g0), h0 = h * group + g0;
   const Blocks bl(a.w, b);
   const int from = (int)((long long)bl.count * blockIdx.x / gridDim.x);
   const int to = (int)((long long)bl.count * (blockIdx.x + 1) / gridDim.x);
 
-  uint32_t q0[D / 8], q1[D / 8];
-  C::load_q(r < heads ? a.q.row(b, h0 + r, 0) : nullptr, t, q0);
-  C::load_q(r + 8 < heads ? a.q.row(b, h0 + r + 8, 0) : nullptr, t, q1);
-  float o[NT][4];
+  C c(a, b, h, lane);
+  int blk = from + warp;
+  if (blk < to) {
+    c.load_k(bl.block(blk) * kBlock, lane);
+    c.load_v(bl.block(blk) * kBlock, lane);
+  }
+  uint32_t q[HT][D / 8];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows r, r + 8 (log2 units)
+  for (int ht = 0; ht < HT; ++ht)
+    C::load_q(8 * ht + r < heads ? a.q.row(b, h0 + 8 * ht + r, 0) : nullptr, t, q[ht]);
+  c.prepare(q, lane);
+  float o[HT][MT][4];
+  float m[HT][2], l[HT][2];  // heads 8 ht + 2 t, + 1; maxima in log2 units
+#pragma unroll
+  for (int ht = 0; ht < HT; ++ht) {
+    m[ht][0] = m[ht][1] = -INFINITY;
+    l[ht][0] = l[ht][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o[ht][i][0] = o[ht][i][1] = o[ht][i][2] = o[ht][i][3] = 0.f;
+  }
   const float sl2 = a.scale * kLog2eD;
 
-  C c;
-  int blk = from + warp;
-  if (blk < to) c.load_k(a, b, h, bl.block(blk) * kBlock, lane);
   for (; blk < to; blk += kWarps) {
     const int j0 = bl.block(blk) * kBlock;
-    c.load_v(a, b, h, j0, lane);
-    float s[2][4];
-    c.scores(q0, q1, s);
-    if (blk + kWarps < to) c.load_k(a, b, h, bl.block(blk + kWarps) * kBlock, lane);
-    // all 16 keys visible: inside the window, or among the sinks
-    const bool whole = j0 + kBlock <= bl.len && (j0 >= bl.lo || j0 + kBlock <= a.w.sinks);
+    float s[HT][4];
+    c.scores(q, s);
+    const int next = blk + kWarps < to ? bl.block(blk + kWarps) * kBlock : -1;
+    if (next >= 0) c.load_k(next, lane);
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+    for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int j = j0 + 8 * half + 2 * t + x;
-        const bool see = whole || (j < bl.len && (j >= bl.lo || j < a.w.sinks));
-        s[half][x] = see ? s[half][x] * sl2 : -INFINITY;
-        s[half][2 + x] = see ? s[half][2 + x] * sl2 : -INFINITY;
-        if (!see) c.drop_v(2 * half + x);
-      }
-    float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-    float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+      for (int e = 0; e < 4; ++e) s[ht][e] *= sl2;
+    // not all 16 keys inside the window, or among the sinks?
+    if (j0 + kBlock > bl.len || (j0 < bl.lo && j0 + kBlock > a.w.sinks)) {
+      auto sees = [&](int j) { return j < bl.len && (j >= bl.lo || j < a.w.sinks); };
+      const bool mine[2] = {sees(j0 + r), sees(j0 + 8 + r)};
+      const bool value[4] = {sees(j0 + 2 * t), sees(j0 + 2 * t + 1), sees(j0 + 2 * t + 8), sees(j0 + 2 * t + 9)};
 #pragma unroll
-    for (int m = 1; m <= 2; m <<= 1) {
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, m));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, m));
+      for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!mine[e / 2]) s[ht][e] = -INFINITY;
+      c.drop_v(value);
+      c.drop_scales(mine);
     }
-    // the running maximum moves only when it grows by more than 2^8: output and sum share
-    // the stale one, so the result is the same
-    const bool grow = x0 > m0 + 8.f || x1 > m1 + 8.f;
+    bool grow = false;
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht)
+      grow |= fmaxf(s[ht][0], s[ht][2]) > m[ht][0] + 8.f || fmaxf(s[ht][1], s[ht][3]) > m[ht][1] + 8.f;
     if (__any_sync(0xffffffffu, grow)) {
-      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-      const float f0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
-      const float f1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
-      m0 = n0;
-      m1 = n1;
-      l0 *= f0;
-      l1 *= f1;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        o[i][0] *= f0;
-        o[i][1] *= f0;
-        o[i][2] *= f1;
-        o[i][3] *= f1;
+      for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float n = fmaxf(s[ht][e], s[ht][2 + e]);
+          n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 4));
+          n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 8));
+          n = fmaxf(m[ht][e], fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 16)));
+          const float f = n == -INFINITY ? 1.f : fast_exp2(m[ht][e] - n);
+          m[ht][e] = n;
+          l[ht][e] *= f;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            o[ht][i][e] *= f;
+            o[ht][i][2 + e] *= f;
+          }
+        }
       }
     }
-    const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      s[half][0] = fast_exp2(s[half][0] - b0);
-      s[half][1] = fast_exp2(s[half][1] - b0);
-      s[half][2] = fast_exp2(s[half][2] - b1);
-      s[half][3] = fast_exp2(s[half][3] - b1);
-      l0 += s[half][0] + s[half][1];
-      l1 += s[half][2] + s[half][3];
-    }
+    for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float base = m[ht][e] == -INFINITY ? 0.f : m[ht][e];
+        s[ht][e] = fast_exp2(s[ht][e] - base);
+        s[ht][2 + e] = fast_exp2(s[ht][2 + e] - base);
+        l[ht][e] += s[ht][e] + s[ht][2 + e];
+      }
     c.mix(s, o);
+    if (next >= 0) c.load_v(next, lane);
   }
-  // the four lanes of a row each summed their own columns
+  // the eight lanes of a head each summed their own keys
 #pragma unroll
-  for (int m = 1; m <= 2; m <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, m);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, m);
-  }
-  if (t == 0) {
-    sm_m[warp][r] = m0;
-    sm_m[warp][r + 8] = m1;
-    sm_l[warp][r] = l0;
-    sm_l[warp][r + 8] = l1;
-  }
+  for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int x = 4; x <= 16; x <<= 1) l[ht][e] += __shfl_xor_sync(0xffffffffu, l[ht][e], x);
+      if (r == 0) {
+        sm_m[warp][8 * ht + 2 * t + e] = m[ht][e];
+        sm_l[warp][8 * ht + 2 * t + e] = l[ht][e];
+      }
+    }
   __syncthreads();
-  float n0 = -INFINITY, n1 = -INFINITY;
+  float f[HT][2];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    n0 = fmaxf(n0, sm_m[w][r]);
-    n1 = fmaxf(n1, sm_m[w][r + 8]);
-  }
-  const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0);
-  const float f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
+  for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float n = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) n = fmaxf(n, sm_m[w][8 * ht + 2 * t + e]);
+      f[ht][e] = m[ht][e] == -INFINITY ? 0.f : fast_exp2(m[ht][e] - n);
+    }
   // the warps add their outputs one after another: a fixed order
   for (int w = 0; w < kWarps; ++w) {
     if (warp == w) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float* d0 = &sm_o[r][C::channel(i, 2 * t + e)];
-          float* d1 = &sm_o[r + 8][C::channel(i, 2 * t + e)];
-          *d0 = (w == 0 ? 0.f : *d0) + o[i][e] * f0;
-          *d1 = (w == 0 ? 0.f : *d1) + o[i][2 + e] * f1;
-        }
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float* d = &sm_o[8 * ht + 2 * t + (e & 1)][C::channel(i, r, e >> 1)];
+            *d = (w == 0 ? 0.f : *d) + o[ht][i][e] * f[ht][e & 1];
+          }
     }
     __syncthreads();
   }
   for (int u = threadIdx.x; u < heads * D; u += kThreads) {
     const int row = u / D, ch = u % D;
-    float n = -INFINITY, l = 0.f;
+    float n = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) n = fmaxf(n, sm_m[w][row]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      l += sm_m[w][row] == -INFINITY ? 0.f : sm_l[w][row] * fast_exp2(sm_m[w][row] - n);
+      sum += sm_m[w][row] == -INFINITY ? 0.f : sm_l[w][row] * fast_exp2(sm_m[w][row] - n);
     if (gridDim.x == 1) {
-      a.o.row(b, h0 + row, 0)[ch] = __float2bfloat16_rn(l > 0.f ? sm_o[row][ch] / l : 0.f);
+      a.o.row(b, h0 + row, 0)[ch] = __float2bfloat16_rn(sum > 0.f ? sm_o[row][ch] / sum : 0.f);
     } else {
       // partial result: D outputs relative to the maximum n, then n and the sum
       float* dst = a.ws + (((long long)b * a.w.nh + h0 + row) * gridDim.x + blockIdx.x) * (D + 2);
       dst[ch] = sm_o[row][ch];
       if (ch == 0) {
         dst[D] = n;
-        dst[D + 1] = l;
+        dst[D + 1] = sum;
       }
     }
   }
@@ -450,12 +531,15 @@ __global__ void __launch_bounds__(D) window_join_kernel(const DecodeArgs a, int 
   a.o.row(b, h, 0)[threadIdx.x] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
 }
 
+// Query heads of a tile: eight where a group has no more (half the registers), else sixteen.
+int head_tile(const Window& w) { return w.nh / w.nkv <= 8 ? 8 : 16; }
+
 template <int D, bool kKv4>
 cudaError_t decode(const DecodeArgs& a, cudaStream_t st) {
-  const int group = a.w.nh / a.w.nkv, tiles = (group + kRows - 1) / kRows;
+  const int group = a.w.nh / a.w.nkv, tile = head_tile(a.w), tiles = (group + tile - 1) / tile;
   const int splits = decode_splits(a.w);
-  cudaError_t e = launch_pdl(window_decode_kernel<D, kKv4>, dim3(splits, a.w.nkv * tiles, a.w.B),
-                             dim3(kThreads), 0, st, a);
+  auto kern = tile == 8 ? window_decode_kernel<D, 1, kKv4> : window_decode_kernel<D, 2, kKv4>;
+  cudaError_t e = launch_pdl(kern, dim3(splits, a.w.nkv * tiles, a.w.B), dim3(kThreads), 0, st, a);
   if (e != cudaSuccess || splits == 1) return e;
   return launch_pdl(window_join_kernel<D>, dim3(a.w.nh, a.w.B), dim3(D), 0, st, a, splits);
 }
@@ -463,13 +547,13 @@ cudaError_t decode(const DecodeArgs& a, cudaStream_t st) {
 }  // namespace
 
 int decode_splits(const Window& w) {
-  const int group = w.nh / w.nkv, tiles = (group + kRows - 1) / kRows;
+  const int group = w.nh / w.nkv, tiles = (group + head_tile(w) - 1) / head_tile(w);
   // the most blocks a sequence can see
   const long long rows = std::min<long long>(w.nk, (long long)w.left + 1 + w.sinks);
   const long long blocks = (rows + kBlock - 1) / kBlock + 1;
   const long long ctas = (long long)w.B * w.nkv * tiles;
-  // six CTAs per SM between them, but at least four blocks for each warp
-  const long long want = (6LL * 152 + ctas - 1) / ctas, most = std::max<long long>(1, blocks / (4 * kWarps));
+  // eight CTAs per SM between them, but at least four blocks for each warp
+  const long long want = (8LL * 152 + ctas - 1) / ctas, most = std::max<long long>(1, blocks / (4 * kWarps));
   return (int)std::min<long long>(std::min(want, most), 256);
 }
 

@@ -15,7 +15,7 @@
 // registers of one lane, and a byte permute puts them side by side; P, whose rows are keys,
 // becomes the B operand by an 8 x 8 transposition inside the warp.
 //
-// Keys are cut into blocks of 16; the visible blocks (the sinks', then the window's) are
+// Keys are cut into blocks of 16 or 32; the visible blocks (the sinks', then the window's) are
 // dealt to gridDim.x CTAs in contiguous parts and inside a CTA to its warps in turn.  Every
 // warp keeps its own running maximum, sum and output; the maximum moves only when a score
 // exceeds it by more than 2^8 (output and sum share the stale one, so the result is the
@@ -23,14 +23,18 @@
 // memory, and the parts of a sequence by a second small kernel from fp32 partial results.
 // The number of parts goes by the problem's sizes alone: enough CTAs for every SM.
 //
-// 4 bits: a code n becomes the bf16 number 128 + n by setting the bits around it
-// (0x4300 | n).  For V 136 is subtracted, exactly: three instructions for two values.  For K
-// the sums start at -136 times the query's sum over the group instead: fp32 partial scores
-// lose 5 of their 24 bits by that, far below what rounding P to bf16 costs.  (V's sums run
-// over all keys, where the same would leave nothing.)  A key's scale multiplies its fp32
-// partial score of each group of 32 channels; a value's scale multiplies the probability
-// before it is rounded to bf16.
+// 4 bits: what bounds the kernel there is the integer work of widening codes, so it is kept
+// small.  K: a code at bits 0-3 or 4-7 of a 16-bit half becomes the fp16 number 1024 + n or
+// 64 + n by one masked OR, without a shift; the query, in fp16 too (scaled by a power of two
+// to a maximum of 1), takes the offsets off again: the fp32 sums start at minus the query's sums
+// times 1032 and 72, which costs them 8 of their 24 bits, far less than rounding P to bf16.
+// V: 128 + n in bf16 (P times a scale needs its range), shifted on the multipliers, less 136,
+// exactly; its sums run over all keys, where subtracting at the end would leave nothing.  A
+// key's scale multiplies its fp32 partial score of each group of 32 channels; a value's scale
+// multiplies the probability before it is rounded to bf16.
 #include <algorithm>
+
+#include <cuda_fp16.h>
 
 #include "lm.cuh"
 #include "ptx.cuh"
@@ -40,17 +44,29 @@ namespace {
 
 constexpr int kWarps = 4;        // per CTA
 constexpr int kThreads = 32 * kWarps;
-constexpr int kBlock = 16;       // keys of a block
+constexpr int kLongBlock = 32;   // most keys that a warp takes at a time
 constexpr float kLog2eD = 1.4426950408889634074f;
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+// d = a b + c (m16n8k16, fp32 sums); c's two values are for the columns of a lane, in both its
+// rows.
+#define PSA_MMA(NAME, TYPE)                                                                        \
+  __device__ __forceinline__ void NAME(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,       \
+                                       uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1) { \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                     \
+        ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"                 \
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                           \
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));                 \
+  }                                                                                                \
+  __device__ __forceinline__ void NAME(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,       \
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {                    \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                     \
+        ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"                     \
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                           \
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));                                   \
+  }
+PSA_MMA(mma16816, "bf16")
+PSA_MMA(mma16816_f16, "f16")
+#undef PSA_MMA
 
 // An 8 x 8 matrix of 16-bit values, two neighbours of a row per lane, transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -59,12 +75,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// (128 + n, 128 + n') for the nibbles n, n' at bits i4 and i4 + 16
-__device__ __forceinline__ uint32_t nibbles_plus128(uint32_t x, int i4) {
-  return ((x >> i4) & 0x000F000Fu) | 0x43004300u;
-}
-__device__ __forceinline__ uint32_t nibbles_bf16(uint32_t x, int i4) {
-  const uint32_t u = nibbles_plus128(x, i4);
+// n - 8, n' - 8 in bf16 for the nibbles n, n' at bits 4 i and 4 i + 16
+template <int i>
+__device__ __forceinline__ uint32_t nibbles_bf16(uint32_t x) {
+  const uint32_t u = ((x >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
   const uint32_t k136 = 0x43084308u;
   const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
                                    *reinterpret_cast<const __nv_bfloat162*>(&k136));
@@ -93,6 +107,7 @@ __device__ __forceinline__ uint32_t load4(const void* p) {
 }
 
 // The visible rows of sequence b: blocks 0 .. sink - 1, then first .. (count in all).
+template <int kBlock>
 struct Blocks {
   int len, lo, sink, first, count;
   __device__ __forceinline__ Blocks(const Window& w, int b) {
@@ -108,15 +123,18 @@ struct Blocks {
 // One lane's part of a block of 16 keys, lane = 4 g + t: of K the keys g and g + 8, every
 // fourth 16 bytes of their channels by t; of V the keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9,
 // channels by g.  HT: tiles of 8 query heads.
-template <int D, int HT, bool kKv4>
+// kShort: the cache has fewer rows than a block, so rows behind the last are read as that one
+// (they are hidden); otherwise the last block starts early enough to end inside the cache.
+template <int D, int HT, bool kKv4, bool kShort>
 struct Cache;
 
-template <int D, int HT>
-struct Cache<D, HT, false> {
+template <int D, int HT, bool kShort>
+struct Cache<D, HT, false, kShort> {
+  static constexpr int U = 1;  // blocks of 16 keys at a time
   const __nv_bfloat16 *kp, *vp;
   long long kn, vn;
   int last;
-  uint4 k[2][D / 32], v[4][D / 64];
+  uint4 k[U][2][D / 32], v[U][4][D / 64];
 
   __device__ __forceinline__ Cache(const DecodeArgs& a, int b, int h, int lane) {
     kp = a.k.row(b, h, 0) + 8 * (lane & 3);
@@ -125,22 +143,30 @@ struct Cache<D, HT, false> {
     vn = a.v.sn;
     last = a.w.nk - 1;
   }
-  __device__ __forceinline__ void prepare(const uint32_t (&)[HT][D / 8], int) {}
+  __device__ __forceinline__ void prepare(uint32_t (&)[HT][D / 8], float (&up)[HT][2], int) {
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht) up[ht][0] = up[ht][1] = 1.f;
+  }
+  __device__ __forceinline__ int row(int j) const { return kShort ? min(j, last) : j; }
   __device__ __forceinline__ void load_k(int j0, int lane) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const __nv_bfloat16* p = kp + min(j0 + 8 * x + (lane >> 2), last) * kn;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) k[x][i] = load16(p + 32 * i);
-    }
+      for (int x = 0; x < 2; ++x) {
+        const __nv_bfloat16* p = kp + row(j0 + 16 * u + 8 * x + (lane >> 2)) * kn;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) k[u][x][i] = load16(p + 32 * i);
+      }
   }
   __device__ __forceinline__ void load_v(int j0, int lane) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const __nv_bfloat16* p = vp + min(j0 + 2 * (lane & 3) + (x & 1) + 8 * (x >> 1), last) * vn;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) v[x][i] = load16(p + 64 * i);
-    }
+      for (int x = 0; x < 4; ++x) {
+        const __nv_bfloat16* p = vp + row(j0 + 16 * u + 2 * (lane & 3) + (x & 1) + 8 * (x >> 1)) * vn;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) v[u][x][i] = load16(p + 64 * i);
+      }
   }
   // channels 32 i + 8 t + 2 s, + 1 are the lane's pair s of products 2 i and 2 i + 1
   static __device__ __forceinline__ void load_q(const __nv_bfloat16* row, int t, uint32_t (&q)[D / 8]) {
@@ -153,31 +179,31 @@ struct Cache<D, HT, false> {
       q[4 * i + 3] = u.w;
     }
   }
-  __device__ __forceinline__ void scores(const uint32_t (&q)[HT][D / 8], float (&s)[HT][4]) const {
+  __device__ __forceinline__ void scores(int u, const uint32_t (&q)[HT][D / 8], float (&s)[HT][4]) const {
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
       // two chains of products, added at the end
       float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint4 u = k[0][i], w = k[1][i];
-        mma16816(c[0], u.x, w.x, u.y, w.y, q[ht][4 * i], q[ht][4 * i + 1]);
-        mma16816(c[1], u.z, w.z, u.w, w.w, q[ht][4 * i + 2], q[ht][4 * i + 3]);
+        const uint4 x = k[u][0][i], y = k[u][1][i];
+        mma16816(c[0], x.x, y.x, x.y, y.y, q[ht][4 * i], q[ht][4 * i + 1]);
+        mma16816(c[1], x.z, y.z, x.w, y.w, q[ht][4 * i + 2], q[ht][4 * i + 3]);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[ht][e] = c[0][e] + c[1][e];
     }
   }
   // rows that are not visible may hold anything (NaN times a probability of 0)
-  __device__ __forceinline__ void drop_v(const bool (&see)[4]) {
+  __device__ __forceinline__ void drop_v(int u, const bool (&see)[4]) {
 #pragma unroll
     for (int x = 0; x < 4; ++x)
 #pragma unroll
       for (int i = 0; i < D / 64; ++i)
-        if (!see[x]) v[x][i] = make_uint4(0, 0, 0, 0);
+        if (!see[x]) v[u][x][i] = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void drop_scales(const bool (&)[2]) {}
-  __device__ __forceinline__ void mix(const float (&p)[HT][4], float (&o)[HT][D / 16][4]) const {
+  __device__ __forceinline__ void drop_scales(int, const bool (&)[2]) {}
+  __device__ __forceinline__ void mix(int u, const float (&p)[HT][4], float (&o)[HT][D / 16][4]) const {
     uint32_t b0[HT], b1[HT];
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
@@ -186,10 +212,10 @@ struct Cache<D, HT, false> {
     }
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
-      const uint32_t w[4][4] = {{v[0][i].x, v[0][i].y, v[0][i].z, v[0][i].w},
-                                {v[1][i].x, v[1][i].y, v[1][i].z, v[1][i].w},
-                                {v[2][i].x, v[2][i].y, v[2][i].z, v[2][i].w},
-                                {v[3][i].x, v[3][i].y, v[3][i].z, v[3][i].w}};
+      const uint32_t w[4][4] = {{v[u][0][i].x, v[u][0][i].y, v[u][0][i].z, v[u][0][i].w},
+                                {v[u][1][i].x, v[u][1][i].y, v[u][1][i].z, v[u][1][i].w},
+                                {v[u][2][i].x, v[u][2][i].y, v[u][2][i].z, v[u][2][i].w},
+                                {v[u][3][i].x, v[u][3][i].y, v[u][3][i].z, v[u][3][i].w}};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t a0 = __byte_perm(w[0][e], w[1][e], 0x5410), a1 = __byte_perm(w[0][e], w[1][e], 0x7632);
@@ -205,36 +231,58 @@ struct Cache<D, HT, false> {
   }
 };
 
-template <int D, int HT>
-struct Cache<D, HT, true> {
+template <int D, int HT, bool kShort>
+struct Cache<D, HT, true, kShort> {
   static constexpr int G = D / 32, W = G / 2;  // groups, and words that hold a value for each
+  // two blocks of 16 keys at a time: twice the bytes in flight and half the steps' overhead
+  // (long contexts 123 -> 98 us); sixteen heads leave no registers for that
+  static constexpr int U = HT == 1 ? 2 : 1;
   const char *kp, *vp, *ksp, *vsp;
   int last;
-  uint32_t k[2][G], v[4][W], ks[2][W], vs[2][W];  // codes; scales of keys g and g + 8
-  float q0[HT][G][2];                             // -136 times the sums of heads 2 t and 2 t + 1
+  uint32_t k[U][2][G], v[U][4][W], ks[U][2][W], vs[U][2][W];  // codes; scales of keys g and g + 8
+  float q0[HT][G][2];  // minus what the codes' offsets add to the sums of heads 2 t and 2 t + 1
 
   __device__ __forceinline__ Cache(const DecodeArgs& a, int b, int h, int lane) {
     const long long base = ((long long)b * a.w.nkv + h) * a.w.nk;
-    kp = static_cast<const char*>(a.kcodes) + base * (D / 2) + (D / 8) * (lane & 3);
-    vp = static_cast<const char*>(a.vcodes) + base * (D / 2) + (D / 16) * (lane >> 2);
-    ksp = static_cast<const char*>(a.kscales) + base * (2 * G);
-    vsp = static_cast<const char*>(a.vscales) + base * (2 * G);
+    const int g = lane >> 2, t = lane & 3;
+    kp = static_cast<const char*>(a.kcodes) + (base + g) * (D / 2) + (D / 8) * t;
+    vp = static_cast<const char*>(a.vcodes) + (base + 2 * t) * (D / 2) + (D / 16) * g;
+    ksp = static_cast<const char*>(a.kscales) + (base + g) * (2 * G);
+    vsp = static_cast<const char*>(a.vscales) + (base + g) * (2 * G);
     last = a.w.nk - 1;
   }
-  __device__ __forceinline__ void prepare(const uint32_t (&q)[HT][D / 8], int lane) {
+  // The query in fp16, scaled to a maximum of 1 .. 2, and what that has to be undone by.
+  __device__ __forceinline__ void prepare(uint32_t (&q)[HT][D / 8], float (&up)[HT][2], int lane) {
 #pragma unroll
-    for (int ht = 0; ht < HT; ++ht)
+    for (int ht = 0; ht < HT; ++ht) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(q[ht][i] << 16)), fabsf(__uint_as_float(q[ht][i] & 0xffff0000u))));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      // powers of two: 2^-e and 2^e for m in 2^e .. 2^(e + 1), both normal numbers
+      const uint32_t e = min(max(__float_as_uint(m) >> 23, 1u), 253u);
+      const float down = __uint_as_float((254u - e) << 23);
+      const float mine = __uint_as_float(e << 23);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         float s = 0.f;  // this lane's 8 channels of head lane / 4, then its four lanes'
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s += __uint_as_float(q[ht][4 * g + i] << 16) + __uint_as_float(q[ht][4 * g + i] & 0xffff0000u);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t& x = q[ht][4 * g + i];
+          const __half2 y = __floats2half2_rn(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
+          x = *reinterpret_cast<const uint32_t*>(&y);
+          s -= (i & 1 ? 72.f : 1032.f) * (__low2float(y) + __high2float(y));
+        }
         s += __shfl_xor_sync(0xffffffffu, s, 1);
         s += __shfl_xor_sync(0xffffffffu, s, 2);
-        q0[ht][g][0] = -136.f * __shfl_sync(0xffffffffu, s, 8 * (lane & 3));
-        q0[ht][g][1] = -136.f * __shfl_sync(0xffffffffu, s, 8 * (lane & 3) + 4);
+        q0[ht][g][0] = __shfl_sync(0xffffffffu, s, 8 * (lane & 3));
+        q0[ht][g][1] = __shfl_sync(0xffffffffu, s, 8 * (lane & 3) + 4);
       }
+      up[ht][0] = __shfl_sync(0xffffffffu, mine, 8 * (lane & 3));
+      up[ht][1] = __shfl_sync(0xffffffffu, mine, 8 * (lane & 3) + 4);
+    }
   }
   static __device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[W]) {
     if constexpr (W == 2) {
@@ -245,35 +293,40 @@ struct Cache<D, HT, true> {
       w[0] = load4(p);
     }
   }
+  // row of a block relative to its first: the lane's own is in the pointers already
+  __device__ __forceinline__ int row(int n, int j0, int own) const {
+    return kShort ? min(n, last - j0 - own) : n;
+  }
   __device__ __forceinline__ void load_k(int j0, int lane) {
+    const char *p = kp + (long long)j0 * (D / 2), *sp = ksp + (long long)j0 * (2 * G);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const long long j = min(j0 + 8 * x + (lane >> 2), last);
-      const char* p = kp + j * (D / 2);
-      if constexpr (G == 4) {
-        const uint4 u = load16(p);
-        k[x][0] = u.x;
-        k[x][1] = u.y;
-        k[x][2] = u.z;
-        k[x][3] = u.w;
-      } else {
-        const uint2 u = load8(p);
-        k[x][0] = u.x;
-        k[x][1] = u.y;
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int n = row(16 * u + 8 * x, j0, lane >> 2);
+        if constexpr (G == 4) {
+          const uint4 w = load16(p + n * (D / 2));
+          k[u][x][0] = w.x;
+          k[u][x][1] = w.y;
+          k[u][x][2] = w.z;
+          k[u][x][3] = w.w;
+        } else {
+          const uint2 w = load8(p + n * (D / 2));
+          k[u][x][0] = w.x;
+          k[u][x][1] = w.y;
+        }
+        load_words(sp + n * (2 * G), ks[u][x]);
       }
-      load_words(ksp + j * (2 * G), ks[x]);
-    }
   }
   __device__ __forceinline__ void load_v(int j0, int lane) {
+    const char *p = vp + (long long)j0 * (D / 2), *sp = vsp + (long long)j0 * (2 * G);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const long long j = min(j0 + 2 * (lane & 3) + (x & 1) + 8 * (x >> 1), last);
-      load_words(vp + j * (D / 2), v[x]);
-    }
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const long long j = min(j0 + 8 * x + (lane >> 2), last);
-      load_words(vsp + j * (2 * G), vs[x]);
+      for (int x = 0; x < 4; ++x)
+        load_words(p + row(16 * u + (x & 1) + 8 * (x >> 1), j0, 2 * (lane & 3)) * (D / 2), v[u][x]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) load_words(sp + row(16 * u + 8 * x, j0, lane >> 2) * (2 * G), vs[u][x]);
     }
   }
   // channels 32 g + 8 t + i and 32 g + 8 t + 4 + i are pair i of group g
@@ -290,27 +343,26 @@ struct Cache<D, HT, true> {
   static __device__ __forceinline__ float scale_of(const uint32_t (&s)[W], int g) {
     return __uint_as_float((g & 1) ? s[g / 2] & 0xffff0000u : s[g / 2] << 16);
   }
-  __device__ __forceinline__ void scores(const uint32_t (&q)[HT][D / 8], float (&s)[HT][4]) const {
+  __device__ __forceinline__ void scores(int u, const uint32_t (&q)[HT][D / 8], float (&s)[HT][4]) const {
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) s[ht][0] = s[ht][1] = s[ht][2] = s[ht][3] = 0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       // words of a = 2 t come first, those of a = 2 t + 1 after them
       const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;
-      const uint32_t x = __byte_perm(k[0][g / 2], k[0][W + g / 2], sel);
-      const uint32_t y = __byte_perm(k[1][g / 2], k[1][W + g / 2], sel);
-      uint32_t a[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[2 * i] = nibbles_plus128(x, 4 * i);
-        a[2 * i + 1] = nibbles_plus128(y, 4 * i);
-      }
-      const float s0 = scale_of(ks[0], g), s1 = scale_of(ks[1], g);
+      const uint32_t x = __byte_perm(k[u][0][g / 2], k[u][0][W + g / 2], sel);
+      const uint32_t y = __byte_perm(k[u][1][g / 2], k[u][1][W + g / 2], sel);
+      const uint32_t x8 = x >> 8, y8 = y >> 8;
+      const uint32_t a[8] = {(x & 0x000F000Fu) | 0x64006400u,  (y & 0x000F000Fu) | 0x64006400u,
+                             (x & 0x00F000F0u) | 0x54005400u,  (y & 0x00F000F0u) | 0x54005400u,
+                             (x8 & 0x000F000Fu) | 0x64006400u, (y8 & 0x000F000Fu) | 0x64006400u,
+                             (x8 & 0x00F000F0u) | 0x54005400u, (y8 & 0x00F000F0u) | 0x54005400u};
+      const float s0 = scale_of(ks[u][0], g), s1 = scale_of(ks[u][1], g);
 #pragma unroll
       for (int ht = 0; ht < HT; ++ht) {
-        float c[4] = {q0[ht][g][0], q0[ht][g][1], q0[ht][g][0], q0[ht][g][1]};
-        mma16816(c, a[0], a[1], a[2], a[3], q[ht][4 * g], q[ht][4 * g + 1]);
-        mma16816(c, a[4], a[5], a[6], a[7], q[ht][4 * g + 2], q[ht][4 * g + 3]);
+        float c[4];
+        mma16816_f16(c, a[0], a[1], a[2], a[3], q[ht][4 * g], q[ht][4 * g + 1], q0[ht][g][0], q0[ht][g][1]);
+        mma16816_f16(c, a[4], a[5], a[6], a[7], q[ht][4 * g + 2], q[ht][4 * g + 3]);
         s[ht][0] += c[0] * s0;
         s[ht][1] += c[1] * s0;
         s[ht][2] += c[2] * s1;
@@ -319,18 +371,18 @@ struct Cache<D, HT, true> {
     }
   }
   // codes are finite whatever they are: only the scales of hidden keys may be NaN
-  __device__ __forceinline__ void drop_v(const bool (&)[4]) {}
-  __device__ __forceinline__ void drop_scales(const bool (&see)[2]) {
+  __device__ __forceinline__ void drop_v(int, const bool (&)[4]) {}
+  __device__ __forceinline__ void drop_scales(int u, const bool (&see)[2]) {
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int i = 0; i < W; ++i)
-        if (!see[x]) vs[x][i] = 0;
+        if (!see[x]) vs[u][x][i] = 0;
   }
-  __device__ __forceinline__ void mix(const float (&p)[HT][4], float (&o)[HT][D / 16][4]) const {
+  __device__ __forceinline__ void mix(int u, const float (&p)[HT][4], float (&o)[HT][D / 16][4]) const {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const float s0 = scale_of(vs[0], g), s1 = scale_of(vs[1], g);
+      const float s0 = scale_of(vs[u][0], g), s1 = scale_of(vs[u][1], g);
       uint32_t b0[HT], b1[HT];
 #pragma unroll
       for (int ht = 0; ht < HT; ++ht) {
@@ -338,14 +390,14 @@ struct Cache<D, HT, true> {
         b1[ht] = transpose8x8(pack2(p[ht][2] * s1, p[ht][3] * s1));
       }
       const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;
-      const uint32_t x = __byte_perm(v[0][g / 2], v[1][g / 2], sel);
-      const uint32_t y = __byte_perm(v[2][g / 2], v[3][g / 2], sel);
+      const uint32_t x = __byte_perm(v[u][0][g / 2], v[u][1][g / 2], sel);
+      const uint32_t y = __byte_perm(v[u][2][g / 2], v[u][3][g / 2], sel);
+      const uint32_t a[8] = {nibbles_bf16<0>(x), nibbles_bf16<1>(x), nibbles_bf16<0>(y), nibbles_bf16<1>(y),
+                             nibbles_bf16<2>(x), nibbles_bf16<3>(x), nibbles_bf16<2>(y), nibbles_bf16<3>(y)};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t a0 = nibbles_bf16(x, 8 * i), a1 = nibbles_bf16(x, 8 * i + 4);
-        const uint32_t a2 = nibbles_bf16(y, 8 * i), a3 = nibbles_bf16(y, 8 * i + 4);
-#pragma unroll
-        for (int ht = 0; ht < HT; ++ht) mma16816(o[ht][2 * g + i], a0, a1, a2, a3, b0[ht], b1[ht]);
+      for (int ht = 0; ht < HT; ++ht) {
+        mma16816(o[ht][2 * g], a[0], a[1], a[2], a[3], b0[ht], b1[ht]);
+        mma16816(o[ht][2 * g + 1], a[4], a[5], a[6], a[7], b0[ht], b1[ht]);
       }
     }
   }
@@ -354,11 +406,11 @@ struct Cache<D, HT, true> {
   }
 };
 
-template <int D, int HT, bool kKv4>
+template <int D, int HT, bool kKv4, bool kShort>
 __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 ? 3 : 4)
     window_decode_kernel(const DecodeArgs a) {
-  using C = Cache<D, HT, kKv4>;
-  constexpr int MT = D / 16, kHeads = 8 * HT;
+  using C = Cache<D, HT, kKv4, kShort>;
+  constexpr int MT = D / 16, kHeads = 8 * HT, U = C::U, kBlock = 16 * U;
   __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
   __shared__ float sm_o[kHeads][D + 4];
   pdl_launch_dependents();
@@ -367,21 +419,30 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 ? 3 : 4)
   const int group = a.w.nh / a.w.nkv, tiles = (group + kHeads - 1) / kHeads;
   const int b = blockIdx.z, h = blockIdx.y / tiles, g0 = (blockIdx.y % tiles) * kHeads;
   const int heads = min(kHeads, group - g0), h0 = h * group + g0;
-  const Blocks bl(a.w, b);
+  const Blocks<kBlock> bl(a.w, b);
   const int from = (int)((long long)bl.count * blockIdx.x / gridDim.x);
   const int to = (int)((long long)bl.count * (blockIdx.x + 1) / gridDim.x);
 
   C c(a, b, h, lane);
   int blk = from + warp;
+  // where a block's 16 rows are read from: the cache's last block reaches back into the one
+  // before it (whose keys are hidden there)
+  const int top = max(0, a.w.nk - kBlock);
+  auto start = [&](int i) { return min(bl.block(i) * kBlock, top); };
   if (blk < to) {
-    c.load_k(bl.block(blk) * kBlock, lane);
-    c.load_v(bl.block(blk) * kBlock, lane);
+    c.load_k(start(blk), lane);
+    c.load_v(start(blk), lane);
   }
   uint32_t q[HT][D / 8];
 #pragma unroll
   for (int ht = 0; ht < HT; ++ht)
     C::load_q(8 * ht + r < heads ? a.q.row(b, h0 + 8 * ht + r, 0) : nullptr, t, q[ht]);
-  c.prepare(q, lane);
+  float sl2[HT][2];
+  c.prepare(q, sl2, lane);
+#pragma unroll
+  for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) sl2[ht][e] *= a.scale * kLog2eD;
   float o[HT][MT][4];
   float m[HT][2], l[HT][2];  // heads 8 ht + 2 t, + 1; maxima in log2 units
 #pragma unroll
@@ -391,41 +452,53 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 ? 3 : 4)
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[ht][i][0] = o[ht][i][1] = o[ht][i][2] = o[ht][i][3] = 0.f;
   }
-  const float sl2 = a.scale * kLog2eD;
-
   for (; blk < to; blk += kWarps) {
-    const int j0 = bl.block(blk) * kBlock;
-    float s[HT][4];
-    c.scores(q, s);
-    const int next = blk + kWarps < to ? bl.block(blk + kWarps) * kBlock : -1;
+    const int first = bl.block(blk) * kBlock, j0 = min(first, top);
+    float s[U][HT][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) c.scores(u, q, s[u]);
+    const int next = blk + kWarps < to ? start(blk + kWarps) : -1;
     if (next >= 0) c.load_k(next, lane);
 #pragma unroll
-    for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[ht][e] *= sl2;
-    // not all 16 keys inside the window, or among the sinks?
-    if (j0 + kBlock > bl.len || (j0 < bl.lo && j0 + kBlock > a.w.sinks)) {
-      auto sees = [&](int j) { return j < bl.len && (j >= bl.lo || j < a.w.sinks); };
-      const bool mine[2] = {sees(j0 + r), sees(j0 + 8 + r)};
-      const bool value[4] = {sees(j0 + 2 * t), sees(j0 + 2 * t + 1), sees(j0 + 2 * t + 8), sees(j0 + 2 * t + 9)};
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (!mine[e / 2]) s[ht][e] = -INFINITY;
-      c.drop_v(value);
-      c.drop_scales(mine);
+        for (int e = 0; e < 4; ++e) s[u][ht][e] *= sl2[ht][e & 1];
+    // not all keys inside the window, or among the sinks?
+    if (j0 < first || j0 + kBlock > bl.len || (j0 < bl.lo && j0 + kBlock > a.w.sinks)) {
+      auto sees = [&](int j) { return j >= first && j < bl.len && (j >= bl.lo || j < a.w.sinks); };
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = j0 + 16 * u, v = k + 2 * t;
+        const bool mine[2] = {sees(k + r), sees(k + 8 + r)};
+        const bool value[4] = {sees(v), sees(v + 1), sees(v + 8), sees(v + 9)};
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!mine[e / 2]) s[u][ht][e] = -INFINITY;
+        c.drop_v(u, value);
+        c.drop_scales(u, mine);
+      }
     }
     bool grow = false;
+    float top2[HT][2];
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht)
-      grow |= fmaxf(s[ht][0], s[ht][2]) > m[ht][0] + 8.f || fmaxf(s[ht][1], s[ht][3]) > m[ht][1] + 8.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        top2[ht][e] = fmaxf(s[0][ht][e], s[0][ht][2 + e]);
+#pragma unroll
+        for (int u = 1; u < U; ++u) top2[ht][e] = fmax3(top2[ht][e], s[u][ht][e], s[u][ht][2 + e]);
+        grow |= top2[ht][e] > m[ht][e] + 8.f;
+      }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float n = fmaxf(s[ht][e], s[ht][2 + e]);
+          float n = top2[ht][e];
           n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 4));
           n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 8));
           n = fmaxf(m[ht][e], fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 16)));
@@ -441,15 +514,18 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 ? 3 : 4)
       }
     }
 #pragma unroll
-    for (int ht = 0; ht < HT; ++ht)
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float base = m[ht][e] == -INFINITY ? 0.f : m[ht][e];
-        s[ht][e] = fast_exp2(s[ht][e] - base);
-        s[ht][2 + e] = fast_exp2(s[ht][2 + e] - base);
-        l[ht][e] += s[ht][e] + s[ht][2 + e];
-      }
-    c.mix(s, o);
+      for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float base = m[ht][e] == -INFINITY ? 0.f : m[ht][e];
+          s[u][ht][e] = fast_exp2(s[u][ht][e] - base);
+          s[u][ht][2 + e] = fast_exp2(s[u][ht][2 + e] - base);
+          l[ht][e] += s[u][ht][e] + s[u][ht][2 + e];
+        }
+      c.mix(u, s[u], o);
+    }
     if (next >= 0) c.load_v(next, lane);
   }
   // the eight lanes of a head each summed their own keys
@@ -538,7 +614,9 @@ template <int D, bool kKv4>
 cudaError_t decode(const DecodeArgs& a, cudaStream_t st) {
   const int group = a.w.nh / a.w.nkv, tile = head_tile(a.w), tiles = (group + tile - 1) / tile;
   const int splits = decode_splits(a.w);
-  auto kern = tile == 8 ? window_decode_kernel<D, 1, kKv4> : window_decode_kernel<D, 2, kKv4>;
+  auto kern = a.w.nk < kLongBlock
+                  ? (tile == 8 ? window_decode_kernel<D, 1, kKv4, true> : window_decode_kernel<D, 2, kKv4, true>)
+                  : (tile == 8 ? window_decode_kernel<D, 1, kKv4, false> : window_decode_kernel<D, 2, kKv4, false>);
   cudaError_t e = launch_pdl(kern, dim3(splits, a.w.nkv * tiles, a.w.B), dim3(kThreads), 0, st, a);
   if (e != cudaSuccess || splits == 1) return e;
   return launch_pdl(window_join_kernel<D>, dim3(a.w.nh, a.w.B), dim3(D), 0, st, a, splits);
@@ -550,9 +628,9 @@ int decode_splits(const Window& w) {
   const int group = w.nh / w.nkv, tiles = (group + head_tile(w) - 1) / head_tile(w);
   // the most blocks a sequence can see
   const long long rows = std::min<long long>(w.nk, (long long)w.left + 1 + w.sinks);
-  const long long blocks = (rows + kBlock - 1) / kBlock + 1;
+  const long long blocks = (rows + 15) / 16 + 1;
   const long long ctas = (long long)w.B * w.nkv * tiles;
-  // eight CTAs per SM between them, but at least four blocks for each warp
+  // eight CTAs per SM between them, but at least four blocks of 16 for each warp
   const long long want = (8LL * 152 + ctas - 1) / ctas, most = std::max<long long>(1, blocks / (4 * kWarps));
   return (int)std::min<long long>(std::min(want, most), 256);
 }

@@ -65,9 +65,9 @@ struct NormRopeArgs {
   bool interleaved;
   float eps;
 };
-// Most CTAs of the backward whose partial sums of one weight's gradient the workspace
-// holds (eight per SM).
-constexpr int kNormRopeParts = 1216;
+// Most CTAs of the backward, each with a partial sum of one weight's gradient in the
+// workspace (four per SM).
+constexpr int kNormRopeParts = 608;
 template <typename T>
 cudaError_t launch_norm_rope_fwd(const NormRopeArgs<T>& a, int d, cudaStream_t st);
 template <typename T>

@@ -20,12 +20,28 @@ namespace psa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 2;  // heads whose rows a group loads at once, backward
 
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
   for (int m = LANES / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
   return v;
+}
+
+// Pairs of channels: one instruction for two.
+__device__ __forceinline__ float2 at2(const float* x) { return make_float2(x[0], x[1]); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ void set2(float* x, float2 v) {
+  x[0] = v.x;
+  x[1] = v.y;
+}
+template <int VEC>
+__device__ __forceinline__ float dot(const float (&x)[VEC], const float (&y)[VEC]) {
+  float2 s = __fmul2_rn(at2(x), at2(y));
+#pragma unroll
+  for (int e = 2; e < VEC; e += 2) s = __ffma2_rn(at2(x + e), at2(y + e), s);
+  return s.x + s.y;
 }
 
 // One lane's part of a token's rotation: y = c o x + s o x', where x' is the partner
@@ -83,49 +99,70 @@ struct Turn {
     }
   }
 
-  // every lane of the warp takes part (shuffles)
-  __device__ __forceinline__ void apply(bool interleaved, float (&x)[VEC]) const {
-    float y[VEC];
+  // c o x + s o x' of a packed row (every lane of the warp takes part: shuffles); x returns the
+  // row itself
+  template <typename T>
+  __device__ __forceinline__ void apply(bool interleaved, const uint4& raw, float (&x)[VEC],
+                                        float (&y)[VEC]) const {
+    unpack_vec(raw, x);
     if (interleaved) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) y[e] = x[e ^ 1];
     } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], partner);
+      uint4 other;
+      other.x = __shfl_sync(0xffffffffu, raw.x, partner);
+      other.y = __shfl_sync(0xffffffffu, raw.y, partner);
+      other.z = __shfl_sync(0xffffffffu, raw.z, partner);
+      other.w = __shfl_sync(0xffffffffu, raw.w, partner);
+      unpack_vec(other, y);
     }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] = c[e] * x[e] + s[e] * y[e];
+    for (int e = 0; e < VEC; e += 2)
+      set2(y + e, __ffma2_rn(at2(c + e), at2(x + e), __fmul2_rn(at2(s + e), at2(y + e))));
+  }
+  // the weights of x and of x' go into c and s
+  __device__ __forceinline__ void weigh(bool interleaved, const float (&w)[VEC]) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      c[e] *= w[e];
+      s[e] *= interleaved ? w[e ^ 1] : __shfl_sync(0xffffffffu, w[e], partner);
+    }
   }
 };
 
+// (the weights need only be 4-byte aligned)
 template <int VEC>
 __device__ __forceinline__ void load_weight(const float* w, int c0, float (&x)[VEC]) {
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) x[e] = w ? w[c0 + e] : 1.f;
+  for (int e = 0; e < VEC; ++e) x[e] = 1.f;
+  if (w) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[e] = w[c0 + e];
+  }
 }
 
 // A group takes HEADS heads of its token: blockIdx.y counts the chunks of q's heads (nqc of
 // them), then those of k's, so that no chunk holds heads of both.
 template <typename T, int D, int HEADS>
-__global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const NormRopeArgs<T> a, int nqc) {
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_fwd_kernel(const NormRopeArgs<T> a, int nqc) {
   constexpr int VEC = kVec<T>, LANES = D / VEC, GROUPS = kThreads / LANES;
   pdl_launch_dependents();
   pdl_wait();
   const int lr = threadIdx.x % LANES, c0 = lr * VEC;
-  const long long token = (long long)blockIdx.x * GROUPS + threadIdx.x / LANES;
-  const bool live = token < (long long)a.B * a.N;
-  const int b = live ? (int)(token / a.N) : 0, n = live ? (int)(token % a.N) : 0;
+  const unsigned token = blockIdx.x * GROUPS + threadIdx.x / LANES;
+  const bool live = token < (unsigned)(a.B * a.N);
+  const int b = live ? token / (unsigned)a.N : 0, n = live ? token - b * a.N : 0;
   const bool is_q = (int)blockIdx.y < nqc;
   const int h0 = (is_q ? blockIdx.y : blockIdx.y - nqc) * HEADS;
-  const int heads = is_q ? a.nh : a.nkv;
-  const View<const T> in = is_q ? a.q : a.k;
-  const View<T> out = is_q ? a.oq : a.ok;
+  const int heads = (live ? is_q ? a.nh : a.nkv : 0) - h0;  // this group's
+  const long long in_sh = is_q ? a.q.sh : a.k.sh, out_sh = is_q ? a.oq.sh : a.ok.sh;
+  const T* in = (is_q ? a.q.row(b, h0, n) : a.k.row(b, h0, n)) + c0;
+  T* out = (is_q ? a.oq.row(b, h0, n) : a.ok.row(b, h0, n)) + c0;
 
   uint4 raw[HEADS];
 #pragma unroll
   for (int i = 0; i < HEADS; ++i)
-    raw[i] = live && h0 + i < heads ? *reinterpret_cast<const uint4*>(in.row(b, h0 + i, n) + c0)
-                                    : make_uint4(0, 0, 0, 0);
+    raw[i] = i < heads ? *reinterpret_cast<const uint4*>(in + i * in_sh) : make_uint4(0, 0, 0, 0);
   int pos = n;
   if (a.positions && live) pos = a.positions[token];
   const bool valid = live && pos >= 0 && pos < a.max_pos;
@@ -133,37 +170,33 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const NormRopeA
   turn.load(a, valid ? pos : 0, lr, LANES, 1.f);
   float w[VEC];
   load_weight(is_q ? a.wq : a.wk, c0, w);
+  turn.weigh(a.interleaved, w);
 #pragma unroll
   for (int i = 0; i < HEADS; ++i) {
-    float x[VEC];
-    unpack_vec(raw[i], x);
-    float ss = 0.f;
+    // y = r (R (w o x)): the root's factor comes last
+    float x[VEC], y[VEC];
+    turn.template apply<T>(a.interleaved, raw[i], x, y);
+    const float r = rsqrtf(group_sum<LANES>(dot(x, x)) * (1.f / D) + a.eps);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) ss += x[e] * x[e];
-    const float r = rsqrtf(group_sum<LANES>(ss) * (1.f / D) + a.eps);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] = x[e] * r * w[e];
-    turn.apply(a.interleaved, x);
-    if (valid && h0 + i < heads)
-      *reinterpret_cast<uint4*>(out.row(b, h0 + i, n) + c0) = pack_vec(x);
+    for (int e = 0; e < VEC; e += 2) set2(y + e, __fmul2_rn(at2(y + e), both(r)));
+    if (valid && i < heads) *reinterpret_cast<uint4*>(out + i * out_sh) = pack_vec(y);
   }
 }
 
 // A CTA goes through tokens blockIdx.x * GROUPS + group, + gridDim.x * GROUPS, ... and a
 // chunk of heads of q or of k; its sum of g' o xhat is one row of partial sums.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     norm_rope_bwd_kernel(const NormRopeArgs<T> a, int nqc, int heads_per) {
   constexpr int VEC = kVec<T>, LANES = D / VEC, GROUPS = kThreads / LANES;
   __shared__ float part[GROUPS][D];
   pdl_launch_dependents();
   pdl_wait();
   const int lr = threadIdx.x % LANES, grp = threadIdx.x / LANES, c0 = lr * VEC;
-  const long long tokens = (long long)a.B * a.N;
+  const unsigned tokens = a.B * a.N;
   const bool is_q = (int)blockIdx.y < nqc;
   const int chunk = is_q ? blockIdx.y : blockIdx.y - nqc;
-  const int heads = is_q ? a.nh : a.nkv;
-  const int h0 = chunk * heads_per, h1 = min(heads, h0 + heads_per);
+  const int h0 = chunk * heads_per, heads = min((is_q ? a.nh : a.nkv) - h0, heads_per);
   const View<const T> in = is_q ? a.q : a.k, gin = is_q ? a.gq : a.gk;
   const View<T> out = is_q ? a.oq : a.ok;
   float w[VEC], dw[VEC];
@@ -171,42 +204,58 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int e = 0; e < VEC; ++e) dw[e] = 0.f;
 
-  for (long long t0 = (long long)blockIdx.x * GROUPS; t0 < tokens; t0 += (long long)gridDim.x * GROUPS) {
-    const long long token = t0 + grp;
+  for (unsigned t0 = blockIdx.x * GROUPS; t0 < tokens; t0 += gridDim.x * GROUPS) {
+    const unsigned token = t0 + grp;
     const bool live = token < tokens;
-    const int b = live ? (int)(token / a.N) : 0, n = live ? (int)(token % a.N) : 0;
+    const int b = live ? token / (unsigned)a.N : 0, n = live ? token - b * a.N : 0;
     int pos = n;
     if (a.positions && live) pos = a.positions[token];
     const bool valid = live && pos >= 0 && pos < a.max_pos;
+    const T *x0 = in.row(b, h0, n) + c0, *g0 = gin.row(b, h0, n) + c0;
+    T* d0 = out.row(b, h0, n) + c0;
     Turn<VEC> turn;
     turn.load(a, valid ? pos : 0, lr, LANES, -1.f);
-    for (int h = h0; h < h1; ++h) {
-      uint4 rx = make_uint4(0, 0, 0, 0), rg = rx;
-      if (valid) {
-        rx = *reinterpret_cast<const uint4*>(in.row(b, h, n) + c0);
-        rg = *reinterpret_cast<const uint4*>(gin.row(b, h, n) + c0);
-      }
-      float x[VEC], g[VEC];
-      unpack_vec(rx, x);
-      unpack_vec(rg, g);
-      turn.apply(a.interleaved, g);
-      float ss = 0.f, gx = 0.f;
+    // the next kBatch heads' rows are on their way while these are worked on
+    uint4 nx[kBatch], ng[kBatch];
+    auto load = [&](int h) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        ss += x[e] * x[e];
-        gx += g[e] * w[e] * x[e];
+      for (int i = 0; i < kBatch; ++i) {
+        nx[i] = ng[i] = make_uint4(0, 0, 0, 0);
+        if (valid && h + i < heads) {
+          nx[i] = *reinterpret_cast<const uint4*>(x0 + (h + i) * in.sh);
+          ng[i] = *reinterpret_cast<const uint4*>(g0 + (h + i) * gin.sh);
+        }
       }
-      ss = group_sum<LANES>(ss);
-      gx = group_sum<LANES>(gx);
-      const float r = rsqrtf(ss * (1.f / D) + a.eps);
-      const float back = gx * r * r * (1.f / D);
+    };
+    load(0);
+    for (int h = 0; h < heads; h += kBatch) {
+      uint4 rx[kBatch], rg[kBatch];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        // rows of padding hold zeros here: their share is 0 and their dx is 0
-        dw[e] += g[e] * (x[e] * r);
-        x[e] = r * (g[e] * w[e] - x[e] * back);
+      for (int i = 0; i < kBatch; ++i) {
+        rx[i] = nx[i];
+        rg[i] = ng[i];
       }
-      if (live) *reinterpret_cast<uint4*>(out.row(b, h, n) + c0) = pack_vec(x);
+      load(h + kBatch);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        float x[VEC], g[VEC], raw[VEC];
+        unpack_vec(rx[i], x);
+        turn.template apply<T>(a.interleaved, rg[i], raw, g);
+        float gw[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) set2(gw + e, __fmul2_rn(at2(g + e), at2(w + e)));
+        const float ss = group_sum<LANES>(dot(x, x)), gx = group_sum<LANES>(dot(gw, x));
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        const float2 r2 = both(r), back = both(-gx * r * r * (1.f / D));
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+          // rows of padding hold zeros here: their share is 0 and their dx is 0
+          const float2 xe = at2(x + e);
+          set2(dw + e, __ffma2_rn(at2(g + e), __fmul2_rn(xe, r2), at2(dw + e)));
+          set2(x + e, __fmul2_rn(r2, __ffma2_rn(xe, back, at2(gw + e))));
+        }
+        if (live && h + i < heads) *reinterpret_cast<uint4*>(d0 + (h + i) * out.sh) = pack_vec(x);
+      }
     }
   }
 #pragma unroll
@@ -234,7 +283,7 @@ __global__ void __launch_bounds__(1024)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
   const float* src = ws + (blockIdx.y == 0 ? 0 : kNormRopeParts * D) + c;
   float s = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int r = warp; r < rows; r += 32) s += src[r * D];
   part[warp][lane] = s;
   __syncthreads();
@@ -260,18 +309,20 @@ template <typename T, int D>
 cudaError_t fwd(const NormRopeArgs<T>& a, cudaStream_t st) {
   // four heads per group once that still fills the device's threads
   const long long rows = (long long)a.B * a.N * (a.nh + a.nkv);
-  return rows * (D / kVec<T>) / 4 >= 152 * 2048LL ? fwd<T, D, 4>(a, st) : fwd<T, D, 1>(a, st);
+  return rows * (D / kVec<T>) / 8 >= 152 * 2048LL ? fwd<T, D, 8>(a, st) : rows * (D / kVec<T>) / 4 >= 152 * 2048LL ? fwd<T, D, 4>(a, st) : fwd<T, D, 1>(a, st);
 }
 
 template <typename T, int D>
 cudaError_t bwd(const NormRopeArgs<T>& a, cudaStream_t st) {
   constexpr int GROUPS = kThreads / (D / kVec<T>);
-  // at most kNormRopeParts partial rows for each weight: chunks of at least 4 heads, and
-  // as many token blocks as fit
-  const int most = std::max(a.nh, a.nkv);
-  const int heads_per = std::max(4, cdiv(most, 256));
+  // up to four CTAs per SM between the chunks of heads, each with one partial row: chunks of
+  // 8 heads (the angles are loaded once for them) where there are tokens enough, else of 4
+  const int blocks = cdiv((long long)a.B * a.N, GROUPS);
+  const int chunks8 = cdiv(a.nh, 8) + cdiv(a.nkv, 8);
+  int heads_per = (long long)blocks * chunks8 >= kNormRopeParts ? 8 : 4;
+  heads_per = std::max(heads_per, cdiv(std::max(a.nh, a.nkv), kNormRopeParts / 2));
   const int nqc = cdiv(a.nh, heads_per), nkc = cdiv(a.nkv, heads_per);
-  const int gx = std::max(1, std::min(cdiv((long long)a.B * a.N, GROUPS), kNormRopeParts / std::max(nqc, nkc)));
+  const int gx = std::max(1, std::min(blocks, kNormRopeParts / (nqc + nkc)));
   cudaError_t e = launch_pdl(norm_rope_bwd_kernel<T, D>, dim3(gx, nqc + nkc), dim3(kThreads), 0, st,
                              a, nqc, heads_per);
   if (e != cudaSuccess || (!a.dwq && !a.dwk)) return e;

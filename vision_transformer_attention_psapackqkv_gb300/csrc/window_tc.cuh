@@ -48,6 +48,21 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int r0, int r1, i
   fence_proxy_async_smem();
 }
 
+// The keys of a 32-column chunk that a row sees, one bit each: columns lo .. hi and those below
+// sk, all relative to the chunk's first.
+__device__ __forceinline__ uint32_t visible32(int lo, int hi, int sk) {
+  const uint32_t upto = hi >= 31 ? 0xffffffffu : hi < 0 ? 0u : (2u << hi) - 1u;
+  const uint32_t from = lo <= 0 ? 0xffffffffu : lo > 31 ? 0u : 0xffffffffu << lo;
+  const uint32_t sinks = sk <= 0 ? 0u : sk > 31 ? 0xffffffffu : (1u << sk) - 1u;
+  return upto & (from | sinks);
+}
+// Scores whose bit is not set become -infinity.
+__device__ __forceinline__ void hide(uint32_t* x, uint32_t mask) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (!(mask & (1u << c))) x[c] = 0xff800000u;
+}
+
 // 64 columns of this thread's lane, one wait.
 __device__ __forceinline__ void load_cols64(uint32_t t, uint32_t (&r)[64]) {
   using Chunk = uint32_t[32];

@@ -16,8 +16,9 @@
 // zeroes the rows of padding where they are an operand (0 times NaN is NaN).  bf16 operands
 // made by the row threads stay in tensor memory: each thread writes them over the columns
 // that it read.  All products come from one warp and complete in the order they are issued:
-//   dQ kernel     dQ += dS K (dS in dP's columns), then the next tile's dP behind it, then S of
-//                 the tile after (two buffers), so the row threads always find S
+//   dQ kernel     the next tile's S as soon as this one's is in registers, its dP (two buffers),
+//                 then this tile's dQ += dS K (dS in dP's columns), so the row threads find
+//                 both operands when they come to the next tile
 //   dK/dV kernel  S^T = K Q^T and dP^T = V dO^T have keys as rows: dV += P^T dO and the next
 //                 S^T behind it, while the row threads make dS^T; dK += dS^T Q and the next
 //                 dP^T, while they make P^T.
@@ -116,16 +117,16 @@ struct DqCfg {
   static constexpr uint32_t OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KST * TILE;
   static constexpr uint32_t OFF_BAR = OFF_V + VST * TILE, SMEM = OFF_BAR + 512 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static constexpr uint32_t TM_S = 0, TM_DP = 256, TM_DQ = 384;  // S: two buffers
+  static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DQ = 384;  // dP: two buffers
 };
 struct DqBars {
   uint64_t q_full, q_empty, do_full, do_empty, k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t k_fixed[4], s_full[2], s_free[2], dp_full, ds_full, dq_full, done;
+  uint64_t k_fixed[4], s_full, s_free, dp_full[2], ds_full, dq_full, done;
 };
 
 // A unit of the dQ kernel: 128 query rows of a head.
 struct DqUnit {
-  int b, h, hk, row0, len, edge;
+  int b, h, hk, row0, len, edge, end;  // end: keys from here on are seen by no row
   KeyTiles<kTile> tiles;
   int p0, p1;
   __device__ __forceinline__ DqUnit(const BwdParams& a, int u) {
@@ -140,6 +141,7 @@ struct DqUnit {
     p0 = max(0, row0 + off);
     p1 = min(len, min(row0 + kTile, w.nq) + off) - 1;
     tiles = KeyTiles<kTile>(w, len, p0, p1);
+    end = min(len, p1 + w.right + 1);
     // the key tile with rows of padding, always the last one if it is visited
     edge = len % kTile != 0 && len < w.nk ? len / kTile : -1;
   }
@@ -172,11 +174,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.v_full[i], 1);
       mbar_init(&bar.v_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.s_free[i], 256);
-    }
-    mbar_init(&bar.dp_full, 1);
+    mbar_init(&bar.s_full, 1);
+    mbar_init(&bar.s_free, 256);
+    mbar_init(&bar.dp_full[0], 1);
+    mbar_init(&bar.dp_full[1], 1);
     mbar_init(&bar.ds_full, 256);
     mbar_init(&bar.dq_full, 1);
     mbar_init(&bar.done, 1);
@@ -251,25 +252,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dQ = desc_rows_by_channels(sbase), dDO = desc_rows_by_channels(sbase + C::OFF_DO);
     const uint64_t dK = desc_rows_by_channels(sbase + C::OFF_K), dV = desc_rows_by_channels(sbase + C::OFF_V);
     const uint64_t dKb = desc_channels_by_rows(sbase + C::OFF_K);
-    const uint32_t idS = idesc_bf16_f32(128, 128, false, false), idQ = idesc_bf16_f32(128, D, false, true);
+    const uint32_t idQ = idesc_bf16_f32(128, D, false, true);
     bool ok = true;
     int kc = 0, uc = 0;
     for (int i = 0; ok && unit_of(i) < a.units; ++i) {
       const DqUnit u(a, unit_of(i));
       const int n = u.tiles.count;
       if (n == 0) continue;
+      // tiles of which few columns are seen (sinks, the last one) work on those only
+      auto cols_of = [&](int t) { return used_columns(u.tiles.tile(t), u.tiles.first, u.end, a.w.sinks); };
+      auto scores = [&](uint32_t tX, uint64_t dA, uint64_t dB, int cols) {
+        auto go = [&](uint32_t id) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16_warp(tX, dA + kstep_channels(kk), dB + kstep_channels(kk), id, kk > 0 ? 1u : 0u);
+        };
+        if (cols == kTile) go(idesc_bf16_f32(128, kTile, false, false));
+        else go(idesc_bf16_f32(128, cols, false, false));
+      };
+      // S and dP of tile t
       auto issue_s = [&](int t) -> bool {
-        const int c = kc + t, st = c % C::KST, sb = c & 1;
+        const int c = kc + t, st = c % C::KST;
         if (!mbar_wait(&bar.k_full[st], (c / C::KST) & 1, abort) ||
-            (c >= 2 && !mbar_wait(&bar.s_free[sb], (c / 2 - 1) & 1, abort)))
+            (c >= 1 && !mbar_wait(&bar.s_free, (c - 1) & 1, abort)))
           return false;
         tc_fence_after();
-        const uint64_t d = dK + (uint64_t)(st * C::TILE >> 4);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16_warp(tmem + C::TM_S + 128 * sb, dQ + kstep_channels(kk), d + kstep_channels(kk), idS,
-                        kk > 0 ? 1u : 0u);
-        mma_commit_warp(&bar.s_full[sb]);
+        scores(tmem + C::TM_S, dQ, dK + (uint64_t)(st * C::TILE >> 4), cols_of(t));
+        mma_commit_warp(&bar.s_full);
         if (t == n - 1) mma_commit_warp(&bar.q_empty);
         return true;
       };
@@ -277,33 +286,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = kc + t, st = c % C::VST;
         if (!mbar_wait(&bar.v_full[st], (c / C::VST) & 1, abort)) return false;
         tc_fence_after();
-        const uint64_t d = dV + (uint64_t)(st * C::TILE >> 4);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16_warp(tmem + C::TM_DP, dDO + kstep_channels(kk), d + kstep_channels(kk), idS, kk > 0 ? 1u : 0u);
-        mma_commit_warp(&bar.dp_full);
+        scores(tmem + C::TM_DP + 128 * (c & 1), dDO, dV + (uint64_t)(st * C::TILE >> 4), cols_of(t));
+        mma_commit_warp(&bar.dp_full[c & 1]);
         mma_commit_warp(&bar.v_empty[st]);
         if (t == n - 1) mma_commit_warp(&bar.do_empty);
         return true;
       };
       ok = mbar_wait(&bar.q_full, uc & 1, abort) && issue_s(0) && mbar_wait(&bar.do_full, uc & 1, abort) &&
-           issue_dp(0) && (n == 1 || issue_s(1));
+           issue_dp(0);
       for (int t = 0; ok && t < n; ++t) {
         const int c = kc + t, st = c % C::KST;
-        if (!mbar_wait(&bar.ds_full, c & 1, abort) || !mbar_wait(&bar.k_fixed[st], (c / C::KST) & 1, abort)) {
+        if (t + 1 < n && !(issue_s(t + 1) && issue_dp(t + 1))) ok = false;
+        if (!ok || !mbar_wait(&bar.ds_full, c & 1, abort) ||
+            !mbar_wait(&bar.k_fixed[st], (c / C::KST) & 1, abort)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint64_t d = dKb + (uint64_t)(st * C::TILE >> 4);
+        const uint32_t tDS = tmem + C::TM_DP + 128 * (c & 1);
+        const int cols = cols_of(t);
         // 16 keys' dS are 8 columns; those of keys 64 .. 127 start at column 64
+        if (cols == kTile) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_bf16_ts_warp(tmem + C::TM_DQ, tmem + C::TM_DP + 64 * (kk / 4) + 8 * (kk % 4), d + kk * kKstepRows, idQ,
-                           t > 0 || kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts_warp(tmem + C::TM_DQ, tDS + 64 * (kk / 4) + 8 * (kk % 4), d + kk * kKstepRows, idQ,
+                             t > 0 || kk > 0 ? 1u : 0u);
+        } else {
+#pragma unroll 1
+          for (int kk = 0; 16 * kk < cols; ++kk)
+            mma_bf16_ts_warp(tmem + C::TM_DQ, tDS + 64 * (kk / 4) + 8 * (kk % 4), d + kk * kKstepRows, idQ,
+                             t > 0 || kk > 0 ? 1u : 0u);
+        }
         mma_commit_warp(&bar.k_empty[st]);
         if (t == n - 1) mma_commit_warp(&bar.dq_full);
-        else ok = issue_dp(t + 1) && (t + 2 >= n || issue_s(t + 2));
       }
       kc += n;
       ++uc;
@@ -348,22 +364,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 nlse = make_float2(stat[0], stat[0]), ndelta = make_float2(stat[kTile], stat[kTile]);
       const float2 sl = make_float2(a.sl2, a.sl2);
       for (int t = 0; t < u.tiles.count; ++t, ++kc) {
-        const int tile0 = u.tiles.tile(t) * kTile, j0 = tile0 + 64 * half, sb = kc & 1;
-        if (!mbar_wait(&bar.s_full[sb], (kc / 2) & 1, abort)) {
+        const int tile0 = u.tiles.tile(t) * kTile, j0 = tile0 + 64 * half;
+        const uint32_t tDP = tP + 128 * (kc & 1);
+        if (!mbar_wait(&bar.s_full, kc & 1, abort)) {
           ok = false;
           break;
         }
         tc_fence_after();
         uint32_t x[64];
-        load_cols64(tS + 128 * sb, x);
+        load_cols64(tS, x);
         tc_fence_before();
-        mbar_arrive(&bar.s_free[sb]);
+        mbar_arrive(&bar.s_free);
         const bool whole = tile0 + kTile <= whole_hi && (tile0 >= whole_lo || tile0 + kTile <= a.w.sinks);
         if (!whole) {
+          // -inf: P = 0 (columns that were not worked on among them)
           const int hi = jhi - j0, lo = jlo - j0, sk = a.w.sinks - j0;
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c > hi || (c < lo && c >= sk)) x[c] = 0xff800000u;  // -inf: P = 0
+          hide(x, visible32(lo, hi, sk));
+          hide(x + 32, visible32(lo - 32, hi - 32, sk - 32));
         }
 #pragma unroll
         for (int c = 0; c < 64; c += 2) {
@@ -371,21 +388,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           x[c] = __float_as_uint(fast_exp2(e.x));
           x[c + 1] = __float_as_uint(fast_exp2(e.y));
         }
-        if (!mbar_wait(&bar.dp_full, kc & 1, abort)) {
+        if (!mbar_wait(&bar.dp_full[kc & 1], (kc / 2) & 1, abort)) {
           ok = false;
           break;
         }
         tc_fence_after();
         uint32_t y[64];
-        load_cols64(tP, y);
+        load_cols64(tDP, y);
         if (!whole) drop_masked(x, y);
 #pragma unroll
         for (int c = 0; c < 64; c += 2) {
           const float2 d = __fmul2_rn(pair(x + c), __fadd2_rn(pair(y + c), ndelta));
           y[c / 2] = pack2(d.x, d.y);
         }
-        tmem_store16_async(tP, y);
-        tmem_store16_async(tP + 16, y + 16);
+        tmem_store16_async(tDP, y);
+        tmem_store16_async(tDP + 16, y + 16);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bar.ds_full);
@@ -710,10 +727,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_cols64(tS, x);
         const bool whole = q0 >= whole_lo && q0 + kTile - 1 <= whole_hi;
         if (!whole) {
-          const int lo = qlo - q0 - 64 * half, hi = qhi - q0 - 64 * half;
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c < lo || c > hi) x[c] = 0xff800000u;  // -inf: P = 0
+          const int lo = qlo - q0 - 64 * half, hi = qhi - q0 - 64 * half;  // -inf: P = 0
+          hide(x, visible32(lo, hi, 0));
+          hide(x + 32, visible32(lo - 32, hi - 32, 0));
         }
         uint32_t pk[32];
 #pragma unroll

@@ -12,10 +12,13 @@
 // lists), two neighbouring row tiles of one head otherwise.
 //   warps 0-3, 4-7   softmax of slot 0, 1: one thread per row (TMEM lane), 128 columns
 //   warp 8           TMA producer: Q of both slots, a ring of K tiles and one of V tiles
-//   warps 9, 10      issuer of slot 0, 1 (one thread): per key tile O += P V, then the next
-//                    tile's S = Q K^T right behind it: P lies in S's own columns of tensor
-//                    memory, and products of one thread complete in order, so neither
-//                    waits for the other in software, and s_full says that both are done
+//   warp 9           issuer of both slots in turn: per key tile O += P V, then the next tile's
+//                    S = Q K^T right behind it: P lies in S's own columns of tensor memory,
+//                    and products complete in order, so neither waits for the other in
+//                    software, and s_full says that both are done.  The warp runs converged
+//                    (descriptors in uniform registers); two issuing threads, one per slot,
+//                    interleave on the pipe and make both chains longer (1050 against 732 us
+//                    at 16384 causal)
 //   warp 10          TMA stores of finished rows, which the softmax threads leave in a
 //                    staging tile (stores of their own would hit 32 rows at a time, half a
 //                    sector each, and hold up their next arrival until acknowledged)
@@ -102,13 +105,6 @@ struct Unit {
     }
   }
 };
-
-// Columns of a key tile that some row sees, in steps of the product's 16: all up to the last
-// visible key, or in front of the window the sinks alone.
-__device__ __forceinline__ int used_columns(int tile, int first, int end, int sinks) {
-  const int to = (tile < first ? min(sinks, end) : end) - tile * kTile;
-  return min(kTile, (to + 15) & ~15);
-}
 
 // The tiles a unit visits (those of both slots), and which of them a slot takes part in.
 struct Walk {

@@ -48,6 +48,13 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int r0, int r1, i
   fence_proxy_async_smem();
 }
 
+// Columns of a key tile that some row sees, in steps of the product's 16: all up to the last
+// visible key, or in front of the window the sinks alone.
+__device__ __forceinline__ int used_columns(int tile, int first, int end, int sinks) {
+  const int to = (tile < first ? min(sinks, end) : end) - tile * kTile;
+  return min(kTile, (to + 15) & ~15);
+}
+
 // The keys of a 32-column chunk that a row sees, one bit each: columns lo .. hi and those below
 // sk, all relative to the chunk's first.
 __device__ __forceinline__ uint32_t visible32(int lo, int hi, int sk) {

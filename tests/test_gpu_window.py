@@ -162,6 +162,21 @@ def test_reruns_are_bitwise_identical():
         assert all(torch.equal(x, y) for x, y in zip(runs[0], again))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_runs_of_a_long_sequence_agree(d):
+    """Long runs of tiles per thread block, again and again: threads of a block that drift apart by a
+    tile must not meet one another's barriers (a wait that gives up shows as a device error)."""
+    n, scale = 16384, d ** -0.5
+    q, k, v, do = _inputs(1, 16, 2, n, n, d, BF16, 20)
+    first = None
+    for _ in range(40):
+        o, lse = _fwd(q, k, v, None, -1, 0, 0, scale)
+        got = (o, lse) + _bwd(q, k, v, o, do, lse, None, -1, 0, 0, scale)
+        first = first or got
+        assert all(torch.equal(x, y) for x, y in zip(first, got))
+    assert B.psa_get_last_device_error() == B.PSA_OK
+
+
 def test_graph_replays_on_new_inputs_and_another_stream():
     q, k, v, do = _inputs(2, 4, 2, 333, 333, 64, BF16, 15)
     lens = torch.tensor([333, 200], dtype=torch.int32, device="cuda")

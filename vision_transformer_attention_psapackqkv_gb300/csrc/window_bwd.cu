@@ -121,7 +121,7 @@ struct DqCfg {
 };
 struct DqBars {
   uint64_t q_full, q_empty, do_full, do_empty, k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t k_fixed[4], s_full, s_free, dp_full[2], ds_full, dq_full, done;
+  uint64_t k_fixed[4], s_full, s_free, dp_full[2], ds_full[2], dq_full, done;
 };
 
 // A unit of the dQ kernel: 128 query rows of a head.
@@ -176,9 +176,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&bar.s_full, 1);
     mbar_init(&bar.s_free, 256);
-    mbar_init(&bar.dp_full[0], 1);
-    mbar_init(&bar.dp_full[1], 1);
-    mbar_init(&bar.ds_full, 256);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.dp_full[i], 1);
+      mbar_init(&bar.ds_full[i], 256);  // by dP buffer: a thread may be a tile ahead of another
+    }
     mbar_init(&bar.dq_full, 1);
     mbar_init(&bar.done, 1);
     *abort = 0;
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; ok && t < n; ++t) {
         const int c = kc + t, st = c % C::KST;
         if (t + 1 < n && !(issue_s(t + 1) && issue_dp(t + 1))) ok = false;
-        if (!ok || !mbar_wait(&bar.ds_full, c & 1, abort) ||
+        if (!ok || !mbar_wait(&bar.ds_full[c & 1], (c / 2) & 1, abort) ||
             !mbar_wait(&bar.k_fixed[st], (c / C::KST) & 1, abort)) {
           ok = false;
           break;
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_store16_async(tDP + 16, y + 16);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bar.ds_full);
+        mbar_arrive(&bar.ds_full[kc & 1]);
       }
       if (!ok) break;
       // ---- dQ of this row: half of its channels per thread

@@ -154,6 +154,23 @@ def test_append_and_read(N, rows, starts, counts, d, dtype):
     assert torch.equal(front, ko[:, :, :rows - 1]) and (few[:, 0] == 7.0).all() and (few[:, rows:] == 7.0).all()
 
 
+def test_quotients_near_ties():
+    """Codes of many values, exact ties and their neighbours among them, and of scales from the
+    smallest to the largest, against the division of the format's definition."""
+    x = _randn(16, 1, 2, 8192, 128) * torch.exp2(torch.randint(-140, 120, (1, 2, 8192, 1), generator=_gen(17), device="cuda").float())
+    top = x[..., :32].abs().amax(-1, keepdim=True)
+    scale = (top / torch.full_like(top, 7)).to(BF16).float()
+    half = (torch.randint(-7, 7, (1, 2, 8192, 16), generator=_gen(18), device="cuda") + 0.5) * scale  # exact
+    x[..., 1:17] = torch.where(x[..., 1:17].abs() <= x[..., :32].abs().amax(-1, keepdim=True), half, x[..., 1:17])
+    bits = x[..., 9:17].contiguous().view(torch.int32)
+    x[..., 9:17] = (bits + torch.randint(-1, 2, bits.shape, generator=_gen(19), device="cuda", dtype=torch.int32)).view(torch.float32)
+    x = torch.where(torch.isfinite(x), x, 1.0)
+    cache = tuple(torch.zeros(1, 2, 8192, n, dtype=t, device="cuda") for n, t in ((64, torch.uint8), (4, BF16)) * 2)
+    B.psa_kv4_append(x, -x, torch.zeros(1, dtype=torch.int32, device="cuda"), None, *cache)
+    for got, want in zip(cache, quantise(x) + quantise(-x)):
+        assert torch.equal(got, want)
+
+
 def test_values_that_are_not_finite_do_not_read_back_as_finite():
     k = _randn(15, 1, 1, 4, 64)
     k[0, 0, 1, 3], k[0, 0, 2, 40] = math.nan, math.inf

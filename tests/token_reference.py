@@ -139,7 +139,8 @@ def quantise(x):
     scales = torch.zeros(*x.shape[:-1], groups, dtype=torch.bfloat16, device=x.device)
     for g in range(groups):
         part = x[..., 32 * g:32 * g + 32]
-        sc = (part.abs().amax(-1) / 7).to(torch.bfloat16)
+        top = part.abs().amax(-1)
+        sc = (top / torch.full_like(top, 7)).to(torch.bfloat16)  # (by a scalar it may be a product)
         scales[..., g] = sc
         step = sc.float()
         for e in range(32):

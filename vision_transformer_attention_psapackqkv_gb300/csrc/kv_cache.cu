@@ -62,43 +62,60 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// Quantises lane t's channels of one row.  Every lane of the warp calls it.  A group that
-// holds a NaN or an infinity gets an infinite scale, so it does not read back as finite.
+// Quantises lane t's channels of one row (any row where it is not live).  Every lane of the
+// warp calls it.  A group that
+// holds a NaN or an infinity gets a scale that is not finite, and does not read back as finite.
 template <typename T, int D>
 __device__ __forceinline__ void quantise_row(const T* src, uint8_t* codes, __nv_bfloat16* scales,
                                              int t, bool live) {
   constexpr int G = D / 32;
   uint32_t lo[G], hi[G];  // four nibbles of a = 2 t and of a = 2 t + 1, for each group
   uint32_t sc[G];
+  float all[G][8];
+#pragma unroll
+  for (int g = 0; g < G; ++g) load8(src + 32 * g + 8 * t, all[g]);
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    float x[8];
+    const float(&x)[8] = all[g];
+    // magnitudes compare as integers do, a NaN above all
+    uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    if (live) load8(src + 32 * g + 8 * t, x);
-    float m = 0.f;
-    bool nan = false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      m = fmaxf(m, fabsf(x[e]));
-      nan |= isnan(x[e]);
-    }
-    if (nan) m = INFINITY;
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const __nv_bfloat16 s = __float2bfloat16_rn(__fdiv_rn(m, 7.f));
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const __nv_bfloat16 s = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.f));
     const float step = __bfloat162float(s);
     sc[g] = *reinterpret_cast<const uint16_t*>(&s);
+    // The format's quotient is rounded to fp32, then to a whole number.  With the correctly
+    // rounded reciprocal, one correction by the exact remainder makes a quotient within a unit of
+    // the last place the correctly rounded one (Markstein, "Computation of elementary functions
+    // on the IBM RISC System/6000 processor", 1990); x times the reciprocal may be a unit and a
+    // half off, so there is a correction before it.  Below 2^-100, where the reciprocal may overflow and a bf16 scale may
+    // be far from max / 7, it is the division itself, clamped; elsewhere |q| < 7.5.
+    // Adding 1.5 2^23 + 8 rounds (ties to even) and leaves the code in the lowest four bits; the
+    // constant's low 16 bits are those of the 8 alone, so four such sums shifted by multiplication
+    // add up to four codes in the low half.
+    const float inv = __fdiv_rn(1.f, step);
+    constexpr float kRound = 12582920.f;
+    float q[8];
+    if (step >= 7.9e-31f) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = x[e] * inv, z = fmaf(fmaf(-y, step, x[e]), inv, y);
+        q[e] = fmaf(fmaf(-z, step, x[e]), inv, z);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = step > 0.f ? fminf(fmaxf(__fdiv_rn(x[e], step), -7.f), 7.f) : 0.f;
+    }
     lo[g] = hi[g] = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      // the quotient is rounded to fp32 before it is rounded to a whole number: the
-      // format's definition, reproducible with any IEEE division
-      const float q = step > 0.f ? rintf(__fdiv_rn(x[e], step)) : 0.f;
-      const uint32_t code = (uint32_t)(int)(fminf(fmaxf(q, -7.f), 7.f) + 8.f);
-      if (e < 4) lo[g] |= code << (4 * e);
-      else hi[g] |= code << (4 * (e - 4));
+    for (int e = 3; e >= 0; --e) {
+      lo[g] = lo[g] * 16u + __float_as_uint(q[e] + kRound);
+      hi[g] = hi[g] * 16u + __float_as_uint(q[4 + e] + kRound);
     }
+    lo[g] &= 0xffffu;
+    hi[g] &= 0xffffu;
   }
   if (!live) return;
   if constexpr (G == 4) {

@@ -21,18 +21,19 @@ namespace psa {
 namespace {
 
 constexpr int kB = 64;  // rows of a tile, on either side
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // 16 threads a row, 4 rows a thread, kGap rows between them
+constexpr int kR = 4, kGap = kB / kR;
 constexpr int kLdP = kB + 4;  // row pitch of a tile of scores
 
 template <int D>
 constexpr int kLd = D + 4;
 
 // Rows i0 .. i0 + 63 of one head into shared memory in fp32; rows outside [lo, hi) as 0.
-template <int D, typename T>
+template <int D, typename T, int kN = kThreads>
 __device__ __forceinline__ void load_rows(float* dst, const T* base, long long sn, int i0, int lo,
                                           int hi) {
   constexpr int VEC = kVec<T>, PER = D / VEC;
-  for (int u = threadIdx.x; u < kB * PER; u += kThreads) {
+  for (int u = threadIdx.x; u < kB * PER; u += kN) {
     const int r = u / PER, c = (u % PER) * VEC, i = i0 + r;
     float x[VEC];
 #pragma unroll
@@ -43,46 +44,47 @@ __device__ __forceinline__ void load_rows(float* dst, const T* base, long long s
   }
 }
 
-// acc[i][j] = sum over d of A[ty + 16 i][d] B[tx + 16 j][d]
-template <int D>
+// acc[i][j] = sum over d of A[ty + (64 / R) i][d] B[tx + 16 j][d]
+template <int D, int R>
 __device__ __forceinline__ void dot_tile(const float* A, const float* B, int ty, int tx,
-                                         float (&acc)[4][4]) {
+                                         float (&acc)[R][4]) {
+  constexpr int kR = R, kGap = kB / R;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kR; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 #pragma unroll 4
   for (int k = 0; k < D; k += 4) {
-    float4 x[4], y[4];
+    float4 x[kR], y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * kLd<D> + k);
-      y[i] = *reinterpret_cast<const float4*>(B + (tx + 16 * i) * kLd<D> + k);
-    }
+    for (int i = 0; i < kR; ++i) x[i] = *reinterpret_cast<const float4*>(A + (ty + kGap * i) * kLd<D> + k);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * kLd<D> + k);
+#pragma unroll
+    for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         acc[i][j] += x[i].x * y[j].x + x[i].y * y[j].y + x[i].z * y[j].z + x[i].w * y[j].w;
   }
 }
 
-// acc[i][4 c + e] += sum over the 64 rows m of P[ty + 16 i][m] B[m][4 tx + 64 c + e]
-template <int D>
+// acc[i][4 c + e] += sum over the 64 rows m of P[ty + (64 / R) i][m] B[m][4 tx + 64 c + e]
+template <int D, int R>
 __device__ __forceinline__ void mix_tile(const float* P, const float* B, int ty, int tx,
-                                         float (&acc)[4][D / 16]) {
-#pragma unroll 2
+                                         float (&acc)[R][D / 16]) {
+  constexpr int kR = R, kGap = kB / R;
+#pragma unroll 4
   for (int m = 0; m < kB; m += 4) {
-    float4 p[4];
+    float4 p[kR];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(P + (ty + 16 * i) * kLdP + m);
+    for (int i = 0; i < kR; ++i) p[i] = *reinterpret_cast<const float4*>(P + (ty + kGap * i) * kLdP + m);
 #pragma unroll
     for (int mm = 0; mm < 4; ++mm) {
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         const float4 y = *reinterpret_cast<const float4*>(B + (m + mm) * kLd<D> + 4 * tx + 64 * c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kR; ++i) {
           const float w = mm == 0 ? p[i].x : mm == 1 ? p[i].y : mm == 2 ? p[i].z : p[i].w;
           acc[i][4 * c] += w * y.x;
           acc[i][4 * c + 1] += w * y.y;
@@ -117,8 +119,9 @@ __device__ __forceinline__ void store4(T* dst, float a, float b, float c, float 
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(a, b), pack2(c, d));
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowArgs<T> a) {
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(16 * kB / R) window_fwd_simt_kernel(const WindowArgs<T> a) {
+  constexpr int kR = R, kGap = kB / R, kN = 16 * kGap;
   extern __shared__ float sm[];
   float *Q = sm, *K = Q + kB * kLd<D>, *V = K + kB * kLd<D>, *P = V + kB * kLd<D>;
   pdl_launch_dependents();
@@ -130,11 +133,11 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowA
   const int i0 = (gridDim.x - 1 - blockIdx.x) * kB;
   const int p0 = i0 + off;
   const KeyTiles<kB> tiles(a.w, len, max(p0, 0), min(min(p0 + kB, a.w.nk) - 1, len - 1));
-  load_rows<D>(Q, a.q.row(b, h, 0), a.q.sn, i0, max(0, -off), min(a.w.nq, len - off));
+  load_rows<D, T, kN>(Q, a.q.row(b, h, 0), a.q.sn, i0, max(0, -off), min(a.w.nq, len - off));
 
-  float o[4][D / 16], m[4], l[4];
+  float o[kR][D / 16], m[kR], l[kR];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kR; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
@@ -143,14 +146,14 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowA
   for (int t = 0; t < tiles.count; ++t) {
     const int j0 = tiles.tile(t) * kB;
     __syncthreads();
-    load_rows<D>(K, a.k.row(b, hk, 0), a.k.sn, j0, 0, len);
-    load_rows<D>(V, a.v.row(b, hk, 0), a.v.sn, j0, 0, len);
+    load_rows<D, T, kN>(K, a.k.row(b, hk, 0), a.k.sn, j0, 0, len);
+    load_rows<D, T, kN>(V, a.v.row(b, hk, 0), a.v.sn, j0, 0, len);
     __syncthreads();
-    float s[4][4];
+    float s[kR][4];
     dot_tile<D>(Q, K, ty, tx, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = p0 + ty + 16 * i;
+    for (int i = 0; i < kR; ++i) {
+      const int p = p0 + ty + kGap * i;
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowA
       for (int j = 0; j < 4; ++j) {
         const float e = expf(s[i][j] - base);
         sum += e;
-        P[(ty + 16 * i) * kLdP + tx + 16 * j] = e;
+        P[(ty + kGap * i) * kLdP + tx + 16 * j] = e;
       }
       l[i] = l[i] * alpha + row_reduce<false>(sum);
 #pragma unroll
@@ -177,8 +180,8 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowA
     mix_tile<D>(P, V, ty, tx, o);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int q = i0 + ty + 16 * i;
+  for (int i = 0; i < kR; ++i) {
+    const int q = i0 + ty + kGap * i;
     if (q >= a.w.nq) continue;
     const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
     T* dst = a.out.row(b, h, q) + 4 * tx;
@@ -234,10 +237,10 @@ __global__ void __launch_bounds__(kThreads) window_dq_simt_kernel(const WindowAr
   const int lo = max(0, -off), hi = min(a.w.nq, len - off);
   load_rows<D>(Q, a.q.row(b, h, 0), a.q.sn, i0, lo, hi);
   load_rows<D>(dO, a.dO.row(b, h, 0), a.dO.sn, i0, lo, hi);
-  float acc[4][D / 16], lse[4], delta[4];
+  float acc[kR][D / 16], lse[kR], delta[kR];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int q = i0 + ty + 16 * i;
+  for (int i = 0; i < kR; ++i) {
+    const int q = i0 + ty + kGap * i;
     const bool in = q >= lo && q < hi;
     lse[i] = in ? a.lse[(long long)blockIdx.y * a.w.nq + q] : 0.f;
     delta[i] = in ? a.delta[(long long)blockIdx.y * a.w.nq + q] : 0.f;
@@ -250,23 +253,23 @@ __global__ void __launch_bounds__(kThreads) window_dq_simt_kernel(const WindowAr
     load_rows<D>(K, a.k.row(b, hk, 0), a.k.sn, j0, 0, len);
     load_rows<D>(V, a.v.row(b, hk, 0), a.v.sn, j0, 0, len);
     __syncthreads();
-    float s[4][4], dp[4][4];
+    float s[kR][4], dp[kR][4];
     dot_tile<D>(Q, K, ty, tx, s);
     dot_tile<D>(dO, V, ty, tx, dp);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bool see = sees(a.w, len, p0 + ty + 16 * i, j0 + tx + 16 * j);
-        S[(ty + 16 * i) * kLdP + tx + 16 * j] =
+        const bool see = sees(a.w, len, p0 + ty + kGap * i, j0 + tx + 16 * j);
+        S[(ty + kGap * i) * kLdP + tx + 16 * j] =
             see ? expf(s[i][j] * a.scale - lse[i]) * (dp[i][j] - delta[i]) : 0.f;
       }
     __syncthreads();
     mix_tile<D>(S, K, ty, tx, acc);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int q = i0 + ty + 16 * i;
+  for (int i = 0; i < kR; ++i) {
+    const int q = i0 + ty + kGap * i;
     if (q >= a.w.nq) continue;
     T* dst = a.dq.row(b, h, q) + 4 * tx;
 #pragma unroll
@@ -292,9 +295,9 @@ __global__ void __launch_bounds__(kThreads) window_dkdv_simt_kernel(const Window
   query_range(a.w, len, j0, min(j0 + kB, a.w.nk) - 1, i0, nq);
   load_rows<D>(K, a.k.row(b, hk, 0), a.k.sn, j0, 0, len);
   load_rows<D>(V, a.v.row(b, hk, 0), a.v.sn, j0, 0, len);
-  float dk[4][D / 16], dv[4][D / 16];
+  float dk[kR][D / 16], dv[kR][D / 16];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kR; ++i)
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
   for (int h = hk * group; h < (hk + 1) * group; ++h) {
@@ -309,18 +312,18 @@ __global__ void __launch_bounds__(kThreads) window_dkdv_simt_kernel(const Window
         delta[threadIdx.x] = i < i0 + nq ? a.delta[at] : 0.f;
       }
       __syncthreads();
-      float s[4][4], dp[4][4];  // rows: keys, columns: queries
+      float s[kR][4], dp[kR][4];  // rows: keys, columns: queries
       dot_tile<D>(K, Q, ty, tx, s);
       dot_tile<D>(V, dO, ty, tx, dp);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kR; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = tx + 16 * j;
-          const bool see = i1 + c < i0 + nq && sees(a.w, len, i1 + c + off, j0 + ty + 16 * i);
+          const bool see = i1 + c < i0 + nq && sees(a.w, len, i1 + c + off, j0 + ty + kGap * i);
           const float p = see ? expf(s[i][j] * a.scale - lse[c]) : 0.f;
-          P[(ty + 16 * i) * kLdP + c] = p;
-          S[(ty + 16 * i) * kLdP + c] = see ? p * (dp[i][j] - delta[c]) : 0.f;
+          P[(ty + kGap * i) * kLdP + c] = p;
+          S[(ty + kGap * i) * kLdP + c] = see ? p * (dp[i][j] - delta[c]) : 0.f;
         }
       __syncthreads();
       mix_tile<D>(P, dO, ty, tx, dv);
@@ -328,8 +331,8 @@ __global__ void __launch_bounds__(kThreads) window_dkdv_simt_kernel(const Window
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = j0 + ty + 16 * i;
+  for (int i = 0; i < kR; ++i) {
+    const int j = j0 + ty + kGap * i;
     if (j >= a.w.nk) continue;
     T *dkr = a.dk.row(b, hk, j) + 4 * tx, *dvr = a.dv.row(b, hk, j) + 4 * tx;
 #pragma unroll
@@ -341,13 +344,19 @@ __global__ void __launch_bounds__(kThreads) window_dkdv_simt_kernel(const Window
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int R>
 cudaError_t fwd(const WindowArgs<T>& a, cudaStream_t st) {
   constexpr int smem = (3 * kB * kLd<D> + kB * kLdP) * 4;
-  auto kern = window_fwd_simt_kernel<T, D>;
+  auto kern = window_fwd_simt_kernel<T, D, R>;
   const cudaError_t e = set_max_dynamic_smem((const void*)kern, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((a.w.nq + kB - 1) / kB, a.w.B * a.w.nh), dim3(kThreads), smem, st, a);
+  return launch_pdl(kern, dim3((a.w.nq + kB - 1) / kB, a.w.B * a.w.nh), dim3(16 * kB / R), smem, st, a);
+}
+
+template <typename T, int D>
+cudaError_t fwd(const WindowArgs<T>& a, cudaStream_t st) {
+  const long long ctas = (long long)((a.w.nq + kB - 1) / kB) * a.w.B * a.w.nh;
+  return ctas <= device_sm_count() ? fwd<T, D, 2>(a, st) : fwd<T, D, 4>(a, st);
 }
 
 template <typename T, int D>

@@ -70,32 +70,48 @@ __device__ __forceinline__ int unit_of(int i) {
 }
 
 // -lse log2(e) and -delta of every row; rows that see nothing, and those behind n_q, get 0:
-// their scores are masked.  One row per LANES lanes.
+// their scores are masked.  D / 8 lanes share a row, 16 bytes of dO and of O in each, and take
+// four rows, all on their way at once.
+constexpr int kStatRows = 4;
 template <int D>
 __global__ void __launch_bounds__(256)
     window_stat_kernel(const WindowArgs<__nv_bfloat16> a, float* stat, int padded) {
-  constexpr int LANES = D / 8;
+  constexpr int LANES = D / 8, GROUPS = 256 / LANES;
   pdl_launch_dependents();
   pdl_wait();
-  const int lr = threadIdx.x % LANES, i = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
-  const int b = blockIdx.y / a.w.nh, h = blockIdx.y % a.w.nh;
-  const int p = i + a.w.nk - a.w.nq;
-  const bool live = i < a.w.nq && p >= 0 && p < a.w.len(b);
-  float s = 0.f, lse = 0.f;
-  if (live) {
-    float x[8], y[8];
-    unpack_vec(*reinterpret_cast<const uint4*>(a.dO.row(b, h, i) + 8 * lr), x);
-    unpack_vec(*reinterpret_cast<const uint4*>(a.o.row(b, h, i) + 8 * lr), y);
+  const int lr = threadIdx.x % LANES, i0 = blockIdx.x * (GROUPS * kStatRows) + threadIdx.x / LANES;
+  const int b = blockIdx.y / a.w.nh, h = blockIdx.y % a.w.nh, off = a.w.nk - a.w.nq;
+  const int from = max(0, -off), to = min(a.w.nq, a.w.len(b) - off);  // rows that see something
+  const __nv_bfloat16 *g = a.dO.row(b, h, i0) + 8 * lr, *o = a.o.row(b, h, i0) + 8 * lr;
+  const float* lse = a.lse + (long long)blockIdx.y * a.w.nq;
+  uint4 rg[kStatRows], ro[kStatRows];
+  float l[kStatRows];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s += x[e] * y[e];
-    lse = a.lse[(long long)blockIdx.y * a.w.nq + i];
+  for (int k = 0; k < kStatRows; ++k) {
+    const int i = i0 + GROUPS * k;
+    rg[k] = ro[k] = make_uint4(0, 0, 0, 0);
+    l[k] = 0.f;
+    if (i >= from && i < to) {
+      rg[k] = *reinterpret_cast<const uint4*>(g + GROUPS * k * a.dO.sn);
+      ro[k] = *reinterpret_cast<const uint4*>(o + GROUPS * k * a.o.sn);
+      l[k] = lse[i];
+    }
   }
 #pragma unroll
-  for (int m = LANES / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-  if (lr == 0 && i < padded) {
-    float* at = stat + 2 * ((long long)blockIdx.y * padded + i / kTile * kTile) + i % kTile;
-    at[0] = -lse * kLog2;
-    at[kTile] = -s;
+  for (int k = 0; k < kStatRows; ++k) {
+    const int i = i0 + GROUPS * k;
+    float x[8], y[8], s = 0.f;
+    unpack_vec(rg[k], x);
+    unpack_vec(ro[k], y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += x[e] * y[e];
+#pragma unroll
+    for (int m = LANES / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (lr == 0 && i < padded) {
+      float* at = stat + 2 * ((long long)blockIdx.y * padded + i / kTile * kTile) + i % kTile;
+      at[0] = -l[k] * kLog2;
+      at[kTile] = -s;
+    }
   }
 }
 
@@ -929,7 +945,7 @@ cudaError_t bwd(const WindowArgs<__nv_bfloat16>& x, cudaStream_t st) {
   auto dkdv = window_dkdv_tc_kernel<D>;
   cudaError_t e = set_max_dynamic_smem((const void*)dq, DqCfg<D>::SMEM);
   if (e == cudaSuccess) e = set_max_dynamic_smem((const void*)dkdv, DkvCfg<D>::SMEM);
-  const int rows = 256 / (D / 8), padded = padded_rows(w);
+  const int rows = 256 / (D / 8) * kStatRows, padded = padded_rows(w);
   if (e == cudaSuccess)
     e = launch_pdl(window_stat_kernel<D>, dim3((padded + rows - 1) / rows, w.B * w.nh), dim3(256), 0, st, x, stat,
                    padded);

@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(OUT_DIR, "libpsa_gb300.so")
 SOURCES = ["api.cu", "layout.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_fused.cu", "attn_simt.cu",
            "qkv_conv.cu", "noalloc.cu", "lm_api.cu", "norm_rope.cu", "window_simt.cu", "kv_cache.cu",
            "window_decode.cu", "window_fwd.cu", "window_bwd.cu"]
-HEADERS = ["ptx.cuh", "attn.cuh", "layout.cuh", "tiles.cuh", "lm.cuh", "window_tc.cuh"]
+HEADERS = ["ptx.cuh", "attn.cuh", "layout.cuh", "tiles.cuh", "lm.cuh", "window_tc.cuh", "ptx_tiles4d.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-rdc=true", "-Xcompiler", "-fPIC",
          "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]

@@ -125,6 +125,8 @@ psa_status_t check_window(const psa_window_t& p) {
   if (p.head_dim != 64 && p.head_dim != 128) return PSA_ERR_UNSUPPORTED;
   if ((long long)p.B * p.num_heads > 65535 || p.n_q > kMaxRows || p.n_k > kMaxRows)
     return PSA_ERR_UNSUPPORTED;
+  // rows in all, so that the kernels' tile counts are ints
+  if ((long long)p.B * p.num_heads * std::max(p.n_q, p.n_k) > (1LL << 36)) return PSA_ERR_UNSUPPORTED;
   return PSA_OK;
 }
 

@@ -106,6 +106,18 @@ __device__ __forceinline__ uint32_t load4(const void* p) {
   return v;
 }
 
+// reads of this lane's own place that stay where they are (kept out of registers)
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float2 shared8(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+  return v;
+}
+
 // The visible rows of sequence b: blocks 0 .. sink - 1, then first .. (count in all).
 template <int kBlock>
 struct Blocks {
@@ -143,7 +155,13 @@ struct Cache<D, HT, false, kShort> {
     vn = a.v.sn;
     last = a.w.nk - 1;
   }
-  __device__ __forceinline__ void prepare(uint32_t (&)[HT][D / 8], float (&up)[HT][2], int) {
+  uint32_t q[HT][D / 8];
+  struct Shared {};
+  __device__ __forceinline__ void prepare(const uint32_t (&q_)[HT][D / 8], float (&up)[HT][2], int, Shared&) {
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) q[ht][i] = q_[ht][i];
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) up[ht][0] = up[ht][1] = 1.f;
   }
@@ -179,20 +197,22 @@ struct Cache<D, HT, false, kShort> {
       q[4 * i + 3] = u.w;
     }
   }
-  __device__ __forceinline__ void scores(int u, const uint32_t (&q)[HT][D / 8], float (&s)[HT][4]) const {
+  __device__ __forceinline__ void scores(float (&s)[U][HT][4]) const {
 #pragma unroll
-    for (int ht = 0; ht < HT; ++ht) {
-      // two chains of products, added at the end
-      float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 x = k[u][0][i], y = k[u][1][i];
-        mma16816(c[0], x.x, y.x, x.y, y.y, q[ht][4 * i], q[ht][4 * i + 1]);
-        mma16816(c[1], x.z, y.z, x.w, y.w, q[ht][4 * i + 2], q[ht][4 * i + 3]);
+      for (int ht = 0; ht < HT; ++ht) {
+        // two chains of products, added at the end
+        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 x = k[u][0][i], y = k[u][1][i];
+          mma16816(c[0], x.x, y.x, x.y, y.y, q[ht][4 * i], q[ht][4 * i + 1]);
+          mma16816(c[1], x.z, y.z, x.w, y.w, q[ht][4 * i + 2], q[ht][4 * i + 3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[u][ht][e] = c[0][e] + c[1][e];
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[ht][e] = c[0][e] + c[1][e];
-    }
   }
   // rows that are not visible may hold anything (NaN times a probability of 0)
   __device__ __forceinline__ void drop_v(int u, const bool (&see)[4]) {
@@ -235,12 +255,19 @@ template <int D, int HT, bool kShort>
 struct Cache<D, HT, true, kShort> {
   static constexpr int G = D / 32, W = G / 2;  // groups, and words that hold a value for each
   // two blocks of 16 keys at a time: twice the bytes in flight and half the steps' overhead
-  // (long contexts 123 -> 98 us); sixteen heads leave no registers for that
-  static constexpr int U = HT == 1 ? 2 : 1;
+  // (16 x 32768 keys 123 -> 112 us)
+  static constexpr int U = 2;
   const char *kp, *vp, *ksp, *vsp;
   int last;
   uint32_t k[U][2][G], v[U][4][W], ks[U][2][W], vs[U][2][W];  // codes; scales of keys g and g + 8
-  float q0[HT][G][2];  // minus what the codes' offsets add to the sums of heads 2 t and 2 t + 1
+  // The query, and minus what the codes' offsets add to the sums of heads 2 t and 2 t + 1, lie in
+  // shared memory, each lane's at its place: they are read once per step, and the registers
+  // hold more loads instead.
+  struct Shared {
+    uint4 q[HT][G][32];
+    float2 q0[HT][G][32];
+  };
+  uint32_t q_at, q0_at;
 
   __device__ __forceinline__ Cache(const DecodeArgs& a, int b, int h, int lane) {
     const long long base = ((long long)b * a.w.nkv + h) * a.w.nk;
@@ -252,7 +279,10 @@ struct Cache<D, HT, true, kShort> {
     last = a.w.nk - 1;
   }
   // The query in fp16, scaled to a maximum of 1 .. 2, and what that has to be undone by.
-  __device__ __forceinline__ void prepare(uint32_t (&q)[HT][D / 8], float (&up)[HT][2], int lane) {
+  // (every warp writes the same values)
+  __device__ __forceinline__ void prepare(uint32_t (&q)[HT][D / 8], float (&up)[HT][2], int lane, Shared& sh) {
+    q_at = smem_addr(&sh.q[0][0][lane]);
+    q0_at = smem_addr(&sh.q0[0][0][lane]);
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
       float m = 0.f;
@@ -277,8 +307,10 @@ struct Cache<D, HT, true, kShort> {
         }
         s += __shfl_xor_sync(0xffffffffu, s, 1);
         s += __shfl_xor_sync(0xffffffffu, s, 2);
-        q0[ht][g][0] = __shfl_sync(0xffffffffu, s, 8 * (lane & 3));
-        q0[ht][g][1] = __shfl_sync(0xffffffffu, s, 8 * (lane & 3) + 4);
+        const float o0 = __shfl_sync(0xffffffffu, s, 8 * (lane & 3));
+        const float o1 = __shfl_sync(0xffffffffu, s, 8 * (lane & 3) + 4);
+        sh.q[ht][g][lane] = make_uint4(q[ht][4 * g], q[ht][4 * g + 1], q[ht][4 * g + 2], q[ht][4 * g + 3]);
+        sh.q0[ht][g][lane] = make_float2(o0, o1);
       }
       up[ht][0] = __shfl_sync(0xffffffffu, mine, 8 * (lane & 3));
       up[ht][1] = __shfl_sync(0xffffffffu, mine, 8 * (lane & 3) + 4);
@@ -343,30 +375,42 @@ struct Cache<D, HT, true, kShort> {
   static __device__ __forceinline__ float scale_of(const uint32_t (&s)[W], int g) {
     return __uint_as_float((g & 1) ? s[g / 2] & 0xffff0000u : s[g / 2] << 16);
   }
-  __device__ __forceinline__ void scores(int u, const uint32_t (&q)[HT][D / 8], float (&s)[HT][4]) const {
+  __device__ __forceinline__ void scores(float (&s)[U][HT][4]) const {
 #pragma unroll
-    for (int ht = 0; ht < HT; ++ht) s[ht][0] = s[ht][1] = s[ht][2] = s[ht][3] = 0.f;
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht) s[u][ht][0] = s[u][ht][1] = s[u][ht][2] = s[u][ht][3] = 0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      // words of a = 2 t come first, those of a = 2 t + 1 after them
-      const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;
-      const uint32_t x = __byte_perm(k[u][0][g / 2], k[u][0][W + g / 2], sel);
-      const uint32_t y = __byte_perm(k[u][1][g / 2], k[u][1][W + g / 2], sel);
-      const uint32_t x8 = x >> 8, y8 = y >> 8;
-      const uint32_t a[8] = {(x & 0x000F000Fu) | 0x64006400u,  (y & 0x000F000Fu) | 0x64006400u,
-                             (x & 0x00F000F0u) | 0x54005400u,  (y & 0x00F000F0u) | 0x54005400u,
-                             (x8 & 0x000F000Fu) | 0x64006400u, (y8 & 0x000F000Fu) | 0x64006400u,
-                             (x8 & 0x00F000F0u) | 0x54005400u, (y8 & 0x00F000F0u) | 0x54005400u};
-      const float s0 = scale_of(ks[u][0], g), s1 = scale_of(ks[u][1], g);
+      uint4 q[HT];
+      float2 o[HT];
 #pragma unroll
       for (int ht = 0; ht < HT; ++ht) {
-        float c[4];
-        mma16816_f16(c, a[0], a[1], a[2], a[3], q[ht][4 * g], q[ht][4 * g + 1], q0[ht][g][0], q0[ht][g][1]);
-        mma16816_f16(c, a[4], a[5], a[6], a[7], q[ht][4 * g + 2], q[ht][4 * g + 3]);
-        s[ht][0] += c[0] * s0;
-        s[ht][1] += c[1] * s0;
-        s[ht][2] += c[2] * s1;
-        s[ht][3] += c[3] * s1;
+        q[ht] = shared16(q_at + (ht * G + g) * 512);
+        o[ht] = shared8(q0_at + (ht * G + g) * 256);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        // words of a = 2 t come first, those of a = 2 t + 1 after them
+        const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;
+        const uint32_t x = __byte_perm(k[u][0][g / 2], k[u][0][W + g / 2], sel);
+        const uint32_t y = __byte_perm(k[u][1][g / 2], k[u][1][W + g / 2], sel);
+        const uint32_t x8 = x >> 8, y8 = y >> 8;
+        const uint32_t a[8] = {(x & 0x000F000Fu) | 0x64006400u,  (y & 0x000F000Fu) | 0x64006400u,
+                               (x & 0x00F000F0u) | 0x54005400u,  (y & 0x00F000F0u) | 0x54005400u,
+                               (x8 & 0x000F000Fu) | 0x64006400u, (y8 & 0x000F000Fu) | 0x64006400u,
+                               (x8 & 0x00F000F0u) | 0x54005400u, (y8 & 0x00F000F0u) | 0x54005400u};
+        const float s0 = scale_of(ks[u][0], g), s1 = scale_of(ks[u][1], g);
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht) {
+          float c[4];
+          mma16816_f16(c, a[0], a[1], a[2], a[3], q[ht].x, q[ht].y, o[ht].x, o[ht].y);
+          mma16816_f16(c, a[4], a[5], a[6], a[7], q[ht].z, q[ht].w);
+          s[u][ht][0] += c[0] * s0;
+          s[u][ht][1] += c[1] * s0;
+          s[u][ht][2] += c[2] * s1;
+          s[u][ht][3] += c[3] * s1;
+        }
       }
     }
   }
@@ -407,7 +451,7 @@ struct Cache<D, HT, true, kShort> {
 };
 
 template <int D, int HT, bool kKv4, bool kShort>
-__global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 : 4)
     window_decode_kernel(const DecodeArgs a) {
   using C = Cache<D, HT, kKv4, kShort>;
   constexpr int MT = D / 16, kHeads = 8 * HT, U = C::U, kBlock = 16 * U;
@@ -438,7 +482,9 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 ? 3 : 4)
   for (int ht = 0; ht < HT; ++ht)
     C::load_q(8 * ht + r < heads ? a.q.row(b, h0 + 8 * ht + r, 0) : nullptr, t, q[ht]);
   float sl2[HT][2];
-  c.prepare(q, sl2, lane);
+  __shared__ typename C::Shared sh;
+  c.prepare(q, sl2, lane, sh);
+  __syncthreads();
 #pragma unroll
   for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
@@ -455,8 +501,7 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 ? 3 : 4)
   for (; blk < to; blk += kWarps) {
     const int first = bl.block(blk) * kBlock, j0 = min(first, top);
     float s[U][HT][4];
-#pragma unroll
-    for (int u = 0; u < U; ++u) c.scores(u, q, s[u]);
+    c.scores(s);
     const int next = blk + kWarps < to ? start(blk + kWarps) : -1;
     if (next >= 0) c.load_k(next, lane);
 #pragma unroll

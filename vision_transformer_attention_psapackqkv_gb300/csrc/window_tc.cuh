@@ -3,7 +3,7 @@
 #pragma once
 
 #include "lm.cuh"
-#include "ptx.cuh"
+#include "ptx_tiles4d.cuh"
 
 namespace psa {
 

@@ -208,6 +208,21 @@ def test_graph_replays_on_new_inputs_and_another_stream():
     assert all(torch.equal(x, y) for x, y in zip(got, (o, lse, dq, dk, dv)))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,left,lens", [(1, -1, None), (200, 0, None), (150, 3, [1, 1]), (300, -1, None)])
+def test_rows_that_see_one_key_pass_no_gradient(n, left, lens, dtype):
+    """Their probability is 1 whatever the score: exactly 0, not what is left of dP - delta."""
+    q, k, v, do = _inputs(2, 4, 2, n, n, 128, dtype, 21)
+    lens_t = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = _fwd(q, k, v, lens_t, left, 0, 0, 0.3)
+    dq, dk, dv = _bwd(q, k, v, o, do, lse, lens_t, left, 0, 0, 0.3)
+    assert (dq[:, :, 0] == 0).all()  # position 0 sees itself alone
+    if n != 300:
+        assert (dq == 0).all() and (dk == 0).all() and (dv[:, :, 0] != 0).any()
+    else:
+        assert (dk[:, :, 1:] != 0).any()
+
+
 def test_a_window_as_wide_as_the_sequence_is_no_window():
     q, k, v, _ = _inputs(1, 2, 2, 200, 200, 64, BF16, 17)
     a = _fwd(q, k, v, None, -1, 0, 0, 0.1)

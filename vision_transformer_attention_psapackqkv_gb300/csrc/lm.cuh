@@ -105,6 +105,12 @@ struct KeyTiles {
   __device__ __forceinline__ int tile(int t) const { return t < sink ? t : first + t - sink; }
 };
 
+// Whether position p sees one key only: its probability is 1 whatever the score, so that no
+// gradient passes through it (dP - delta would leave a rounding error instead of 0).
+__device__ __forceinline__ bool sees_one(const Window& w, int len, int p) {
+  return p == 0 ? w.right == 0 || len == 1 : w.left == 0 && w.right == 0 && w.sinks == 0;
+}
+
 // The query rows (first, count) that see a key among k0 .. k1, clipped to n_q rows.
 __host__ __device__ __forceinline__ void query_range(const Window& w, int len, int k0, int k1,
                                                      int& i0, int& n) {

@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; ok && unit_of(i) < a.units; ++i) {
       const DqUnit u(a, unit_of(i));
       const int q = u.row0 + r, p = q + off;
-      const int jhi = p >= 0 && p < u.len && q < a.w.nq ? min(u.len - 1, p + a.w.right) : -1;
+      // (a row that sees one key has dS = 0: nothing else is made of P here)
+      const int jhi = p >= 0 && p < u.len && q < a.w.nq && !sees_one(a.w, u.len, p) ? min(u.len - 1, p + a.w.right) : -1;
       const int jlo = p - a.w.left;
       const bool rows = u.row0 + off >= 0 && u.row0 + off + kTile <= u.len && u.row0 + kTile <= a.w.nq;
       const int whole_lo = u.p1 - a.w.left, whole_hi = rows ? min(u.len, u.p0 + a.w.right + 1) : 0;
@@ -730,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // tiles between these see every key of the unit
       const int whole_lo = u.k0 + kTile <= u.len ? max(u.i0, u.k0 + kTile - 1 - a.w.right - off) : 1 << 30;
       const int whole_hi = min(u.i1 - 1, u.k0 + kTile <= a.w.sinks ? u.i1 - 1 : u.k0 + a.w.left - off);
+      const bool first_one = sees_one(a.w, u.len, 0), all_one = sees_one(a.w, u.len, 1);
       int tile = n > 0 ? u.tile0 + u.from % u.tiles : 0;
       for (int t = 0; t < n; ++t, ++qc) {
         const int st = qc % C::ST, q0 = tile * kTile;
@@ -774,7 +776,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         uint32_t y[64];
         load_cols64(tP, y);
-        if (!whole) drop_masked(x, y);
+        if (!whole) {
+          // queries that see one key have dS = 0 (a tile that holds one is never seen whole):
+          // position 0's column, or all of them
+          const int at = -(q0 + 64 * half + off);
+          if (all_one || (first_one && at >= 0 && at < 64)) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (all_one || c == at) x[c] = 0u;
+          }
+          drop_masked(x, y);
+        }
 #pragma unroll
         for (int c = 0; c < 64; c += 4) {
           const float4 nd = stat[32 + c / 4];

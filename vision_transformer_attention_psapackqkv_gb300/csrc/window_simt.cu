@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(kThreads) window_dq_simt_kernel(const WindowAr
     for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bool see = sees(a.w, len, p0 + ty + kGap * i, j0 + tx + 16 * j);
+        const int p = p0 + ty + kGap * i;
+        const bool see = sees(a.w, len, p, j0 + tx + 16 * j) && !sees_one(a.w, len, p);
         S[(ty + kGap * i) * kLdP + tx + 16 * j] =
             see ? expf(s[i][j] * a.scale - lse[i]) * (dp[i][j] - delta[i]) : 0.f;
       }
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) window_dkdv_simt_kernel(const Window
           const bool see = i1 + c < i0 + nq && sees(a.w, len, i1 + c + off, j0 + ty + kGap * i);
           const float p = see ? expf(s[i][j] * a.scale - lse[c]) : 0.f;
           P[(ty + kGap * i) * kLdP + c] = p;
-          S[(ty + kGap * i) * kLdP + c] = see ? p * (dp[i][j] - delta[c]) : 0.f;
+          S[(ty + kGap * i) * kLdP + c] = see && !sees_one(a.w, len, i1 + c + off) ? p * (dp[i][j] - delta[c]) : 0.f;
         }
       __syncthreads();
       mix_tile<D>(P, dO, ty, tx, dv);

@@ -364,11 +364,12 @@ psa_status_t psa_kv_append(psa_rows_t k, psa_rows_t v, const int *starts, const 
 
 /* A cache held in 4 bits: codes uint8 [B, num_kv_heads, max_len, d / 2] and scales bf16
  * [B, num_kv_heads, max_len, d / 32], dense and 16-byte aligned.  Each group of 32
- * channels of a row has one scale, its largest magnitude / 7 rounded to bf16; a code is
- * the nearest multiple of it (ties to even, clamped to -7 .. 7; 0 where the scale is 0)
- * plus 8, and stands for (code - 8) * scale.  The code of channel 32 g + 4 a + i is the
- * nibble (a * (d / 32) + g) * 4 + i of its row, low nibble of a byte first.  This
- * quantises and stores the rows of k and v; head_dim 64 or 128, rows bf16 or fp32. */
+ * channels of a row has one scale, its largest magnitude times 1/7 (an fp32 product)
+ * rounded to bf16; a code is the nearest multiple of it (an fp32 quotient, ties to even,
+ * clamped to -7 .. 7; 0 where the scale is 0) plus 8, and stands for (code - 8) * scale.
+ * The code of channel 32 g + 4 a + i is the nibble (a * (d / 32) + g) * 4 + i of its row,
+ * low nibble of a byte first.  This quantises and stores the rows of k and v; head_dim 64
+ * or 128, rows bf16 or fp32. */
 psa_status_t psa_kv4_append(psa_rows_t k, psa_rows_t v, const int *starts, const int *counts,
                             void *k_codes, void *k_scales, void *v_codes, void *v_scales,
                             psa_cache_t p, cudaStream_t stream);

@@ -159,7 +159,7 @@ def test_quotients_near_ties():
     smallest to the largest, against the division of the format's definition."""
     x = _randn(16, 1, 2, 8192, 128) * torch.exp2(torch.randint(-140, 120, (1, 2, 8192, 1), generator=_gen(17), device="cuda").float())
     top = x[..., :32].abs().amax(-1, keepdim=True)
-    scale = (top / torch.full_like(top, 7)).to(BF16).float()
+    scale = (top * torch.full_like(top, 1 / 7)).to(BF16).float()
     half = (torch.randint(-7, 7, (1, 2, 8192, 16), generator=_gen(18), device="cuda") + 0.5) * scale  # exact
     x[..., 1:17] = torch.where(x[..., 1:17].abs() <= x[..., :32].abs().amax(-1, keepdim=True), half, x[..., 1:17])
     bits = x[..., 9:17].contiguous().view(torch.int32)

@@ -140,7 +140,7 @@ def quantise(x):
     for g in range(groups):
         part = x[..., 32 * g:32 * g + 32]
         top = part.abs().amax(-1)
-        sc = (top / torch.full_like(top, 7)).to(torch.bfloat16)  # (by a scalar it may be a product)
+        sc = (top * torch.full_like(top, 1 / 7)).to(torch.bfloat16)
         scales[..., g] = sc
         step = sc.float()
         for e in range(32):

@@ -1,7 +1,7 @@
 // kv_cache.cu -- rows into a cache: as they are (psa_kv_append), or in 4 bits
 // (psa_kv4_append) and back (psa_kv4_read).
 //
-// 4 bits: for each group g of 32 channels of a row, scale = bf16(max|x| / 7) and
+// 4 bits: for each group g of 32 channels of a row, scale = bf16(max|x| (1 / 7)) and
 // code(x) = round(x / scale) + 8 (ties to even, clamped to 1 .. 15), which stands for
 // (code - 8) * scale: 4.5 bits a value.  The code of channel 32 g + 4 a + i (a < 8, i < 4)
 // is nibble (a * G + g) * 4 + i of the row's d / 2 bytes, G = d / 32.  In this order a
@@ -83,7 +83,7 @@ __device__ __forceinline__ void quantise_row(const T* src, uint8_t* codes, __nv_
     for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const __nv_bfloat16 s = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.f));
+    const __nv_bfloat16 s = __float2bfloat16_rn(__fmul_rn(__uint_as_float(top), 1.f / 7.f));
     const float step = __bfloat162float(s);
     sc[g] = *reinterpret_cast<const uint16_t*>(&s);
     // The format's quotient is rounded to fp32, then to a whole number.  With the correctly
@@ -91,7 +91,7 @@ __device__ __forceinline__ void quantise_row(const T* src, uint8_t* codes, __nv_
     // the last place the correctly rounded one (Markstein, "Computation of elementary functions
     // on the IBM RISC System/6000 processor", 1990); x times the reciprocal may be a unit and a
     // half off, so there is a correction before it.  Below 2^-100, where the reciprocal may overflow and a bf16 scale may
-    // be far from max / 7, it is the division itself, clamped; elsewhere |q| < 7.5.
+    // be far from a seventh of the maximum, it is the division itself, clamped; elsewhere |q| < 7.5.
     // Adding 1.5 2^23 + 8 rounds (ties to even) and leaves the code in the lowest four bits; the
     // constant's low 16 bits are those of the 8 alone, so four such sums shifted by multiplication
     // add up to four codes in the low half.

@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (a row that sees one key has dS = 0: nothing else is made of P here)
       const int jhi = p >= 0 && p < u.len && q < a.w.nq && !sees_one(a.w, u.len, p) ? min(u.len - 1, p + a.w.right) : -1;
       const int jlo = p - a.w.left;
-      const bool rows = u.row0 + off >= 0 && u.row0 + off + kTile <= u.len && u.row0 + kTile <= a.w.nq;
-      const int whole_lo = u.p1 - a.w.left, whole_hi = rows ? min(u.len, u.p0 + a.w.right + 1) : 0;
+      // rows that do not exist or are padding get anything here and 0 at the end
+      const int whole_lo = u.p1 - a.w.left, whole_hi = min(u.len, u.p0 + a.w.right + 1);
       const float* stat = a.stat + 2 * ((long long)(u.b * a.w.nh + u.h) * a.row_tiles * kTile + u.row0) + r;
       const float2 nlse = make_float2(stat[0], stat[0]), ndelta = make_float2(stat[kTile], stat[kTile]);
       const float2 sl = make_float2(a.sl2, a.sl2);
@@ -445,11 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 32; ++k) o[k] = 0.f;
         }
         if (in) {
+          const bool valid = q + off >= 0 && q + off < u.len;
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            *reinterpret_cast<uint4*>(dst + c + k) =
-                make_uint4(pack2(o[k] * a.scale, o[k + 1] * a.scale), pack2(o[k + 2] * a.scale, o[k + 3] * a.scale),
-                           pack2(o[k + 4] * a.scale, o[k + 5] * a.scale), pack2(o[k + 6] * a.scale, o[k + 7] * a.scale));
+          for (int k = 0; k < 32; k += 8) {
+            const uint4 v = make_uint4(pack2(o[k] * a.scale, o[k + 1] * a.scale), pack2(o[k + 2] * a.scale, o[k + 3] * a.scale),
+                                       pack2(o[k + 4] * a.scale, o[k + 5] * a.scale),
+                                       pack2(o[k + 6] * a.scale, o[k + 7] * a.scale));
+            *reinterpret_cast<uint4*>(dst + c + k) = valid ? v : make_uint4(0, 0, 0, 0);
+          }
         }
       }
       tc_fence_before();

@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     bool ok = true;
     for (int i = 0; ok && unit_of(i) < a.units; ++i) {
       int b, h, q, len, jhi, jlo;  // this row, and the keys it sees: none if jhi < 0
-      int whole_lo, whole_hi;      // tiles between these are seen whole by every row
+      int whole_lo, whole_hi;      // tiles between these are seen whole by every valid row
       int end;
       KeyTiles<kTile> tiles;
       {
@@ -508,9 +508,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         jhi = p >= 0 && p < len && q < a.w.nq ? min(len - 1, p + a.w.right) : -1;
         jlo = p - a.w.left;
         tiles = KeyTiles<kTile>(a.w, len, me.p0, me.p1);
-        const bool rows = me.row0 + off >= 0 && me.row0 + off + kTile <= len && me.row0 + kTile <= a.w.nq;
+        // rows that do not exist or are padding get anything here and 0 at the end
         whole_lo = me.p1 - a.w.left;
-        whole_hi = rows ? min(len, me.p0 + a.w.right + 1) : 0;
+        whole_hi = min(len, me.p0 + a.w.right + 1);
         end = min(len, me.p1 + a.w.right + 1);
       }
       float m = -INFINITY, l = 0.f;
@@ -540,7 +540,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         tc_fence_after();
       }
       if (q - r >= a.w.nq) continue;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const bool sees = jhi >= 0;
+      const float inv = 1.f / l;
       // the staging tile is this slot's once the use before it has been read
       if (s || uses > 0) {
         if (!mbar_wait(&bar.stored[s], (s ? uses : uses - 1) & 1, abort)) break;
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (some) {
           tmem_load32(tO + c, o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] *= inv;
+          for (int k = 0; k < 32; ++k) o[k] = sees ? o[k] * inv : 0.f;
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0.f;
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(&bar.staged);
       if (q < a.w.nq && a.lse)
-        a.lse[((long long)b * a.w.nh + h) * a.w.nq + q] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+        a.lse[((long long)b * a.w.nh + h) * a.w.nq + q] = sees ? m * kLn2 + logf(l) : -INFINITY;
     }
   }
 

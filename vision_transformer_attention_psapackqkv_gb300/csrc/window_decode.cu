@@ -32,6 +32,11 @@
 // exactly; its sums run over all keys, where subtracting at the end would leave nothing.  A
 // key's scale multiplies its fp32 partial score of each group of 32 channels; a value's scale
 // multiplies the probability before it is rounded to bf16.
+//
+// Measured: bf16, 32 sequences of up to 8192 keys, 4096 visible, 32 heads of 128 on 8: 84 us (5.9
+// TB/s, 0.89 of the copy bandwidth); 4 bits, 16 sequences of up to 32768 keys: 111 us (3.5 TB/s,
+// 0.52; the integer pipe is busy 65 % of the time, tensor instructions 19 %).  One sequence of
+// 1024 visible keys: 5.5 us with the join.
 #include <algorithm>
 
 #include <cuda_fp16.h>

@@ -28,6 +28,12 @@
 // row's maximum grows by more than 2^8 (O and the sum share the stale maximum, so the result
 // is the same).  P is rounded to bf16 for the product with V, as its operand; the sum is of
 // the unrounded values.
+// Measured: 16384 tokens causal, 16 heads of 128 on 2: 735 us (1.5 PFLOP/s of visible pairs,
+// 0.78 of cuBLAS's bf16 rate, the pipe busy 65 % of the time); 8192 tokens, 32 heads on 8, a
+// window of 1024 and 4 sinks: 147 us (0.88 PFLOP/s: of ten tiles a row tile visits, two are half
+// empty and one holds the sinks, and each unit starts its chain anew); head dim 64: 648 us at
+// 16384 causal (0.85 PFLOP/s: the chain S, softmax, P V of a slot is longer than the other
+// slot's products, 2.7k cycles a step).
 #include <math.h>
 
 #include <algorithm>

@@ -9,6 +9,8 @@
 // other side that its rows see, so a score exists only in registers and shared memory.
 // 256 threads as 16 x 16: a thread holds the 4 x 4 scores of rows ty + 16 i and columns
 // tx + 16 j, and of each product with V (K, dO, Q) its rows' channels 4 tx + 64 c .. + 3.
+// Measured, fp32: 4 maps of 400 positions, 4 heads of 64, 121 keys a query: 31 us; 2 x 1024
+// causal, 8 heads of 128: 237 us forward, 780 us backward.
 // Tiles lie row by row in shared memory with 4 floats of padding: 16-byte reads of eight
 // neighbouring rows then fall into different banks.  Every key/value head's gradient is
 // summed by one CTA over its query heads and tiles in order, so reruns are bitwise equal.

@@ -209,18 +209,25 @@ def test_graph_replays_on_new_inputs_and_another_stream():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("n,left,lens", [(1, -1, None), (200, 0, None), (150, 3, [1, 1]), (300, -1, None)])
-def test_rows_that_see_one_key_pass_no_gradient(n, left, lens, dtype):
+@pytest.mark.parametrize("n,left,right,lens,rows", [(1, -1, 0, None, "all"), (200, 0, 0, None, "all"), (2, 0, 0, None, "all"),
+                                                    (150, 3, 0, [1, 1], "all"), (300, -1, 0, None, [0]),
+                                                    (200, 0, 5, None, [199]), (2, 0, 1, None, [1]),
+                                                    (260, 0, 300, [260, 131], [[259], [130]])])
+def test_rows_that_see_one_key_pass_no_gradient(n, left, right, lens, rows, dtype):
     """Their probability is 1 whatever the score: exactly 0, not what is left of dP - delta."""
     q, k, v, do = _inputs(2, 4, 2, n, n, 128, dtype, 21)
     lens_t = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
-    o, lse = _fwd(q, k, v, lens_t, left, 0, 0, 0.3)
-    dq, dk, dv = _bwd(q, k, v, o, do, lse, lens_t, left, 0, 0, 0.3)
-    assert (dq[:, :, 0] == 0).all()  # position 0 sees itself alone
-    if n != 300:
+    o, lse = _fwd(q, k, v, lens_t, left, right, 0, 0.3)
+    dq, dk, dv = _bwd(q, k, v, o, do, lse, lens_t, left, right, 0, 0.3)
+    if rows == "all":
         assert (dq == 0).all() and (dk == 0).all() and (dv[:, :, 0] != 0).any()
     else:
-        assert (dk[:, :, 1:] != 0).any()
+        for b in range(2):
+            one = rows[b] if isinstance(rows[0], list) else rows
+            m = n if lens is None else lens[b]
+            assert (dq[b, :, one] == 0).all()
+            assert all((dq[b, :, i] != 0).any() for i in range(m) if i not in one)
+    _check(q, k, v, do, lens, left, right, 0, 0.3)
 
 
 def test_a_window_as_wide_as_the_sequence_is_no_window():

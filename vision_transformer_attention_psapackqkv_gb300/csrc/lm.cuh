@@ -106,9 +106,11 @@ struct KeyTiles {
 };
 
 // Whether position p sees one key only: its probability is 1 whatever the score, so that no
-// gradient passes through it (dP - delta would leave a rounding error instead of 0).
+// gradient passes through it (dP - delta would leave a rounding error instead of 0).  These are
+// position 0, or the last one, or all of them, as the window is.
 __device__ __forceinline__ bool sees_one(const Window& w, int len, int p) {
-  return p == 0 ? w.right == 0 || len == 1 : w.left == 0 && w.right == 0 && w.sinks == 0;
+  if (p == 0) return w.right == 0 || len == 1;
+  return w.left == 0 && w.sinks == 0 && (w.right == 0 || p == len - 1);
 }
 
 // The query rows (first, count) that see a key among k0 .. k1, clipped to n_q rows.

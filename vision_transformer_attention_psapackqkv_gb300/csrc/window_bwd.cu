@@ -738,7 +738,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // tiles between these see every key of the unit
       const int whole_lo = u.k0 + kTile <= u.len ? max(u.i0, u.k0 + kTile - 1 - a.w.right - off) : 1 << 30;
       const int whole_hi = min(u.i1 - 1, u.k0 + kTile <= a.w.sinks ? u.i1 - 1 : u.k0 + a.w.left - off);
-      const bool first_one = sees_one(a.w, u.len, 0), all_one = sees_one(a.w, u.len, 1);
+      const bool first_one = sees_one(a.w, u.len, 0), last_one = sees_one(a.w, u.len, u.len - 1);
+      const bool all_one = last_one && a.w.right == 0 && a.w.left == 0 && a.w.sinks == 0;
       int tile = n > 0 ? u.tile0 + u.from % u.tiles : 0;
       for (int t = 0; t < n; ++t, ++qc) {
         const int st = qc % C::ST, q0 = tile * kTile;
@@ -784,13 +785,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t y[64];
         load_cols64(tP, y);
         if (!whole) {
-          // queries that see one key have dS = 0 (a tile that holds one is never seen whole):
-          // position 0's column, or all of them
-          const int at = -(q0 + 64 * half + off);
-          if (all_one || (first_one && at >= 0 && at < 64)) {
+          // queries that see one key have dS = 0 (a tile that holds one is never seen whole): the
+          // columns of position 0 and of the last one, or all of them
+          const int at0 = -(q0 + 64 * half + off), at1 = at0 + u.len - 1;
+          const bool one0 = first_one && at0 >= 0 && at0 < 64, one1 = last_one && at1 >= 0 && at1 < 64;
+          if (all_one || one0 || one1) {
 #pragma unroll
             for (int c = 0; c < 64; ++c)
-              if (all_one || c == at) x[c] = 0u;
+              if (all_one || (one0 && c == at0) || (one1 && c == at1)) x[c] = 0u;
           }
           drop_masked(x, y);
         }

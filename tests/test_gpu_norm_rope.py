@@ -130,3 +130,25 @@ def test_on_another_stream():
     B.psa_qk_norm_rope_fwd(c["q"], c["k"], c["wq"], c["wk"], c["cos"], c["sin"], c["pos"], q, k, p, s)
     s.synchronize()
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_eps_zero_with_odd_heads_and_padding(dtype):
+    """Without eps, rows that are not there (past the last head, the last token, padding) have no
+    norm to divide by: they must not reach the weights' gradients."""
+    c = _case(2, 5, 1, 7, 64, 32, dtype, 9)
+    pad = torch.zeros(2, 7, dtype=torch.bool, device="cuda")
+    pad[0, 2], pad[1, 5:] = True, True
+    for n in ("gq", "gk"):
+        c[n].transpose(1, 2)[pad] = 0
+    dq, dk, dwq, dwk = _backward(c, False, 0.0)
+    for x, w, g, dx, dw, what in ((c["q"], c["wq"], c["gq"], dq, dwq, "q"), (c["k"], c["wk"], c["gk"], dk, dwk, "k")):
+        rdx, tdx, rdw, tdw = norm_rope(x, w, c["cos"], c["sin"], c["pos"], False, 0.0, g, HALF[dtype])
+        within(dx, rdx, tdx, "d" + what)
+        within(dw, rdw, tdw, "dw" + what)
+    c["pos"][pad] = -1
+    padded = _backward(c, False, 0.0)
+    for dx, was in ((padded[0], dq), (padded[1], dk)):
+        assert (dx.transpose(1, 2)[pad] == 0).all()
+        assert torch.equal(dx.transpose(1, 2)[~pad], was.transpose(1, 2)[~pad])
+    assert torch.equal(padded[2], dwq) and torch.equal(padded[3], dwk)

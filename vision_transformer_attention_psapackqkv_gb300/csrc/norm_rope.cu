@@ -249,11 +249,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int e = 0; e < VEC; e += 2) set2(gw + e, __fmul2_rn(at2(g + e), at2(w + e)));
         const float ss = group_sum<LANES>(dot(x, x)), gx = group_sum<LANES>(dot(gw, x));
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        // rows of padding, and those past the last head, hold zeros here: with r = 0 (without it
+        // eps = 0 makes NaN of them) their share is 0 and their dx is 0
+        const float r = valid && h + i < heads ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
         const float2 r2 = both(r), back = both(-gx * r * r * (1.f / D));
 #pragma unroll
         for (int e = 0; e < VEC; e += 2) {
-          // rows of padding hold zeros here: their share is 0 and their dx is 0
           const float2 xe = at2(x + e);
           set2(dw + e, __ffma2_rn(at2(g + e), __fmul2_rn(xe, r2), at2(dw + e)));
           set2(x + e, __fmul2_rn(r2, __ffma2_rn(xe, back, at2(gw + e))));
@@ -311,9 +312,9 @@ cudaError_t fwd(const NormRopeArgs<T>& a, cudaStream_t st) {
 
 template <typename T, int D>
 cudaError_t fwd(const NormRopeArgs<T>& a, cudaStream_t st) {
-  // four heads per group once that still fills the device's threads
-  const long long rows = (long long)a.B * a.N * (a.nh + a.nkv);
-  return rows * (D / kVec<T>) / 8 >= 152 * 2048LL ? fwd<T, D, 8>(a, st) : rows * (D / kVec<T>) / 4 >= 152 * 2048LL ? fwd<T, D, 4>(a, st) : fwd<T, D, 1>(a, st);
+  // eight heads per group, or four, once that still fills the device's threads
+  const long long lanes = (long long)a.B * a.N * (a.nh + a.nkv) * (D / kVec<T>), full = 152 * 2048;
+  return lanes / 8 >= full ? fwd<T, D, 8>(a, st) : lanes / 4 >= full ? fwd<T, D, 4>(a, st) : fwd<T, D, 1>(a, st);
 }
 
 template <typename T, int D>

@@ -181,3 +181,24 @@ def test_values_that_are_not_finite_do_not_read_back_as_finite():
     assert torch.isfinite(ko[0, 0, [0, 3]]).all()
     assert not torch.isfinite(ko[0, 0, 1, :32]).any() and torch.isfinite(ko[0, 0, 1, 32:]).all()
     assert not torch.isfinite(ko[0, 0, 2, 32:]).any() and torch.isfinite(ko[0, 0, 2, :32]).all()
+
+
+@pytest.mark.parametrize("rows", [20, 40, 3000])
+def test_a_nan_that_is_seen_stays_one(rows):
+    """One among the scores, or the query's own: not the zeros of a row that sees nothing."""
+    d = 64
+    q = _randn(31, 2, 4, 1, d).to(BF16)
+    k, v = _randn(32, 2, 2, rows, d).to(BF16), _randn(33, 2, 2, rows, d).to(BF16)
+    lens = [rows, rows - 3]
+    clean = _decode(q, k, v, lens, -1, 0, 0.2)
+    cache = quantise(k) + quantise(v)
+    clean4 = _decode4(q, cache, lens, -1, 0, 0.2)
+    k[0, 1, rows // 2, 5] = math.nan
+    cache[1][0, 1, rows // 2, 0] = math.nan
+    for o, was in ((_decode(q, k, v, lens, -1, 0, 0.2), clean), (_decode4(q, cache, lens, -1, 0, 0.2), clean4)):
+        assert o[0, 2:].isnan().all()
+        assert torch.equal(o[0, :2], was[0, :2]) and torch.equal(o[1], was[1])
+    q[1, 3, 0, 0] = math.nan
+    for o, was in ((_decode(q, k, v, lens, -1, 0, 0.2), clean), (_decode4(q, cache, lens, -1, 0, 0.2), clean4)):
+        # (head 2 shares its products with head 3, and the steps at which maxima move)
+        assert o[1, 3].isnan().all() and torch.equal(o[1, :2], was[1, :2]) and o[1, 2].isfinite().all()

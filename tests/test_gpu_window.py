@@ -246,3 +246,15 @@ def test_causal_attention_next_to_flash_attn2():
     r = window_attention(q, k, v, None, -1, -1, 0, 0.125)
     within(o[0], o2, 2 * r["o_tol"][0], "o")
     within(lse[0], lse2, 2 * r["lse_tol"][0], "lse")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_nan_in_a_query_stays_in_its_row(dtype):
+    q, k, v, _ = _inputs(1, 2, 1, 150, 150, 64, dtype, 31)
+    o, lse = _fwd(q, k, v, None, -1, 0, 0, 0.2)
+    q[0, 1, 70, 3] = math.nan
+    o2, lse2 = _fwd(q, k, v, None, -1, 0, 0, 0.2)
+    assert o2[0, 1, 70].isnan().all() and lse2[0, 1, 70].isnan()
+    keep = torch.ones(2, 150, dtype=torch.bool, device="cuda")
+    keep[1, 70] = False
+    assert torch.equal(o2[0, 0], o[0, 0]) and o2[0][keep].isfinite().all() and lse2[0][keep].isfinite().all()

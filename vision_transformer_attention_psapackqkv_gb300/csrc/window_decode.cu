@@ -617,15 +617,16 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 
     __syncthreads();
   }
   for (int u = threadIdx.x; u < heads * D; u += kThreads) {
+    // a sum of 0 is a row that sees nothing; a NaN among the scores stays one
     const int row = u / D, ch = u % D;
     float n = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) n = fmaxf(n, sm_m[w][row]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      sum += sm_m[w][row] == -INFINITY ? 0.f : sm_l[w][row] * fast_exp2(sm_m[w][row] - n);
+      sum += sm_l[w][row] * (sm_m[w][row] == -INFINITY ? 0.f : fast_exp2(sm_m[w][row] - n));
     if (gridDim.x == 1) {
-      a.o.row(b, h0 + row, 0)[ch] = __float2bfloat16_rn(sum > 0.f ? sm_o[row][ch] / sum : 0.f);
+      a.o.row(b, h0 + row, 0)[ch] = __float2bfloat16_rn(sum != 0.f ? sm_o[row][ch] / sum : 0.f);
     } else {
       // partial result: D outputs relative to the maximum n, then n and the sum
       float* dst = a.ws + (((long long)b * a.w.nh + h0 + row) * gridDim.x + blockIdx.x) * (D + 2);
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(D) window_join_kernel(const DecodeArgs a, int 
     l += src[s * (D + 2) + D + 1] * f;
     o += src[s * (D + 2) + threadIdx.x] * f;
   }
-  a.o.row(b, h, 0)[threadIdx.x] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
+  a.o.row(b, h, 0)[threadIdx.x] = __float2bfloat16_rn(l != 0.f ? o / l : 0.f);
 }
 
 // Query heads of a tile: eight where a group has no more (half the registers), else sixteen.

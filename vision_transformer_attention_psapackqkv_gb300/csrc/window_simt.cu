@@ -185,14 +185,15 @@ __global__ void __launch_bounds__(16 * kB / R) window_fwd_simt_kernel(const Wind
   for (int i = 0; i < kR; ++i) {
     const int q = i0 + ty + kGap * i;
     if (q >= a.w.nq) continue;
-    const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+    // a sum of 0 is a row that sees nothing; a NaN among the scores stays one
+    const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
     T* dst = a.out.row(b, h, q) + 4 * tx;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
       store4<D>(dst + 64 * c, o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv,
                 o[i][4 * c + 3] * inv);
     if (a.lse && tx == 0)
-      a.lse[(long long)blockIdx.y * a.w.nq + q] = l[i] > 0.f ? m[i] + logf(l[i]) : -INFINITY;
+      a.lse[(long long)blockIdx.y * a.w.nq + q] = l[i] != 0.f ? m[i] + logf(l[i]) : -INFINITY;
   }
 }
 

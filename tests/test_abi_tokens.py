@@ -222,3 +222,17 @@ def test_binding_refuses_on_the_host():
         B.psa_kv4_append(k, k, torch.zeros(1, dtype=torch.int32), None, torch.zeros(1, 2, 8, 32, dtype=torch.uint8),
                          torch.zeros(1, 2, 8, 4, dtype=torch.bfloat16), torch.zeros(1, 2, 8, 32, dtype=torch.uint8),
                          torch.zeros(1, 2, 8, 2, dtype=torch.bfloat16))
+
+
+def test_windows_wider_than_an_int():
+    """A limit that no C int holds is no limit, not what is left of its lower bits."""
+    import torch
+
+    from vision_transformer_attention_psapackqkv_gb300 import binding as B
+
+    q = torch.zeros(1, 2, 8, 64)
+    win = B.window_of(q, q, 2 ** 32, 2 ** 40, 2 ** 33 + 1)
+    assert (win.window_left, win.window_right, win.sinks) == (8, 8, 8)
+    win = B.window_of(q, q, -2 ** 32, -2 ** 33, 0)
+    assert (win.window_left, win.window_right, win.sinks) == (-1, -1, 0)
+    assert B.window_of(q, q, 0, 0, -2 ** 32).sinks == -1  # refused by the calls

@@ -364,8 +364,10 @@ def window_of(q, k, window_left: int = -1, window_right: int = 0, sinks: int = 0
     """The problem of q [B, num_heads, n_q, d] against keys, a cache or its codes k
     [B, num_kv_heads, n_k, ...]; a negative window has no limit on that side."""
     B, nh, n_q, d = q.shape
-    return PsaWindow(B, nh, k.shape[1], n_q, k.shape[2], d, dtype_code(q), int(window_left), int(window_right),
-                     int(sinks))
+    n_k = k.shape[2]
+    # nothing is past n_k, and all that is negative is alike; a C int would drop the upper bits
+    left, right, sinks = (max(-1, min(int(w), n_k)) for w in (window_left, window_right, sinks))
+    return PsaWindow(B, nh, k.shape[1], n_q, n_k, d, dtype_code(q), left, right, sinks)
 
 
 def _window_shapes(win: PsaWindow):

@@ -258,3 +258,11 @@ def test_a_nan_in_a_query_stays_in_its_row(dtype):
     keep = torch.ones(2, 150, dtype=torch.bool, device="cuda")
     keep[1, 70] = False
     assert torch.equal(o2[0, 0], o[0, 0]) and o2[0][keep].isfinite().all() and lse2[0][keep].isfinite().all()
+
+
+@pytest.mark.parametrize("Bn,nh,nkv,n,d,left,right,sinks,lens", [(3, 8, 8, 420, 64, 60, 60, 4, [420, 1, 333]),
+                                                              (2, 32, 4, 260, 64, -1, 0, 0, None),
+                                                              (2, 6, 3, 700, 128, 99, 0, 3, [700, 650])])
+def test_fp32_of_many_heads(Bn, nh, nkv, n, d, left, right, sinks, lens):
+    """More rows than the tiles for few of them take, on both sides or on the queries' alone."""
+    _check(*_inputs(Bn, nh, nkv, n, n, d, F32, 41), lens, left, right, sinks, 0.2)

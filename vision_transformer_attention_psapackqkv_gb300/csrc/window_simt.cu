@@ -5,12 +5,18 @@
 //   dV = P^T dO, dP = dO V^T, dS = P o (dP - delta), delta = rowsum(dO o O),
 //   dQ = scale dS K, dK = scale dS^T Q.
 //
-// A CTA owns 64 query rows (64 key rows in dK/dV) and goes through the 64-row tiles of the
-// other side that its rows see, so a score exists only in registers and shared memory.
-// 256 threads as 16 x 16: a thread holds the 4 x 4 scores of rows ty + 16 i and columns
-// tx + 16 j, and of each product with V (K, dO, Q) its rows' channels 4 tx + 64 c .. + 3.
-// Measured, fp32: 4 maps of 400 positions, 4 heads of 64, 121 keys a query: 31 us; 2 x 1024
-// causal, 8 heads of 128: 237 us forward, 780 us backward.
+// A CTA owns 32 or 16 query rows (key rows in dK/dV) and goes through the 64-row tiles of the
+// other side that its rows see, so a score exists only in registers and shared memory.  16
+// threads share a row: a thread holds the scores of 4 (or 2) rows, kGap apart, and columns
+// tx + 16 j, and of each product with V (K, dO, Q) its rows' channels 4 tx + 64 c .. + 3.  What
+// bounds it is reads of shared memory (busy 66 to 78 % of the time, the FMA pipe 20 to 33 %,
+// each of its instructions two products).  Few rows in a CTA waste less at a window's or a
+// triangle's edge and balance better: 2 x 1024 causal, 8 heads of 128, forward 196 us with 64
+// rows, 187 with 32, backward 670 and 629; eight rows a thread would read less, but leave too
+// few warps (214).  Tiles come asynchronously, the forward's V during the scores and K's next
+// during P V (4 maps of 400: 31 -> 28 us with 64 rows), dQ's next V during dS K.
+// Measured, fp32: 4 maps of 400 positions, 4 heads of 64, 121 keys a query: 22 us forward, 80
+// backward; 2 x 1024 causal, 8 heads of 128: 187 and 629 us.
 // Tiles lie row by row in shared memory with 4 floats of padding: 16-byte reads of eight
 // neighbouring rows then fall into different banks.  Every key/value head's gradient is
 // summed by one CTA over its query heads and tiles in order, so reruns are bitwise equal.
@@ -23,38 +29,38 @@ namespace psa {
 namespace {
 
 constexpr int kB = 64;  // rows of a tile, on either side
-constexpr int kThreads = 256;  // 16 threads a row, 4 rows a thread, kGap rows between them
-constexpr int kR = 4, kGap = kB / kR;
+constexpr int kThreads = 256;  // of the kernel of delta
 constexpr int kLdP = kB + 4;  // row pitch of a tile of scores
 
 template <int D>
 constexpr int kLd = D + 4;
 
-// Rows i0 .. i0 + 63 of one head into shared memory in fp32; rows outside [lo, hi) as 0.
-template <int D, typename T, int kN = kThreads>
-__device__ __forceinline__ void load_rows(float* dst, const T* base, long long sn, int i0, int lo,
-                                          int hi) {
-  constexpr int VEC = kVec<T>, PER = D / VEC;
-  for (int u = threadIdx.x; u < kB * PER; u += kN) {
-    const int r = u / PER, c = (u % PER) * VEC, i = i0 + r;
-    float x[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] = 0.f;
-    if (i >= lo && i < hi) unpack_vec(*reinterpret_cast<const uint4*>(base + i * sn + c), x);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) dst[r * kLd<D> + c + e] = x[e];
+// Rows i0 .. i0 + kRows - 1 of one head into shared memory; rows outside [lo, hi) as 0.
+// Asynchronously: to be waited for with fetched(), then a barrier.
+template <int D, int kN, int kRows>
+__device__ __forceinline__ void fetch_rows(float* dst, const float* base, long long sn, int i0, int lo,
+                                           int hi) {
+  for (int u = threadIdx.x; u < kRows * (D / 4); u += kN) {
+    const int r = u / (D / 4), c = u % (D / 4) * 4, i = i0 + r;
+    const bool in = i >= lo && i < hi;
+    // no byte is read for a row outside, its 16 are zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst + r * kLd<D> + c)),
+                 "l"(base + (in ? i * sn + c : 0)), "r"(in ? 16 : 0)
+                 : "memory");
   }
 }
+__device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// acc[i][j] = sum over d of A[ty + (64 / R) i][d] B[tx + 16 j][d]
-template <int D, int R>
+// acc[i][j] = sum over d of A[ty + kGap i][d] B[tx + 16 j][d]
+template <int D, int R, int kGap>
 __device__ __forceinline__ void dot_tile(const float* A, const float* B, int ty, int tx,
                                          float (&acc)[R][4]) {
-  constexpr int kR = R, kGap = kB / R;
+  constexpr int kR = R;
+  float2 sum[kR][4];  // of the even and of the odd channels: two products per instruction
 #pragma unroll
   for (int i = 0; i < kR; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) sum[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
   for (int k = 0; k < D; k += 4) {
     float4 x[kR], y[4];
@@ -65,16 +71,22 @@ __device__ __forceinline__ void dot_tile(const float* A, const float* B, int ty,
 #pragma unroll
     for (int i = 0; i < kR; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] += x[i].x * y[j].x + x[i].y * y[j].y + x[i].z * y[j].z + x[i].w * y[j].w;
+      for (int j = 0; j < 4; ++j) {
+        sum[i][j] = __ffma2_rn(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), sum[i][j]);
+        sum[i][j] = __ffma2_rn(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), sum[i][j]);
+      }
   }
+#pragma unroll
+  for (int i = 0; i < kR; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = sum[i][j].x + sum[i][j].y;
 }
 
-// acc[i][4 c + e] += sum over the 64 rows m of P[ty + (64 / R) i][m] B[m][4 tx + 64 c + e]
-template <int D, int R>
+// acc[i][4 c + e] += sum over the 64 rows m of P[ty + kGap i][m] B[m][4 tx + 64 c + e]
+template <int D, int R, int kGap>
 __device__ __forceinline__ void mix_tile(const float* P, const float* B, int ty, int tx,
                                          float (&acc)[R][D / 16]) {
-  constexpr int kR = R, kGap = kB / R;
+  constexpr int kR = R;
 #pragma unroll 4
   for (int m = 0; m < kB; m += 4) {
     float4 p[kR];
@@ -88,10 +100,13 @@ __device__ __forceinline__ void mix_tile(const float* P, const float* B, int ty,
 #pragma unroll
         for (int i = 0; i < kR; ++i) {
           const float w = mm == 0 ? p[i].x : mm == 1 ? p[i].y : mm == 2 ? p[i].z : p[i].w;
-          acc[i][4 * c] += w * y.x;
-          acc[i][4 * c + 1] += w * y.y;
-          acc[i][4 * c + 2] += w * y.z;
-          acc[i][4 * c + 3] += w * y.w;
+          float* o = acc[i] + 4 * c;
+          const float2 lo = __ffma2_rn(make_float2(w, w), make_float2(y.x, y.y), make_float2(o[0], o[1]));
+          const float2 hi = __ffma2_rn(make_float2(w, w), make_float2(y.z, y.w), make_float2(o[2], o[3]));
+          o[0] = lo.x;
+          o[1] = lo.y;
+          o[2] = hi.x;
+          o[3] = hi.y;
         }
       }
     }
@@ -121,21 +136,23 @@ __device__ __forceinline__ void store4(T* dst, float a, float b, float c, float 
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(a, b), pack2(c, d));
 }
 
-template <typename T, int D, int R>
-__global__ void __launch_bounds__(16 * kB / R) window_fwd_simt_kernel(const WindowArgs<T> a) {
-  constexpr int kR = R, kGap = kB / R, kN = 16 * kGap;
+template <typename T, int D, int kRows, int R>
+__global__ void __launch_bounds__(16 * kRows / R) window_fwd_simt_kernel(const WindowArgs<T> a) {
+  constexpr int kR = R, kGap = kRows / R, kN = 16 * kGap;
   extern __shared__ float sm[];
-  float *Q = sm, *K = Q + kB * kLd<D>, *V = K + kB * kLd<D>, *P = V + kB * kLd<D>;
+  float *Q = sm, *K = Q + kRows * kLd<D>, *V = K + kB * kLd<D>, *P = V + kB * kLd<D>;
   pdl_launch_dependents();
   pdl_wait();
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int b = blockIdx.y / a.w.nh, h = blockIdx.y % a.w.nh, hk = h / (a.w.nh / a.w.nkv);
   const int len = a.w.len(b), off = a.w.nk - a.w.nq;
   // the last tiles of a causal problem see the most keys: they start first
-  const int i0 = (gridDim.x - 1 - blockIdx.x) * kB;
+  const int i0 = (gridDim.x - 1 - blockIdx.x) * kRows;
   const int p0 = i0 + off;
-  const KeyTiles<kB> tiles(a.w, len, max(p0, 0), min(min(p0 + kB, a.w.nk) - 1, len - 1));
-  load_rows<D, T, kN>(Q, a.q.row(b, h, 0), a.q.sn, i0, max(0, -off), min(a.w.nq, len - off));
+  const KeyTiles<kB> tiles(a.w, len, max(p0, 0), min(min(p0 + kRows, a.w.nk) - 1, len - 1));
+  fetch_rows<D, kN, kRows>(Q, a.q.row(b, h, 0), a.q.sn, i0, max(0, -off), min(a.w.nq, len - off));
+  const float *k = a.k.row(b, hk, 0), *v = a.v.row(b, hk, 0);
+  if (tiles.count > 0) fetch_rows<D, kN, kB>(K, k, a.k.sn, tiles.tile(0) * kB, 0, len);
 
   float o[kR][D / 16], m[kR], l[kR];
 #pragma unroll
@@ -147,12 +164,12 @@ __global__ void __launch_bounds__(16 * kB / R) window_fwd_simt_kernel(const Wind
   }
   for (int t = 0; t < tiles.count; ++t) {
     const int j0 = tiles.tile(t) * kB;
+    // K's tile is there and V's is free; V's comes during the scores, K's next during P V
+    fetched();
     __syncthreads();
-    load_rows<D, T, kN>(K, a.k.row(b, hk, 0), a.k.sn, j0, 0, len);
-    load_rows<D, T, kN>(V, a.v.row(b, hk, 0), a.v.sn, j0, 0, len);
-    __syncthreads();
+    fetch_rows<D, kN, kB>(V, v, a.v.sn, j0, 0, len);
     float s[kR][4];
-    dot_tile<D>(Q, K, ty, tx, s);
+    dot_tile<D, kR, kGap>(Q, K, ty, tx, s);
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
       const int p = p0 + ty + kGap * i;
@@ -178,9 +195,12 @@ __global__ void __launch_bounds__(16 * kB / R) window_fwd_simt_kernel(const Wind
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) o[i][c] *= alpha;
     }
+    fetched();
     __syncthreads();
-    mix_tile<D>(P, V, ty, tx, o);
+    if (t + 1 < tiles.count) fetch_rows<D, kN, kB>(K, k, a.k.sn, tiles.tile(t + 1) * kB, 0, len);
+    mix_tile<D, kR, kGap>(P, V, ty, tx, o);
   }
+  fetched();  // (a block without keys still has Q on its way)
 #pragma unroll
   for (int i = 0; i < kR; ++i) {
     const int q = i0 + ty + kGap * i;
@@ -224,22 +244,24 @@ __global__ void __launch_bounds__(kThreads) window_delta_kernel(const WindowArgs
   if (lr == 0 && i < a.w.nq) a.delta[(long long)blockIdx.y * a.w.nq + i] = s;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) window_dq_simt_kernel(const WindowArgs<T> a) {
+template <typename T, int D, int kRows, int R>
+__global__ void __launch_bounds__(16 * kRows / R) window_dq_simt_kernel(const WindowArgs<T> a) {
+  constexpr int kR = R, kGap = kRows / R, kN = 16 * kGap;
   extern __shared__ float sm[];
-  float *Q = sm, *dO = Q + kB * kLd<D>, *K = dO + kB * kLd<D>, *V = K + kB * kLd<D>,
+  float *Q = sm, *dO = Q + kRows * kLd<D>, *K = dO + kRows * kLd<D>, *V = K + kB * kLd<D>,
         *S = V + kB * kLd<D>;
   pdl_launch_dependents();
   pdl_wait();
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int b = blockIdx.y / a.w.nh, h = blockIdx.y % a.w.nh, hk = h / (a.w.nh / a.w.nkv);
   const int len = a.w.len(b), off = a.w.nk - a.w.nq;
-  const int i0 = (gridDim.x - 1 - blockIdx.x) * kB;
+  const int i0 = (gridDim.x - 1 - blockIdx.x) * kRows;
   const int p0 = i0 + off;
-  const KeyTiles<kB> tiles(a.w, len, max(p0, 0), min(min(p0 + kB, a.w.nk) - 1, len - 1));
+  const KeyTiles<kB> tiles(a.w, len, max(p0, 0), min(min(p0 + kRows, a.w.nk) - 1, len - 1));
   const int lo = max(0, -off), hi = min(a.w.nq, len - off);
-  load_rows<D>(Q, a.q.row(b, h, 0), a.q.sn, i0, lo, hi);
-  load_rows<D>(dO, a.dO.row(b, h, 0), a.dO.sn, i0, lo, hi);
+  fetch_rows<D, kN, kRows>(Q, a.q.row(b, h, 0), a.q.sn, i0, lo, hi);
+  fetch_rows<D, kN, kRows>(dO, a.dO.row(b, h, 0), a.dO.sn, i0, lo, hi);
+  const float* v = a.v.row(b, hk, 0);
   float acc[kR][D / 16], lse[kR], delta[kR];
 #pragma unroll
   for (int i = 0; i < kR; ++i) {
@@ -253,12 +275,13 @@ __global__ void __launch_bounds__(kThreads) window_dq_simt_kernel(const WindowAr
   for (int t = 0; t < tiles.count; ++t) {
     const int j0 = tiles.tile(t) * kB;
     __syncthreads();
-    load_rows<D>(K, a.k.row(b, hk, 0), a.k.sn, j0, 0, len);
-    load_rows<D>(V, a.v.row(b, hk, 0), a.v.sn, j0, 0, len);
+    fetch_rows<D, kN, kB>(K, a.k.row(b, hk, 0), a.k.sn, j0, 0, len);
+    if (t == 0) fetch_rows<D, kN, kB>(V, v, a.v.sn, j0, 0, len);
+    fetched();
     __syncthreads();
     float s[kR][4], dp[kR][4];
-    dot_tile<D>(Q, K, ty, tx, s);
-    dot_tile<D>(dO, V, ty, tx, dp);
+    dot_tile<D, kR, kGap>(Q, K, ty, tx, s);
+    dot_tile<D, kR, kGap>(dO, V, ty, tx, dp);
 #pragma unroll
     for (int i = 0; i < kR; ++i)
 #pragma unroll
@@ -269,8 +292,11 @@ __global__ void __launch_bounds__(kThreads) window_dq_simt_kernel(const WindowAr
             see ? expf(s[i][j] * a.scale - lse[i]) * (dp[i][j] - delta[i]) : 0.f;
       }
     __syncthreads();
-    mix_tile<D>(S, K, ty, tx, acc);
+    // V's next tile comes during dS K
+    if (t + 1 < tiles.count) fetch_rows<D, kN, kB>(V, v, a.v.sn, tiles.tile(t + 1) * kB, 0, len);
+    mix_tile<D, kR, kGap>(S, K, ty, tx, acc);
   }
+  fetched();
 #pragma unroll
   for (int i = 0; i < kR; ++i) {
     const int q = i0 + ty + kGap * i;
@@ -283,22 +309,23 @@ __global__ void __launch_bounds__(kThreads) window_dq_simt_kernel(const WindowAr
   }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) window_dkdv_simt_kernel(const WindowArgs<T> a) {
+template <typename T, int D, int kRows, int R>
+__global__ void __launch_bounds__(16 * kRows / R) window_dkdv_simt_kernel(const WindowArgs<T> a) {
+  constexpr int kR = R, kGap = kRows / R, kN = 16 * kGap;
   extern __shared__ float sm[];
-  float *K = sm, *V = K + kB * kLd<D>, *Q = V + kB * kLd<D>, *dO = Q + kB * kLd<D>,
-        *P = dO + kB * kLd<D>, *S = P + kB * kLdP;
+  float *K = sm, *V = K + kRows * kLd<D>, *Q = V + kRows * kLd<D>, *dO = Q + kB * kLd<D>,
+        *P = dO + kB * kLd<D>, *S = P + kRows * kLdP;
   __shared__ float lse[kB], delta[kB];
   pdl_launch_dependents();
   pdl_wait();
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int b = blockIdx.y / a.w.nkv, hk = blockIdx.y % a.w.nkv, group = a.w.nh / a.w.nkv;
   const int len = a.w.len(b), off = a.w.nk - a.w.nq;
-  const int j0 = blockIdx.x * kB;
+  const int j0 = blockIdx.x * kRows;
   int i0, nq;
-  query_range(a.w, len, j0, min(j0 + kB, a.w.nk) - 1, i0, nq);
-  load_rows<D>(K, a.k.row(b, hk, 0), a.k.sn, j0, 0, len);
-  load_rows<D>(V, a.v.row(b, hk, 0), a.v.sn, j0, 0, len);
+  query_range(a.w, len, j0, min(j0 + kRows, a.w.nk) - 1, i0, nq);
+  fetch_rows<D, kN, kRows>(K, a.k.row(b, hk, 0), a.k.sn, j0, 0, len);
+  fetch_rows<D, kN, kRows>(V, a.v.row(b, hk, 0), a.v.sn, j0, 0, len);
   float dk[kR][D / 16], dv[kR][D / 16];
 #pragma unroll
   for (int i = 0; i < kR; ++i)
@@ -307,18 +334,19 @@ __global__ void __launch_bounds__(kThreads) window_dkdv_simt_kernel(const Window
   for (int h = hk * group; h < (hk + 1) * group; ++h) {
     for (int i1 = i0; i1 < i0 + nq; i1 += kB) {
       __syncthreads();
-      load_rows<D>(Q, a.q.row(b, h, 0), a.q.sn, i1, i1, i0 + nq);
-      load_rows<D>(dO, a.dO.row(b, h, 0), a.dO.sn, i1, i1, i0 + nq);
-      if (threadIdx.x < kB) {
-        const int i = i1 + threadIdx.x;
+      fetch_rows<D, kN, kB>(Q, a.q.row(b, h, 0), a.q.sn, i1, i1, i0 + nq);
+      fetch_rows<D, kN, kB>(dO, a.dO.row(b, h, 0), a.dO.sn, i1, i1, i0 + nq);
+      for (int u = threadIdx.x; u < kB; u += kN) {
+        const int i = i1 + u;
         const long long at = ((long long)b * a.w.nh + h) * a.w.nq + i;
-        lse[threadIdx.x] = i < i0 + nq ? a.lse[at] : 0.f;
-        delta[threadIdx.x] = i < i0 + nq ? a.delta[at] : 0.f;
+        lse[u] = i < i0 + nq ? a.lse[at] : 0.f;
+        delta[u] = i < i0 + nq ? a.delta[at] : 0.f;
       }
+      fetched();
       __syncthreads();
       float s[kR][4], dp[kR][4];  // rows: keys, columns: queries
-      dot_tile<D>(K, Q, ty, tx, s);
-      dot_tile<D>(V, dO, ty, tx, dp);
+      dot_tile<D, kR, kGap>(K, Q, ty, tx, s);
+      dot_tile<D, kR, kGap>(V, dO, ty, tx, dp);
 #pragma unroll
       for (int i = 0; i < kR; ++i)
 #pragma unroll
@@ -330,10 +358,11 @@ __global__ void __launch_bounds__(kThreads) window_dkdv_simt_kernel(const Window
           S[(ty + kGap * i) * kLdP + c] = see && !sees_one(a.w, len, i1 + c + off) ? p * (dp[i][j] - delta[c]) : 0.f;
         }
       __syncthreads();
-      mix_tile<D>(P, dO, ty, tx, dv);
-      mix_tile<D>(S, Q, ty, tx, dk);
+      mix_tile<D, kR, kGap>(P, dO, ty, tx, dv);
+      mix_tile<D, kR, kGap>(S, Q, ty, tx, dk);
     }
   }
+  fetched();  // (a block that no query sees still has K and V on their way)
 #pragma unroll
   for (int i = 0; i < kR; ++i) {
     const int j = j0 + ty + kGap * i;
@@ -348,38 +377,57 @@ __global__ void __launch_bounds__(kThreads) window_dkdv_simt_kernel(const Window
   }
 }
 
-template <typename T, int D, int R>
+// Tiles of 16 rows, with twice the threads a score, rather than 32, where that leaves no more
+// than three CTAs per SM, which all run at once (heads of 64).  4 x 4 heads of 400 positions, 121
+// visible: forward 22 us against 27, backward 80 against 98; 4 x 8 heads: 40 against 30, 128
+// against 122.  Heads of 128 fill shared memory: 4 x 4 heads 47 against 37, 154 against 148.
+template <int D>
+bool few_rows(int rows, int heads) {
+  return D == 64 && (long long)((rows + 15) / 16) * heads <= 3LL * device_sm_count();
+}
+
+template <typename T, int D, int kRows, int R>
 cudaError_t fwd(const WindowArgs<T>& a, cudaStream_t st) {
-  constexpr int smem = (3 * kB * kLd<D> + kB * kLdP) * 4;
-  auto kern = window_fwd_simt_kernel<T, D, R>;
+  constexpr int smem = ((2 * kB + kRows) * kLd<D> + kRows * kLdP) * 4;
+  auto kern = window_fwd_simt_kernel<T, D, kRows, R>;
   const cudaError_t e = set_max_dynamic_smem((const void*)kern, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((a.w.nq + kB - 1) / kB, a.w.B * a.w.nh), dim3(16 * kB / R), smem, st, a);
+  return launch_pdl(kern, dim3((a.w.nq + kRows - 1) / kRows, a.w.B * a.w.nh), dim3(16 * kRows / R), smem, st, a);
 }
 
 template <typename T, int D>
 cudaError_t fwd(const WindowArgs<T>& a, cudaStream_t st) {
-  const long long ctas = (long long)((a.w.nq + kB - 1) / kB) * a.w.B * a.w.nh;
-  return ctas <= device_sm_count() ? fwd<T, D, 2>(a, st) : fwd<T, D, 4>(a, st);
+  return few_rows<D>(a.w.nq, a.w.B * a.w.nh) ? fwd<T, D, 16, 2>(a, st) : fwd<T, D, 32, 4>(a, st);
+}
+
+template <typename T, int D, int kRows, int R>
+cudaError_t dq(const WindowArgs<T>& a, cudaStream_t st) {
+  constexpr int smem = ((2 * kB + 2 * kRows) * kLd<D> + kRows * kLdP) * 4;
+  auto kern = window_dq_simt_kernel<T, D, kRows, R>;
+  const cudaError_t e = set_max_dynamic_smem((const void*)kern, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3((a.w.nq + kRows - 1) / kRows, a.w.B * a.w.nh), dim3(16 * kRows / R), smem, st, a);
+}
+
+template <typename T, int D, int kRows, int R>
+cudaError_t dkdv(const WindowArgs<T>& a, cudaStream_t st) {
+  constexpr int smem = ((2 * kB + 2 * kRows) * kLd<D> + 2 * kRows * kLdP) * 4;
+  auto kern = window_dkdv_simt_kernel<T, D, kRows, R>;
+  const cudaError_t e = set_max_dynamic_smem((const void*)kern, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3((a.w.nk + kRows - 1) / kRows, a.w.B * a.w.nkv), dim3(16 * kRows / R), smem, st, a);
 }
 
 template <typename T, int D>
 cudaError_t bwd(const WindowArgs<T>& a, cudaStream_t st) {
-  constexpr int smem_dq = (4 * kB * kLd<D> + kB * kLdP) * 4, smem_kv = smem_dq + kB * kLdP * 4;
   constexpr int PER = D / kVec<T>, LANES = PER < 16 ? PER : 16;
-  auto dq = window_dq_simt_kernel<T, D>;
-  auto dkdv = window_dkdv_simt_kernel<T, D>;
-  cudaError_t e = set_max_dynamic_smem((const void*)dq, smem_dq);
-  if (e == cudaSuccess) e = set_max_dynamic_smem((const void*)dkdv, smem_kv);
   const int rows = kThreads / LANES;
-  if (e == cudaSuccess)
-    e = launch_pdl(window_delta_kernel<T, D>, dim3((a.w.nq + rows - 1) / rows, a.w.B * a.w.nh),
-                   dim3(kThreads), 0, st, a);
-  if (e == cudaSuccess)
-    e = launch_pdl(dq, dim3((a.w.nq + kB - 1) / kB, a.w.B * a.w.nh), dim3(kThreads), smem_dq, st, a);
-  if (e == cudaSuccess)
-    e = launch_pdl(dkdv, dim3((a.w.nk + kB - 1) / kB, a.w.B * a.w.nkv), dim3(kThreads), smem_kv, st, a);
-  return e;
+  cudaError_t e = launch_pdl(window_delta_kernel<T, D>, dim3((a.w.nq + rows - 1) / rows, a.w.B * a.w.nh),
+                             dim3(kThreads), 0, st, a);
+  if (e != cudaSuccess) return e;
+  e = few_rows<D>(a.w.nq, a.w.B * a.w.nh) ? dq<T, D, 16, 2>(a, st) : dq<T, D, 32, 4>(a, st);
+  if (e != cudaSuccess) return e;
+  return few_rows<D>(a.w.nk, a.w.B * a.w.nkv) ? dkdv<T, D, 16, 2>(a, st) : dkdv<T, D, 32, 4>(a, st);
 }
 
 }  // namespace

@@ -236,3 +236,28 @@ def test_windows_wider_than_an_int():
     win = B.window_of(q, q, -2 ** 32, -2 ** 33, 0)
     assert (win.window_left, win.window_right, win.sinks) == (-1, -1, 0)
     assert B.window_of(q, q, 0, 0, -2 ** 32).sinks == -1  # refused by the calls
+
+
+def test_tensors_of_another_type_than_the_problem_s():
+    """A problem made for fp32 rows reads twice the bytes of bf16 ones: past their end."""
+    import torch
+
+    from vision_transformer_attention_psapackqkv_gb300 import binding as B
+
+    t = {torch.float32: (torch.zeros(1, 4, 8, 64), torch.zeros(1, 2, 8, 64))}
+    t[torch.bfloat16] = tuple(x.bfloat16() for x in t[torch.float32])
+    cos, w, ws = torch.zeros(8, 32), torch.zeros(64), torch.zeros(1 << 20, dtype=torch.uint8)
+    lse, lens, u8 = torch.zeros(1, 4, 8), torch.zeros(1, dtype=torch.int32), torch.uint8
+    cache = tuple(torch.zeros(1, 2, 8, n, dtype=e) for n, e in ((32, u8), (2, torch.bfloat16)) * 2)
+    for mine, other in ((torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)):
+        q, k = t[mine]
+        q1, p = q[:, :, :1], B.norm_rope_of(*t[other], cos)
+        win, win1 = B.window_of(*t[other]), B.window_of(t[other][0][:, :, :1], t[other][1])
+        for call in (lambda: B.psa_qk_norm_rope_fwd(q, k, w, w, cos, cos, None, q, k, p),
+                     lambda: B.psa_qk_norm_rope_bwd(q, k, w, w, cos, cos, None, q, k, q, k, w, w, ws, p),
+                     lambda: B.psa_window_attn_fwd(q, k, k, None, q, None, win, 0.1),
+                     lambda: B.psa_window_attn_bwd(q, k, k, q, q, lse, None, q, k, k, ws, win, 0.1),
+                     lambda: B.psa_window_attn_decode(q1, k, k, lens, q1, ws, win1, 0.1),
+                     lambda: B.psa_window_attn_decode_kv4(q1, *cache, lens, q1, ws, win1, 0.1)):
+            with pytest.raises(TypeError, match="problem"):
+                call()

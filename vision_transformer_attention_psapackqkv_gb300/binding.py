@@ -288,6 +288,13 @@ def _dense(t, shape, dtype, what: str):
     return t.data_ptr()
 
 
+def _type_of(p, t):
+    """The type of t, which problem p has to have been made for: its kernels read rows of that type."""
+    if dtype_code(t) != p.dtype:
+        raise TypeError(f"the problem was made for another type than {t.dtype}")
+    return t.dtype
+
+
 def _on_device(fn: str, tensors, stream, *args):
     """Calls entry point `fn` with its arguments on the tensors' one CUDA device."""
     import torch
@@ -329,7 +336,7 @@ def norm_rope_of(q, k, cos, eps: float = 1e-6, interleaved: bool = False) -> Psa
 def _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p):
     import torch
 
-    B, N, d, f32, t = p.B, p.N, p.head_dim, torch.float32, q.dtype
+    B, N, d, f32, t = p.B, p.N, p.head_dim, torch.float32, _type_of(p, q)
     table, by_q, by_k = (p.max_pos, p.rotary_dim // 2), (B, p.num_heads, N, d), (B, p.num_kv_heads, N, d)
     return by_q, by_k, (_rows(q, by_q, t, "q"), _rows(k, by_k, t, "k"), _dense(q_weight, (d,), f32, "q_weight"),
                         _dense(k_weight, (d,), f32, "k_weight"), _dense(cos, table, f32, "cos"),
@@ -386,7 +393,7 @@ def psa_window_attn_fwd(q, k, v, lens, o, lse, win: PsaWindow, scale: float, str
     import torch
 
     by_q, by_k = _window_shapes(win)
-    t = q.dtype
+    t = _type_of(win, q)
     _on_device("psa_window_attn_fwd", (q, k, v, lens, o, lse), stream, _rows(q, by_q, t, "q"), _rows(k, by_k, t, "k"),
                _rows(v, by_k, t, "v"), _lens(lens, win), _rows(o, by_q, t, "o"),
                _dense(lse, by_q[:3], torch.float32, "lse"), win, scale)
@@ -401,7 +408,7 @@ def psa_window_attn_bwd(q, k, v, o, do, lse, lens, dq, dk, dv, workspace, win: P
     import torch
 
     by_q, by_k = _window_shapes(win)
-    t = q.dtype
+    t = _type_of(win, q)
     _on_device("psa_window_attn_bwd", (q, k, v, o, do, lse, lens, dq, dk, dv, workspace), stream,
                _rows(q, by_q, t, "q"), _rows(k, by_k, t, "k"), _rows(v, by_k, t, "v"), _rows(o, by_q, t, "o"),
                _rows(do, by_q, t, "do"), _dense(lse, by_q[:3], torch.float32, "lse"), _lens(lens, win),
@@ -415,7 +422,7 @@ def psa_window_attn_decode_workspace_size(win: PsaWindow) -> int:
 
 def psa_window_attn_decode(q, k_cache, v_cache, lens, o, workspace, win: PsaWindow, scale: float, stream=None):
     by_q, by_k = _window_shapes(win)
-    t = q.dtype
+    t = _type_of(win, q)
     _on_device("psa_window_attn_decode", (q, k_cache, v_cache, lens, o, workspace), stream, _rows(q, by_q, t, "q"),
                _rows(k_cache, by_k, t, "k_cache"), _rows(v_cache, by_k, t, "v_cache"), _lens(lens, win),
                _rows(o, by_q, t, "o"), *_workspace(workspace, "psa_window_attn_decode"), win, scale)
@@ -469,8 +476,9 @@ def psa_window_attn_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, lens, o,
                                scale: float, stream=None):
     cache = (k_codes, k_scales, v_codes, v_scales)
     by_q, (B, nkv, max_len, d) = _window_shapes(win)
-    _on_device("psa_window_attn_decode_kv4", (q, *cache, lens, o, workspace), stream, _rows(q, by_q, q.dtype, "q"),
-               *_kv4(*cache, B, nkv, max_len, d), _lens(lens, win), _rows(o, by_q, q.dtype, "o"),
+    t = _type_of(win, q)
+    _on_device("psa_window_attn_decode_kv4", (q, *cache, lens, o, workspace), stream, _rows(q, by_q, t, "q"),
+               *_kv4(*cache, B, nkv, max_len, d), _lens(lens, win), _rows(o, by_q, t, "o"),
                *_workspace(workspace, "psa_window_attn_decode_kv4"), win, scale)
 
 

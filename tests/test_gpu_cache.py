@@ -202,3 +202,22 @@ def test_a_nan_that_is_seen_stays_one(rows):
     for o, was in ((_decode(q, k, v, lens, -1, 0, 0.2), clean), (_decode4(q, cache, lens, -1, 0, 0.2), clean4)):
         # (head 2 shares its products with head 3, and the steps at which maxima move)
         assert o[1, 3].isnan().all() and torch.equal(o[1, :2], was[1, :2]) and o[1, 2].isfinite().all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nh", [4, 24])
+@pytest.mark.parametrize("size", [10.0, 100.0, 1000.0])
+def test_4_bit_scores_of_large_one_signed_queries(size, nh, d):
+    """Half of a query's channels are large and of one sign, and meet one large code in every group, so
+    that all keys' scores are large and alike; what tells them apart is in the other half."""
+    Bn, rows, G = 32, 8, d // 32
+    large = torch.arange(d, device="cuda") % 32 < 16
+    q = torch.where(large, size, 0.1 * _randn(51, Bn, nh, 1, d)).to(BF16)
+    k = torch.where(large, 0.0, (7 * _randn(52, Bn, 1, rows, d)).round().clamp(-7, 7)).unflatten(-1, (G, 32))
+    k.scatter_(-1, torch.randint(0, 16, (Bn, 1, rows, G, 1), generator=_gen(53), device="cuda"), 7.0)
+    step = 1.0 + torch.randint(0, 2, (Bn, 1, rows, 1, 1), generator=_gen(54), device="cuda")
+    k = (k * torch.cat([step, 3 - step] * (G // 2), 3)).flatten(-2)
+    cache = quantise(k) + quantise(_randn(55, Bn, 1, rows, d))
+    assert torch.equal(dequantise(*cache[:2]), k.double())
+    lens, scale = [rows] * Bn, d ** -0.5
+    within(_decode4(q, cache, lens, -1, 0, scale), *_reference(q, k, dequantise(*cache[2:]), lens, -1, 0, scale), "o")

@@ -25,16 +25,16 @@
 //
 // 4 bits: what bounds the kernel there is the integer work of widening codes, so it is kept
 // small.  K: a code at bits 0-3 or 4-7 of a 16-bit half becomes the fp16 number 1024 + n or
-// 64 + n by one masked OR, without a shift; the query, in fp16 too (scaled by a power of two
-// to a maximum of 1), takes the offsets off again: the fp32 sums start at minus the query's sums
-// times 1032 and 72, which costs them 8 of their 24 bits, far less than rounding P to bf16.
-// V: 128 + n in bf16 (P times a scale needs its range), shifted on the multipliers, less 136,
-// exactly; its sums run over all keys, where subtracting at the end would leave nothing.  A
-// key's scale multiplies its fp32 partial score of each group of 32 channels; a value's scale
-// multiplies the probability before it is rounded to bf16.
+// 64 + n by one masked OR, without a shift, and n - 8 by an exact subtraction of two at once.
+// (Sums that start at minus 1032 and 72 times the query's sums would do without it, but lose 8 of
+// their 24 bits: large keys that differ little then stand off by more than P's rounding.)  The
+// query is in fp16 too, scaled by a power of two to a maximum of 1 .. 2.  V: 128 + n in bf16 (P
+// times a scale needs its range), shifted on the multipliers, less 136, exactly.  A key's scale
+// multiplies its fp32 partial score of each group of 32 channels; a value's scale multiplies the
+// probability before it is rounded to bf16.
 //
 // Measured: bf16, 32 sequences of up to 8192 keys, 4096 visible, 32 heads of 128 on 8: 84 us (5.9
-// TB/s, 0.89 of the copy bandwidth); 4 bits, 16 sequences of up to 32768 keys: 111 us (3.5 TB/s,
+// TB/s, 0.89 of the copy bandwidth); 4 bits, 16 sequences of up to 32768 keys: 110 us (3.5 TB/s,
 // 0.52; the integer pipe is busy 65 % of the time, tensor instructions 19 %).  One sequence of
 // 1024 visible keys: 5.5 us with the join.
 #include <algorithm>
@@ -52,16 +52,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kLongBlock = 32;   // most keys that a warp takes at a time
 constexpr float kLog2eD = 1.4426950408889634074f;
 
-// d = a b + c (m16n8k16, fp32 sums); c's two values are for the columns of a lane, in both its
-// rows.
+// d += a b (m16n8k16, fp32 sums)
 #define PSA_MMA(NAME, TYPE)                                                                        \
-  __device__ __forceinline__ void NAME(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,       \
-                                       uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1) { \
-    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                     \
-        ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"                 \
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                           \
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));                 \
-  }                                                                                                \
   __device__ __forceinline__ void NAME(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,       \
                                        uint32_t a3, uint32_t b0, uint32_t b1) {                    \
     asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                     \
@@ -80,6 +72,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+// n - 8, n' - 8 in fp16 for the nibbles n, n' at bits 0 and 16 (High: 4 and 20)
+template <bool High>
+__device__ __forceinline__ uint32_t nibbles_fp16(uint32_t x) {
+  const uint32_t u = High ? (x & 0x00F000F0u) | 0x54005400u : (x & 0x000F000Fu) | 0x64006400u;
+  const uint32_t k = High ? 0x54805480u : 0x64086408u;  // 72, 1032
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 // n - 8, n' - 8 in bf16 for the nibbles n, n' at bits 4 i and 4 i + 16
 template <int i>
 __device__ __forceinline__ uint32_t nibbles_bf16(uint32_t x) {
@@ -117,12 +117,6 @@ __device__ __forceinline__ uint4 shared16(uint32_t at) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
   return v;
 }
-__device__ __forceinline__ float2 shared8(uint32_t at) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
-  return v;
-}
-
 // The visible rows of sequence b: blocks 0 .. sink - 1, then first .. (count in all).
 template <int kBlock>
 struct Blocks {
@@ -265,14 +259,12 @@ struct Cache<D, HT, true, kShort> {
   const char *kp, *vp, *ksp, *vsp;
   int last;
   uint32_t k[U][2][G], v[U][4][W], ks[U][2][W], vs[U][2][W];  // codes; scales of keys g and g + 8
-  // The query, and minus what the codes' offsets add to the sums of heads 2 t and 2 t + 1, lie in
-  // shared memory, each lane's at its place: they are read once per step, and the registers
-  // hold more loads instead.
+  // The query lies in shared memory, each lane's part at its place: it is read once per step, and
+  // the registers hold more loads instead.
   struct Shared {
     uint4 q[HT][G][32];
-    float2 q0[HT][G][32];
   };
-  uint32_t q_at, q0_at;
+  uint32_t q_at;
 
   __device__ __forceinline__ Cache(const DecodeArgs& a, int b, int h, int lane) {
     const long long base = ((long long)b * a.w.nkv + h) * a.w.nk;
@@ -287,7 +279,6 @@ struct Cache<D, HT, true, kShort> {
   // (every warp writes the same values)
   __device__ __forceinline__ void prepare(uint32_t (&q)[HT][D / 8], float (&up)[HT][2], int lane, Shared& sh) {
     q_at = smem_addr(&sh.q[0][0][lane]);
-    q0_at = smem_addr(&sh.q0[0][0][lane]);
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
       float m = 0.f;
@@ -302,20 +293,13 @@ struct Cache<D, HT, true, kShort> {
       const float mine = __uint_as_float(e << 23);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        float s = 0.f;  // this lane's 8 channels of head lane / 4, then its four lanes'
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t& x = q[ht][4 * g + i];
           const __half2 y = __floats2half2_rn(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
           x = *reinterpret_cast<const uint32_t*>(&y);
-          s -= (i & 1 ? 72.f : 1032.f) * (__low2float(y) + __high2float(y));
         }
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        const float o0 = __shfl_sync(0xffffffffu, s, 8 * (lane & 3));
-        const float o1 = __shfl_sync(0xffffffffu, s, 8 * (lane & 3) + 4);
         sh.q[ht][g][lane] = make_uint4(q[ht][4 * g], q[ht][4 * g + 1], q[ht][4 * g + 2], q[ht][4 * g + 3]);
-        sh.q0[ht][g][lane] = make_float2(o0, o1);
       }
       up[ht][0] = __shfl_sync(0xffffffffu, mine, 8 * (lane & 3));
       up[ht][1] = __shfl_sync(0xffffffffu, mine, 8 * (lane & 3) + 4);
@@ -388,12 +372,8 @@ struct Cache<D, HT, true, kShort> {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       uint4 q[HT];
-      float2 o[HT];
 #pragma unroll
-      for (int ht = 0; ht < HT; ++ht) {
-        q[ht] = shared16(q_at + (ht * G + g) * 512);
-        o[ht] = shared8(q0_at + (ht * G + g) * 256);
-      }
+      for (int ht = 0; ht < HT; ++ht) q[ht] = shared16(q_at + (ht * G + g) * 512);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         // words of a = 2 t come first, those of a = 2 t + 1 after them
@@ -401,15 +381,13 @@ struct Cache<D, HT, true, kShort> {
         const uint32_t x = __byte_perm(k[u][0][g / 2], k[u][0][W + g / 2], sel);
         const uint32_t y = __byte_perm(k[u][1][g / 2], k[u][1][W + g / 2], sel);
         const uint32_t x8 = x >> 8, y8 = y >> 8;
-        const uint32_t a[8] = {(x & 0x000F000Fu) | 0x64006400u,  (y & 0x000F000Fu) | 0x64006400u,
-                               (x & 0x00F000F0u) | 0x54005400u,  (y & 0x00F000F0u) | 0x54005400u,
-                               (x8 & 0x000F000Fu) | 0x64006400u, (y8 & 0x000F000Fu) | 0x64006400u,
-                               (x8 & 0x00F000F0u) | 0x54005400u, (y8 & 0x00F000F0u) | 0x54005400u};
+        const uint32_t a[8] = {nibbles_fp16<false>(x),  nibbles_fp16<false>(y),  nibbles_fp16<true>(x),  nibbles_fp16<true>(y),
+                               nibbles_fp16<false>(x8), nibbles_fp16<false>(y8), nibbles_fp16<true>(x8), nibbles_fp16<true>(y8)};
         const float s0 = scale_of(ks[u][0], g), s1 = scale_of(ks[u][1], g);
 #pragma unroll
         for (int ht = 0; ht < HT; ++ht) {
-          float c[4];
-          mma16816_f16(c, a[0], a[1], a[2], a[3], q[ht].x, q[ht].y, o[ht].x, o[ht].y);
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816_f16(c, a[0], a[1], a[2], a[3], q[ht].x, q[ht].y);
           mma16816_f16(c, a[4], a[5], a[6], a[7], q[ht].z, q[ht].w);
           s[u][ht][0] += c[0] * s0;
           s[u][ht][1] += c[1] * s0;

@@ -383,8 +383,8 @@ psa_status_t psa_kv4_read(const void *k_codes, const void *k_scales, const void 
 /* psa_window_attn_decode over a cache held in 4 bits (p.n_k rows, p.dtype that of q and
  * o: bf16).  The codes' values enter the products exactly; scales multiply fp32 sums
  * (keys) and probabilities (values; rounded to bf16 after it).  For the products with keys
- * q is held in fp16 relative to its largest channel: a channel loses at most 2^-25 of
- * that, nothing down to 2^-17 of it. */
+ * each group of 32 channels of q is held in fp16 relative to its largest one: a channel
+ * loses at most 2^-25 of that, nothing down to 2^-17 of it. */
 psa_status_t psa_window_attn_decode_kv4(psa_rows_t q, const void *k_codes, const void *k_scales,
                                         const void *v_codes, const void *v_scales,
                                         const int *lens, psa_rows_t o, void *workspace,

@@ -221,3 +221,16 @@ def test_4_bit_scores_of_large_one_signed_queries(size, nh, d):
     assert torch.equal(dequantise(*cache[:2]), k.double())
     lens, scale = [rows] * Bn, d ** -0.5
     within(_decode4(q, cache, lens, -1, 0, scale), *_reference(q, k, dequantise(*cache[2:]), lens, -1, 0, scale), "o")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nh", [4, 24])
+@pytest.mark.parametrize("e", [4, 12, 40])
+def test_4_bit_scores_of_groups_of_unlike_sizes(e, nh, d):
+    """Channels that are large in the queries are small in the keys, and the other way round."""
+    rows, lens, scale = 600, [600, 391], d ** -0.5
+    up = torch.where(torch.arange(d, device="cuda") // 32 % 2 == 0, 2.0 ** e, 2.0 ** -e)
+    q = (_randn(61, 2, nh, 1, d) * up).to(BF16)
+    cache = quantise(_randn(62, 2, 2, rows, d) / up) + quantise(_randn(63, 2, 2, rows, d))
+    within(_decode4(q, cache, lens, -1, 0, scale),
+           *_reference(q, dequantise(*cache[:2]), dequantise(*cache[2:]), lens, -1, 0, scale), "o")

@@ -28,14 +28,16 @@
 // 64 + n by one masked OR, without a shift, and n - 8 by an exact subtraction of two at once.
 // (Sums that start at minus 1032 and 72 times the query's sums would do without it, but lose 8 of
 // their 24 bits: large keys that differ little then stand off by more than P's rounding.)  The
-// query is in fp16 too, scaled by a power of two to a maximum of 1 .. 2.  V: 128 + n in bf16 (P
-// times a scale needs its range), shifted on the multipliers, less 136, exactly.  A key's scale
-// multiplies its fp32 partial score of each group of 32 channels; a value's scale multiplies the
-// probability before it is rounded to bf16.
+// query is in fp16 too, each group of 32 channels scaled by a power of two of its own to a
+// maximum of 1 .. 2, so that what is lost is at most 2^-25 of the group's largest channel; bf16's
+// 8 bits fit down to 2^-17 of it.  V: 128 + n in bf16 (P times a scale needs its range), shifted on the
+// multipliers, less 136, exactly.  A key's scale, times the query's power of two, multiplies its
+// fp32 partial score of each group; a value's scale multiplies the probability before it is
+// rounded to bf16.
 //
 // Measured: bf16, 32 sequences of up to 8192 keys, 4096 visible, 32 heads of 128 on 8: 84 us (5.9
-// TB/s, 0.89 of the copy bandwidth); 4 bits, 16 sequences of up to 32768 keys: 110 us (3.5 TB/s,
-// 0.52; the integer pipe is busy 65 % of the time, tensor instructions 19 %).  One sequence of
+// TB/s, 0.89 of the copy bandwidth); 4 bits, 16 sequences of up to 32768 keys: 114 us (3.4 TB/s,
+// 0.51; the integer pipe is busy 65 % of the time, tensor instructions 19 %).  One sequence of
 // 1024 visible keys: 5.5 us with the join.
 #include <algorithm>
 
@@ -117,6 +119,12 @@ __device__ __forceinline__ uint4 shared16(uint32_t at) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
   return v;
 }
+__device__ __forceinline__ float2 shared8(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+  return v;
+}
+
 // The visible rows of sequence b: blocks 0 .. sink - 1, then first .. (count in all).
 template <int kBlock>
 struct Blocks {
@@ -156,13 +164,11 @@ struct Cache<D, HT, false, kShort> {
   }
   uint32_t q[HT][D / 8];
   struct Shared {};
-  __device__ __forceinline__ void prepare(const uint32_t (&q_)[HT][D / 8], float (&up)[HT][2], int, Shared&) {
+  __device__ __forceinline__ void prepare(const uint32_t (&q_)[HT][D / 8], int, Shared&) {
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) q[ht][i] = q_[ht][i];
-#pragma unroll
-    for (int ht = 0; ht < HT; ++ht) up[ht][0] = up[ht][1] = 1.f;
   }
   __device__ __forceinline__ int row(int j) const { return kShort ? min(j, last) : j; }
   __device__ __forceinline__ void load_k(int j0, int lane) {
@@ -259,12 +265,14 @@ struct Cache<D, HT, true, kShort> {
   const char *kp, *vp, *ksp, *vsp;
   int last;
   uint32_t k[U][2][G], v[U][4][W], ks[U][2][W], vs[U][2][W];  // codes; scales of keys g and g + 8
-  // The query lies in shared memory, each lane's part at its place: it is read once per step, and
-  // the registers hold more loads instead.
+  // The query, and what each of its groups has been scaled down by for heads 2 t and 2 t + 1, lie in
+  // shared memory, each lane's at its place: they are read once per step, and the registers
+  // hold more loads instead.
   struct Shared {
     uint4 q[HT][G][32];
+    float2 up[HT][G][32];
   };
-  uint32_t q_at;
+  uint32_t q_at, up_at;
 
   __device__ __forceinline__ Cache(const DecodeArgs& a, int b, int h, int lane) {
     const long long base = ((long long)b * a.w.nkv + h) * a.w.nk;
@@ -275,35 +283,37 @@ struct Cache<D, HT, true, kShort> {
     vsp = static_cast<const char*>(a.vscales) + (base + g) * (2 * G);
     last = a.w.nk - 1;
   }
-  // The query in fp16, scaled to a maximum of 1 .. 2, and what that has to be undone by.
+  // The query in fp16, each group scaled to a maximum of 1 .. 2, and what that has to be undone by.
   // (every warp writes the same values)
-  __device__ __forceinline__ void prepare(uint32_t (&q)[HT][D / 8], float (&up)[HT][2], int lane, Shared& sh) {
+  __device__ __forceinline__ void prepare(const uint32_t (&q)[HT][D / 8], int lane, Shared& sh) {
     q_at = smem_addr(&sh.q[0][0][lane]);
+    up_at = smem_addr(&sh.up[0][0][lane]);
 #pragma unroll
-    for (int ht = 0; ht < HT; ++ht) {
-      float m = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(q[ht][i] << 16)), fabsf(__uint_as_float(q[ht][i] & 0xffff0000u))));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      // powers of two: 2^-e and 2^e for m in 2^e .. 2^(e + 1), both normal numbers
-      const uint32_t e = min(max(__float_as_uint(m) >> 23, 1u), 253u);
-      const float down = __uint_as_float((254u - e) << 23);
-      const float mine = __uint_as_float(e << 23);
+    for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
       for (int g = 0; g < G; ++g) {
+        float m = 0.f;  // of this lane's 8 channels of head lane / 4, then of its four lanes'
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(q[ht][4 * g + i] << 16)),
+                             fabsf(__uint_as_float(q[ht][4 * g + i] & 0xffff0000u))));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        // powers of two: 2^-e and 2^e for m in 2^e .. 2^(e + 1), both normal numbers
+        const uint32_t e = min(max(__float_as_uint(m) >> 23, 1u), 253u);
+        const float down = __uint_as_float((254u - e) << 23);
+        const float mine = __uint_as_float(e << 23);
+        uint32_t y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t& x = q[ht][4 * g + i];
-          const __half2 y = __floats2half2_rn(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
-          x = *reinterpret_cast<const uint32_t*>(&y);
+          const uint32_t x = q[ht][4 * g + i];
+          const __half2 h = __floats2half2_rn(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
+          y[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        sh.q[ht][g][lane] = make_uint4(q[ht][4 * g], q[ht][4 * g + 1], q[ht][4 * g + 2], q[ht][4 * g + 3]);
+        sh.q[ht][g][lane] = make_uint4(y[0], y[1], y[2], y[3]);
+        sh.up[ht][g][lane] = make_float2(__shfl_sync(0xffffffffu, mine, 8 * (lane & 3)),
+                                         __shfl_sync(0xffffffffu, mine, 8 * (lane & 3) + 4));
       }
-      up[ht][0] = __shfl_sync(0xffffffffu, mine, 8 * (lane & 3));
-      up[ht][1] = __shfl_sync(0xffffffffu, mine, 8 * (lane & 3) + 4);
-    }
   }
   static __device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[W]) {
     if constexpr (W == 2) {
@@ -372,8 +382,12 @@ struct Cache<D, HT, true, kShort> {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       uint4 q[HT];
+      float2 up[HT];
 #pragma unroll
-      for (int ht = 0; ht < HT; ++ht) q[ht] = shared16(q_at + (ht * G + g) * 512);
+      for (int ht = 0; ht < HT; ++ht) {
+        q[ht] = shared16(q_at + (ht * G + g) * 512);
+        up[ht] = shared8(up_at + (ht * G + g) * 256);
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         // words of a = 2 t come first, those of a = 2 t + 1 after them
@@ -389,10 +403,13 @@ struct Cache<D, HT, true, kShort> {
           float c[4] = {0.f, 0.f, 0.f, 0.f};
           mma16816_f16(c, a[0], a[1], a[2], a[3], q[ht].x, q[ht].y);
           mma16816_f16(c, a[4], a[5], a[6], a[7], q[ht].z, q[ht].w);
-          s[u][ht][0] += c[0] * s0;
-          s[u][ht][1] += c[1] * s0;
-          s[u][ht][2] += c[2] * s1;
-          s[u][ht][3] += c[3] * s1;
+          const float2 f0 = __fmul2_rn(make_float2(s0, s0), up[ht]), f1 = __fmul2_rn(make_float2(s1, s1), up[ht]);
+          const float2 r0 = __ffma2_rn(make_float2(c[0], c[1]), f0, make_float2(s[u][ht][0], s[u][ht][1]));
+          const float2 r1 = __ffma2_rn(make_float2(c[2], c[3]), f1, make_float2(s[u][ht][2], s[u][ht][3]));
+          s[u][ht][0] = r0.x;
+          s[u][ht][1] = r0.y;
+          s[u][ht][2] = r1.x;
+          s[u][ht][3] = r1.y;
         }
       }
     }
@@ -464,14 +481,10 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 
 #pragma unroll
   for (int ht = 0; ht < HT; ++ht)
     C::load_q(8 * ht + r < heads ? a.q.row(b, h0 + 8 * ht + r, 0) : nullptr, t, q[ht]);
-  float sl2[HT][2];
   __shared__ typename C::Shared sh;
-  c.prepare(q, sl2, lane, sh);
+  c.prepare(q, lane, sh);
   __syncthreads();
-#pragma unroll
-  for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) sl2[ht][e] *= a.scale * kLog2eD;
+  const float sl2 = a.scale * kLog2eD;
   float o[HT][MT][4];
   float m[HT][2], l[HT][2];  // heads 8 ht + 2 t, + 1; maxima in log2 units
 #pragma unroll
@@ -492,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 
 #pragma unroll
       for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[u][ht][e] *= sl2[ht][e & 1];
+        for (int e = 0; e < 4; ++e) s[u][ht][e] *= sl2;
     // not all keys inside the window, or among the sinks?
     if (j0 < first || j0 + kBlock > bl.len || (j0 < bl.lo && j0 + kBlock > a.w.sinks)) {
       auto sees = [&](int j) { return j >= first && j < bl.len && (j >= bl.lo || j < a.w.sinks); };

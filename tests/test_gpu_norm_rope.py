@@ -152,3 +152,45 @@ def test_eps_zero_with_odd_heads_and_padding(dtype):
         assert (dx.transpose(1, 2)[pad] == 0).all()
         assert torch.equal(dx.transpose(1, 2)[~pad], was.transpose(1, 2)[~pad])
     assert torch.equal(padded[2], dwq) and torch.equal(padded[3], dwk)
+
+
+# tokens and heads at which the forward takes 1, 4 and 8 heads a group, by type, the backward 4 and 8
+# (neither divides 23 or 3) and, with very many heads, 9
+MANY = [(1, 23, 3, 1400, 128, 96), (1, 23, 3, 2900, 128, 64), (1, 23, 3, 6100, 128, 128), (2, 23, 3, 6100, 64, 32),
+        (1, 2501, 3, 2, 64, 32)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("Bn,nh,nkv,N,d,rot", MANY)
+def test_many_tokens_of_heads_that_fill_no_group(Bn, nh, nkv, N, d, rot, interleaved, dtype):
+    """Views of a packed projection with padding among the tokens, then in place."""
+    c = _case(Bn, nh, nkv, N, d, rot, dtype, N + d, packed=True)
+    pad = torch.rand(Bn, N, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda") < 0.1
+    eps = 2.0 ** -16
+    real = c["pos"].clone()
+    c["pos"][pad] = torch.where(torch.arange(int(pad.sum()), device="cuda") % 2 == 0, -3, 64).int()
+    for n in ("gq", "gk"):
+        c[n].transpose(1, 2)[pad] = 0  # what the reference sums; the kernels do not read them
+    q, k = _forward(c, interleaved, eps)
+    dq, dk, dwq, dwk = _backward(c, interleaved, eps)
+    for x, w, y, g, dx, dw, what in ((c["q"], c["wq"], q, c["gq"], dq, dwq, "q"),
+                                     (c["k"], c["wk"], k, c["gk"], dk, dwk, "k")):
+        ref, tol = norm_rope(x, w, c["cos"], c["sin"], real, interleaved, eps, half=HALF[dtype])
+        within(y.transpose(1, 2)[~pad], ref.transpose(1, 2)[~pad], tol.transpose(1, 2)[~pad], what)
+        assert (y.transpose(1, 2)[pad] == 7.0).all()
+        rdx, tdx, rdw, tdw = norm_rope(x, w, c["cos"], c["sin"], real, interleaved, eps, g, HALF[dtype])
+        within(dx, rdx, tdx, "d" + what)
+        assert (dx.transpose(1, 2)[pad] == 0).all()
+        within(dw, rdw, tdw, "dw" + what)
+    # the same tokens a few at a time
+    few = {n: c[n][:, :, :9] for n in "qk"} | {n: c[n] for n in ("wq", "wk", "cos", "sin")} | \
+        {"pos": c["pos"][:, :9].contiguous()}
+    for y, was in zip(_forward(few, interleaved, eps), (q, k)):
+        assert torch.equal(y, was[:, :, :9])
+    was = c["q"].clone(), c["k"].clone()
+    p = B.norm_rope_of(c["q"], c["k"], c["cos"], eps, interleaved)
+    B.psa_qk_norm_rope_fwd(c["q"], c["k"], c["wq"], c["wk"], c["cos"], c["sin"], c["pos"], c["q"], c["k"], p)
+    for y, x, before in ((q, c["q"], was[0]), (k, c["k"], was[1])):
+        assert torch.equal(x.transpose(1, 2)[~pad], y.transpose(1, 2)[~pad])
+        assert torch.equal(x.transpose(1, 2)[pad], before.transpose(1, 2)[pad])

@@ -234,3 +234,22 @@ def test_4_bit_scores_of_groups_of_unlike_sizes(e, nh, d):
     cache = quantise(_randn(62, 2, 2, rows, d) / up) + quantise(_randn(63, 2, 2, rows, d))
     within(_decode4(q, cache, lens, -1, 0, scale),
            *_reference(q, dequantise(*cache[:2]), dequantise(*cache[2:]), lens, -1, 0, scale), "o")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nh,nkv", [(4, 2), (40, 2)])
+def test_maxima_that_jump_from_block_to_block(nh, nkv, d):
+    """Scores that rise, or fall, by far more than 2^8 along the cache, in bf16 and in 4 bits."""
+    rows, scale = 900, 0.5
+    u = _randn(41, d)
+    u /= u.norm()
+    q = (_randn(42, 2, nh, 1, d) * 0.3 + 8 * u).to(BF16)
+    ramp = torch.linspace(-20, 20, rows, device="cuda")[:, None] * u
+    k, v = _randn(43, 2, nkv, rows, d) * 0.3 + ramp, _randn(44, 2, nkv, rows, d).to(BF16)
+    k[1] = k[1].flip(1)
+    k = k.to(BF16)
+    lens = [rows, rows - 17]
+    within(_decode(q, k, v, lens, -1, 0, scale), *_reference(q, k, v, lens, -1, 0, scale), "o")
+    cache = quantise(k) + quantise(v)
+    within(_decode4(q, cache, lens, -1, 0, scale),
+           *_reference(q, dequantise(*cache[:2]), dequantise(*cache[2:]), lens, -1, 0, scale), "o4")

@@ -299,9 +299,11 @@ size_t psa_qk_norm_rope_bwd_workspace_size(psa_norm_rope_t p);
  * where a negative window means no limit on that side: window_right = 0 is causal,
  * window_left = 255, window_right = 0 a window of 256 positions.  With per-sequence
  * lengths (lens, int32 [B] on the device; NULL: n_k), positions from lens[b] on are
- * padding: they are seen by none and see none.  A query that sees nothing has output
- * 0 and log-sum-exp -infinity, and gets and gives no gradient.  What rows of padding
- * hold does not matter (NaN included); values inside the lengths must be finite. */
+ * padding: they are seen by none and see none.  So are the first n_q - n_k query rows
+ * where n_q > n_k: they stand in front of position 0 and see nothing, whatever the
+ * window.  A query that sees nothing has output 0 and log-sum-exp -infinity, and gets
+ * and gives no gradient.  What rows of padding hold does not matter (NaN included);
+ * values inside the lengths must be finite. */
 typedef struct {
     int B, num_heads, num_kv_heads, n_q, n_k, head_dim;
     psa_dtype_t dtype;

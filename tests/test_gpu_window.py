@@ -266,3 +266,19 @@ def test_a_nan_in_a_query_stays_in_its_row(dtype):
 def test_fp32_of_many_heads(Bn, nh, nkv, n, d, left, right, sinks, lens):
     """More rows than the tiles for few of them take, on both sides or on the queries' alone."""
     _check(*_inputs(Bn, nh, nkv, n, n, d, F32, 41), lens, left, right, sinks, 0.2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("right", [-1, 30])
+@pytest.mark.parametrize("nq,nk", [(300, 130), (131, 3), (260, 259)])
+def test_rows_in_front_of_position_0_see_nothing(nq, nk, right, dtype):
+    """More queries than keys, and a window that looks ahead."""
+    q, k, v, do = _inputs(1, 2, 2, nq, nk, 64, dtype, 51)
+    front, half = slice(0, nq - nk), 2.0 ** -8 if dtype == BF16 else 2.0 ** -24
+    r = window_attention(q, k, v, None, -1, right, 0, 0.2, do, half, dtype == F32)
+    q[:, :, front], do[:, :, front] = math.nan, math.inf
+    o, lse = _fwd(q, k, v, None, -1, right, 0, 0.2)
+    dq, dk, dv = _bwd(q, k, v, o, do, lse, None, -1, right, 0, 0.2)
+    assert (o[:, :, front] == 0).all() and (lse[:, :, front] == -math.inf).all() and (dq[:, :, front] == 0).all()
+    for name, x in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        within(x, r[name], r[name + "_tol"], name)

@@ -369,7 +369,8 @@ def psa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, 
 
 def window_of(q, k, window_left: int = -1, window_right: int = 0, sinks: int = 0) -> PsaWindow:
     """The problem of q [B, num_heads, n_q, d] against keys, a cache or its codes k
-    [B, num_kv_heads, n_k, ...]; a negative window has no limit on that side."""
+    [B, num_kv_heads, n_k, ...]; a negative window has no limit on that side.  The last query
+    stands at the last key's position: with n_q > n_k the first n_q - n_k see nothing."""
     B, nh, n_q, d = q.shape
     n_k = k.shape[2]
     # nothing is past n_k, and all that is negative is alike; a C int would drop the upper bits

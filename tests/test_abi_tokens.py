@@ -261,3 +261,23 @@ def test_tensors_of_another_type_than_the_problem_s():
                      lambda: B.psa_window_attn_decode_kv4(q1, *cache, lens, q1, ws, win1, 0.1)):
             with pytest.raises(TypeError, match="problem"):
                 call()
+
+
+def test_rows_past_the_range_of_an_int():
+    """More rows than a C int counts are refused, not taken for what is left of their lower bits."""
+    import torch
+
+    from vision_transformer_attention_psapackqkv_gb300 import binding as B
+
+    one = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+    k, cache, st = one.expand(1, 1, 2 ** 32 + 1, 64), torch.zeros(1, 1, 8, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    kv4 = tuple(torch.zeros(1, 1, 8, n, dtype=e) for n, e in ((32, torch.uint8), (2, torch.bfloat16)) * 2)
+    for call in (lambda: B.psa_kv_append(k, k, st, None, cache, cache), lambda: B.psa_kv4_append(k, k, st, None, *kv4),
+                 lambda: B.psa_kv4_read(*kv4, k, k)):
+        with pytest.raises(ValueError, match="shape"):
+            call()
+    long = cache.expand(1, 1, 8, 64)[:, :, :1].expand(1, 1, 2 ** 32 + 8, 64)
+    with pytest.raises(ValueError, match="shape"):
+        B.psa_window_attn_fwd(cache, long, long, None, cache, None, B.window_of(cache, long), 0.1)
+    with pytest.raises(ValueError, match="shape"):
+        B.psa_qk_norm_rope_fwd(k, k, None, None, None, None, None, k, k, B.norm_rope_of(k, k, None))

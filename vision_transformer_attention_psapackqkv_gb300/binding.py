@@ -451,26 +451,26 @@ def _kv4(k_codes, k_scales, v_codes, v_scales, B, nkv, max_len, d):
 
 def psa_kv_append(k, v, starts, counts, k_cache, v_cache, stream=None):
     p = cache_of(k, k_cache.shape[2])
-    cache = (p.B, p.num_kv_heads, p.max_len, p.head_dim)
-    _on_device("psa_kv_append", (k, v, starts, counts, k_cache, v_cache), stream, _rows(k, k.shape, k.dtype, "k"),
-               _rows(v, k.shape, k.dtype, "v"), *_cache_rows(starts, counts, p),
+    rows, cache = (p.B, p.num_kv_heads, p.N, p.head_dim), (p.B, p.num_kv_heads, p.max_len, p.head_dim)
+    _on_device("psa_kv_append", (k, v, starts, counts, k_cache, v_cache), stream, _rows(k, rows, k.dtype, "k"),
+               _rows(v, rows, k.dtype, "v"), *_cache_rows(starts, counts, p),
                _rows(k_cache, cache, k.dtype, "k_cache"), _rows(v_cache, cache, k.dtype, "v_cache"), p)
 
 
 def psa_kv4_append(k, v, starts, counts, k_codes, k_scales, v_codes, v_scales, stream=None):
     p = cache_of(k, k_codes.shape[2])
-    cache = (k_codes, k_scales, v_codes, v_scales)
-    _on_device("psa_kv4_append", (k, v, starts, counts, *cache), stream, _rows(k, k.shape, k.dtype, "k"),
-               _rows(v, k.shape, k.dtype, "v"), *_cache_rows(starts, counts, p),
+    rows, cache = (p.B, p.num_kv_heads, p.N, p.head_dim), (k_codes, k_scales, v_codes, v_scales)
+    _on_device("psa_kv4_append", (k, v, starts, counts, *cache), stream, _rows(k, rows, k.dtype, "k"),
+               _rows(v, rows, k.dtype, "v"), *_cache_rows(starts, counts, p),
                *_kv4(*cache, p.B, p.num_kv_heads, p.max_len, p.head_dim), p)
 
 
 def psa_kv4_read(k_codes, k_scales, v_codes, v_scales, k, v, stream=None):
     """Rows 0 .. N - 1 of the cache into k and v [B, num_kv_heads, N, d]."""
     p = cache_of(k, k_codes.shape[2])
-    cache = (k_codes, k_scales, v_codes, v_scales)
+    rows, cache = (p.B, p.num_kv_heads, p.N, p.head_dim), (k_codes, k_scales, v_codes, v_scales)
     _on_device("psa_kv4_read", (k, v, *cache), stream, *_kv4(*cache, p.B, p.num_kv_heads, p.max_len, p.head_dim),
-               _rows(k, k.shape, k.dtype, "k"), _rows(v, k.shape, k.dtype, "v"), p)
+               _rows(k, rows, k.dtype, "k"), _rows(v, rows, k.dtype, "v"), p)
 
 
 def psa_window_attn_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, lens, o, workspace, win: PsaWindow,

@@ -140,10 +140,8 @@ cudaError_t launch_window_fwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cuda
 cudaError_t launch_window_bwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cudaStream_t st);
 size_t window_bwd_tc_ws_bytes(const Window& w, int d);
 // CUDA cores (window_simt.cu).
-template <typename T>
-cudaError_t launch_window_fwd_simt(const WindowArgs<T>& a, int d, cudaStream_t st);
-template <typename T>
-cudaError_t launch_window_bwd_simt(const WindowArgs<T>& a, int d, cudaStream_t st);
+cudaError_t launch_window_fwd_simt(const WindowArgs<float>& a, int d, cudaStream_t st);
+cudaError_t launch_window_bwd_simt(const WindowArgs<float>& a, int d, cudaStream_t st);
 
 // ---------------------------------------------------------------- caches
 struct CacheArgs {

@@ -58,7 +58,7 @@ struct Turn {
   // sign: +1 forward, -1 the inverse rotation
   template <typename T>
   __device__ __forceinline__ void load(const NormRopeArgs<T>& a, int pos, int lane_in_row,
-                                       int lanes, float sign) {
+                                       float sign) {
     const int c0 = lane_in_row * VEC, half = a.rot / 2;
     const int lane = threadIdx.x & 31;
     partner = lane;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_fwd_kernel(const NormRo
   if (a.positions && live) pos = a.positions[token];
   const bool valid = live && pos >= 0 && pos < a.max_pos;
   Turn<VEC> turn;
-  turn.load(a, valid ? pos : 0, lr, LANES, 1.f);
+  turn.load(a, valid ? pos : 0, lr, 1.f);
   float w[VEC];
   load_weight(is_q ? a.wq : a.wk, c0, w);
   turn.weigh(a.interleaved, w);
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const T *x0 = in.row(b, h0, n) + c0, *g0 = gin.row(b, h0, n) + c0;
     T* d0 = out.row(b, h0, n) + c0;
     Turn<VEC> turn;
-    turn.load(a, valid ? pos : 0, lr, LANES, -1.f);
+    turn.load(a, valid ? pos : 0, lr, -1.f);
     // the next kBatch heads' rows are on their way while these are worked on
     uint4 nx[kBatch], ng[kBatch];
     auto load = [&](int h) {

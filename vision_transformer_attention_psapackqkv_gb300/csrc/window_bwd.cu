@@ -64,7 +64,7 @@ struct BwdParams {
   const float* stat;   // [B, nh, row_tiles, 2, 128]: -lse log2(e), -delta
   float* partial;      // [slots, B * nkv, 2 (dV, dK), 128, D]
   float scale, sl2;
-  int units, row_tiles, key_tiles;
+  int units, row_tiles;
   Cut cut;
 };
 
@@ -961,7 +961,6 @@ cudaError_t bwd(const WindowArgs<__nv_bfloat16>& x, cudaStream_t st) {
   a.scale = x.scale;
   a.sl2 = x.scale * kLog2;
   a.row_tiles = (w.nq + kTile - 1) / kTile;
-  a.key_tiles = (w.nk + kTile - 1) / kTile;
   auto dq = window_dq_tc_kernel<D>;
   auto dkdv = window_dkdv_tc_kernel<D>;
   cudaError_t e = set_max_dynamic_smem((const void*)dq, DqCfg<D>::SMEM);

@@ -128,16 +128,12 @@ __device__ __forceinline__ float row_reduce(float v) {
   return v;
 }
 
-template <int D, typename T>
-__device__ __forceinline__ void store4(T* dst, float a, float b, float c, float d) {
-  if constexpr (sizeof(T) == 4)
-    *reinterpret_cast<float4*>(dst) = make_float4(a, b, c, d);
-  else
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(a, b), pack2(c, d));
+__device__ __forceinline__ void store4(float* dst, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(dst) = make_float4(a, b, c, d);
 }
 
-template <typename T, int D, int kRows, int R>
-__global__ void __launch_bounds__(16 * kRows / R) window_fwd_simt_kernel(const WindowArgs<T> a) {
+template <int D, int kRows, int R>
+__global__ void __launch_bounds__(16 * kRows / R) window_fwd_simt_kernel(const WindowArgs<float> a) {
   constexpr int kR = R, kGap = kRows / R, kN = 16 * kGap;
   extern __shared__ float sm[];
   float *Q = sm, *K = Q + kRows * kLd<D>, *V = K + kB * kLd<D>, *P = V + kB * kLd<D>;
@@ -207,11 +203,11 @@ __global__ void __launch_bounds__(16 * kRows / R) window_fwd_simt_kernel(const W
     if (q >= a.w.nq) continue;
     // a sum of 0 is a row that sees nothing; a NaN among the scores stays one
     const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
-    T* dst = a.out.row(b, h, q) + 4 * tx;
+    float* dst = a.out.row(b, h, q) + 4 * tx;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
-      store4<D>(dst + 64 * c, o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv,
-                o[i][4 * c + 3] * inv);
+      store4(dst + 64 * c, o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv,
+             o[i][4 * c + 3] * inv);
     if (a.lse && tx == 0)
       a.lse[(long long)blockIdx.y * a.w.nq + q] = l[i] != 0.f ? m[i] + logf(l[i]) : -INFINITY;
   }
@@ -219,9 +215,9 @@ __global__ void __launch_bounds__(16 * kRows / R) window_fwd_simt_kernel(const W
 
 // delta = rowsum(dO o O), one row per 16 lanes; 0 for rows that see nothing (whose dO and
 // O may hold anything).
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) window_delta_kernel(const WindowArgs<T> a) {
-  constexpr int VEC = kVec<T>, PER = D / VEC, LANES = PER < 16 ? PER : 16;
+template <int D>
+__global__ void __launch_bounds__(kThreads) window_delta_kernel(const WindowArgs<float> a) {
+  constexpr int LANES = 16;
   pdl_launch_dependents();
   pdl_wait();
   const int lr = threadIdx.x % LANES;
@@ -231,21 +227,22 @@ __global__ void __launch_bounds__(kThreads) window_delta_kernel(const WindowArgs
   const bool live = i < a.w.nq && p >= 0 && p < a.w.len(b);
   float s = 0.f;
 #pragma unroll
-  for (int c = lr * VEC; c < D; c += LANES * VEC) {
+  for (int c = 4 * lr; c < D; c += 4 * LANES) {
     if (!live) continue;
-    float x[VEC], y[VEC];
-    unpack_vec(*reinterpret_cast<const uint4*>(a.dO.row(b, h, i) + c), x);
-    unpack_vec(*reinterpret_cast<const uint4*>(a.o.row(b, h, i) + c), y);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) s += x[e] * y[e];
+    const float4 x = *reinterpret_cast<const float4*>(a.dO.row(b, h, i) + c);
+    const float4 y = *reinterpret_cast<const float4*>(a.o.row(b, h, i) + c);
+    s += x.x * y.x;
+    s += x.y * y.y;
+    s += x.z * y.z;
+    s += x.w * y.w;
   }
 #pragma unroll
   for (int m = LANES / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
   if (lr == 0 && i < a.w.nq) a.delta[(long long)blockIdx.y * a.w.nq + i] = s;
 }
 
-template <typename T, int D, int kRows, int R>
-__global__ void __launch_bounds__(16 * kRows / R) window_dq_simt_kernel(const WindowArgs<T> a) {
+template <int D, int kRows, int R>
+__global__ void __launch_bounds__(16 * kRows / R) window_dq_simt_kernel(const WindowArgs<float> a) {
   constexpr int kR = R, kGap = kRows / R, kN = 16 * kGap;
   extern __shared__ float sm[];
   float *Q = sm, *dO = Q + kRows * kLd<D>, *K = dO + kRows * kLd<D>, *V = K + kB * kLd<D>,
@@ -301,16 +298,16 @@ __global__ void __launch_bounds__(16 * kRows / R) window_dq_simt_kernel(const Wi
   for (int i = 0; i < kR; ++i) {
     const int q = i0 + ty + kGap * i;
     if (q >= a.w.nq) continue;
-    T* dst = a.dq.row(b, h, q) + 4 * tx;
+    float* dst = a.dq.row(b, h, q) + 4 * tx;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
-      store4<D>(dst + 64 * c, acc[i][4 * c] * a.scale, acc[i][4 * c + 1] * a.scale,
-                acc[i][4 * c + 2] * a.scale, acc[i][4 * c + 3] * a.scale);
+      store4(dst + 64 * c, acc[i][4 * c] * a.scale, acc[i][4 * c + 1] * a.scale,
+             acc[i][4 * c + 2] * a.scale, acc[i][4 * c + 3] * a.scale);
   }
 }
 
-template <typename T, int D, int kRows, int R>
-__global__ void __launch_bounds__(16 * kRows / R) window_dkdv_simt_kernel(const WindowArgs<T> a) {
+template <int D, int kRows, int R>
+__global__ void __launch_bounds__(16 * kRows / R) window_dkdv_simt_kernel(const WindowArgs<float> a) {
   constexpr int kR = R, kGap = kRows / R, kN = 16 * kGap;
   extern __shared__ float sm[];
   float *K = sm, *V = K + kRows * kLd<D>, *Q = V + kRows * kLd<D>, *dO = Q + kB * kLd<D>,
@@ -367,12 +364,12 @@ __global__ void __launch_bounds__(16 * kRows / R) window_dkdv_simt_kernel(const 
   for (int i = 0; i < kR; ++i) {
     const int j = j0 + ty + kGap * i;
     if (j >= a.w.nk) continue;
-    T *dkr = a.dk.row(b, hk, j) + 4 * tx, *dvr = a.dv.row(b, hk, j) + 4 * tx;
+    float *dkr = a.dk.row(b, hk, j) + 4 * tx, *dvr = a.dv.row(b, hk, j) + 4 * tx;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-      store4<D>(dkr + 64 * c, dk[i][4 * c] * a.scale, dk[i][4 * c + 1] * a.scale,
-                dk[i][4 * c + 2] * a.scale, dk[i][4 * c + 3] * a.scale);
-      store4<D>(dvr + 64 * c, dv[i][4 * c], dv[i][4 * c + 1], dv[i][4 * c + 2], dv[i][4 * c + 3]);
+      store4(dkr + 64 * c, dk[i][4 * c] * a.scale, dk[i][4 * c + 1] * a.scale,
+             dk[i][4 * c + 2] * a.scale, dk[i][4 * c + 3] * a.scale);
+      store4(dvr + 64 * c, dv[i][4 * c], dv[i][4 * c + 1], dv[i][4 * c + 2], dv[i][4 * c + 3]);
     }
   }
 }
@@ -386,61 +383,56 @@ bool few_rows(int rows, int heads) {
   return D == 64 && (long long)((rows + 15) / 16) * heads <= 3LL * device_sm_count();
 }
 
-template <typename T, int D, int kRows, int R>
-cudaError_t fwd(const WindowArgs<T>& a, cudaStream_t st) {
+template <int D, int kRows, int R>
+cudaError_t fwd(const WindowArgs<float>& a, cudaStream_t st) {
   constexpr int smem = ((2 * kB + kRows) * kLd<D> + kRows * kLdP) * 4;
-  auto kern = window_fwd_simt_kernel<T, D, kRows, R>;
+  auto kern = window_fwd_simt_kernel<D, kRows, R>;
   const cudaError_t e = set_max_dynamic_smem((const void*)kern, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((a.w.nq + kRows - 1) / kRows, a.w.B * a.w.nh), dim3(16 * kRows / R), smem, st, a);
 }
 
-template <typename T, int D>
-cudaError_t fwd(const WindowArgs<T>& a, cudaStream_t st) {
-  return few_rows<D>(a.w.nq, a.w.B * a.w.nh) ? fwd<T, D, 16, 2>(a, st) : fwd<T, D, 32, 4>(a, st);
+template <int D>
+cudaError_t fwd(const WindowArgs<float>& a, cudaStream_t st) {
+  return few_rows<D>(a.w.nq, a.w.B * a.w.nh) ? fwd<D, 16, 2>(a, st) : fwd<D, 32, 4>(a, st);
 }
 
-template <typename T, int D, int kRows, int R>
-cudaError_t dq(const WindowArgs<T>& a, cudaStream_t st) {
+template <int D, int kRows, int R>
+cudaError_t dq(const WindowArgs<float>& a, cudaStream_t st) {
   constexpr int smem = ((2 * kB + 2 * kRows) * kLd<D> + kRows * kLdP) * 4;
-  auto kern = window_dq_simt_kernel<T, D, kRows, R>;
+  auto kern = window_dq_simt_kernel<D, kRows, R>;
   const cudaError_t e = set_max_dynamic_smem((const void*)kern, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((a.w.nq + kRows - 1) / kRows, a.w.B * a.w.nh), dim3(16 * kRows / R), smem, st, a);
 }
 
-template <typename T, int D, int kRows, int R>
-cudaError_t dkdv(const WindowArgs<T>& a, cudaStream_t st) {
+template <int D, int kRows, int R>
+cudaError_t dkdv(const WindowArgs<float>& a, cudaStream_t st) {
   constexpr int smem = ((2 * kB + 2 * kRows) * kLd<D> + 2 * kRows * kLdP) * 4;
-  auto kern = window_dkdv_simt_kernel<T, D, kRows, R>;
+  auto kern = window_dkdv_simt_kernel<D, kRows, R>;
   const cudaError_t e = set_max_dynamic_smem((const void*)kern, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((a.w.nk + kRows - 1) / kRows, a.w.B * a.w.nkv), dim3(16 * kRows / R), smem, st, a);
 }
 
-template <typename T, int D>
-cudaError_t bwd(const WindowArgs<T>& a, cudaStream_t st) {
-  constexpr int PER = D / kVec<T>, LANES = PER < 16 ? PER : 16;
-  const int rows = kThreads / LANES;
-  cudaError_t e = launch_pdl(window_delta_kernel<T, D>, dim3((a.w.nq + rows - 1) / rows, a.w.B * a.w.nh),
+template <int D>
+cudaError_t bwd(const WindowArgs<float>& a, cudaStream_t st) {
+  const int rows = kThreads / 16;
+  cudaError_t e = launch_pdl(window_delta_kernel<D>, dim3((a.w.nq + rows - 1) / rows, a.w.B * a.w.nh),
                              dim3(kThreads), 0, st, a);
   if (e != cudaSuccess) return e;
-  e = few_rows<D>(a.w.nq, a.w.B * a.w.nh) ? dq<T, D, 16, 2>(a, st) : dq<T, D, 32, 4>(a, st);
+  e = few_rows<D>(a.w.nq, a.w.B * a.w.nh) ? dq<D, 16, 2>(a, st) : dq<D, 32, 4>(a, st);
   if (e != cudaSuccess) return e;
-  return few_rows<D>(a.w.nk, a.w.B * a.w.nkv) ? dkdv<T, D, 16, 2>(a, st) : dkdv<T, D, 32, 4>(a, st);
+  return few_rows<D>(a.w.nk, a.w.B * a.w.nkv) ? dkdv<D, 16, 2>(a, st) : dkdv<D, 32, 4>(a, st);
 }
 
 }  // namespace
 
-template <typename T>
-cudaError_t launch_window_fwd_simt(const WindowArgs<T>& a, int d, cudaStream_t st) {
-  return d == 64 ? fwd<T, 64>(a, st) : fwd<T, 128>(a, st);
+cudaError_t launch_window_fwd_simt(const WindowArgs<float>& a, int d, cudaStream_t st) {
+  return d == 64 ? fwd<64>(a, st) : fwd<128>(a, st);
 }
-template <typename T>
-cudaError_t launch_window_bwd_simt(const WindowArgs<T>& a, int d, cudaStream_t st) {
-  return d == 64 ? bwd<T, 64>(a, st) : bwd<T, 128>(a, st);
+cudaError_t launch_window_bwd_simt(const WindowArgs<float>& a, int d, cudaStream_t st) {
+  return d == 64 ? bwd<64>(a, st) : bwd<128>(a, st);
 }
-template cudaError_t launch_window_fwd_simt(const WindowArgs<float>&, int, cudaStream_t);
-template cudaError_t launch_window_bwd_simt(const WindowArgs<float>&, int, cudaStream_t);
 
 }  // namespace psa

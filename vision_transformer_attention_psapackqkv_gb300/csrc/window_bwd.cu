@@ -15,7 +15,9 @@
 // 64 of the 128 columns), a TMA producer, a warp that issues the products, and one that
 // zeroes the rows of padding where they are an operand (0 times NaN is NaN).  bf16 operands
 // made by the row threads stay in tensor memory: each thread writes them over the columns
-// that it read.  All products come from one warp and complete in the order they are issued:
+// that it read.  All products come from one warp and complete in the order they are issued
+// (observed, as in window_fwd.cu: PTX promises it for products of one shape into the same
+// sums, not for S next to dQ):
 //   dQ kernel     the next tile's S as soon as this one's is in registers, its dP (two buffers),
 //                 then this tile's dQ += dS K (dS in dP's columns), so the row threads find
 //                 both operands when they come to the next tile
@@ -897,10 +899,10 @@ int padded_rows(const Window& w) { return (w.nq + kTile - 1) / kTile * kTile; }
 size_t stat_bytes(const Window& w) { return (size_t)w.B * w.nh * padded_rows(w) * sizeof(float2); }
 
 // By the sizes alone (full lengths, 152 SMs).  A tile is cut only where one of them would
-// take much longer than an SM's share of all: sinks behind a window (window_train's first
-// tile has 128 steps, the others 36 to 40), or a long causal triangle of few heads.  Parts
-// are half an SM's share, but no smaller than what a tile of the window has anyway: each
-// costs a tile of fp32 sums written and read.
+// take much longer than an SM's share of all: sinks behind a window (4096 positions, a window
+// of 1024, groups of 4: the sinks' tile has 128 steps, the others 36, and 32 down to 4 at the
+// end), or a long causal triangle of few heads.  Parts are half an SM's share, but no smaller
+// than what a tile of the window has anyway: each costs a tile of fp32 sums written and read.
 Cut cut_of(const Window& w) {
   constexpr int kSms = 152;
   const int key_tiles = (w.nk + kTile - 1) / kTile, group = w.nh / w.nkv;

@@ -324,7 +324,8 @@ psa_status_t psa_window_attn_fwd(psa_rows_t q, psa_rows_t k, psa_rows_t v, const
  * query heads in a fixed order: reruns are bitwise identical).  workspace: 16-byte
  * aligned, at least psa_window_attn_bwd_workspace_size(p) bytes (PSA_ERR_INVALID_ARG
  * if smaller).  Sizes and types as in the forward; bf16: P and dS are rounded to bf16
- * before their products. */
+ * before their products, and delta, the row sums of do_ o o, has the rounding of the o
+ * given; rows that see at most eight keys take it from P, do_ and v in fp32 instead. */
 psa_status_t psa_window_attn_bwd(psa_rows_t q, psa_rows_t k, psa_rows_t v, psa_rows_t o,
                                  psa_rows_t do_, const float *lse, const int *lens, psa_rows_t dq,
                                  psa_rows_t dk, psa_rows_t dv, void *workspace, size_t ws_bytes,

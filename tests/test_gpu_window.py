@@ -282,3 +282,44 @@ def test_rows_in_front_of_position_0_see_nothing(nq, nk, right, dtype):
     assert (o[:, :, front] == 0).all() and (lse[:, :, front] == -math.inf).all() and (dq[:, :, front] == 0).all()
     for name, x in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
         within(x, r[name], r[name + "_tol"], name)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Bn,n,left,right,sinks,lens", [(32, 2, -1, 0, 0, None), (8, 8, -1, 0, 0, None), (4, 5, -1, -1, 0, None),
+                                                        (1, 300, 1, 0, 0, None), (2, 300, 4, 3, 0, [300, 131]),
+                                                        (1, 300, 0, 0, 1, None), (2, 260, 1, 2, 4, [260, 7]),
+                                                        (1, 130, 7, 0, 0, None)])
+def test_gradients_of_rows_that_see_few_keys(Bn, n, left, right, sinks, lens, d):
+    """Up to eight keys: dP - delta may be small next to delta, so that delta is to be as exact as dP,
+    not as o, whose rounding to bf16 is of delta's size.  Roundings of P, dS and the outputs to bf16
+    are counted, and fp32 sums of products; no rounding of o."""
+    nh, nkv, scale, half, u = 4, 2, d ** -0.5, 2.0 ** -8, 2.0 ** -24
+    q, k, v, do = _inputs(Bn, nh, nkv, n, n, d, BF16, 71 + n)
+    lens_t = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = _fwd(q, k, v, lens_t, left, right, sinks, scale)
+    dq, dk, dv = _bwd(q, k, v, o, do, lse, lens_t, left, right, sinks, scale)
+    p = torch.arange(n, device="cuda")[:, None] + torch.zeros(n, dtype=torch.int64, device="cuda")
+    j = p.T
+    for b in range(Bn):
+        m = n if lens is None else lens[b]
+        ok = (p < m) & (j < m)
+        ok &= (j >= p - left) | (j < sinks) if left >= 0 else ok
+        ok &= j <= p + right if right >= 0 else ok
+        assert ok.sum(1).max() <= 8
+        for hk in range(nkv):
+            dk64 = torch.zeros(n, d, dtype=torch.float64, device="cuda")
+            dk_tol = torch.zeros_like(dk64)
+            for h in range(hk * nh // nkv, (hk + 1) * nh // nkv):
+                qq, kk, vv, g = (t.double() for t in (q[b, h], k[b, hk], v[b, hk], do[b, h]))
+                x = torch.where(ok, qq @ kk.T * scale, -math.inf)
+                prob = torch.softmax(x, 1).nan_to_num(0.0)
+                dp, dpm = g @ vv.T, g.abs() @ vv.abs().T
+                ds = prob * (dp - (prob * dp).sum(1, keepdim=True))
+                # P in fp32: the scores' sums of d products, the exponent's rounding and the lse's, ex2
+                ex = u * ((d + 4) * float((qq.abs() @ kk.abs().T).max()) * scale + 64)
+                every = (prob * dpm).sum(1, keepdim=True)  # magnitudes of delta's terms
+                ds_err = half * ds.abs() + prob * (((d + 16) * u + 2 * ex) * (dpm + every))
+                within(dq[b, h], scale * ds @ kk, half * (scale * ds @ kk).abs() + scale * (ds_err + 16 * u * ds.abs()) @ kk.abs(), "dq")
+                dk64 += scale * ds.T @ qq
+                dk_tol += scale * (ds_err + 64 * u * ds.abs()).T @ qq.abs()
+            within(dk[b, hk], dk64, half * dk64.abs() + dk_tol, "dk")

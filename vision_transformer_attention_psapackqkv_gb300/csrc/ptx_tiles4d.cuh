@@ -1,5 +1,5 @@
 // ptx_tiles4d.cuh -- PTX wrappers of the token-sequence kernels beside those of ptx.cuh: TMA copies
-// of 4-D views, bulk loads, and tcgen05 products issued by a converged warp.
+// of 4-D views, bulk loads, tcgen05 products issued by a converged warp, and a warp's own products.
 #pragma once
 
 #include "ptx.cuh"
@@ -64,5 +64,18 @@ __device__ __forceinline__ void mma_commit_warp(uint64_t* bar) {
           smem_addr(bar))
       : "memory");
 }
+
+// d += a b (m16n8k16, fp32 sums)
+#define PSA_MMA(NAME, TYPE)                                                                        \
+  __device__ __forceinline__ void NAME(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,       \
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {                    \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                     \
+        ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"                     \
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                           \
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));                                   \
+  }
+PSA_MMA(mma16816, "bf16")
+PSA_MMA(mma16816_f16, "f16")
+#undef PSA_MMA
 
 }  // namespace psa

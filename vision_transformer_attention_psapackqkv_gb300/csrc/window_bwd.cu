@@ -26,7 +26,8 @@
 //                 dP^T, while they make P^T.
 // delta and lse come from a small kernel in front: for each tile of 128 rows (the last one
 // padded) 128 values of -lse log2(e), then 128 of -delta, so that a tile's 1024 bytes are one
-// bulk copy and two neighbouring columns' values one operand of a paired instruction.
+// bulk copy and two neighbouring columns' values one operand of a paired instruction.  delta is
+// rowsum(dO o O), or for rows that see few keys the sum of P dP.
 // Measured: 2 x 4096 tokens, 16 heads of 128 on 4, a window of 1024 and 4 sinks: 239 us (dK/dV 128
 // with the pipe busy 61 % of the time, dQ 94 with 48 %, statistics and parts 10 each; 0.63 PFLOP/s
 // counting five products); 16384 tokens causal, 16 heads on 2: 2.65 ms (1.04 PFLOP/s; dK/dV 75 %,
@@ -78,18 +79,137 @@ __device__ __forceinline__ int unit_of(int i) {
 // -lse log2(e) and -delta of every row; rows that see nothing, and those behind n_q, get 0:
 // their scores are masked.  D / 8 lanes share a row, 16 bytes of dO and of O in each, and take
 // four rows, all on their way at once.
-constexpr int kStatRows = 4;
+//
+// Rows that see few keys have a delta of their own: there dP - delta may be small next to delta,
+// and o, rounded to bf16, leaves delta a rounding error of its own size (dQ and dK of two keys 3.5 to
+// 5e-3 off in the 2-norm, where the roundings of dS and the output alone give 2.4e-3).  It is
+// sum P dP in fp32, S and dP by tensor instructions, 16 rows and 8 keys a warp.  The error falls
+// with the root of the number of keys: from nine on it is under 0.7 of the rounding of dS, and o as
+// given does.  The grid's first `again` blocks are for these rows, next to the others rather than
+// behind them.
+constexpr int kStatRows = 4, kFewKeys = 8;
 template <int D>
-__global__ void __launch_bounds__(256)
-    window_stat_kernel(const WindowArgs<__nv_bfloat16> a, float* stat, int padded) {
+constexpr int kStatBlock = 256 / (D / 8) * kStatRows;  // rows of a block
+constexpr int kFewBlock = 8 * 16;                      // of one for rows that see few keys
+
+// The keys that row i sees: 0 .. front - 1 and lo .. hi, if they are few (and some).
+struct FewKeys {
+  int front, lo, hi;
+  bool any;
+  __device__ __forceinline__ FewKeys(const Window& w, int len, int i) {
+    const int p = i + w.nk - w.nq;
+    lo = max(0, p - w.left);
+    hi = min(len - 1, p + w.right);
+    front = min(w.sinks, lo);
+    any = i < w.nq && p >= 0 && p < len && front + hi - lo + 1 <= kFewKeys;
+  }
+};
+// Whether one of the rows i0 .. i1 may be such: false if the first and the last one are far enough
+// from the sequence's ends and the window is wide enough.
+__device__ __forceinline__ bool may_see_few(const Window& w, int len, int i0, int i1) {
+  const int off = w.nk - w.nq;
+  return min(min(max(0, i0 + off) + w.right + 1, len), w.left + min(w.right + 1, len - off - i1)) <= kFewKeys;
+}
+
+// -delta of those among a warp's 16 rows from i0 on.  kTiles: of 8 keys, that they see between them
+// (16 rows of 8 keys see 23, and the sinks; positions 0 .. 7 behind a wider window see keys 0 .. 7).
+template <int D, int kTiles>
+__device__ __forceinline__ void few_keys_delta(const WindowArgs<__nv_bfloat16>& a, float* stat, int b, int h, int len,
+                                               int i0) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, hk = h / (a.w.nh / a.w.nkv);
+  const FewKeys f[2] = {FewKeys(a.w, len, i0 + g), FewKeys(a.w, len, i0 + g + 8)};
+  if (!__any_sync(0xffffffffu, f[0].any || f[1].any)) return;
+  int first = a.w.nk, last = -1, front = 0;  // of all rows
+  float nlse[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    nlse[r] = f[r].any ? -a.lse[((long long)b * a.w.nh + h) * a.w.nq + i0 + g + 8 * r] * kLog2 : 0.f;
+    if (!f[r].any) continue;
+    first = min(first, f[r].lo);
+    last = max(last, f[r].hi);
+    front = max(front, f[r].front);
+  }
+  first = __reduce_min_sync(0xffffffffu, first);
+  last = __reduce_max_sync(0xffffffffu, last);
+  front = __reduce_max_sync(0xffffffffu, front);
+  const int sink = front > 0;  // the sinks' tile, then the windows'
+  auto from = [&](int tile) { return tile < sink ? 0 : first + 8 * (tile - sink); };
+  auto end = [&](int tile) { return tile < sink ? front : last + 1; };
+  float x[kTiles][4], y[kTiles][4];
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[n][e] = y[n][e] = 0.f;
+  // (the order of the channels is free: each lane takes 16 neighbouring bytes)
+  auto load = [&](const View<const __nv_bfloat16>& v, int head, int row, int c, bool on) {
+    return on ? *reinterpret_cast<const uint4*>(v.row(b, head, row) + 32 * c + 8 * t) : make_uint4(0, 0, 0, 0);
+  };
+#pragma unroll(kTiles == 1 ? D / 32 : 2)
+  for (int c = 0; c < D / 32; ++c) {
+    const uint4 q0 = load(a.q, h, i0 + g, c, f[0].any), q1 = load(a.q, h, i0 + g + 8, c, f[1].any);
+    const uint4 d0 = load(a.dO, h, i0 + g, c, f[0].any), d1 = load(a.dO, h, i0 + g + 8, c, f[1].any);
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) {
+      if (from(n) > last) continue;
+      const int j = from(n) + g;
+      const uint4 k = load(a.k, hk, j, c, j < end(n)), v = load(a.v, hk, j, c, j < end(n));
+      mma16816(x[n], q0.x, q1.x, q0.y, q1.y, k.x, k.y);
+      mma16816(x[n], q0.z, q1.z, q0.w, q1.w, k.z, k.w);
+      mma16816(y[n], d0.x, d1.x, d0.y, d1.y, v.x, v.y);
+      mma16816(y[n], d0.z, d1.z, d0.w, d1.w, v.z, v.w);
+    }
+  }
+  float s[2] = {0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const FewKeys& m = f[e / 2];
+      const int j = from(n) + 2 * t + e % 2;
+      if (m.any && (n < sink ? j < m.front : j >= m.lo && j <= m.hi))
+        s[e / 2] += fast_exp2(x[n][e] * (a.scale * kLog2) + nlse[e / 2]) * y[n][e];
+    }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
+    s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
+    const int i = i0 + g + 8 * r;
+    if (t == 0 && f[r].any) stat[i / kTile * (2 * kTile) + kTile + i % kTile] = -s[r];
+  }
+}
+
+template <int D, bool kNarrow>
+__global__ void __launch_bounds__(256, kNarrow ? 2 : 4)
+    window_stat_kernel(const WindowArgs<__nv_bfloat16> a, float* stat, int padded, int blocks, int again) {
   constexpr int LANES = D / 8, GROUPS = 256 / LANES;
   pdl_launch_dependents();
   pdl_wait();
-  const int lr = threadIdx.x % LANES, i0 = blockIdx.x * (GROUPS * kStatRows) + threadIdx.x / LANES;
-  const int b = blockIdx.y / a.w.nh, h = blockIdx.y % a.w.nh, off = a.w.nk - a.w.nq;
-  const int from = max(0, -off), to = min(a.w.nq, a.w.len(b) - off);  // rows that see something
+  const int off = a.w.nk - a.w.nq;
+  if ((int)blockIdx.x < again) {
+    const int warp = threadIdx.x / 32;
+    int head, i;
+    if constexpr (kNarrow) {  // any row of a head
+      const int n = (a.w.nq + kFewBlock - 1) / kFewBlock;
+      head = blockIdx.x / n;
+      i = blockIdx.x % n * kFewBlock + 16 * warp;
+    } else {  // the first rows of one head for each warp
+      head = 8 * blockIdx.x + warp;
+      i = max(0, -off);
+      if (head >= a.w.B * a.w.nh) return;
+    }
+    const int len = a.w.len(head / a.w.nh);
+    if (may_see_few(a.w, len, i, i + 15))
+      few_keys_delta<D, kNarrow ? 4 : 1>(a, stat + 2 * (long long)head * padded, head / a.w.nh, head % a.w.nh, len, i);
+    return;
+  }
+  const int head = (blockIdx.x - again) / blocks, start = (blockIdx.x - again) % blocks * kStatBlock<D>;
+  const int b = head / a.w.nh, h = head % a.w.nh, len = a.w.len(b);
+  const int from = max(0, -off), to = min(a.w.nq, len - off);  // rows that see something
+  stat += 2 * (long long)head * padded;
+  const int lr = threadIdx.x % LANES, i0 = start + threadIdx.x / LANES;
+  const bool few = may_see_few(a.w, len, start, start + kStatBlock<D> - 1);
   const __nv_bfloat16 *g = a.dO.row(b, h, i0) + 8 * lr, *o = a.o.row(b, h, i0) + 8 * lr;
-  const float* lse = a.lse + (long long)blockIdx.y * a.w.nq;
+  const float* lse = a.lse + (long long)head * a.w.nq;
   uint4 rg[kStatRows], ro[kStatRows];
   float l[kStatRows];
 #pragma unroll
@@ -98,9 +218,10 @@ __global__ void __launch_bounds__(256)
     rg[k] = ro[k] = make_uint4(0, 0, 0, 0);
     l[k] = 0.f;
     if (i >= from && i < to) {
+      l[k] = lse[i];
+      if (kNarrow && few && FewKeys(a.w, len, i).any) continue;  // its delta is not made here
       rg[k] = *reinterpret_cast<const uint4*>(g + GROUPS * k * a.dO.sn);
       ro[k] = *reinterpret_cast<const uint4*>(o + GROUPS * k * a.o.sn);
-      l[k] = lse[i];
     }
   }
 #pragma unroll
@@ -114,9 +235,9 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int m = LANES / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
     if (lr == 0 && i < padded) {
-      float* at = stat + 2 * ((long long)blockIdx.y * padded + i / kTile * kTile) + i % kTile;
+      float* at = stat + i / kTile * (2 * kTile) + i % kTile;
       at[0] = -l[k] * kLog2;
-      at[kTile] = -s;
+      if (!few || !FewKeys(a.w, len, i).any) at[kTile] = -s;
     }
   }
 }
@@ -967,10 +1088,13 @@ cudaError_t bwd(const WindowArgs<__nv_bfloat16>& x, cudaStream_t st) {
   auto dkdv = window_dkdv_tc_kernel<D>;
   cudaError_t e = set_max_dynamic_smem((const void*)dq, DqCfg<D>::SMEM);
   if (e == cudaSuccess) e = set_max_dynamic_smem((const void*)dkdv, DkvCfg<D>::SMEM);
-  const int rows = 256 / (D / 8) * kStatRows, padded = padded_rows(w);
+  // with a window this wide to the left, only positions 0 .. kFewKeys - 1 can see few keys
+  const bool narrow = w.left < kFewKeys;
+  const int heads = w.B * w.nh, padded = padded_rows(w), blocks = (padded + kStatBlock<D> - 1) / kStatBlock<D>;
+  const int again = narrow ? (w.nq + kFewBlock - 1) / kFewBlock * heads : (heads + 7) / 8;
   if (e == cudaSuccess)
-    e = launch_pdl(window_stat_kernel<D>, dim3((padded + rows - 1) / rows, w.B * w.nh), dim3(256), 0, st, x, stat,
-                   padded);
+    e = launch_pdl(narrow ? window_stat_kernel<D, true> : window_stat_kernel<D, false>, dim3(blocks * heads + again),
+                   dim3(256), 0, st, x, stat, padded, blocks, again);
   a.cut = cut_of(w);
   a.partial = reinterpret_cast<float*>(reinterpret_cast<char*>(x.delta) + stat_bytes(w));
   if (e == cudaSuccess) {

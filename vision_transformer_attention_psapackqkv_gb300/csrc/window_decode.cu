@@ -44,7 +44,7 @@
 #include <cuda_fp16.h>
 
 #include "lm.cuh"
-#include "ptx.cuh"
+#include "ptx_tiles4d.cuh"
 
 namespace psa {
 namespace {
@@ -53,19 +53,6 @@ constexpr int kWarps = 4;        // per CTA
 constexpr int kThreads = 32 * kWarps;
 constexpr int kLongBlock = 32;   // most keys that a warp takes at a time
 constexpr float kLog2eD = 1.4426950408889634074f;
-
-// d += a b (m16n8k16, fp32 sums)
-#define PSA_MMA(NAME, TYPE)                                                                        \
-  __device__ __forceinline__ void NAME(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,       \
-                                       uint32_t a3, uint32_t b0, uint32_t b1) {                    \
-    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                     \
-        ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"                     \
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                           \
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));                                   \
-  }
-PSA_MMA(mma16816, "bf16")
-PSA_MMA(mma16816_f16, "f16")
-#undef PSA_MMA
 
 // An 8 x 8 matrix of 16-bit values, two neighbours of a row per lane, transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {

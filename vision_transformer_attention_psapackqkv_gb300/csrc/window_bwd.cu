@@ -28,8 +28,8 @@
 // padded) 128 values of -lse log2(e), then 128 of -delta, so that a tile's 1024 bytes are one
 // bulk copy and two neighbouring columns' values one operand of a paired instruction.  delta is
 // rowsum(dO o O), or for rows that see few keys the sum of P dP.
-// Measured: 2 x 4096 tokens, 16 heads of 128 on 4, a window of 1024 and 4 sinks: 239 us (dK/dV 128
-// with the pipe busy 61 % of the time, dQ 94 with 48 %, statistics and parts 10 each; 0.63 PFLOP/s
+// Measured: 2 x 4096 tokens, 16 heads of 128 on 4, a window of 1024 and 4 sinks: 238 us (dK/dV 127
+// with the pipe busy 61 % of the time, dQ 93 with 49 %, statistics and parts 10 each; 0.63 PFLOP/s
 // counting five products); 16384 tokens causal, 16 heads on 2: 2.65 ms (1.04 PFLOP/s; dK/dV 75 %,
 // dQ 67 %).
 #include <math.h>
@@ -85,7 +85,8 @@ __device__ __forceinline__ int unit_of(int i) {
 // 5e-3 off in the 2-norm, where the roundings of dS and the output alone give 2.4e-3).  It is
 // sum P dP in fp32, S and dP by tensor instructions, 16 rows and 8 keys a warp.  The error falls
 // with the root of the number of keys: from nine on it is under 0.7 of the rounding of dS, and o as
-// given does.  The grid's first `again` blocks are for these rows, next to the others rather than
+// given does.  (3 x 1000 rows, 8 heads: 33.6 -> 34.3 us a backward; 8192 rows, 32 heads on 8, all with
+// eight keys: 188 -> 247.)  The grid's first `again` blocks are for these rows, next to the others rather than
 // behind them.
 constexpr int kStatRows = 4, kFewKeys = 8;
 template <int D>

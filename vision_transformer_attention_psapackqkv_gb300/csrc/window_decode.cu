@@ -30,14 +30,14 @@
 // their 24 bits: large keys that differ little then stand off by more than P's rounding.)  The
 // query is in fp16 too, each group of 32 channels scaled by a power of two of its own to a
 // maximum of 1 .. 2, so that what is lost is at most 2^-25 of the group's largest channel; bf16's
-// 8 bits fit down to 2^-17 of it.  V: 128 + n in bf16 (P times a scale needs its range), shifted on the
-// multipliers, less 136, exactly.  A key's scale, times the query's power of two, multiplies its
-// fp32 partial score of each group; a value's scale multiplies the probability before it is
+// 8 bits fit down to 2^-17 of it.  V: 128 + n in bf16 (P times a scale needs its range), shifted on
+// the multipliers, less 136, exactly.  A key's scale, times the query's power of two, multiplies
+// its fp32 partial score of each group; a value's scale multiplies the probability before it is
 // rounded to bf16.
 //
-// Measured: bf16, 32 sequences of up to 8192 keys, 4096 visible, 32 heads of 128 on 8: 84 us (5.9
-// TB/s, 0.89 of the copy bandwidth); 4 bits, 16 sequences of up to 32768 keys: 114 us (3.4 TB/s,
-// 0.51; the integer pipe is busy 65 % of the time, tensor instructions 19 %).  One sequence of
+// Measured: bf16, 32 sequences of up to 8192 keys, 4096 visible, 32 heads of 128 on 8: 85 us (5.9
+// TB/s, 0.88 of the copy bandwidth); 4 bits, 16 sequences of up to 32768 keys: 113 us (3.4 TB/s,
+// 0.51; the integer pipe is busy 62 % of the time, tensor instructions 18 %).  One sequence of
 // 1024 visible keys: 5.5 us with the join.
 #include <algorithm>
 

@@ -337,11 +337,12 @@ size_t psa_window_attn_bwd_workspace_size(psa_window_t p);
 /* Single-token form over a cache: n_q is 1, k_cache and v_cache are views [B,
  * num_kv_heads, n_k, d] of which sequence b has filled the first lens[b] rows (int32 on
  * the device, required; values above n_k count as n_k), its query's own key included:
- * the query stands at position lens[b] - 1 and window_right plays no part.  Only the
- * visible rows are read.  A sequence of length 0 or less gets output 0.  bf16, rounded
- * as in the forward (fp32: PSA_ERR_UNSUPPORTED), head_dim 64 or 128, any num_heads /
- * num_kv_heads.  workspace:
- * 16-byte aligned, at least psa_window_attn_decode_workspace_size(p) bytes. */
+ * the query stands at position lens[b] - 1 and window_right plays no part.  Rows that
+ * are not visible may hold anything (NaN included), and only blocks of 16 or 32 rows
+ * with a visible one are read.  A sequence of length 0 or less gets output 0.  bf16,
+ * rounded as in the forward (fp32: PSA_ERR_UNSUPPORTED), head_dim 64 or 128, any
+ * num_heads / num_kv_heads.  workspace: 16-byte aligned, at least
+ * psa_window_attn_decode_workspace_size(p) bytes. */
 psa_status_t psa_window_attn_decode(psa_rows_t q, psa_rows_t k_cache, psa_rows_t v_cache,
                                     const int *lens, psa_rows_t o, void *workspace,
                                     size_t ws_bytes, psa_window_t p, float scale,

@@ -291,6 +291,36 @@ psa_status_t psa_qk_norm_rope_bwd(psa_rows_t q, psa_rows_t k, const float *q_wei
 /* Bytes of device workspace for psa_qk_norm_rope_bwd (0 for an invalid problem). */
 size_t psa_qk_norm_rope_bwd_workspace_size(psa_norm_rope_t p);
 
+/* The same with positions of several axes (time, height and width of video, two axes of a
+ * feature map, text next to images): pair i of a token's channels turns with the entry
+ * [its position on axis axis_of_pair[i], i] of the tables. */
+typedef struct {
+    psa_norm_rope_t rope; /* max_pos: rows of the tables, which all axes index */
+    int axes;             /* 1 .. 4 */
+    int grid[4];          /* extents of the axes where positions is NULL, the last one innermost */
+    int normalize;        /* 1: norms as above; 0: y = R(pos) (w o x), eps plays no part */
+    unsigned char axis_of_pair[64]; /* below axes, for each of rope.rotary_dim / 2 pairs */
+} psa_rope_axes_t;
+
+/* positions: int32 [axes, B, N] on the device; a token with any position outside 0 ..
+ * max_pos - 1 is padding.  NULL: token n of every sequence is cell n of a grid in raster
+ * order (grid[0 .. axes - 1], each 1 .. max_pos, their product N).  Everything else as in
+ * psa_qk_norm_rope_fwd; with one axis and normalize 1 the results are the same bits. */
+psa_status_t psa_qk_norm_rope_axes_fwd(psa_rows_t q, psa_rows_t k, const float *q_weight,
+                                       const float *k_weight, const float *cos, const float *sin,
+                                       const int *positions, psa_rows_t q_out, psa_rows_t k_out,
+                                       psa_rope_axes_t p, cudaStream_t stream);
+
+/* Its backward, as psa_qk_norm_rope_bwd, with a workspace of at least
+ * psa_qk_norm_rope_bwd_workspace_size(p.rope) bytes.  With normalize 0, q and k are read for
+ * the weights' gradients alone. */
+psa_status_t psa_qk_norm_rope_axes_bwd(psa_rows_t q, psa_rows_t k, const float *q_weight,
+                                       const float *k_weight, const float *cos, const float *sin,
+                                       const int *positions, psa_rows_t dq_out, psa_rows_t dk_out,
+                                       psa_rows_t dq, psa_rows_t dk, float *dq_weight,
+                                       float *dk_weight, void *workspace, size_t ws_bytes,
+                                       psa_rope_axes_t p, cudaStream_t stream);
+
 /* Attention with a sliding window and first tokens that stay visible: q
  * [B, num_heads, n_q, d], k and v [B, num_kv_heads, n_k, d]; query head h reads
  * key/value head h / (num_heads / num_kv_heads).  Query row i stands at position

@@ -9,6 +9,8 @@ has not been built, the first call raises RuntimeError.
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 
 from . import _build
@@ -44,6 +46,11 @@ class PsaNormRope(ctypes.Structure):
                 ("eps", ctypes.c_float)]
 
 
+class PsaRopeAxes(ctypes.Structure):
+    _fields_ = [("rope", PsaNormRope), ("axes", ctypes.c_int), ("grid", ctypes.c_int * 4),
+                ("normalize", ctypes.c_int), ("axis_of_pair", ctypes.c_ubyte * 64)]
+
+
 class PsaWindow(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("num_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
                 ("n_q", ctypes.c_int), ("n_k", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int),
@@ -60,7 +67,8 @@ EXPORTED = (
     "flash_attn2_fwd", "flash_attn2_bwd_dq", "flash_attn2_bwd_dkdv", "psa_attention_fwd",
     "psa_attention_fwd_residual", "psa_attention_bwd", "psa_attention_bwd_dq", "psa_attention_bwd_dkdv", "psa_attention_bwd_noalloc",
     "psa_attention_bwd_workspace_size", "psa_qk_norm_rope_fwd", "psa_qk_norm_rope_bwd",
-    "psa_qk_norm_rope_bwd_workspace_size", "psa_window_attn_fwd", "psa_window_attn_bwd",
+    "psa_qk_norm_rope_bwd_workspace_size", "psa_qk_norm_rope_axes_fwd", "psa_qk_norm_rope_axes_bwd",
+    "psa_window_attn_fwd", "psa_window_attn_bwd",
     "psa_window_attn_bwd_workspace_size", "psa_window_attn_decode", "psa_window_attn_decode_workspace_size",
     "psa_kv_append", "psa_kv4_append", "psa_kv4_read", "psa_window_attn_decode_kv4", "psa_status_string",
     "psa_get_last_device_error", "psa_debug_wait_timeout",
@@ -81,7 +89,7 @@ def load(path: str | None = None):
         raise RuntimeError(f"libpsa_gb300.so is not built ({path}); run __graft_entry__.build()")
     lib = ctypes.CDLL(path)
     P, I, F, S, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, PsaShape, ctypes.c_size_t
-    R, NR, WN, CA = PsaRows, PsaNormRope, PsaWindow, PsaCache
+    R, NR, RA, WN, CA = PsaRows, PsaNormRope, PsaRopeAxes, PsaWindow, PsaCache
     sigs = {
         "psa_qkv_conv": [P, P, P, P, I, I, I, I, I, P],
         "psa_pack_qkv": [P, P, S, P],
@@ -102,6 +110,8 @@ def load(path: str | None = None):
         "psa_qk_norm_rope_fwd": [R, R, P, P, P, P, P, R, R, NR, P],
         "psa_qk_norm_rope_bwd": [R, R, P, P, P, P, P, R, R, R, R, P, P, P, Z, NR, P],
         "psa_qk_norm_rope_bwd_workspace_size": [NR],
+        "psa_qk_norm_rope_axes_fwd": [R, R, P, P, P, P, P, R, R, RA, P],
+        "psa_qk_norm_rope_axes_bwd": [R, R, P, P, P, P, P, R, R, R, R, P, P, P, Z, RA, P],
         "psa_window_attn_fwd": [R, R, R, P, R, P, WN, F, P],
         "psa_window_attn_bwd": [R, R, R, R, R, P, P, R, R, R, P, Z, WN, F, P],
         "psa_window_attn_bwd_workspace_size": [WN],
@@ -333,14 +343,14 @@ def norm_rope_of(q, k, cos, eps: float = 1e-6, interleaved: bool = False) -> Psa
     return PsaNormRope(B, nh, k.shape[1], N, d, dtype_code(q), rot, int(bool(interleaved)), max_pos, float(eps))
 
 
-def _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p):
+def _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p, axes=()):
     import torch
 
     B, N, d, f32, t = p.B, p.N, p.head_dim, torch.float32, _type_of(p, q)
     table, by_q, by_k = (p.max_pos, p.rotary_dim // 2), (B, p.num_heads, N, d), (B, p.num_kv_heads, N, d)
     return by_q, by_k, (_rows(q, by_q, t, "q"), _rows(k, by_k, t, "k"), _dense(q_weight, (d,), f32, "q_weight"),
                         _dense(k_weight, (d,), f32, "k_weight"), _dense(cos, table, f32, "cos"),
-                        _dense(sin, table, f32, "sin"), _dense(positions, (B, N), torch.int32, "positions"))
+                        _dense(sin, table, f32, "sin"), _dense(positions, (*axes, B, N), torch.int32, "positions"))
 
 
 def psa_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, p: PsaNormRope,
@@ -365,6 +375,61 @@ def psa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, 
                 workspace), stream, *args, _rows(dq_out, by_q, t, "dq_out"), _rows(dk_out, by_k, t, "dk_out"),
                _rows(dq, by_q, t, "dq"), _rows(dk, by_k, t, "dk"), _dense(dq_weight, d, torch.float32, "dq_weight"),
                _dense(dk_weight, d, torch.float32, "dk_weight"), *_workspace(workspace, "psa_qk_norm_rope_bwd"), p)
+
+
+@functools.lru_cache(maxsize=64)
+def _axes_of_pairs(sections, alternate: bool):
+    """The axis of each pair of channels, as the C array that problems copy."""
+    if not 1 <= len(sections) <= 4 or min(sections) < 0 or sum(sections) > 64:
+        raise ValueError(f"sections {sections}: one to four axes with at most 64 pairs between them are possible")
+    pairs = [(i if alternate else 0, axis, i) for axis, n in enumerate(sections) for i in range(n)]
+    return (ctypes.c_ubyte * 64)(*(axis for _, axis, _ in sorted(pairs)))
+
+
+@functools.lru_cache(maxsize=64)
+def _grid_of(grid, axes: int, tokens: int):
+    if len(grid) != axes or min(grid) < 1 or math.prod(grid) != tokens:
+        raise ValueError(f"grid {grid}: {axes} extents with {tokens} cells between them are needed")
+    return (ctypes.c_int * 4)(*grid)
+
+
+_no_grid = (ctypes.c_int * 4)()
+
+
+def rope_axes_of(q, k, cos, sections, eps: float = 1e-6, interleaved: bool = False, alternate: bool = False,
+                 grid=None, normalize: bool = True) -> PsaRopeAxes:
+    """The problem of norm_rope_of with positions of several axes.  sections: how many pairs of
+    channels turn with each axis, rotary_dim / 2 between them; axis 0's come first, then axis 1's and
+    so on, or with `alternate` the axes take turns for as long as each has pairs left.  grid: the
+    extents of the axes (the last one innermost) of tokens in raster order, for calls without
+    positions."""
+    rope = norm_rope_of(q, k, cos, eps, interleaved)
+    of_pair, axes = _axes_of_pairs(tuple(sections), bool(alternate)), len(sections)
+    if 2 * sum(sections) != rope.rotary_dim:
+        raise ValueError(f"sections {tuple(sections)}: {rope.rotary_dim // 2} pairs between them are needed")
+    cells = _no_grid if grid is None else _grid_of(tuple(grid), axes, rope.N)
+    return PsaRopeAxes(rope, axes, cells, int(bool(normalize)), of_pair)
+
+
+def psa_qk_norm_rope_axes_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, p: PsaRopeAxes,
+                              stream=None):
+    by_q, by_k, args = _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p.rope, (p.axes,))
+    _on_device("psa_qk_norm_rope_axes_fwd", (q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out), stream,
+               *args, _rows(q_out, by_q, q.dtype, "q_out"), _rows(k_out, by_k, q.dtype, "k_out"), p)
+
+
+def psa_qk_norm_rope_axes_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk, dq_weight,
+                              dk_weight, workspace, p: PsaRopeAxes, stream=None):
+    """workspace: psa_qk_norm_rope_bwd_workspace_size(p.rope) bytes."""
+    import torch
+
+    by_q, by_k, args = _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p.rope, (p.axes,))
+    t, d = q.dtype, (p.rope.head_dim,)
+    _on_device("psa_qk_norm_rope_axes_bwd",
+               (q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk, dq_weight, dk_weight,
+                workspace), stream, *args, _rows(dq_out, by_q, t, "dq_out"), _rows(dk_out, by_k, t, "dk_out"),
+               _rows(dq, by_q, t, "dq"), _rows(dk, by_k, t, "dk"), _dense(dq_weight, d, torch.float32, "dq_weight"),
+               _dense(dk_weight, d, torch.float32, "dk_weight"), *_workspace(workspace, "psa_qk_norm_rope_axes_bwd"), p)
 
 
 def window_of(q, k, window_left: int = -1, window_right: int = 0, sinks: int = 0) -> PsaWindow:

@@ -51,6 +51,13 @@ __device__ __forceinline__ uint4 pack_vec(const float (&x)[4]) {
 }
 
 // ---------------------------------------------------------------- norms + rotation
+// Positions of several axes: which axis each pair of channels turns with, and where a token
+// stands on each.
+struct RopeAxes {
+  int axes, grid[4];     // grid: extents, the last axis innermost, where positions is null
+  uint32_t axis_of[4];   // two bits for each pair of channels
+  bool normalize;
+};
 template <typename T>
 struct NormRopeArgs {
   View<const T> q, k;        // inputs
@@ -58,12 +65,13 @@ struct NormRopeArgs {
   View<T> oq, ok;            // forward: outputs; backward: gradients of the inputs
   const float *wq, *wk;      // [d] or null
   const float *cos, *sin;    // [max_pos, rot / 2]
-  const int* positions;      // [B, N] or null
+  const int* positions;      // [B, N] or null; several axes: [axes, B, N]
   float *dwq, *dwk;          // backward: [d] or null
   float* ws;                 // backward: partial sums
   int B, nh, nkv, N, rot, max_pos;
   bool interleaved;
   float eps;
+  RopeAxes ax;               // several axes
 };
 // Most CTAs of the backward, each with a partial sum of one weight's gradient in the
 // workspace (four per SM).
@@ -72,6 +80,11 @@ template <typename T>
 cudaError_t launch_norm_rope_fwd(const NormRopeArgs<T>& a, int d, cudaStream_t st);
 template <typename T>
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs<T>& a, int d, cudaStream_t st);
+// The same over several axes.
+template <typename T>
+cudaError_t launch_norm_rope_axes_fwd(const NormRopeArgs<T>& a, int d, cudaStream_t st);
+template <typename T>
+cudaError_t launch_norm_rope_axes_bwd(const NormRopeArgs<T>& a, int d, cudaStream_t st);
 
 // ---------------------------------------------------------------- window attention
 // A window problem: query i stands at position i + off (off = n_k - n_q); it sees key j

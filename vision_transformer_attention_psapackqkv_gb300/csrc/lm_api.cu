@@ -71,14 +71,19 @@ psa_status_t check_norm_rope(const psa_norm_rope_t& p) {
   return PSA_OK;
 }
 
-psa_status_t check_tables(const float* qw, const float* kw, const float* cos, const float* sin,
-                          const int* positions, const psa_norm_rope_t& p) {
-  if (p.rotary_dim > 0 && (!cos || !sin)) return PSA_ERR_INVALID_ARG;
-  if (!positions && p.N > p.max_pos) return PSA_ERR_INVALID_ARG;
+psa_status_t check_table_alignment(const float* qw, const float* kw, const float* cos,
+                                   const float* sin, const int* positions) {
   if (!aligned(qw, 4) || !aligned(kw, 4) || !aligned(cos, 16) || !aligned(sin, 16) ||
       !aligned(positions, 4))
     return PSA_ERR_ALIGNMENT;
   return PSA_OK;
+}
+
+psa_status_t check_tables(const float* qw, const float* kw, const float* cos, const float* sin,
+                          const int* positions, const psa_norm_rope_t& p) {
+  if (p.rotary_dim > 0 && (!cos || !sin)) return PSA_ERR_INVALID_ARG;
+  if (!positions && p.N > p.max_pos) return PSA_ERR_INVALID_ARG;
+  return check_table_alignment(qw, kw, cos, sin, positions);
 }
 
 template <typename T>
@@ -114,7 +119,50 @@ psa_status_t run_norm_rope_bwd(psa::NormRopeArgs<T> a, psa_rows_t gq, psa_rows_t
   a.dwq = dwq;
   a.dwk = dwk;
   a.ws = static_cast<float*>(ws);
-  return from_cuda(psa::launch_norm_rope_bwd(a, d, st));
+  return from_cuda(a.ax.axes ? psa::launch_norm_rope_axes_bwd(a, d, st) : psa::launch_norm_rope_bwd(a, d, st));
+}
+
+// What the two backward entry points ask of their own arguments.
+psa_status_t check_norm_rope_bwd(psa_rows_t& dq_out, psa_rows_t& dk_out, psa_rows_t& dq, psa_rows_t& dk,
+                                 const psa_norm_rope_t& p) {
+  PSA_TRY(check_view(dq_out, p.B, p.num_heads, p.N, p.head_dim, p.dtype));
+  PSA_TRY(check_view(dk_out, p.B, p.num_kv_heads, p.N, p.head_dim, p.dtype));
+  PSA_TRY(check_view(dq, p.B, p.num_heads, p.N, p.head_dim, p.dtype));
+  return check_view(dk, p.B, p.num_kv_heads, p.N, p.head_dim, p.dtype);
+}
+psa_status_t check_norm_rope_ws(const float* dq_weight, const float* dk_weight, const void* ws,
+                                size_t ws_bytes, const psa_norm_rope_t& p) {
+  if (!ws) return PSA_ERR_INVALID_ARG;
+  if (!aligned(ws, 16) || !aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return PSA_ERR_ALIGNMENT;
+  return ws_bytes >= psa_qk_norm_rope_bwd_workspace_size(p) ? PSA_OK : PSA_ERR_INVALID_ARG;
+}
+
+psa_status_t check_axes(const psa_rope_axes_t& p, const float* cos, const float* sin,
+                        const int* positions) {
+  PSA_TRY(check_norm_rope(p.rope));
+  if (p.axes < 1 || p.axes > 4 || (p.normalize != 0 && p.normalize != 1)) return PSA_ERR_INVALID_ARG;
+  for (int i = 0; i < p.rope.rotary_dim / 2; ++i)
+    if (p.axis_of_pair[i] >= p.axes) return PSA_ERR_INVALID_ARG;
+  if (!positions) {
+    long long cells = 1;
+    for (int i = 0; i < p.axes; ++i) {
+      if (p.grid[i] < 1 || p.grid[i] > p.rope.max_pos) return PSA_ERR_INVALID_ARG;
+      cells *= p.grid[i];
+      if (cells > p.rope.N) return PSA_ERR_INVALID_ARG;
+    }
+    if (cells != p.rope.N) return PSA_ERR_INVALID_ARG;
+  }
+  return p.rope.rotary_dim > 0 && (!cos || !sin) ? PSA_ERR_INVALID_ARG : PSA_OK;
+}
+
+template <typename T>
+psa::NormRopeArgs<T> with_axes(psa::NormRopeArgs<T> a, const psa_rope_axes_t& p) {
+  a.ax.axes = p.axes;
+  a.ax.normalize = p.normalize != 0;
+  for (int i = 0; i < 4; ++i) a.ax.grid[i] = i < p.axes ? p.grid[i] : 1;
+  for (int i = 0; i < p.rope.rotary_dim / 2; ++i)
+    a.ax.axis_of[i / 16] |= (uint32_t)p.axis_of_pair[i] << (2 * (i % 16));
+  return a;
 }
 
 // ---------------------------------------------------------------- window attention
@@ -262,14 +310,9 @@ psa_status_t psa_qk_norm_rope_bwd(psa_rows_t q, psa_rows_t k, const float* q_wei
   PSA_TRY(check_norm_rope(p));
   PSA_TRY(check_view(q, p.B, p.num_heads, p.N, p.head_dim, p.dtype));
   PSA_TRY(check_view(k, p.B, p.num_kv_heads, p.N, p.head_dim, p.dtype));
-  PSA_TRY(check_view(dq_out, p.B, p.num_heads, p.N, p.head_dim, p.dtype));
-  PSA_TRY(check_view(dk_out, p.B, p.num_kv_heads, p.N, p.head_dim, p.dtype));
-  PSA_TRY(check_view(dq, p.B, p.num_heads, p.N, p.head_dim, p.dtype));
-  PSA_TRY(check_view(dk, p.B, p.num_kv_heads, p.N, p.head_dim, p.dtype));
+  PSA_TRY(check_norm_rope_bwd(dq_out, dk_out, dq, dk, p));
   PSA_TRY(check_tables(q_weight, k_weight, cos, sin, positions, p));
-  if (!ws) return PSA_ERR_INVALID_ARG;
-  if (!aligned(ws, 16) || !aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return PSA_ERR_ALIGNMENT;
-  if (ws_bytes < psa_qk_norm_rope_bwd_workspace_size(p)) return PSA_ERR_INVALID_ARG;
+  PSA_TRY(check_norm_rope_ws(dq_weight, dk_weight, ws, ws_bytes, p));
   if (p.dtype == PSA_DTYPE_F32)
     return run_norm_rope_bwd(
         norm_rope_args<float>(q, k, q_weight, k_weight, cos, sin, positions, dq, dk, p), dq_out,
@@ -277,6 +320,50 @@ psa_status_t psa_qk_norm_rope_bwd(psa_rows_t q, psa_rows_t k, const float* q_wei
   return run_norm_rope_bwd(
       norm_rope_args<__nv_bfloat16>(q, k, q_weight, k_weight, cos, sin, positions, dq, dk, p),
       dq_out, dk_out, dq_weight, dk_weight, ws, p.head_dim, st);
+}
+
+psa_status_t psa_qk_norm_rope_axes_fwd(psa_rows_t q, psa_rows_t k, const float* q_weight,
+                                       const float* k_weight, const float* cos, const float* sin,
+                                       const int* positions, psa_rows_t q_out, psa_rows_t k_out,
+                                       psa_rope_axes_t p, cudaStream_t st) {
+  PSA_TRY(check_axes(p, cos, sin, positions));
+  const psa_norm_rope_t& r = p.rope;
+  PSA_TRY(check_view(q, r.B, r.num_heads, r.N, r.head_dim, r.dtype));
+  PSA_TRY(check_view(k, r.B, r.num_kv_heads, r.N, r.head_dim, r.dtype));
+  PSA_TRY(check_view(q_out, r.B, r.num_heads, r.N, r.head_dim, r.dtype));
+  PSA_TRY(check_view(k_out, r.B, r.num_kv_heads, r.N, r.head_dim, r.dtype));
+  PSA_TRY(check_table_alignment(q_weight, k_weight, cos, sin, positions));
+  if (r.dtype == PSA_DTYPE_F32)
+    return from_cuda(psa::launch_norm_rope_axes_fwd(
+        with_axes(norm_rope_args<float>(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, r), p),
+        r.head_dim, st));
+  using T = __nv_bfloat16;
+  return from_cuda(psa::launch_norm_rope_axes_fwd(
+      with_axes(norm_rope_args<T>(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, r), p),
+      r.head_dim, st));
+}
+
+psa_status_t psa_qk_norm_rope_axes_bwd(psa_rows_t q, psa_rows_t k, const float* q_weight,
+                                       const float* k_weight, const float* cos, const float* sin,
+                                       const int* positions, psa_rows_t dq_out, psa_rows_t dk_out,
+                                       psa_rows_t dq, psa_rows_t dk, float* dq_weight,
+                                       float* dk_weight, void* ws, size_t ws_bytes,
+                                       psa_rope_axes_t p, cudaStream_t st) {
+  PSA_TRY(check_axes(p, cos, sin, positions));
+  const psa_norm_rope_t& r = p.rope;
+  PSA_TRY(check_view(q, r.B, r.num_heads, r.N, r.head_dim, r.dtype));
+  PSA_TRY(check_view(k, r.B, r.num_kv_heads, r.N, r.head_dim, r.dtype));
+  PSA_TRY(check_norm_rope_bwd(dq_out, dk_out, dq, dk, r));
+  PSA_TRY(check_table_alignment(q_weight, k_weight, cos, sin, positions));
+  PSA_TRY(check_norm_rope_ws(dq_weight, dk_weight, ws, ws_bytes, r));
+  if (r.dtype == PSA_DTYPE_F32)
+    return run_norm_rope_bwd(
+        with_axes(norm_rope_args<float>(q, k, q_weight, k_weight, cos, sin, positions, dq, dk, r), p),
+        dq_out, dk_out, dq_weight, dk_weight, ws, r.head_dim, st);
+  using T = __nv_bfloat16;
+  return run_norm_rope_bwd(
+      with_axes(norm_rope_args<T>(q, k, q_weight, k_weight, cos, sin, positions, dq, dk, r), p), dq_out,
+      dk_out, dq_weight, dk_weight, ws, r.head_dim, st);
 }
 
 psa_status_t psa_window_attn_fwd(psa_rows_t q, psa_rows_t k, psa_rows_t v, const int* lens,

@@ -48,6 +48,46 @@ __device__ __forceinline__ float dot(const float (&x)[VEC], const float (&y)[VEC
   return s.x + s.y;
 }
 
+// Where a token stands: its row of the tables, or one row for each axis.
+template <bool kAxes>
+struct Place {
+  int pos[kAxes ? 4 : 1];
+  bool valid;  // false: padding; pos is 0 then
+
+  template <typename T>
+  __device__ __forceinline__ Place(const NormRopeArgs<T>& a, unsigned token, int n, bool live) {
+    if constexpr (!kAxes) {
+      pos[0] = n;
+      if (a.positions && live) pos[0] = a.positions[token];
+      valid = live && pos[0] >= 0 && pos[0] < a.max_pos;
+      if (!valid) pos[0] = 0;
+    } else {
+      unsigned rest = n;
+      valid = live;
+#pragma unroll
+      for (int i = 3; i >= 0; --i) {
+        pos[i] = 0;
+        if (i >= a.ax.axes) continue;
+        if (a.positions) {
+          if (live) pos[i] = a.positions[(long long)i * a.B * a.N + token];
+        } else {
+          const unsigned up = rest / (unsigned)a.ax.grid[i];
+          pos[i] = rest - up * a.ax.grid[i];
+          rest = up;
+        }
+        valid &= pos[i] >= 0 && pos[i] < a.max_pos;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!valid) pos[i] = 0;
+    }
+  }
+  __device__ __forceinline__ int on(uint32_t axis) const {
+    if constexpr (!kAxes) return pos[0];
+    else return axis & 2 ? (axis & 1 ? pos[3] : pos[2]) : (axis & 1 ? pos[1] : pos[0]);
+  }
+};
+
 // One lane's part of a token's rotation: y = c o x + s o x', where x' is the partner
 // channel of each (in this lane, interleaved; in lane `partner`, split halves).
 template <int VEC>
@@ -56,9 +96,9 @@ struct Turn {
   int partner;
 
   // sign: +1 forward, -1 the inverse rotation
-  template <typename T>
-  __device__ __forceinline__ void load(const NormRopeArgs<T>& a, int pos, int lane_in_row,
-                                       float sign) {
+  template <bool kAxes, typename T>
+  __device__ __forceinline__ void load(const NormRopeArgs<T>& a, const Place<kAxes>& at,
+                                       int lane_in_row, float sign) {
     const int c0 = lane_in_row * VEC, half = a.rot / 2;
     const int lane = threadIdx.x & 31;
     partner = lane;
@@ -68,8 +108,44 @@ struct Turn {
       s[e] = 0.f;
     }
     if (c0 >= a.rot) return;
-    const float* ct = a.cos + (long long)pos * half;
-    const float* st = a.sin + (long long)pos * half;
+    uint32_t axis = 0;
+    if constexpr (kAxes) {
+      // the axes of this lane's pairs, two bits each (its first pair is a multiple of their
+      // number, so that they lie in one word); where they are not all the same each pair has a
+      // row of its own
+      constexpr uint32_t ones = 0x55555555u;
+      const int i0 = a.interleaved ? c0 / 2 : c0 < half ? c0 : c0 - half;
+      const int pairs = a.interleaved ? VEC / 2 : VEC;
+      const uint32_t mask = 0xffffu >> (16 - 2 * pairs);
+      const uint32_t axes = (a.ax.axis_of[i0 / 16] >> (2 * (i0 % 16))) & mask;
+      axis = axes & 3;
+      if (axes != (axis * ones & mask)) {
+        const float sg = a.interleaved || c0 >= half ? sign : -sign;
+        if (!a.interleaved) partner = c0 < half ? lane + half / VEC : lane - half / VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          if (e >= pairs) break;
+          const long long row = (long long)at.on(axes >> (2 * e)) * half + i0 + e;
+          const float cc = a.cos[row], ss = sg * a.sin[row];
+          if (a.interleaved) {
+            // (compile-time indexes: registers)
+#pragma unroll
+            for (int f = 0; f < VEC / 2; ++f)
+              if (f == e) {
+                c[2 * f] = c[2 * f + 1] = cc;
+                s[2 * f] = -ss;
+                s[2 * f + 1] = ss;
+              }
+          } else {
+            c[e] = cc;
+            s[e] = ss;
+          }
+        }
+        return;
+      }
+    }
+    const float* ct = a.cos + (long long)at.on(axis) * half;
+    const float* st = a.sin + (long long)at.on(axis) * half;
     if (a.interleaved) {
 #pragma unroll
       for (int e = 0; e < VEC; e += 4) {
@@ -147,7 +223,7 @@ __device__ __forceinline__ void load_weight(const float* w, int c0, float (&x)[V
 
 // A group takes HEADS heads of its token: blockIdx.y counts the chunks of q's heads (nqc of
 // them), then those of k's, so that no chunk holds heads of both.
-template <typename T, int D, int HEADS>
+template <typename T, int D, int HEADS, bool kAxes>
 __global__ void __launch_bounds__(kThreads, 3) norm_rope_fwd_kernel(const NormRopeArgs<T> a, int nqc) {
   constexpr int VEC = kVec<T>, LANES = D / VEC, GROUPS = kThreads / LANES;
   pdl_launch_dependents();
@@ -167,11 +243,9 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_fwd_kernel(const NormRo
 #pragma unroll
   for (int i = 0; i < HEADS; ++i)
     raw[i] = i < heads ? *reinterpret_cast<const uint4*>(in + i * in_sh) : make_uint4(0, 0, 0, 0);
-  int pos = n;
-  if (a.positions && live) pos = a.positions[token];
-  const bool valid = live && pos >= 0 && pos < a.max_pos;
+  const Place<kAxes> at(a, token, n, live);
   Turn<VEC> turn;
-  turn.load(a, valid ? pos : 0, lr, 1.f);
+  turn.load(a, at, lr, 1.f);
   float w[VEC];
   load_weight(is_q ? a.wq : a.wk, c0, w);
   turn.weigh(a.interleaved, w);
@@ -180,16 +254,17 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_fwd_kernel(const NormRo
     // y = r (R (w o x)): the root's factor comes last
     float x[VEC], y[VEC];
     turn.template apply<T>(a.interleaved, raw[i], x, y);
-    const float r = rsqrtf(group_sum<LANES>(dot(x, x)) * (1.f / D) + a.eps);
+    float r = 1.f;
+    if (!kAxes || a.ax.normalize) r = rsqrtf(group_sum<LANES>(dot(x, x)) * (1.f / D) + a.eps);
 #pragma unroll
     for (int e = 0; e < VEC; e += 2) set2(y + e, __fmul2_rn(at2(y + e), both(r)));
-    if (valid && i < heads) *reinterpret_cast<uint4*>(out + i * out_sh) = pack_vec(y);
+    if (at.valid && i < heads) *reinterpret_cast<uint4*>(out + i * out_sh) = pack_vec(y);
   }
 }
 
 // A CTA goes through tokens blockIdx.x * GROUPS + group, + gridDim.x * GROUPS, ... and a
 // chunk of heads of q or of k; its sum of g' o xhat is one row of partial sums.
-template <typename T, int D>
+template <typename T, int D, bool kAxes>
 __global__ void __launch_bounds__(kThreads, 2)
     norm_rope_bwd_kernel(const NormRopeArgs<T> a, int nqc, int heads_per) {
   constexpr int VEC = kVec<T>, LANES = D / VEC, GROUPS = kThreads / LANES;
@@ -203,6 +278,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int h0 = chunk * heads_per, heads = min((is_q ? a.nh : a.nkv) - h0, heads_per);
   const View<const T> in = is_q ? a.q : a.k, gin = is_q ? a.gq : a.gk;
   const View<T> out = is_q ? a.oq : a.ok;
+  // without norms dx does not depend on x, only the weight's gradient does
+  const bool norm = !kAxes || a.ax.normalize, read_x = norm || (is_q ? a.dwq : a.dwk);
   float w[VEC], dw[VEC];
   load_weight(is_q ? a.wq : a.wk, c0, w);
 #pragma unroll
@@ -212,13 +289,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     const unsigned token = t0 + grp;
     const bool live = token < tokens;
     const int b = live ? token / (unsigned)a.N : 0, n = live ? token - b * a.N : 0;
-    int pos = n;
-    if (a.positions && live) pos = a.positions[token];
-    const bool valid = live && pos >= 0 && pos < a.max_pos;
+    const Place<kAxes> at(a, token, n, live);
+    const bool valid = at.valid;
     const T *x0 = in.row(b, h0, n) + c0, *g0 = gin.row(b, h0, n) + c0;
     T* d0 = out.row(b, h0, n) + c0;
     Turn<VEC> turn;
-    turn.load(a, valid ? pos : 0, lr, -1.f);
+    turn.load(a, at, lr, -1.f);
     // the next kBatch heads' rows are on their way while these are worked on
     uint4 nx[kBatch], ng[kBatch];
     auto load = [&](int h) {
@@ -226,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < kBatch; ++i) {
         nx[i] = ng[i] = make_uint4(0, 0, 0, 0);
         if (valid && h + i < heads) {
-          nx[i] = *reinterpret_cast<const uint4*>(x0 + (h + i) * in.sh);
+          if (read_x) nx[i] = *reinterpret_cast<const uint4*>(x0 + (h + i) * in.sh);
           ng[i] = *reinterpret_cast<const uint4*>(g0 + (h + i) * gin.sh);
         }
       }
@@ -251,13 +327,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float ss = group_sum<LANES>(dot(x, x)), gx = group_sum<LANES>(dot(gw, x));
         // rows of padding, and those past the last head, hold zeros here: with r = 0 (without it
         // eps = 0 makes NaN of them) their share is 0 and their dx is 0
-        const float r = valid && h + i < heads ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
+        const float r = valid && h + i < heads ? norm ? rsqrtf(ss * (1.f / D) + a.eps) : 1.f : 0.f;
         const float2 r2 = both(r), back = both(-gx * r * r * (1.f / D));
 #pragma unroll
         for (int e = 0; e < VEC; e += 2) {
           const float2 xe = at2(x + e);
           set2(dw + e, __ffma2_rn(at2(g + e), __fmul2_rn(xe, r2), at2(dw + e)));
-          set2(x + e, __fmul2_rn(r2, __ffma2_rn(xe, back, at2(gw + e))));
+          set2(x + e, __fmul2_rn(r2, norm ? __ffma2_rn(xe, back, at2(gw + e)) : at2(gw + e)));
         }
         if (live && h + i < heads) *reinterpret_cast<uint4*>(d0 + (h + i) * out.sh) = pack_vec(x);
       }
@@ -302,22 +378,24 @@ __global__ void __launch_bounds__(1024)
 
 int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-template <typename T, int D, int HEADS>
-cudaError_t fwd(const NormRopeArgs<T>& a, cudaStream_t st) {
+template <typename T, int D, int HEADS, bool kAxes>
+cudaError_t fwd_heads(const NormRopeArgs<T>& a, cudaStream_t st) {
   constexpr int GROUPS = kThreads / (D / kVec<T>);
   const int nqc = cdiv(a.nh, HEADS), nkc = cdiv(a.nkv, HEADS);
-  return launch_pdl(norm_rope_fwd_kernel<T, D, HEADS>,
+  return launch_pdl(norm_rope_fwd_kernel<T, D, HEADS, kAxes>,
                     dim3(cdiv((long long)a.B * a.N, GROUPS), nqc + nkc), dim3(kThreads), 0, st, a, nqc);
 }
 
-template <typename T, int D>
+template <bool kAxes, typename T, int D>
 cudaError_t fwd(const NormRopeArgs<T>& a, cudaStream_t st) {
   // eight heads per group, or four, once that still fills the device's threads
   const long long lanes = (long long)a.B * a.N * (a.nh + a.nkv) * (D / kVec<T>), full = 152 * 2048;
-  return lanes / 8 >= full ? fwd<T, D, 8>(a, st) : lanes / 4 >= full ? fwd<T, D, 4>(a, st) : fwd<T, D, 1>(a, st);
+  return lanes / 8 >= full   ? fwd_heads<T, D, 8, kAxes>(a, st)
+         : lanes / 4 >= full ? fwd_heads<T, D, 4, kAxes>(a, st)
+                             : fwd_heads<T, D, 1, kAxes>(a, st);
 }
 
-template <typename T, int D>
+template <bool kAxes, typename T, int D>
 cudaError_t bwd(const NormRopeArgs<T>& a, cudaStream_t st) {
   constexpr int GROUPS = kThreads / (D / kVec<T>);
   // up to four CTAs per SM between the chunks of heads, each with one partial row: chunks of
@@ -328,7 +406,7 @@ cudaError_t bwd(const NormRopeArgs<T>& a, cudaStream_t st) {
   heads_per = std::max(heads_per, cdiv(std::max(a.nh, a.nkv), kNormRopeParts / 2));
   const int nqc = cdiv(a.nh, heads_per), nkc = cdiv(a.nkv, heads_per);
   const int gx = std::max(1, std::min(blocks, kNormRopeParts / (nqc + nkc)));
-  cudaError_t e = launch_pdl(norm_rope_bwd_kernel<T, D>, dim3(gx, nqc + nkc), dim3(kThreads), 0, st,
+  cudaError_t e = launch_pdl(norm_rope_bwd_kernel<T, D, kAxes>, dim3(gx, nqc + nkc), dim3(kThreads), 0, st,
                              a, nqc, heads_per);
   if (e != cudaSuccess || (!a.dwq && !a.dwk)) return e;
   return launch_pdl(norm_rope_dw_kernel, dim3(D / 32, 2), dim3(1024), 0, st, (const float*)a.ws,
@@ -337,17 +415,17 @@ cudaError_t bwd(const NormRopeArgs<T>& a, cudaStream_t st) {
 
 }  // namespace
 
-template <typename T>
-cudaError_t launch_norm_rope_fwd(const NormRopeArgs<T>& a, int d, cudaStream_t st) {
-  return d == 32 ? fwd<T, 32>(a, st) : d == 64 ? fwd<T, 64>(a, st) : fwd<T, 128>(a, st);
-}
-template <typename T>
-cudaError_t launch_norm_rope_bwd(const NormRopeArgs<T>& a, int d, cudaStream_t st) {
-  return d == 32 ? bwd<T, 32>(a, st) : d == 64 ? bwd<T, 64>(a, st) : bwd<T, 128>(a, st);
-}
-template cudaError_t launch_norm_rope_fwd(const NormRopeArgs<float>&, int, cudaStream_t);
-template cudaError_t launch_norm_rope_fwd(const NormRopeArgs<__nv_bfloat16>&, int, cudaStream_t);
-template cudaError_t launch_norm_rope_bwd(const NormRopeArgs<float>&, int, cudaStream_t);
-template cudaError_t launch_norm_rope_bwd(const NormRopeArgs<__nv_bfloat16>&, int, cudaStream_t);
+#define PSA_NORM_ROPE(NAME, WHAT, AXES)                                                              \
+  template <typename T>                                                                            \
+  cudaError_t NAME(const NormRopeArgs<T>& a, int d, cudaStream_t st) {                             \
+    return d == 32 ? WHAT<AXES, T, 32>(a, st) : d == 64 ? WHAT<AXES, T, 64>(a, st) : WHAT<AXES, T, 128>(a, st); \
+  }                                                                                                \
+  template cudaError_t NAME(const NormRopeArgs<float>&, int, cudaStream_t);                        \
+  template cudaError_t NAME(const NormRopeArgs<__nv_bfloat16>&, int, cudaStream_t);
+PSA_NORM_ROPE(launch_norm_rope_fwd, fwd, false)
+PSA_NORM_ROPE(launch_norm_rope_bwd, bwd, false)
+PSA_NORM_ROPE(launch_norm_rope_axes_fwd, fwd, true)
+PSA_NORM_ROPE(launch_norm_rope_axes_bwd, bwd, true)
+#undef PSA_NORM_ROPE
 
 }  // namespace psa

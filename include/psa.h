@@ -426,6 +426,55 @@ psa_status_t psa_window_attn_decode_kv4(psa_rows_t q, const void *k_codes, const
                                         size_t ws_bytes, psa_window_t p, float scale,
                                         cudaStream_t stream);
 
+/* Attention weights summed for each key of a cache, and the eviction of the keys that have
+ * least.  weights: fp32 [B, num_kv_heads, n_k], dense: a key/value head's row j holds the sum,
+ * over the query heads that share it and all queries so far, of the softmax probability that key
+ * j had.  Rows behind a sequence's length are kept at 0 by the caller, or by psa_kv_evict.
+ *
+ * psa_window_attn_decode that also adds the probabilities of its step's visible keys to weights
+ * (fp32, from the scores before any rounding; heads are added in order: reruns are bitwise
+ * identical; entries of keys that are not visible are left as they are).  The same partial sums,
+ * joined in another order, make the output.  Same sizes and errors, with up to 4096 query heads
+ * for each key/value head (PSA_ERR_UNSUPPORTED); workspace: at least
+ * psa_window_attn_decode_weights_workspace_size(p) bytes, which hold the step's scores. */
+psa_status_t psa_window_attn_decode_weights(psa_rows_t q, psa_rows_t k_cache, psa_rows_t v_cache,
+                                            const int *lens, psa_rows_t o, float *weights,
+                                            void *workspace, size_t ws_bytes, psa_window_t p,
+                                            float scale, cudaStream_t stream);
+
+/* Bytes of device workspace for psa_window_attn_decode_weights (0 for an invalid problem). */
+size_t psa_window_attn_decode_weights_workspace_size(psa_window_t p);
+
+/* Eviction: every sequence that has more than keep rows (lens, int32 [B] on the device) is cut to
+ * keep rows in each key/value head.  Those with the largest weights stay; of equal weights those
+ * of the lower rows (0 and -0 are equal; NaN is above infinity); before all others those at
+ * positions below sinks and at the last `recent` positions: positions, int32 [B, num_kv_heads,
+ * max_len], dense, says for each row which token of its sequence it holds, and the last one is the
+ * largest among a head's rows.  What stays lies in rows 0 .. keep - 1 afterwards: a row that stays
+ * and lies there already is not touched, and those that stay from behind fill the gaps, in the
+ * order of their rows.  (The order of a cache's rows plays no part in attention over all of
+ * them.)  The caches are changed in place, rows from keep on left as they are.
+ *
+ * weights_out, positions_out: the same for the rows that stay; in front of the old length and
+ * behind them weights_out is set to 0, so that rows appended later start from nothing, and
+ * positions_out is left as it was.  They may be the same arrays as weights and positions.  lens_out
+ * [B]: min(lens, keep) (0 for a negative one), not the same array as lens.  All outputs are written for the sequences that
+ * have no more than keep rows too.  max_len up to 2^24 (PSA_ERR_UNSUPPORTED); head_dim 64 or 128;
+ * bf16 or fp32. */
+typedef struct {
+    int B, num_kv_heads, max_len, head_dim;
+    psa_dtype_t dtype;
+    int keep, sinks, recent; /* sinks + recent <= keep */
+} psa_evict_t;
+
+psa_status_t psa_kv_evict(const float *weights, const int *positions, const int *lens,
+                          psa_rows_t k_cache, psa_rows_t v_cache, float *weights_out,
+                          int *positions_out, int *lens_out, void *workspace, size_t ws_bytes,
+                          psa_evict_t p, cudaStream_t stream);
+
+/* Bytes of device workspace for psa_kv_evict (0 for an invalid problem). */
+size_t psa_kv_evict_workspace_size(psa_evict_t p);
+
 /* ---- status ------------------------------------------------------------------- */
 
 /* Static description of a status code. */

@@ -62,6 +62,12 @@ class PsaCache(ctypes.Structure):
                 ("max_len", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
+class PsaEvict(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("num_kv_heads", ctypes.c_int), ("max_len", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("keep", ctypes.c_int), ("sinks", ctypes.c_int),
+                ("recent", ctypes.c_int)]
+
+
 EXPORTED = (
     "psa_qkv_conv", "psa_pack_qkv", "psa_unpack_qkv", "psa_extract_v", "psa_merge_attn", "psa_unmerge_attn",
     "flash_attn2_fwd", "flash_attn2_bwd_dq", "flash_attn2_bwd_dkdv", "psa_attention_fwd",
@@ -70,7 +76,9 @@ EXPORTED = (
     "psa_qk_norm_rope_bwd_workspace_size", "psa_qk_norm_rope_axes_fwd", "psa_qk_norm_rope_axes_bwd",
     "psa_window_attn_fwd", "psa_window_attn_bwd",
     "psa_window_attn_bwd_workspace_size", "psa_window_attn_decode", "psa_window_attn_decode_workspace_size",
-    "psa_kv_append", "psa_kv4_append", "psa_kv4_read", "psa_window_attn_decode_kv4", "psa_status_string",
+    "psa_kv_append", "psa_kv4_append", "psa_kv4_read", "psa_window_attn_decode_kv4",
+    "psa_window_attn_decode_weights", "psa_window_attn_decode_weights_workspace_size", "psa_kv_evict",
+    "psa_kv_evict_workspace_size", "psa_status_string",
     "psa_get_last_device_error", "psa_debug_wait_timeout",
 )
 
@@ -89,7 +97,7 @@ def load(path: str | None = None):
         raise RuntimeError(f"libpsa_gb300.so is not built ({path}); run __graft_entry__.build()")
     lib = ctypes.CDLL(path)
     P, I, F, S, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, PsaShape, ctypes.c_size_t
-    R, NR, RA, WN, CA = PsaRows, PsaNormRope, PsaRopeAxes, PsaWindow, PsaCache
+    R, NR, RA, WN, CA, EV = PsaRows, PsaNormRope, PsaRopeAxes, PsaWindow, PsaCache, PsaEvict
     sigs = {
         "psa_qkv_conv": [P, P, P, P, I, I, I, I, I, P],
         "psa_pack_qkv": [P, P, S, P],
@@ -121,6 +129,10 @@ def load(path: str | None = None):
         "psa_kv4_append": [R, R, P, P, P, P, P, P, CA, P],
         "psa_kv4_read": [P, P, P, P, R, R, CA, P],
         "psa_window_attn_decode_kv4": [R, P, P, P, P, P, R, P, Z, WN, F, P],
+        "psa_window_attn_decode_weights": [R, R, R, P, R, P, P, Z, WN, F, P],
+        "psa_window_attn_decode_weights_workspace_size": [WN],
+        "psa_kv_evict": [P, P, P, R, R, P, P, P, P, Z, EV, P],
+        "psa_kv_evict_workspace_size": [EV],
         "psa_status_string": [I],
         "psa_get_last_device_error": [P],
         "psa_debug_wait_timeout": [ctypes.c_ulonglong, P],
@@ -129,7 +141,8 @@ def load(path: str | None = None):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
-    for name in ("psa_attention_bwd", "psa_qk_norm_rope_bwd", "psa_window_attn_bwd", "psa_window_attn_decode"):
+    for name in ("psa_attention_bwd", "psa_qk_norm_rope_bwd", "psa_window_attn_bwd", "psa_window_attn_decode",
+                 "psa_window_attn_decode_weights", "psa_kv_evict"):
         getattr(lib, name + "_workspace_size").restype = ctypes.c_size_t
     lib.psa_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -546,6 +559,52 @@ def psa_window_attn_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, lens, o,
     _on_device("psa_window_attn_decode_kv4", (q, *cache, lens, o, workspace), stream, _rows(q, by_q, t, "q"),
                *_kv4(*cache, B, nkv, max_len, d), _lens(lens, win), _rows(o, by_q, t, "o"),
                *_workspace(workspace, "psa_window_attn_decode_kv4"), win, scale)
+
+
+def _weights(t, by_k, what: str = "weights"):
+    import torch
+
+    if t is None:
+        raise ValueError(f"{what} are required")
+    return _dense(t, by_k[:3], torch.float32, what)
+
+
+def psa_window_attn_decode_weights_workspace_size(win: PsaWindow) -> int:
+    return int(load().psa_window_attn_decode_weights_workspace_size(win))
+
+
+def psa_window_attn_decode_weights(q, k_cache, v_cache, lens, o, weights, workspace, win: PsaWindow, scale: float,
+                                   stream=None):
+    by_q, by_k = _window_shapes(win)
+    t = _type_of(win, q)
+    _on_device("psa_window_attn_decode_weights", (q, k_cache, v_cache, lens, o, weights, workspace), stream,
+               _rows(q, by_q, t, "q"), _rows(k_cache, by_k, t, "k_cache"), _rows(v_cache, by_k, t, "v_cache"),
+               _lens(lens, win), _rows(o, by_q, t, "o"), _weights(weights, by_k),
+               *_workspace(workspace, "psa_window_attn_decode_weights"), win, scale)
+
+
+def evict_of(k_cache, keep: int, sinks: int = 0, recent: int = 0) -> PsaEvict:
+    """The problem of cutting caches like k_cache [B, num_kv_heads, max_len, d] to `keep` rows."""
+    B, nkv, max_len, d = k_cache.shape
+    # no length is past max_len, no position past a C int (which would drop the upper bits)
+    keep, sinks, recent = (max(-1, min(int(x), 2 ** 31 - 1)) for x in (keep, sinks, recent))
+    return PsaEvict(B, nkv, max_len, d, dtype_code(k_cache), keep, sinks, recent)
+
+
+def psa_kv_evict_workspace_size(p: PsaEvict) -> int:
+    return int(load().psa_kv_evict_workspace_size(p))
+
+
+def psa_kv_evict(weights, positions, lens, k_cache, v_cache, weights_out, positions_out, lens_out, workspace,
+                 p: PsaEvict, stream=None):
+    import torch
+
+    cache, t, i32 = (p.B, p.num_kv_heads, p.max_len, p.head_dim), _type_of(p, k_cache), torch.int32
+    _on_device("psa_kv_evict", (k_cache, v_cache, weights, positions, lens, weights_out, positions_out, lens_out,
+                                workspace), stream, _weights(weights, cache), _dense(positions, cache[:3], i32, "positions"),
+               _dense(lens, (p.B,), i32, "lens"), _rows(k_cache, cache, t, "k_cache"), _rows(v_cache, cache, t, "v_cache"),
+               _weights(weights_out, cache, "weights_out"), _dense(positions_out, cache[:3], i32, "positions_out"),
+               _dense(lens_out, (p.B,), i32, "lens_out"), *_workspace(workspace, "psa_kv_evict"), p)
 
 
 def psa_get_last_device_error(stream=None) -> int:

@@ -172,6 +172,20 @@ cudaError_t launch_kv4_read(const CacheArgs& c, const void* kcodes, const void* 
                             const void* vcodes, const void* vscales, View<T> k, View<T> v, int d,
                             cudaStream_t st);
 
+// ---------------------------------------------------------------- eviction from a cache
+struct EvictArgs {
+  int B, nkv, max_len, keep, sinks, recent;
+  const float* weights;    // [B, nkv, max_len]
+  const int* positions;    // [B, nkv, max_len]
+  const int* lens;         // [B]
+  View<uint4> k, v;        // strides in 16 bytes
+  float* weights_out;
+  int *positions_out, *lens_out;
+  int *counts, *moves;     // workspace: moves of each list, then their sources and targets
+};
+size_t evict_ws_bytes(int lists, int keep, int max_len);
+cudaError_t launch_kv_evict(EvictArgs a, int row16, void* ws, cudaStream_t st);
+
 // ---------------------------------------------------------------- one token over a cache
 struct DecodeArgs {
   Window w;  // nq = 1; lens set
@@ -180,10 +194,16 @@ struct DecodeArgs {
   const void *kcodes, *kscales, *vcodes, *vscales;  // 4-bit cache
   float* ws;
   float scale;
+  // along with weights for each key: [B, nkv, n_k], the scores' place in the workspace, and how many
+  // keys of a list have one
+  float *weights, *scores;
+  long long slots;
 };
 // Parts that a sequence's keys are cut into, by the problem's sizes alone.
 int decode_splits(const Window& w);
 size_t decode_ws_bytes(const Window& w, int d);
 cudaError_t launch_window_decode(const DecodeArgs& a, int d, bool kv4, cudaStream_t st);
+size_t decode_weights_ws_bytes(const Window& w, int d);
+cudaError_t launch_window_decode_weights(const DecodeArgs& a, int d, cudaStream_t st);
 
 }  // namespace psa

@@ -251,9 +251,21 @@ psa::CacheArgs cache_args(const psa_cache_t& p, const int* starts, const int* co
   return psa::CacheArgs{p.B, p.num_kv_heads, p.N, p.max_len, starts, counts};
 }
 
-// What both single-token entry points ask of the problem, q, o and the workspace.
+psa_status_t check_evict(const psa_evict_t& p) {
+  if (p.B <= 0 || p.num_kv_heads <= 0 || p.max_len <= 0 || p.head_dim <= 0 || !known(p.dtype) ||
+      p.keep <= 0 || p.sinks < 0 || p.recent < 0 || (long long)p.sinks + p.recent > p.keep)
+    return PSA_ERR_INVALID_ARG;
+  if (p.head_dim != 64 && p.head_dim != 128) return PSA_ERR_UNSUPPORTED;
+  // (so that a list's moves, in pieces of 16 bytes, are an int)
+  if ((long long)p.B * p.num_kv_heads > 65535 || p.max_len > (1 << 24)) return PSA_ERR_UNSUPPORTED;
+  return PSA_OK;
+}
+
+constexpr int kMaxWeightGroup = 4096;  // query heads of a key/value head, whose statistics a CTA holds
+
+// What the single-token entry points ask of the problem, q, o and the workspace.
 psa_status_t check_decode(const psa_window_t& p, psa_rows_t& q, psa_rows_t& o, const int* lens,
-                          const void* ws, size_t ws_bytes, float scale) {
+                          const void* ws, size_t ws_bytes, size_t ws_least, float scale) {
   PSA_TRY(check_window(p));
   PSA_TRY(check_scale(scale));
   if (p.n_q != 1 || !lens || !ws) return PSA_ERR_INVALID_ARG;
@@ -261,7 +273,7 @@ psa_status_t check_decode(const psa_window_t& p, psa_rows_t& q, psa_rows_t& o, c
   PSA_TRY(check_view(q, p.B, p.num_heads, 1, p.head_dim, p.dtype));
   PSA_TRY(check_view(o, p.B, p.num_heads, 1, p.head_dim, p.dtype));
   if (!aligned(ws, 16) || !aligned(lens, 4)) return PSA_ERR_ALIGNMENT;
-  return ws_bytes >= psa_window_attn_decode_workspace_size(p) ? PSA_OK : PSA_ERR_INVALID_ARG;
+  return ws_bytes >= ws_least ? PSA_OK : PSA_ERR_INVALID_ARG;
 }
 
 psa::DecodeArgs decode_args(const psa_window_t& p, const int* lens, psa_rows_t q, psa_rows_t o,
@@ -419,7 +431,7 @@ size_t psa_window_attn_decode_workspace_size(psa_window_t p) {
 psa_status_t psa_window_attn_decode(psa_rows_t q, psa_rows_t k_cache, psa_rows_t v_cache,
                                     const int* lens, psa_rows_t o, void* ws, size_t ws_bytes,
                                     psa_window_t p, float scale, cudaStream_t st) {
-  PSA_TRY(check_decode(p, q, o, lens, ws, ws_bytes, scale));
+  PSA_TRY(check_decode(p, q, o, lens, ws, ws_bytes, psa_window_attn_decode_workspace_size(p), scale));
   PSA_TRY(check_view(k_cache, p.B, p.num_kv_heads, p.n_k, p.head_dim, p.dtype));
   PSA_TRY(check_view(v_cache, p.B, p.num_kv_heads, p.n_k, p.head_dim, p.dtype));
   psa::DecodeArgs a = decode_args(p, lens, q, o, ws, scale);
@@ -428,11 +440,60 @@ psa_status_t psa_window_attn_decode(psa_rows_t q, psa_rows_t k_cache, psa_rows_t
   return from_cuda(psa::launch_window_decode(a, p.head_dim, false, st));
 }
 
+size_t psa_window_attn_decode_weights_workspace_size(psa_window_t p) {
+  if (check_window(p) != PSA_OK || p.n_q != 1 || p.num_heads / p.num_kv_heads > kMaxWeightGroup) return 0;
+  return psa::decode_weights_ws_bytes(window(p, nullptr), p.head_dim);
+}
+
+psa_status_t psa_window_attn_decode_weights(psa_rows_t q, psa_rows_t k_cache, psa_rows_t v_cache,
+                                            const int* lens, psa_rows_t o, float* weights, void* ws,
+                                            size_t ws_bytes, psa_window_t p, float scale,
+                                            cudaStream_t st) {
+  PSA_TRY(check_decode(p, q, o, lens, ws, ws_bytes, psa_window_attn_decode_weights_workspace_size(p), scale));
+  PSA_TRY(check_view(k_cache, p.B, p.num_kv_heads, p.n_k, p.head_dim, p.dtype));
+  PSA_TRY(check_view(v_cache, p.B, p.num_kv_heads, p.n_k, p.head_dim, p.dtype));
+  if (!weights) return PSA_ERR_INVALID_ARG;
+  if (!aligned(weights, 4)) return PSA_ERR_ALIGNMENT;
+  if (p.num_heads / p.num_kv_heads > kMaxWeightGroup) return PSA_ERR_UNSUPPORTED;
+  psa::DecodeArgs a = decode_args(p, lens, q, o, ws, scale);
+  a.k = view<const __nv_bfloat16>(k_cache);
+  a.v = view<const __nv_bfloat16>(v_cache);
+  a.weights = weights;
+  return from_cuda(psa::launch_window_decode_weights(a, p.head_dim, st));
+}
+
+size_t psa_kv_evict_workspace_size(psa_evict_t p) {
+  return check_evict(p) == PSA_OK ? round256(psa::evict_ws_bytes(p.B * p.num_kv_heads, p.keep, p.max_len)) : 0;
+}
+
+psa_status_t psa_kv_evict(const float* weights, const int* positions, const int* lens,
+                          psa_rows_t k_cache, psa_rows_t v_cache, float* weights_out,
+                          int* positions_out, int* lens_out, void* ws, size_t ws_bytes,
+                          psa_evict_t p, cudaStream_t st) {
+  PSA_TRY(check_evict(p));
+  if (!weights || !positions || !lens || !weights_out || !positions_out || !lens_out || !ws ||
+      lens_out == lens)
+    return PSA_ERR_INVALID_ARG;
+  PSA_TRY(check_view(k_cache, p.B, p.num_kv_heads, p.max_len, p.head_dim, p.dtype));
+  PSA_TRY(check_view(v_cache, p.B, p.num_kv_heads, p.max_len, p.head_dim, p.dtype));
+  if (!aligned(weights, 4) || !aligned(positions, 4) || !aligned(lens, 4) || !aligned(weights_out, 4) ||
+      !aligned(positions_out, 4) || !aligned(lens_out, 4) || !aligned(ws, 16))
+    return PSA_ERR_ALIGNMENT;
+  if (ws_bytes < psa_kv_evict_workspace_size(p)) return PSA_ERR_INVALID_ARG;
+  const int per = 16 / elem_bytes(p.dtype);
+  auto rows = [&](const psa_rows_t& v) {
+    return View<uint4>{static_cast<uint4*>(v.ptr), v.stride_b / per, v.stride_h / per, v.stride_n / per};
+  };
+  psa::EvictArgs a{p.B, p.num_kv_heads, p.max_len, p.keep, p.sinks, p.recent, weights, positions, lens,
+                   rows(k_cache), rows(v_cache), weights_out, positions_out, lens_out, nullptr, nullptr};
+  return from_cuda(psa::launch_kv_evict(a, p.head_dim / per, ws, st));
+}
+
 psa_status_t psa_window_attn_decode_kv4(psa_rows_t q, const void* k_codes, const void* k_scales,
                                         const void* v_codes, const void* v_scales, const int* lens,
                                         psa_rows_t o, void* ws, size_t ws_bytes, psa_window_t p,
                                         float scale, cudaStream_t st) {
-  PSA_TRY(check_decode(p, q, o, lens, ws, ws_bytes, scale));
+  PSA_TRY(check_decode(p, q, o, lens, ws, ws_bytes, psa_window_attn_decode_workspace_size(p), scale));
   PSA_TRY(check_kv4(k_codes, k_scales, v_codes, v_scales));
   psa::DecodeArgs a = decode_args(p, lens, q, o, ws, scale);
   a.kcodes = k_codes;

@@ -51,6 +51,7 @@ namespace {
 
 constexpr int kWarps = 4;        // per CTA
 constexpr int kThreads = 32 * kWarps;
+constexpr int kWeightThreads = 256;
 constexpr int kLongBlock = 32;   // most keys that a warp takes at a time
 constexpr float kLog2eD = 1.4426950408889634074f;
 
@@ -437,7 +438,10 @@ struct Cache<D, HT, true, kShort> {
   }
 };
 
-template <int D, int HT, bool kKv4, bool kShort>
+// kPart: a partial result is left even where a sequence has one part only.
+// kScores: so are the scores of the visible keys (log2 units), for window_weights_kernel: those of a
+// key's query heads side by side, keys in the order of the blocks.
+template <int D, int HT, bool kKv4, bool kShort, bool kPart, bool kScores>
 __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 : 4)
     window_decode_kernel(const DecodeArgs a) {
   using C = Cache<D, HT, kKv4, kShort>;
@@ -509,6 +513,19 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 
         c.drop_v(u, value);
         c.drop_scales(u, mine);
       }
+    }
+    if constexpr (kScores) {
+      // (-infinity is a hidden key: the value is not read again)
+      float* dst = a.scores + (((long long)b * a.w.nkv + h) * a.slots + (long long)blk * kBlock + j0 - first) * group + g0;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = 16 * u + 8 * (e >> 1) + r, head = 8 * ht + 2 * t + (e & 1);
+            if (j0 + key >= first && j0 + key < bl.len && head < heads) dst[key * group + head] = s[u][ht][e];
+          }
     }
     bool grow = false;
     float top2[HT][2];
@@ -603,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
       sum += sm_l[w][row] * (sm_m[w][row] == -INFINITY ? 0.f : fast_exp2(sm_m[w][row] - n));
-    if (gridDim.x == 1) {
+    if (!kPart && gridDim.x == 1) {
       a.o.row(b, h0 + row, 0)[ch] = __float2bfloat16_rn(sum != 0.f ? sm_o[row][ch] / sum : 0.f);
     } else {
       // partial result: D outputs relative to the maximum n, then n and the sum
@@ -636,19 +653,101 @@ __global__ void __launch_bounds__(D) window_join_kernel(const DecodeArgs a, int 
   a.o.row(b, h, 0)[threadIdx.x] = __float2bfloat16_rn(l != 0.f ? o / l : 0.f);
 }
 
+// Joins the partial results of a key/value head's query heads (blockIdx.x 0), and adds what its
+// keys got from them to their weights: p = 2^(s - m) / l, summed over the heads in order.
+template <int D>
+__global__ void __launch_bounds__(kWeightThreads) window_weights_kernel(const DecodeArgs a, int splits) {
+  extern __shared__ float2 stats[];  // maximum and 1 / sum of each head of the group
+  pdl_launch_dependents();
+  pdl_wait();
+  const int h = blockIdx.y, b = blockIdx.z, group = a.w.nh / a.w.nkv, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float* src = a.ws + ((long long)b * a.w.nh + (long long)h * group) * splits * (D + 2);
+  for (int g = warp; g < group; g += kWeightThreads / 32) {
+    const float* part = src + (long long)g * splits * (D + 2) + D;
+    float n = -INFINITY, l = 0.f;
+    for (int s = lane; s < splits; s += 32) n = fmaxf(n, part[s * (D + 2)]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, x));
+    for (int s = lane; s < splits; s += 32) {
+      const float m = part[s * (D + 2)];
+      l += part[s * (D + 2) + 1] * (m == -INFINITY ? 0.f : fast_exp2(m - n));
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    if (lane == 0) stats[g] = make_float2(n, l != 0.f ? 1.f / l : 0.f);
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < group * D; i += kWeightThreads) {
+      const int g = i / D, ch = i % D;
+      const float* part = src + (long long)g * splits * (D + 2);
+      const float n = stats[g].x;
+      float o = 0.f;
+      for (int s = 0; s < splits; ++s) {
+        const float m = part[s * (D + 2) + D];
+        o += part[s * (D + 2) + ch] * (m == -INFINITY ? 0.f : fast_exp2(m - n));
+      }
+      a.o.row(b, h * group + g, 0)[ch] = __float2bfloat16_rn(o * stats[g].y);
+    }
+    return;
+  }
+  const Blocks<16> bl(a.w, b);
+  const long long list = (long long)b * a.w.nkv + h;
+  float* out = a.weights + list * a.w.nk;
+  const int slots = bl.count * 16;
+  for (int i = (blockIdx.x - 1) * kWeightThreads + threadIdx.x; i < slots; i += (gridDim.x - 1) * kWeightThreads) {
+    const int j = bl.block(i / 16) * 16 + i % 16;
+    if (j >= bl.len || (j < bl.lo && j >= a.w.sinks)) continue;
+    const float* s = a.scores + (list * a.slots + i) * group;
+    float sum = 0.f;
+    for (int g = 0; g < group; ++g) sum += fast_exp2(s[g] - stats[g].x) * stats[g].y;
+    out[j] += sum;
+  }
+}
+
 // Query heads of a tile: eight where a group has no more (half the registers), else sixteen.
 int head_tile(const Window& w) { return w.nh / w.nkv <= 8 ? 8 : 16; }
 
+template <int D, bool kKv4, bool kPart, bool kScores>
+cudaError_t parts(const DecodeArgs& a, int splits, cudaStream_t st) {
+  const int group = a.w.nh / a.w.nkv, tile = head_tile(a.w), tiles = (group + tile - 1) / tile;
+  auto kern = a.w.nk < kLongBlock ? (tile == 8 ? window_decode_kernel<D, 1, kKv4, true, kPart, kScores>
+                                               : window_decode_kernel<D, 2, kKv4, true, kPart, kScores>)
+                                  : (tile == 8 ? window_decode_kernel<D, 1, kKv4, false, kPart, kScores>
+                                               : window_decode_kernel<D, 2, kKv4, false, kPart, kScores>);
+  return launch_pdl(kern, dim3(splits, a.w.nkv * tiles, a.w.B), dim3(kThreads), 0, st, a);
+}
+
 template <int D, bool kKv4>
 cudaError_t decode(const DecodeArgs& a, cudaStream_t st) {
-  const int group = a.w.nh / a.w.nkv, tile = head_tile(a.w), tiles = (group + tile - 1) / tile;
   const int splits = decode_splits(a.w);
-  auto kern = a.w.nk < kLongBlock
-                  ? (tile == 8 ? window_decode_kernel<D, 1, kKv4, true> : window_decode_kernel<D, 2, kKv4, true>)
-                  : (tile == 8 ? window_decode_kernel<D, 1, kKv4, false> : window_decode_kernel<D, 2, kKv4, false>);
-  cudaError_t e = launch_pdl(kern, dim3(splits, a.w.nkv * tiles, a.w.B), dim3(kThreads), 0, st, a);
+  const cudaError_t e = parts<D, kKv4, false, false>(a, splits, st);
   if (e != cudaSuccess || splits == 1) return e;
   return launch_pdl(window_join_kernel<D>, dim3(a.w.nh, a.w.B), dim3(D), 0, st, a, splits);
+}
+
+// Rows of scores that a sequence's visible blocks of 16 keys take up at most.
+long long score_slots(const Window& w) {
+  const long long rows = std::min<long long>(w.nk, (long long)w.left + 1 + w.sinks);
+  return std::min<long long>((w.nk + 15) / 16, (rows + 15) / 16 + 2) * 16;
+}
+
+size_t partial_bytes(const Window& w, int d) {
+  return ((size_t)w.B * w.nh * decode_splits(w) * (d + 2) * 4 + 255) / 256 * 256;
+}
+
+template <int D>
+cudaError_t decode_weights(DecodeArgs a, cudaStream_t st) {
+  const int splits = decode_splits(a.w), group = a.w.nh / a.w.nkv;
+  a.slots = score_slots(a.w);
+  a.scores = a.ws + partial_bytes(a.w, D) / 4;
+  const cudaError_t e = parts<D, false, true, true>(a, splits, st);
+  if (e != cudaSuccess) return e;
+  // two keys per thread, as long as that is more than a few CTAs per SM
+  const long long lists = (long long)a.w.B * a.w.nkv, chunks = (a.slots + 2 * kWeightThreads - 1) / (2 * kWeightThreads);
+  const int gx = (int)std::min<long long>(chunks, std::max<long long>(1, 16LL * 152 / lists));
+  return launch_pdl(window_weights_kernel<D>, dim3(1 + gx, a.w.nkv, a.w.B), dim3(kWeightThreads), group * sizeof(float2),
+                    st, a, splits);
 }
 
 }  // namespace
@@ -667,6 +766,14 @@ int decode_splits(const Window& w) {
 size_t decode_ws_bytes(const Window& w, int d) {
   const int s = decode_splits(w);
   return s == 1 ? 256 : ((size_t)w.B * w.nh * s * (d + 2) * 4 + 255) / 256 * 256;
+}
+
+size_t decode_weights_ws_bytes(const Window& w, int d) {
+  return partial_bytes(w, d) + ((size_t)w.B * w.nh * score_slots(w) * 4 + 255) / 256 * 256;
+}
+
+cudaError_t launch_window_decode_weights(const DecodeArgs& a, int d, cudaStream_t st) {
+  return d == 64 ? decode_weights<64>(a, st) : decode_weights<128>(a, st);
 }
 
 cudaError_t launch_window_decode(const DecodeArgs& a, int d, bool kv4, cudaStream_t st) {

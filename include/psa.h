@@ -431,7 +431,19 @@ psa_status_t psa_window_attn_decode_kv4(psa_rows_t q, const void *k_codes, const
  * over the query heads that share it and all queries so far, of the softmax probability that key
  * j had.  Rows behind a sequence's length are kept at 0 by the caller, or by psa_kv_evict.
  *
- * psa_window_attn_decode that also adds the probabilities of its step's visible keys to weights
+ * Adds to weights what the keys of a prompt (k, [B, num_kv_heads, n_k, d]) got from its queries q,
+ * or from its last n_q ones: lse, fp32 [B, num_heads, n_q], is psa_window_attn_fwd's of the same
+ * problem, which says what a query sees.  Scores and sums are fp32, in a fixed order; entries from a
+ * sequence's length on are left as they are.  bf16 (fp32: PSA_ERR_UNSUPPORTED), head_dim 64 or
+ * 128.  workspace: at least psa_window_attn_weights_workspace_size(p) bytes. */
+psa_status_t psa_window_attn_weights(psa_rows_t q, psa_rows_t k, const int *lens, const float *lse,
+                                     float *weights, void *workspace, size_t ws_bytes,
+                                     psa_window_t p, float scale, cudaStream_t stream);
+
+/* Bytes of device workspace for psa_window_attn_weights (0 for an invalid problem). */
+size_t psa_window_attn_weights_workspace_size(psa_window_t p);
+
+/* psa_window_attn_decode that also adds the probabilities of its step's visible keys to weights
  * (fp32, from the scores before any rounding; heads are added in order: reruns are bitwise
  * identical; entries of keys that are not visible are left as they are).  The same partial sums,
  * joined in another order, make the output.  Same sizes and errors, with up to 4096 query heads

@@ -77,6 +77,7 @@ EXPORTED = (
     "psa_window_attn_fwd", "psa_window_attn_bwd",
     "psa_window_attn_bwd_workspace_size", "psa_window_attn_decode", "psa_window_attn_decode_workspace_size",
     "psa_kv_append", "psa_kv4_append", "psa_kv4_read", "psa_window_attn_decode_kv4",
+    "psa_window_attn_weights", "psa_window_attn_weights_workspace_size",
     "psa_window_attn_decode_weights", "psa_window_attn_decode_weights_workspace_size", "psa_kv_evict",
     "psa_kv_evict_workspace_size", "psa_status_string",
     "psa_get_last_device_error", "psa_debug_wait_timeout",
@@ -129,6 +130,8 @@ def load(path: str | None = None):
         "psa_kv4_append": [R, R, P, P, P, P, P, P, CA, P],
         "psa_kv4_read": [P, P, P, P, R, R, CA, P],
         "psa_window_attn_decode_kv4": [R, P, P, P, P, P, R, P, Z, WN, F, P],
+        "psa_window_attn_weights": [R, R, P, P, P, P, Z, WN, F, P],
+        "psa_window_attn_weights_workspace_size": [WN],
         "psa_window_attn_decode_weights": [R, R, R, P, R, P, P, Z, WN, F, P],
         "psa_window_attn_decode_weights_workspace_size": [WN],
         "psa_kv_evict": [P, P, P, R, R, P, P, P, P, Z, EV, P],
@@ -142,7 +145,7 @@ def load(path: str | None = None):
         fn.argtypes = args
         fn.restype = ctypes.c_int
     for name in ("psa_attention_bwd", "psa_qk_norm_rope_bwd", "psa_window_attn_bwd", "psa_window_attn_decode",
-                 "psa_window_attn_decode_weights", "psa_kv_evict"):
+                 "psa_window_attn_weights", "psa_window_attn_decode_weights", "psa_kv_evict"):
         getattr(lib, name + "_workspace_size").restype = ctypes.c_size_t
     lib.psa_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -567,6 +570,20 @@ def _weights(t, by_k, what: str = "weights"):
     if t is None:
         raise ValueError(f"{what} are required")
     return _dense(t, by_k[:3], torch.float32, what)
+
+
+def psa_window_attn_weights_workspace_size(win: PsaWindow) -> int:
+    return int(load().psa_window_attn_weights_workspace_size(win))
+
+
+def psa_window_attn_weights(q, k, lens, lse, weights, workspace, win: PsaWindow, scale: float, stream=None):
+    import torch
+
+    by_q, by_k = _window_shapes(win)
+    t = _type_of(win, q)
+    _on_device("psa_window_attn_weights", (q, k, lens, lse, weights, workspace), stream, _rows(q, by_q, t, "q"),
+               _rows(k, by_k, t, "k"), _lens(lens, win), _dense(lse, by_q[:3], torch.float32, "lse"),
+               _weights(weights, by_k), *_workspace(workspace, "psa_window_attn_weights"), win, scale)
 
 
 def psa_window_attn_decode_weights_workspace_size(win: PsaWindow) -> int:

@@ -201,18 +201,23 @@ psa_status_t check_fa2(const void* const* ptrs, int nptr, int BH, int n_ctx, int
 }  // namespace
 
 // 4-D bf16 map over a view [B, heads, N, d] (channels contiguous, strides in elements), box
-// {64 channels, 128 rows, 1, 1}.
-bool psa::map_view(CUtensorMap* m, const void* base, long long sb, long long sh, long long sn, int B,
-                   int heads, int N, int d) {
+// {64 channels, rows, heads, batches}.
+bool psa::map_view_box(CUtensorMap* m, const void* base, long long sb, long long sh, long long sn, int B,
+                       int heads, int N, int d, int box_rows, int box_heads, int box_batches) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)N, (cuuint64_t)heads, (cuuint64_t)B};
   cuuint64_t strides[3] = {(cuuint64_t)sn * 2, (cuuint64_t)sh * 2, (cuuint64_t)sb * 2};
-  cuuint32_t box[4] = {64, 128, 1, 1};
+  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_heads, (cuuint32_t)box_batches};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool psa::map_view(CUtensorMap* m, const void* base, long long sb, long long sh, long long sn, int B,
+                   int heads, int N, int d) {
+  return map_view_box(m, base, sb, sh, sn, B, heads, N, d, 128, 1, 1);
 }
 
 extern "C" {

@@ -156,6 +156,12 @@ size_t window_bwd_tc_ws_bytes(const Window& w, int d);
 cudaError_t launch_window_fwd_simt(const WindowArgs<float>& a, int d, cudaStream_t st);
 cudaError_t launch_window_bwd_simt(const WindowArgs<float>& a, int d, cudaStream_t st);
 
+// Sums of the probabilities for each key (window_weights.cu).
+size_t window_weights_ws_bytes(const Window& w);
+cudaError_t launch_window_weights(const Window& w, View<const __nv_bfloat16> q, View<const __nv_bfloat16> k,
+                                  const float* lse, float* weights, float* ws, float scale, int d,
+                                  cudaStream_t st);
+
 // ---------------------------------------------------------------- caches
 struct CacheArgs {
   int B, nkv, N, max_len;

@@ -462,6 +462,27 @@ psa_status_t psa_window_attn_decode_weights(psa_rows_t q, psa_rows_t k_cache, ps
   return from_cuda(psa::launch_window_decode_weights(a, p.head_dim, st));
 }
 
+size_t psa_window_attn_weights_workspace_size(psa_window_t p) {
+  return check_window(p) == PSA_OK ? round256(psa::window_weights_ws_bytes(window(p, nullptr))) : 0;
+}
+
+psa_status_t psa_window_attn_weights(psa_rows_t q, psa_rows_t k, const int* lens, const float* lse,
+                                     float* weights, void* ws, size_t ws_bytes, psa_window_t p,
+                                     float scale, cudaStream_t st) {
+  PSA_TRY(check_window(p));
+  PSA_TRY(check_scale(scale));
+  if (!lse || !weights || !ws) return PSA_ERR_INVALID_ARG;
+  if (p.dtype != PSA_DTYPE_BF16) return PSA_ERR_UNSUPPORTED;
+  PSA_TRY(check_view(q, p.B, p.num_heads, p.n_q, p.head_dim, p.dtype));
+  PSA_TRY(check_view(k, p.B, p.num_kv_heads, p.n_k, p.head_dim, p.dtype));
+  if (!aligned(lens, 4) || !aligned(lse, 4) || !aligned(weights, 4) || !aligned(ws, 16))
+    return PSA_ERR_ALIGNMENT;
+  if (ws_bytes < psa_window_attn_weights_workspace_size(p)) return PSA_ERR_INVALID_ARG;
+  using T = const __nv_bfloat16;
+  return from_cuda(psa::launch_window_weights(window(p, lens), view<T>(q), view<T>(k), lse, weights,
+                                              static_cast<float*>(ws), scale, p.head_dim, st));
+}
+
 size_t psa_kv_evict_workspace_size(psa_evict_t p) {
   return check_evict(p) == PSA_OK ? round256(psa::evict_ws_bytes(p.B * p.num_kv_heads, p.keep, p.max_len)) : 0;
 }

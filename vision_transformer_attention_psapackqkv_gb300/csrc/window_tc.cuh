@@ -83,5 +83,8 @@ __device__ __forceinline__ void load_cols64(uint32_t t, uint32_t (&r)[64]) {
 // Tensor map over a view's rows: 4-D (d, N, heads, B), box {64 channels, 128 rows}.
 bool map_view(CUtensorMap* m, const void* base, long long sb, long long sh, long long sn, int B,
               int heads, int N, int d);
+// The same with a box of several heads and batches.
+bool map_view_box(CUtensorMap* m, const void* base, long long sb, long long sh, long long sn, int B,
+                  int heads, int N, int d, int box_rows, int box_heads, int box_batches);
 
 }  // namespace psa

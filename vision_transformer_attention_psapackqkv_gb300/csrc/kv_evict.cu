@@ -6,12 +6,13 @@
 // behind it and targets in front of it, so the moves are independent of one another and need no
 // second cache; a step that evicts one row moves at most one.
 //
-// The selection is a radix select: a CTA for each list (sequence and key/value head) finds the
-// keep-th largest weight as a sortable integer in three passes of 11, 11 and 10 bits over the
-// list's keys in shared memory, then walks the list once more for the gaps and the rows that
-// fill them.  A warp owns a run of neighbouring rows, so that ranks are ballots inside it and
-// one scan over the warps' totals.  The moves are a copy bound by memory: a second kernel over all
-// lists, or, where a list can have no more than kFewMoves, the same one.
+// The selection is a radix select: a CTA for each list (sequence and key/value head) makes
+// sortable integers of the weights in shared memory, counts their first 11 bits, gathers those
+// that share the bits of the keep-th largest, and goes on with 11 and 10 bits among these.  What
+// stays is then one bit per row: ranks, gaps and the rows that fill them are sums over words of
+// 32 rows.  Instructions bound it (one CTA works on a list), so rows are gone through four times
+// at most.  The moves are a copy bound by memory: a second kernel over all lists, or, where a list
+// can have no more than kFewMoves, the same one.
 #include <algorithm>
 
 #include "lm.cuh"
@@ -21,9 +22,10 @@ namespace psa {
 namespace {
 
 constexpr int kBins = 2048;
-constexpr int kKeysInShared = 48 * 1024;  // longer lists are read again in every pass
+constexpr int kKeysInShared = 45 * 1024;  // longer lists are read again in every pass
+constexpr int kGathered = 1024;           // more that share their first bits are counted where they are
 constexpr int kFewMoves = 32;
-constexpr int kMoveThreads = 256, kMoveUnroll = 4;
+constexpr int kMoveThreads = 256, kMoveUnroll = 8;
 constexpr uint32_t kSafe = 0xffffffffu;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -35,25 +37,55 @@ __device__ __forceinline__ uint32_t sortable(float w) {
 }
 
 struct Shared {
-  uint32_t hist[kBins];
-  uint32_t warp[32];
-  uint32_t digit, need;
+  uint32_t hist[kBins], some[kGathered];
+  unsigned long long warp[32];
+  uint32_t digit, need, gathered;
 };
 
-// Sum of x over the warps in front of this one, and over all (x: the same in a warp's lanes).
-__device__ __forceinline__ uint32_t over_warps(Shared& sh, uint32_t x, uint32_t& total) {
+// Sum of x over the threads in front of this one; total: over all.
+__device__ __forceinline__ unsigned long long in_front(Shared& sh, unsigned long long x, unsigned long long& total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  unsigned long long upto = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned long long y = __shfl_up_sync(kAll, upto, d);
+    if (lane >= d) upto += y;
+  }
   __syncthreads();  // of the use before
-  if (lane == 0) sh.warp[warp] = x;
+  if (lane == 31) sh.warp[warp] = upto;
   __syncthreads();
-  const uint32_t v = lane < warps ? sh.warp[lane] : 0u;
-  total = __reduce_add_sync(kAll, v);
-  return __reduce_add_sync(kAll, lane < warp ? v : 0u);
+  unsigned long long before = 0;
+  total = 0;
+  for (int w = 0; w < warps; ++w) {
+    const unsigned long long y = sh.warp[w];
+    if (w < warp) before += y;
+    total += y;
+  }
+  return before + upto - x;
+}
+
+// The bin that holds the need-th largest, from counts that are complete; what is above it is
+// taken off need.
+__device__ __forceinline__ uint32_t find_bin(Shared& sh, uint32_t& need) {
+  const int tid = threadIdx.x, per = kBins / blockDim.x, hi = kBins - 1 - tid * per;
+  uint32_t mine = 0;
+  for (int i = 0; i < per; ++i) mine += sh.hist[hi - i];
+  unsigned long long total;
+  uint32_t above = (uint32_t)in_front(sh, mine, total);
+  if (above < need && need <= above + mine) {
+    int d = hi;
+    while (above + sh.hist[d] < need) above += sh.hist[d--];
+    sh.digit = d;
+    sh.need = need - above;
+  }
+  __syncthreads();
+  need = sh.need;
+  return sh.digit;
 }
 
 __global__ void __launch_bounds__(1024)
     evict_select_kernel(const EvictArgs a, const int cap, const int row16, const bool move) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ uint32_t dynamic[];
   __shared__ Shared sh;
   pdl_launch_dependents();
   pdl_wait();
@@ -75,114 +107,108 @@ __global__ void __launch_bounds__(1024)
     }
     return;
   }
+  for (int i = tid; i < kBins; i += threads) sh.hist[i] = 0;
+  if (tid == 0) sh.gathered = 0;
   // ---- which rows are kept whatever their weight
   long long safe_from = 1LL << 40;
   if (a.recent > 0) {
     int newest = INT_MIN;
+#pragma unroll 4
     for (int r = tid; r < len; r += threads) newest = max(newest, pos[r]);
     newest = __reduce_max_sync(kAll, newest);
     if (lane == 0) sh.warp[warp] = (uint32_t)newest;
     __syncthreads();
-    newest = __reduce_max_sync(kAll, lane < threads / 32 ? (int)sh.warp[lane] : INT_MIN);
+    newest = __reduce_max_sync(kAll, lane < threads / 32 ? (int)(uint32_t)sh.warp[lane] : INT_MIN);
     safe_from = (long long)newest - a.recent + 1;
   }
-  const bool cached = len <= kKeysInShared;
-  auto make = [&](int r) {
+  __syncthreads();
+  // ---- keys, and how many have the same first 11 bits; what stays in its place already
+  const bool cached = len <= kKeysInShared, apart = w_out != w, apart_pos = pos_out != pos;
+  uint32_t* keys = dynamic;
+  auto to_key = [&](float x, int p) { return p < a.sinks || p >= safe_from ? kSafe : sortable(x); };
+#pragma unroll 4
+  for (int r = tid; r < len; r += threads) {
+    const float x = w[r];
     const int p = pos[r];
-    return p < a.sinks || p >= safe_from ? kSafe : sortable(w[r]);
-  };
-  if (cached)
-    for (int r = tid; r < len; r += threads) keys[r] = make(r);
-  auto key = [&](int r) { return cached ? keys[r] : make(r); };
+    const uint32_t k = to_key(x, p);
+    if (cached) keys[r] = k;
+    atomicAdd(&sh.hist[k >> 21], 1u);
+    if (r < count) {  // (gaps are written again below)
+      if (apart) w_out[r] = x;
+      if (apart_pos) pos_out[r] = p;
+    }
+  }
+  auto key = [&](int r) { return cached ? keys[r] : to_key(w[r], pos[r]); };
+  __syncthreads();
+  uint32_t need = count, top = find_bin(sh, need);
 
   // ---- the count-th largest key, and how many of its equals are kept
-  uint32_t top = 0, need = count;
+  const uint32_t shared_by = sh.hist[top];
+  const bool few = shared_by <= kGathered;
+  if (few) {
+    for (int r = tid; r < len; r += threads) {
+      const uint32_t k = key(r);
+      if (k >> 21 == top) sh.some[atomicAdd(&sh.gathered, 1u)] = k;
+    }
+  }
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass < 2 ? 11 : 10;
+  for (int pass = 1; pass < 3; ++pass) {
+    const int shift = pass == 1 ? 10 : 0, bits = pass == 1 ? 11 : 10;
+    __syncthreads();  // gathered, and the counts read
     for (int i = tid; i < kBins; i += threads) sh.hist[i] = 0;
     __syncthreads();
-    for (int r0 = warp * 32; r0 < len; r0 += threads) {
-      const int r = r0 + lane;
-      const uint32_t k = r < len ? key(r) : 0u;
-      const bool in = r < len && (pass == 0 || (k >> (shift + bits)) == top);
-      const uint32_t who = __ballot_sync(kAll, in);
-      if (who == 0) continue;
-      const uint32_t digit = (k >> shift) & ((1u << bits) - 1u);
-      const int first = __ffs(who) - 1;
-      // (equal digits of a whole warp would be added one after another)
-      const uint32_t common = __shfl_sync(kAll, digit, first);
-      if (__all_sync(kAll, !in || digit == common)) {
-        if (lane == first) atomicAdd(&sh.hist[digit], __popc(who));
-      } else if (in) {
-        atomicAdd(&sh.hist[digit], 1u);
-      }
+    const int n = few ? (int)shared_by : len;
+    for (int i = tid; i < n; i += threads) {
+      const uint32_t k = few ? sh.some[i] : key(i);
+      if (k >> (shift + bits) == top) atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
     }
     __syncthreads();
-    // bins from the top: thread t sums those of its share
-    const int per = kBins / threads, hi = kBins - 1 - tid * per;
-    uint32_t mine = 0;
-    for (int i = 0; i < per; ++i) mine += sh.hist[hi - i];
-    uint32_t upto = mine;
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const uint32_t y = __shfl_up_sync(kAll, upto, x);
-      if (lane >= x) upto += y;
-    }
-    uint32_t total;
-    upto += over_warps(sh, __shfl_sync(kAll, upto, 31), total);
-    uint32_t above = upto - mine;
-    if (above < need && need <= upto) {
-      int d = hi;
-      while (above + sh.hist[d] < need) above += sh.hist[d--];
-      sh.digit = d;
-      sh.need = need - above;
-    }
-    __syncthreads();
-    top = top << bits | sh.digit;
-    need = sh.need;
+    const uint32_t digit = find_bin(sh, need);
+    top = top << bits | digit;
   }
 
-  // ---- ranks: a run of rows for each warp
-  const int run = (len + threads - 1) / threads * 32, from = min(len, warp * run), to = min(len, from + run);
-  uint32_t n = 0, total;
-  for (int r0 = from; r0 < to; r0 += 32) {
-    const int r = r0 + lane;
-    n += __popc(__ballot_sync(kAll, r < to && key(r) == top));
+  // ---- one bit per row: larger than that key, or equal to it
+  const int words = (len + 31) / 32;
+  uint32_t* larger = cached ? keys + (len + 3) / 4 * 4 : a.words + (long long)list * 2 * ((a.max_len + 31) / 32);
+  uint32_t* equal = larger + words;
+  for (int x = warp; x < words; x += threads / 32) {
+    const int r = x * 32 + lane;
+    const uint32_t k = r < len ? key(r) : 0u;
+    const uint32_t gt = __ballot_sync(kAll, r < len && k > top), eq = __ballot_sync(kAll, r < len && k == top);
+    if (lane == 0) {
+      larger[x] = gt;
+      equal[x] = eq;
+    }
   }
-  const uint32_t ties = over_warps(sh, n, total);
-  const uint32_t below = (1u << lane) - 1u;
-  // calls f(row, kept, gap, mover) for this warp's rows, ties in the order of rows
-  auto walk = [&](auto f) {
-    uint32_t seen = ties;
-    for (int r0 = from; r0 < to; r0 += 32) {
-      const int r = r0 + lane;
-      const uint32_t k = r < to ? key(r) : 0u;
-      const uint32_t eq = __ballot_sync(kAll, r < to && k == top);
-      const bool kept = r < to && (k > top || (k == top && seen + __popc(eq & below) < need));
-      seen += __popc(eq);
-      f(r, kept, r < to && r < count && !kept, r >= count && kept);
-    }
+  __syncthreads();
+  // a thread has a run of words: of equal keys the first `need` rows stay
+  const int run = (words + threads - 1) / threads, from = min(words, tid * run), to = min(words, from + run);
+  unsigned long long n = 0, total;
+  for (int x = from; x < to; ++x) n += __popc(equal[x]);
+  uint32_t ties = (uint32_t)in_front(sh, n, total);
+  // gaps in the upper half, rows that fill them in the lower one
+  auto in_place = [&](int x) {  // the word's rows below count
+    const int m = count - x * 32;
+    return m >= 32 ? kAll : m <= 0 ? 0u : (1u << m) - 1u;
   };
-  uint32_t gaps = 0, movers = 0;
-  walk([&](int, bool, bool gap, bool mover) {
-    gaps += __popc(__ballot_sync(kAll, gap));
-    movers += __popc(__ballot_sync(kAll, mover));
-  });
-  uint32_t moves;
-  uint32_t gap_at = over_warps(sh, gaps, moves), mover_at = over_warps(sh, movers, total);
-  const bool apart = w_out != w, apart_pos = pos_out != pos;
-  walk([&](int r, bool kept, bool gap, bool mover) {
-    const uint32_t g = __ballot_sync(kAll, gap), m = __ballot_sync(kAll, mover);
-    if (gap) dst[gap_at + __popc(g & below)] = r;
-    if (mover) src[mover_at + __popc(m & below)] = r;
-    gap_at += __popc(g);
-    mover_at += __popc(m);
-    if (kept && r < count) {
-      if (apart) w_out[r] = w[r];
-      if (apart_pos) pos_out[r] = pos[r];
-    }
-  });
+  n = 0;
+  for (int x = from; x < to; ++x) {
+    uint32_t eq = equal[x];
+    const uint32_t c = __popc(eq);
+    for (uint32_t drop = ties + c > need ? min(c, ties + c - need) : 0u; drop > 0; --drop) eq &= ~(0x80000000u >> __clz(eq));
+    ties += c;
+    const uint32_t kept = larger[x] | eq, here = in_place(x);
+    larger[x] = kept;
+    n += (unsigned long long)__popc(~kept & here) << 32 | __popc(kept & ~here);
+  }
+  const unsigned long long at = in_front(sh, n, total);
+  uint32_t gap_at = (uint32_t)(at >> 32), mover_at = (uint32_t)at;
+  const uint32_t moves = (uint32_t)total;
+  for (int x = from; x < to; ++x) {
+    const uint32_t kept = larger[x], here = in_place(x);
+    for (uint32_t g = ~kept & here; g; g &= g - 1) dst[gap_at++] = x * 32 + __ffs(g) - 1;
+    for (uint32_t m = kept & ~here; m; m &= m - 1) src[mover_at++] = x * 32 + __ffs(m) - 1;
+  }
   if (tid == 0) a.counts[list] = moves;
   __syncthreads();
   for (uint32_t i = tid; i < moves; i += threads) {
@@ -212,47 +238,56 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
   pdl_launch_dependents();
   pdl_wait();
   const int list = blockIdx.y, b = list / a.nkv, h = list % a.nkv;
-  const int n = a.counts[list] * 2 * ROW16, first = blockIdx.x * kMoveThreads * kMoveUnroll + threadIdx.x;
+  const int n = a.counts[list], first = blockIdx.x * kMoveThreads * kMoveUnroll + threadIdx.x;
   const int* src = a.moves + (long long)list * 2 * cap;
   const int* dst = src + cap;
   // (a stride of kMoveThreads is a whole number of rows: a thread's column stays)
   const int c = first % (2 * ROW16);
   uint4* base = c < ROW16 ? a.k.row(b, h, 0) + c : a.v.row(b, h, 0) + c - ROW16;
   const long long step = c < ROW16 ? a.k.sn : a.v.sn;
+  const int m0 = first / (2 * ROW16);
   uint4 x[kMoveUnroll];
-  uint4* to[kMoveUnroll];
+  int s[kMoveUnroll], d[kMoveUnroll];
 #pragma unroll
   for (int i = 0; i < kMoveUnroll; ++i) {
-    const int at = first + i * kMoveThreads;
-    to[i] = nullptr;
-    if (at < n) {
-      const int m = at / (2 * ROW16);
-      to[i] = base + dst[m] * step;
-      x[i] = base[src[m] * step];
+    const int m = m0 + i * (kMoveThreads / (2 * ROW16));
+    d[i] = -1;
+    if (m < n) {
+      s[i] = src[m];
+      d[i] = dst[m];
     }
   }
 #pragma unroll
   for (int i = 0; i < kMoveUnroll; ++i)
-    if (to[i]) *to[i] = x[i];
+    if (d[i] >= 0) x[i] = base[s[i] * step];
+#pragma unroll
+  for (int i = 0; i < kMoveUnroll; ++i)
+    if (d[i] >= 0) base[d[i] * step] = x[i];
 }
+
+// Keys, and two bits, of a list.
+constexpr int shared_bytes(int rows) { return (rows + 3) / 4 * 16 + (rows + 31) / 32 * 8; }
 
 int most_moves(int keep, int max_len) { return std::max(0, std::min(keep, max_len - keep)); }
 
 }  // namespace
 
 size_t evict_ws_bytes(int lists, int keep, int max_len) {
-  return ((size_t)lists * 4 + 15) / 16 * 16 + (size_t)lists * 2 * most_moves(keep, max_len) * 4;
+  const size_t words = max_len > kKeysInShared ? (size_t)lists * 2 * ((max_len + 31) / 32) * 4 : 0;
+  return ((size_t)lists * 4 + 15) / 16 * 16 + (size_t)lists * 2 * most_moves(keep, max_len) * 4 + words;
 }
 
 cudaError_t launch_kv_evict(EvictArgs a, int row16, void* ws, cudaStream_t st) {
   const int lists = a.B * a.nkv, cap = most_moves(a.keep, a.max_len);
   a.counts = static_cast<int*>(ws);
   a.moves = reinterpret_cast<int*>(static_cast<char*>(ws) + ((size_t)lists * 4 + 15) / 16 * 16);
-  const cudaError_t e = set_max_dynamic_smem((const void*)evict_select_kernel, kKeysInShared * 4);
+  a.words = reinterpret_cast<uint32_t*>(a.moves + (size_t)lists * 2 * cap);
+  const cudaError_t e = set_max_dynamic_smem((const void*)evict_select_kernel, shared_bytes(kKeysInShared));
   if (e != cudaSuccess) return e;
   const bool fused = cap <= kFewMoves;
-  const int threads = a.max_len > 4096 ? 1024 : 256;
-  const int smem = std::min(a.max_len, kKeysInShared) * 4;
+  // (a power of two that divides the bins)
+  const int threads = a.max_len > 8192 ? 1024 : a.max_len > 1024 ? 512 : 256;
+  const int smem = shared_bytes(std::min(a.max_len, kKeysInShared));
   const cudaError_t s = launch_pdl(evict_select_kernel, dim3(lists), dim3(threads), smem, st, a, cap, row16, fused);
   if (s != cudaSuccess || fused) return s;
   const long long units = (long long)cap * 2 * row16, per = kMoveThreads * kMoveUnroll;

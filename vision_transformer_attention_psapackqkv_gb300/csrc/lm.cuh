@@ -187,7 +187,8 @@ struct EvictArgs {
   View<uint4> k, v;        // strides in 16 bytes
   float* weights_out;
   int *positions_out, *lens_out;
-  int *counts, *moves;     // workspace: moves of each list, then their sources and targets
+  int *counts, *moves;     // workspace: moves of each list, then their sources and targets,
+  uint32_t* words;         // then two bits for each row of lists that shared memory does not hold
 };
 size_t evict_ws_bytes(int lists, int keep, int max_len);
 cudaError_t launch_kv_evict(EvictArgs a, int row16, void* ws, cudaStream_t st);

@@ -506,7 +506,7 @@ psa_status_t psa_kv_evict(const float* weights, const int* positions, const int*
     return View<uint4>{static_cast<uint4*>(v.ptr), v.stride_b / per, v.stride_h / per, v.stride_n / per};
   };
   psa::EvictArgs a{p.B, p.num_kv_heads, p.max_len, p.keep, p.sinks, p.recent, weights, positions, lens,
-                   rows(k_cache), rows(v_cache), weights_out, positions_out, lens_out, nullptr, nullptr};
+                   rows(k_cache), rows(v_cache), weights_out, positions_out, lens_out, nullptr, nullptr, nullptr};
   return from_cuda(psa::launch_kv_evict(a, p.head_dim / per, ws, st));
 }
 

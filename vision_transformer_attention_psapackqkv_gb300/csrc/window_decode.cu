@@ -700,7 +700,18 @@ __global__ void __launch_bounds__(kWeightThreads) window_weights_kernel(const De
     if (j >= bl.len || (j < bl.lo && j >= a.w.sinks)) continue;
     const float* s = a.scores + (list * a.slots + i) * group;
     float sum = 0.f;
-    for (int g = 0; g < group; ++g) sum += fast_exp2(s[g] - stats[g].x) * stats[g].y;
+    auto add = [&](float x, int g) { sum += fast_exp2(x - stats[g].x) * stats[g].y; };
+    if (group % 4 == 0) {  // then a key's scores are 16-byte aligned
+      for (int g = 0; g < group; g += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(s + g);
+        add(x.x, g);
+        add(x.y, g + 1);
+        add(x.z, g + 2);
+        add(x.w, g + 3);
+      }
+    } else {
+      for (int g = 0; g < group; ++g) add(s[g], g);
+    }
     out[j] += sum;
   }
 }

@@ -382,6 +382,40 @@ psa_status_t psa_window_attn_decode(psa_rows_t q, psa_rows_t k_cache, psa_rows_t
  * for an invalid problem); they depend on the problem's sizes, not on the lengths. */
 size_t psa_window_attn_decode_workspace_size(psa_window_t p);
 
+/* Attention of a batch whose sequences all begin with the same prefix, which is held and read
+ * once: k_prefix, v_prefix [1, num_kv_heads, n_prefix, d].  Behind it each sequence has keys of its
+ * own, k and v [B, num_kv_heads, n_k, d]; query head h reads key/value head h / (num_heads /
+ * num_kv_heads).  Every query sees the whole prefix.  bf16 (fp32: PSA_ERR_UNSUPPORTED), rounded as
+ * in psa_window_attn_fwd, head_dim 64 or 128, n_q <= n_k, B * num_heads * n_q up to 2^28. */
+typedef struct {
+    int B, num_heads, num_kv_heads, n_q, n_prefix, n_k, head_dim;
+    psa_dtype_t dtype;
+} psa_prefix_t;
+
+/* Prompts behind the prefix: q [B, num_heads, n_q, d] are the last n_q of each sequence's n_k own
+ * tokens, and query row i also sees the own keys j <= i + n_k - n_q.  lens, int32 [B] on the
+ * device (NULL: n_k): own tokens from lens[b] on are padding, whose queries get output 0 and
+ * log-sum-exp -infinity, and which are seen by none, whatever they hold.  Every row of o is
+ * written, and lse, fp32 [B, num_heads, n_q] (NULL: not wanted).  The attention over a sequence's own
+ * keys is rounded to bf16 before it is joined with the prefix'.  workspace: 16-byte aligned, at least
+ * psa_prefix_attn_workspace_size(p) bytes. */
+psa_status_t psa_prefix_attn_fwd(psa_rows_t q, psa_rows_t k_prefix, psa_rows_t v_prefix,
+                                 psa_rows_t k, psa_rows_t v, const int *lens, psa_rows_t o,
+                                 float *lse, void *workspace, size_t ws_bytes, psa_prefix_t p,
+                                 float scale, cudaStream_t stream);
+
+/* Single tokens (n_q 1) over caches, of which sequence b has filled the first lens[b] rows (int32
+ * on the device, required; values above n_k count as n_k), its query's own key included; a
+ * sequence of length 0 sees the prefix alone, one of negative length is not there and gets output
+ * 0.  Rows behind the sequences may hold anything. */
+psa_status_t psa_prefix_attn_decode(psa_rows_t q, psa_rows_t k_prefix, psa_rows_t v_prefix,
+                                    psa_rows_t k_cache, psa_rows_t v_cache, const int *lens,
+                                    psa_rows_t o, void *workspace, size_t ws_bytes, psa_prefix_t p,
+                                    float scale, cudaStream_t stream);
+
+/* Bytes of device workspace for both (0 for an invalid problem). */
+size_t psa_prefix_attn_workspace_size(psa_prefix_t p);
+
 /* Rows for a cache: row n of sequence b (n < counts[b], int32 [B] on the device; NULL:
  * all N) goes to cache row starts[b] + n (int32 [B] on the device).  Rows that fall
  * outside the cache's max_len rows are dropped; all other cache rows stay as they

@@ -62,6 +62,12 @@ class PsaCache(ctypes.Structure):
                 ("max_len", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
+class PsaPrefix(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("num_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+                ("n_q", ctypes.c_int), ("n_prefix", ctypes.c_int), ("n_k", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
 class PsaEvict(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("num_kv_heads", ctypes.c_int), ("max_len", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("keep", ctypes.c_int), ("sinks", ctypes.c_int),
@@ -77,6 +83,7 @@ EXPORTED = (
     "psa_window_attn_fwd", "psa_window_attn_bwd",
     "psa_window_attn_bwd_workspace_size", "psa_window_attn_decode", "psa_window_attn_decode_workspace_size",
     "psa_kv_append", "psa_kv4_append", "psa_kv4_read", "psa_window_attn_decode_kv4",
+    "psa_prefix_attn_fwd", "psa_prefix_attn_decode", "psa_prefix_attn_workspace_size",
     "psa_window_attn_weights", "psa_window_attn_weights_workspace_size",
     "psa_window_attn_decode_weights", "psa_window_attn_decode_weights_workspace_size", "psa_kv_evict",
     "psa_kv_evict_workspace_size", "psa_status_string",
@@ -98,7 +105,8 @@ def load(path: str | None = None):
         raise RuntimeError(f"libpsa_gb300.so is not built ({path}); run __graft_entry__.build()")
     lib = ctypes.CDLL(path)
     P, I, F, S, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, PsaShape, ctypes.c_size_t
-    R, NR, RA, WN, CA, EV = PsaRows, PsaNormRope, PsaRopeAxes, PsaWindow, PsaCache, PsaEvict
+    R, NR, RA, WN, CA = PsaRows, PsaNormRope, PsaRopeAxes, PsaWindow, PsaCache
+    PR, EV = PsaPrefix, PsaEvict
     sigs = {
         "psa_qkv_conv": [P, P, P, P, I, I, I, I, I, P],
         "psa_pack_qkv": [P, P, S, P],
@@ -130,6 +138,9 @@ def load(path: str | None = None):
         "psa_kv4_append": [R, R, P, P, P, P, P, P, CA, P],
         "psa_kv4_read": [P, P, P, P, R, R, CA, P],
         "psa_window_attn_decode_kv4": [R, P, P, P, P, P, R, P, Z, WN, F, P],
+        "psa_prefix_attn_fwd": [R, R, R, R, R, P, R, P, P, Z, PR, F, P],
+        "psa_prefix_attn_decode": [R, R, R, R, R, P, R, P, Z, PR, F, P],
+        "psa_prefix_attn_workspace_size": [PR],
         "psa_window_attn_weights": [R, R, P, P, P, P, Z, WN, F, P],
         "psa_window_attn_weights_workspace_size": [WN],
         "psa_window_attn_decode_weights": [R, R, R, P, R, P, P, Z, WN, F, P],
@@ -145,7 +156,7 @@ def load(path: str | None = None):
         fn.argtypes = args
         fn.restype = ctypes.c_int
     for name in ("psa_attention_bwd", "psa_qk_norm_rope_bwd", "psa_window_attn_bwd", "psa_window_attn_decode",
-                 "psa_window_attn_weights", "psa_window_attn_decode_weights", "psa_kv_evict"):
+                 "psa_prefix_attn", "psa_window_attn_weights", "psa_window_attn_decode_weights", "psa_kv_evict"):
         getattr(lib, name + "_workspace_size").restype = ctypes.c_size_t
     lib.psa_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -562,6 +573,43 @@ def psa_window_attn_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, lens, o,
     _on_device("psa_window_attn_decode_kv4", (q, *cache, lens, o, workspace), stream, _rows(q, by_q, t, "q"),
                *_kv4(*cache, B, nkv, max_len, d), _lens(lens, win), _rows(o, by_q, t, "o"),
                *_workspace(workspace, "psa_window_attn_decode_kv4"), win, scale)
+
+
+def prefix_of(q, k_prefix, k) -> PsaPrefix:
+    """The problem of q [B, num_heads, n_q, d] behind a prefix [1, num_kv_heads, n_prefix, d], with
+    the sequences' own keys or caches k [B, num_kv_heads, n_k, d]."""
+    B, nh, n_q, d = q.shape
+    return PsaPrefix(B, nh, k.shape[1], n_q, k_prefix.shape[2], k.shape[2], d, dtype_code(q))
+
+
+def psa_prefix_attn_workspace_size(p: PsaPrefix) -> int:
+    return int(load().psa_prefix_attn_workspace_size(p))
+
+
+def _prefix_inputs(q, k_prefix, v_prefix, k, v, lens, o, p):
+    import torch
+
+    t, nkv, d = _type_of(p, q), p.num_kv_heads, p.head_dim
+    by_q, shared, by_k = (p.B, p.num_heads, p.n_q, d), (1, nkv, p.n_prefix, d), (p.B, nkv, p.n_k, d)
+    return (_rows(q, by_q, t, "q"), _rows(k_prefix, shared, t, "k_prefix"), _rows(v_prefix, shared, t, "v_prefix"),
+            _rows(k, by_k, t, "k"), _rows(v, by_k, t, "v"), _dense(lens, (p.B,), torch.int32, "lens"), _rows(o, by_q, t, "o"))
+
+
+def psa_prefix_attn_fwd(q, k_prefix, v_prefix, k, v, lens, o, lse, workspace, p: PsaPrefix, scale: float,
+                        stream=None):
+    import torch
+
+    _on_device("psa_prefix_attn_fwd", (q, k_prefix, v_prefix, k, v, lens, o, lse, workspace), stream,
+               *_prefix_inputs(q, k_prefix, v_prefix, k, v, lens, o, p),
+               _dense(lse, (p.B, p.num_heads, p.n_q), torch.float32, "lse"),
+               *_workspace(workspace, "psa_prefix_attn_fwd"), p, scale)
+
+
+def psa_prefix_attn_decode(q, k_prefix, v_prefix, k_cache, v_cache, lens, o, workspace, p: PsaPrefix, scale: float,
+                           stream=None):
+    _on_device("psa_prefix_attn_decode", (q, k_prefix, v_prefix, k_cache, v_cache, lens, o, workspace), stream,
+               *_prefix_inputs(q, k_prefix, v_prefix, k_cache, v_cache, lens, o, p),
+               *_workspace(workspace, "psa_prefix_attn_decode"), p, scale)
 
 
 def _weights(t, by_k, what: str = "weights"):

@@ -212,5 +212,26 @@ size_t decode_ws_bytes(const Window& w, int d);
 cudaError_t launch_window_decode(const DecodeArgs& a, int d, bool kv4, cudaStream_t st);
 size_t decode_weights_ws_bytes(const Window& w, int d);
 cudaError_t launch_window_decode_weights(const DecodeArgs& a, int d, cudaStream_t st);
+// The parts' results alone, [B, nh, decode_splits][d + 2]: outputs relative to the maximum (log2
+// units), the maximum, the sum.
+size_t decode_parts_ws_bytes(const Window& w, int d);
+cudaError_t launch_window_decode_parts(const DecodeArgs& a, int d, cudaStream_t st);
+
+// ---------------------------------------------------------------- behind a shared prefix
+struct PrefixShape {
+  int B, nh, nkv, nq, P, nk;
+};
+struct PrefixArgs {
+  PrefixShape s;
+  View<const __nv_bfloat16> q, kp, vp, k, v;
+  View<__nv_bfloat16> o;
+  const int* lens;
+  float* lse;  // prompts; or null
+  void* ws;
+  float scale;
+};
+constexpr int kMaxPrefixParts = 64;
+size_t prefix_ws_bytes(const PrefixShape& s, int d);
+cudaError_t launch_prefix_attn(const PrefixArgs& a, int d, bool decode, cudaStream_t st);
 
 }  // namespace psa

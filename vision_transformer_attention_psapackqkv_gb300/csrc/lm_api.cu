@@ -261,6 +261,43 @@ psa_status_t check_evict(const psa_evict_t& p) {
   return PSA_OK;
 }
 
+psa_window_t own_part(const psa_prefix_t& p) {
+  return psa_window_t{p.B, p.num_heads, p.num_kv_heads, p.n_q, p.n_k, p.head_dim, p.dtype, -1, 0, 0};
+}
+
+psa_status_t check_prefix(const psa_prefix_t& p) {
+  PSA_TRY(check_window(own_part(p)));
+  if (p.n_prefix <= 0 || p.n_q > p.n_k) return PSA_ERR_INVALID_ARG;
+  if (p.dtype != PSA_DTYPE_BF16 || p.n_prefix > kMaxRows) return PSA_ERR_UNSUPPORTED;
+  // rows of the product with the prefix, so that tile counts are ints
+  return (long long)p.B * p.num_heads * p.n_q > (1LL << 28) ? PSA_ERR_UNSUPPORTED : PSA_OK;
+}
+
+psa::PrefixShape prefix_shape(const psa_prefix_t& p) {
+  return psa::PrefixShape{p.B, p.num_heads, p.num_kv_heads, p.n_q, p.n_prefix, p.n_k};
+}
+
+psa_status_t run_prefix(psa_rows_t q, psa_rows_t kp, psa_rows_t vp, psa_rows_t k, psa_rows_t v, const int* lens,
+                        psa_rows_t o, float* lse, void* ws, size_t ws_bytes, const psa_prefix_t& p,
+                        float scale, bool decode, cudaStream_t st) {
+  PSA_TRY(check_prefix(p));
+  PSA_TRY(check_scale(scale));
+  if (!ws || (decode && (p.n_q != 1 || !lens))) return PSA_ERR_INVALID_ARG;
+  PSA_TRY(check_view(q, p.B, p.num_heads, p.n_q, p.head_dim, p.dtype));
+  PSA_TRY(check_view(kp, 1, p.num_kv_heads, p.n_prefix, p.head_dim, p.dtype));
+  PSA_TRY(check_view(vp, 1, p.num_kv_heads, p.n_prefix, p.head_dim, p.dtype));
+  PSA_TRY(check_view(k, p.B, p.num_kv_heads, p.n_k, p.head_dim, p.dtype));
+  PSA_TRY(check_view(v, p.B, p.num_kv_heads, p.n_k, p.head_dim, p.dtype));
+  PSA_TRY(check_view(o, p.B, p.num_heads, p.n_q, p.head_dim, p.dtype));
+  if (!aligned(lens, 4) || !aligned(lse, 4) || !aligned(ws, 16)) return PSA_ERR_ALIGNMENT;
+  if (ws_bytes < psa_prefix_attn_workspace_size(p)) return PSA_ERR_INVALID_ARG;
+  using T = const __nv_bfloat16;
+  return from_cuda(psa::launch_prefix_attn(
+      psa::PrefixArgs{prefix_shape(p), view<T>(q), view<T>(kp), view<T>(vp), view<T>(k), view<T>(v),
+                      view<__nv_bfloat16>(o), lens, lse, ws, scale},
+      p.head_dim, decode, st));
+}
+
 constexpr int kMaxWeightGroup = 4096;  // query heads of a key/value head, whose statistics a CTA holds
 
 // What the single-token entry points ask of the problem, q, o and the workspace.
@@ -522,6 +559,23 @@ psa_status_t psa_window_attn_decode_kv4(psa_rows_t q, const void* k_codes, const
   a.vcodes = v_codes;
   a.vscales = v_scales;
   return from_cuda(psa::launch_window_decode(a, p.head_dim, true, st));
+}
+
+size_t psa_prefix_attn_workspace_size(psa_prefix_t p) {
+  return check_prefix(p) == PSA_OK ? psa::prefix_ws_bytes(prefix_shape(p), p.head_dim) : 0;
+}
+
+psa_status_t psa_prefix_attn_fwd(psa_rows_t q, psa_rows_t k_prefix, psa_rows_t v_prefix, psa_rows_t k,
+                                 psa_rows_t v, const int* lens, psa_rows_t o, float* lse, void* ws,
+                                 size_t ws_bytes, psa_prefix_t p, float scale, cudaStream_t st) {
+  return run_prefix(q, k_prefix, v_prefix, k, v, lens, o, lse, ws, ws_bytes, p, scale, false, st);
+}
+
+psa_status_t psa_prefix_attn_decode(psa_rows_t q, psa_rows_t k_prefix, psa_rows_t v_prefix,
+                                    psa_rows_t k_cache, psa_rows_t v_cache, const int* lens,
+                                    psa_rows_t o, void* ws, size_t ws_bytes, psa_prefix_t p,
+                                    float scale, cudaStream_t st) {
+  return run_prefix(q, k_prefix, v_prefix, k_cache, v_cache, lens, o, nullptr, ws, ws_bytes, p, scale, true, st);
 }
 
 psa_status_t psa_kv_append(psa_rows_t k, psa_rows_t v, const int* starts, const int* counts,

@@ -779,6 +779,13 @@ size_t decode_ws_bytes(const Window& w, int d) {
   return s == 1 ? 256 : ((size_t)w.B * w.nh * s * (d + 2) * 4 + 255) / 256 * 256;
 }
 
+size_t decode_parts_ws_bytes(const Window& w, int d) { return partial_bytes(w, d); }
+
+cudaError_t launch_window_decode_parts(const DecodeArgs& a, int d, cudaStream_t st) {
+  const int splits = decode_splits(a.w);
+  return d == 64 ? parts<64, false, true, false>(a, splits, st) : parts<128, false, true, false>(a, splits, st);
+}
+
 size_t decode_weights_ws_bytes(const Window& w, int d) {
   return partial_bytes(w, d) + ((size_t)w.B * w.nh * score_slots(w) * 4 + 255) / 256 * 256;
 }

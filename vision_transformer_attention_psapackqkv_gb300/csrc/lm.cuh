@@ -230,7 +230,7 @@ struct PrefixArgs {
   void* ws;
   float scale;
 };
-constexpr int kMaxPrefixParts = 64;
+constexpr int kPrefixCtas = 152;  // of the kernel over the prefix, at most
 size_t prefix_ws_bytes(const PrefixShape& s, int d);
 cudaError_t launch_prefix_attn(const PrefixArgs& a, int d, bool decode, cudaStream_t st);
 

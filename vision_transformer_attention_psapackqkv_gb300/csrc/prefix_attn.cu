@@ -13,8 +13,8 @@
 //   warps 0-3, 4-7   softmax of slot 0, 1: one thread per row
 //   warp 8           TMA producer: Q of both slots, a ring of K tiles and one of V tiles
 //   warp 9           issuer of the products, tensor memory
-// The prefix is cut into parts, so that all SMs are busy when rows are few, and every part leaves
-// its rows' sums (fp32, relative to the part's maximum) in the workspace.  They lie with a row's
+// All SMs get an equal run of key tiles, whatever the rows; where a run ends inside the prefix a
+// row's sums come in pieces (fp32, relative to the piece's maximum).  They lie in the workspace with a row's
 // neighbours in the tile side by side, four channels each: what 32 lanes write, and read again, is
 // contiguous.
 // Own keys: the single-token kernel's partial sums (decoding), or the window kernel's output and
@@ -43,13 +43,22 @@ struct Bars {
   uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
 };
 
-// The rows' tiles and the prefix' parts.
+// The rows' tiles, and how the work is dealt: units (a key/value head's pair of row tiles) of
+// key_tiles steps lie one behind another, and CTA c of `ctas` takes an equal run of all steps.  A
+// unit that several CTAs share leaves a piece of every row's sums from each.
 struct Plan {
   int B, nh, nkv, group, nq, P;
-  int tq, tg, tb;              // a row tile's box
+  int tq, tg, tb;  // a row tile's box
   int q_tiles, g_tiles, row_tiles;
-  int key_tiles, parts;
-  int slots() const { return row_tiles % 2 ? 2 * parts : parts; }  // places for a row's sums
+  int key_tiles, ctas;
+  long long steps;
+  int slots;  // places for a row's sums
+  __host__ __device__ __forceinline__ long long from(int cta) const { return steps * cta / ctas; }
+  __host__ __device__ __forceinline__ int cta_of(long long step) const { return (int)(((step + 1) * ctas - 1) / steps); }
+  __host__ __device__ __forceinline__ int first_cta(int unit) const { return cta_of((long long)unit * key_tiles); }
+  __host__ __device__ __forceinline__ int pieces(int unit) const {
+    return cta_of((long long)(unit + 1) * key_tiles - 1) - first_cta(unit) + 1;
+  }
 };
 
 struct Params {
@@ -57,34 +66,28 @@ struct Params {
   float4* sums;   // [nkv * row_tiles][slots][D / 4][128]
   float2* stats;  // [nkv * row_tiles][slots][128]: maximum (log2 units), sum
   float sl2;      // scale * log2(e)
-  int units, slots;
 };
 
-struct Unit {
-  int hk, part, t0, n;  // key tiles t0 .. t0 + n - 1
-  int rt;               // slot 0's row tile
-  bool alone;           // slot 1 has the same one, and every second key tile
-  __device__ __forceinline__ Unit(const Params& a, int u) {
-    const int pairs = (a.p.row_tiles + 1) / 2;
-    rt = 2 * (u % pairs);
-    u /= pairs;
-    part = u % a.p.parts;
-    hk = u / a.p.parts;
-    t0 = (int)((long long)a.p.key_tiles * part / a.p.parts);
-    n = (int)((long long)a.p.key_tiles * (part + 1) / a.p.parts) - t0;
+// What a CTA does of a unit: it begins at step `pos` of all.
+struct Piece {
+  int hk, index, t0, n;  // key tiles t0 .. t0 + n - 1
+  int rt;                // slot 0's row tile
+  bool alone;            // slot 1 has the same one, and every second key tile
+  __device__ __forceinline__ Piece(const Params& a, long long pos, long long end) {
+    const int pairs = (a.p.row_tiles + 1) / 2, unit = (int)(pos / a.p.key_tiles);
+    t0 = (int)(pos - (long long)unit * a.p.key_tiles);
+    n = (int)min((long long)(a.p.key_tiles - t0), end - pos);
+    index = blockIdx.x - a.p.first_cta(unit);
+    hk = unit / pairs;
+    rt = 2 * (unit - hk * pairs);
     alone = rt + 1 >= a.p.row_tiles;
   }
   __device__ __forceinline__ bool takes(int slot, int e) const { return !alone || (e & 1) == slot; }
   __device__ __forceinline__ int first(int slot) const { return alone ? slot : 0; }
-  // one past a slot's last entry; first if it has none
   __device__ __forceinline__ bool some(int slot) const { return first(slot) < n; }
   __device__ __forceinline__ int last(int slot) const { return alone ? n - 1 - ((n - 1 - slot) & 1) : n - 1; }
   __device__ __forceinline__ int row_tile(int slot) const { return alone ? rt : rt + slot; }
 };
-
-__device__ __forceinline__ int unit_of(int i) {
-  return i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-}
 
 // Where a row tile's box begins.
 struct Box {
@@ -143,6 +146,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const uint32_t tmem = *tmem_at;
   pdl_launch_dependents();
   pdl_wait();
+  const long long begin = p.from(blockIdx.x), end = p.from(blockIdx.x + 1);
 
   if (warp == C::kProducer) {
     // ------------------------------------------------------------ TMA producer
@@ -152,8 +156,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       tma_prefetch_desc(&tmV);
       bool ok = true;
       int q_count[2] = {0, 0}, kv = 0;
-      for (int i = 0; ok && unit_of(i) < a.units; ++i) {
-        const Unit u(a, unit_of(i));
+      for (long long pos = begin; ok && pos < end;) {
+        const Piece u(a, pos, end);
+        pos += u.n;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (!ok || !u.some(s)) continue;
@@ -201,8 +206,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint32_t idO = idesc_bf16_f32(128, D, false, true);
     bool ok = true;
     int kv0 = 0, q_count[2] = {0, 0}, steps[2] = {0, 0};  // kv0: ring index of the unit's first tile
-    for (int i = 0; ok && unit_of(i) < a.units; ++i) {
-      const Unit u(a, unit_of(i));
+    for (long long pos = begin; ok && pos < end;) {
+      const Piece u(a, pos, end);
+      pos += u.n;
       auto cols = [&](int e) { return min(kTile, (p.P - (u.t0 + e) * kTile + 15) & ~15); };
       bool first[2] = {true, true};
       // S of slot s and entry e, or the tile's release
@@ -287,17 +293,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint32_t tS = tmem + C::TM_S + 128 * s + lanes, tO = tmem + C::TM_O + D * s + lanes;
     int steps = 0, outs = 0;
     bool ok = true;
-    for (int i = 0; ok && unit_of(i) < a.units; ++i) {
-      const Unit u(a, unit_of(i));
+    for (long long pos = begin; ok && pos < end;) {
+      int n, e0, step, valid;  // what the loop needs (the piece again behind it: registers)
+      {
+        const Piece u(a, pos, end);
+        n = u.n;
+        e0 = u.first(s);
+        step = u.alone ? 2 : 1;
+        valid = p.P - (u.t0 + e0) * kTile;  // columns from the entry's tile on
+      }
       float m = -INFINITY, l = 0.f;
-      for (int e = u.first(s); e < u.n; e += u.alone ? 2 : 1) {
-        const int valid = p.P - (u.t0 + e) * kTile;  // columns of the prefix' last tile
+      for (int e = e0; e < n; e += step, valid -= step * kTile) {
         if (!mbar_wait(&bar.s_full[s], steps & 1, abort)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const bool first = e == u.first(s);
+        const bool first = e == e0;
         if (valid >= kTile) whole_step<D>(tS, tO, a.sl2, first, m, l);
         else masked_step<D>(tS, tO, (valid + 15) & ~15, 0, valid - 1, 0, a.sl2, first, m, l);
         tmem_wait_st();
@@ -307,7 +319,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       }
       if (!ok) break;
       // ---- the rows' sums
-      const long long at = ((long long)u.hk * p.row_tiles + u.row_tile(s)) * a.slots + (u.alone ? 2 * u.part + s : u.part);
+      const Piece u(a, pos, end);
+      pos += n;
+      const long long at = ((long long)u.hk * p.row_tiles + u.row_tile(s)) * p.slots + (u.alone ? 2 * u.index + s : u.index);
       if (u.some(s)) {
         if (!mbar_wait(&bar.o_full[s], outs & 1, abort)) break;
         ++outs;
@@ -338,13 +352,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------- a row's sums, joined
-constexpr int kJoinRows = 32, kJoinChannels = 32, kJoinThreads = 256;
+constexpr int kJoinRows = 32, kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
 struct JoinArgs {
   Plan p;
   const float4* sums;
   const float2* stats;
-  int slots;
   View<__nv_bfloat16> o;
   const int* lens;
   int nk;
@@ -356,105 +369,151 @@ struct JoinArgs {
   float* lse;
 };
 
-// 32 rows of a tile, 32 channels: lanes are rows while the prefix' sums are added (each warp
-// four channels), then channels.
-template <int D, bool kDecode>
+// 32 rows of a tile, CH channels.  Lanes are rows while the prefix' sums are added (each warp some
+// of the channels), then channels.
+template <int D, int CH, bool kDecode>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const JoinArgs a) {
-  __shared__ float sum[kJoinRows][kJoinChannels + 4];
-  __shared__ float top[kJoinRows], total[kJoinRows];
+  constexpr int Q = CH / 4 / kJoinWarps;  // fours of channels that a warp adds
+  extern __shared__ float2 stats[];       // [sums of a row][32]
+  __shared__ __align__(16) float sum[kJoinRows][CH + 4];
+  __shared__ float own_m[kJoinRows], own_l[kJoinRows], top[kJoinRows], total[kJoinRows];
   pdl_launch_dependents();
   pdl_wait();
   const Plan& p = a.p;
-  const int groups = kTile / kJoinRows;
-  const int tile = blockIdx.x / groups, rt = tile % p.row_tiles, hk = tile / p.row_tiles;
-  const int r0 = blockIdx.x % groups * kJoinRows, c0 = blockIdx.y * kJoinChannels;
+  constexpr int groups = kTile / kJoinRows;
+  const int tile = blockIdx.x / groups, hk = tile / p.row_tiles, rt = tile - hk * p.row_tiles;
+  const int r0 = blockIdx.x % groups * kJoinRows, c0 = blockIdx.y * CH;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = p.tq * p.tg * p.tb;
   if (r0 >= rows) return;
   const Box box(p, rt);
-  // row r of the tile
   struct Row {
     int b, h, q;
     bool valid;
   };
   auto row_of = [&](int r) {
     Row x;
-    const int i = r % p.tq, g = r / p.tq % p.tg, bb = r / (p.tq * p.tg);
+    const int g = r / p.tq, bb = g / p.tg;
     x.b = box.b + bb;
-    x.h = hk * p.group + box.g + g;
-    x.q = box.q + i;
-    x.valid = r < rows && x.b < p.B && box.g + g < p.group && x.q < p.nq;
+    x.h = box.g + g - bb * p.tg;
+    x.q = box.q + r - g * p.tq;
+    x.valid = r < rows && x.b < p.B && x.h < p.group && x.q < p.nq;
+    x.h += hk * p.group;
     return x;
   };
-  const int mine = rt == p.row_tiles - 1 && p.row_tiles % 2 ? 2 * p.parts : p.parts;  // sums of a row
-  const long long at = ((long long)hk * p.row_tiles + rt) * a.slots;
-  const float2* stats = a.stats + at * kTile + r0 + lane;
-  const Row me = row_of(r0 + lane);
-  // ---- maximum over the parts and the own keys (every warp for itself)
-  float m = -INFINITY, l = 0.f;
-  float2 own = make_float2(-INFINITY, 0.f);
-  if (me.valid) {
-#pragma unroll 4
-    for (int s = 0; s < mine; ++s) m = fmaxf(m, stats[s * kTile].x);
-    if constexpr (kDecode) {
-      const float* src = a.own + ((long long)me.b * p.nh + me.h) * a.splits * (D + 2) + D;
-      for (int s = 0; s < a.splits; ++s) own.x = fmaxf(own.x, src[s * (D + 2)]);
-      for (int s = 0; s < a.splits; ++s) {
-        const float x = src[s * (D + 2)];
-        own.y += src[s * (D + 2) + 1] * (x == -INFINITY ? 0.f : fast_exp2(x - own.x));
+  const int pairs = (p.row_tiles + 1) / 2;
+  const bool alone = rt == p.row_tiles - 1 && p.row_tiles % 2;
+  const int mine = p.pieces(hk * pairs + rt / 2) * (alone ? 2 : 1);  // sums of a row
+  const long long at = ((long long)hk * p.row_tiles + rt) * p.slots;
+  for (int s = warp; s < mine; s += kJoinWarps) stats[s * 32 + lane] = a.stats[(at + s) * kTile + r0 + lane];
+  // the own keys' maximum and sum
+  if constexpr (kDecode) {
+    for (int i = warp; i < kJoinRows; i += kJoinWarps) {
+      const Row x = row_of(r0 + i);
+      float m = -INFINITY, l = 0.f;
+      if (x.valid) {
+        const float* src = a.own + ((long long)x.b * p.nh + x.h) * a.splits * (D + 2) + D;
+        for (int s = lane; s < a.splits; s += 32) {
+          const float n = fmaxf(m, src[s * (D + 2)]), f = src[s * (D + 2)] == -INFINITY ? 0.f : fast_exp2(src[s * (D + 2)] - n);
+          l = l * (m == -INFINITY ? 0.f : fast_exp2(m - n)) + src[s * (D + 2) + 1] * f;
+          m = n;
+        }
       }
-    } else {
-      own = make_float2(kLog2 * a.own_lse[((long long)me.b * p.nh + me.h) * p.nq + me.q], 1.f);
-      if (own.x == -INFINITY) own.y = 0.f;
-    }
-    m = fmaxf(m, own.x);
-  }
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (me.valid) {
-    const float4* src = a.sums + (at * (D / 4) + c0 / 4 + warp) * kTile + r0 + lane;
-#pragma unroll 4
-    for (int s = 0; s < mine; ++s) {
-      const float2 x = stats[s * kTile];
-      const float f = x.x == -INFINITY ? 0.f : fast_exp2(x.x - m);
-      l += x.y * f;
-      if (x.y != 0.f) {  // (a part that had no tile has left nothing)
-        const float4 v = src[(long long)s * (D / 4) * kTile];
-        acc.x += v.x * f;
-        acc.y += v.y * f;
-        acc.z += v.z * f;
-        acc.w += v.w * f;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, d), l2 = __shfl_xor_sync(0xffffffffu, l, d), n = fmaxf(m, m2);
+        l = l * (m == -INFINITY ? 0.f : fast_exp2(m - n)) + l2 * (m2 == -INFINITY ? 0.f : fast_exp2(m2 - n));
+        m = n;
+      }
+      if (lane == 0) {
+        own_m[i] = m;
+        own_l[i] = l;
       }
     }
-    l += own.y * (own.x == -INFINITY ? (own.y != own.y ? own.y : 0.f) : fast_exp2(own.x - m));
-  }
-  *reinterpret_cast<float4*>(&sum[lane][4 * warp]) = acc;
-  if (warp == 0) {
-    top[lane] = m;
-    total[lane] = l;
+  } else if (warp == 0) {
+    const Row x = row_of(r0 + lane);
+    const float m = x.valid ? kLog2 * a.own_lse[((long long)x.b * p.nh + x.h) * p.nq + x.q] : -INFINITY;
+    own_m[lane] = m;
+    own_l[lane] = m == -INFINITY ? 0.f : 1.f;
   }
   __syncthreads();
-  for (int i = warp; i < kJoinRows; i += kJoinThreads / 32) {
+  float m = own_m[lane], l = 0.f;
+  for (int s = 0; s < mine; ++s) m = fmaxf(m, stats[s * 32 + lane].x);
+  float4 acc[Q];
+#pragma unroll
+  for (int c = 0; c < Q; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r0 + lane < rows) {
+    const float4* src = a.sums + (at * (D / 4) + c0 / 4 + warp * Q) * kTile + r0 + lane;
+    constexpr int U = Q > 2 ? 2 : 8;  // pieces on their way at a time
+    for (int s0 = 0; s0 < mine; s0 += U) {
+      float4 v[U][Q];
+      float f[U];
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        const float2 st = s0 + x < mine ? stats[(s0 + x) * 32 + lane] : make_float2(-INFINITY, 0.f);
+        f[x] = st.x == -INFINITY ? 0.f : fast_exp2(st.x - m);
+        l += st.y * f[x];
+#pragma unroll
+        for (int c = 0; c < Q; ++c)  // (a piece that had no tile for the slot has left nothing)
+          v[x][c] = st.y != 0.f ? src[((long long)(s0 + x) * (D / 4) + c) * kTile] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int x = 0; x < U; ++x)
+#pragma unroll
+        for (int c = 0; c < Q; ++c) {
+          acc[c].x += v[x][c].x * f[x];
+          acc[c].y += v[x][c].y * f[x];
+          acc[c].z += v[x][c].z * f[x];
+          acc[c].w += v[x][c].w * f[x];
+        }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < Q; ++c) *reinterpret_cast<float4*>(&sum[lane][4 * (warp * Q + c)]) = acc[c];
+  if (warp == 0) {
+    // (a NaN among the own keys' scores stays one: their sum is NaN then)
+    const float f = own_m[lane] == -INFINITY ? 0.f : fast_exp2(own_m[lane] - m);
+    top[lane] = m;
+    total[lane] = l + own_l[lane] * f;
+  }
+  __syncthreads();
+  constexpr int W = CH / 32;  // neighbouring channels of a lane
+  for (int i = warp; i < kJoinRows; i += kJoinWarps) {
     const Row x = row_of(r0 + i);
     if (!x.valid) continue;
     // padding: a slot of the batch that is not in use, or a row behind its sequence
     const int n = a.lens ? a.lens[x.b] : a.nk;
     const bool pad = kDecode ? n < 0 : x.q + a.nk - p.nq >= min(n, a.nk);
-    const float mm = top[i];
-    float v = sum[i][lane];
-    __nv_bfloat16* o = a.o.row(x.b, x.h, x.q) + c0 + lane;
+    const float mm = top[i], inv = 1.f / total[i];
+    float v[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) v[w] = sum[i][lane * W + w];
+    __nv_bfloat16* o = a.o.row(x.b, x.h, x.q) + c0 + lane * W;
     if constexpr (kDecode) {
       const float* src = a.own + ((long long)x.b * p.nh + x.h) * a.splits * (D + 2);
       for (int s = 0; s < a.splits; ++s) {
         const float y = src[s * (D + 2) + D];
-        if (y != -INFINITY) v += src[s * (D + 2) + c0 + lane] * fast_exp2(y - mm);
+        if (y == -INFINITY) continue;
+        const float f = fast_exp2(y - mm);
+#pragma unroll
+        for (int w = 0; w < W; ++w) v[w] += src[s * (D + 2) + c0 + lane * W + w] * f;
       }
-    } else {
-      const long long row = ((long long)x.b * p.nh + x.h) * p.nq + x.q;
-      const float y = kLog2 * a.own_lse[row];
-      if (y != -INFINITY) v += __bfloat162float(*o) * fast_exp2(y - mm);
-      if (a.lse && blockIdx.y == 0 && lane == 0) a.lse[row] = pad ? -INFINITY : mm * kLn2 + logf(total[i]);
+    } else if (own_m[i] != -INFINITY) {
+      const float f = fast_exp2(own_m[i] - mm);
+#pragma unroll
+      for (int w = 0; w < W; ++w) v[w] += __bfloat162float(o[w]) * f;
     }
-    *o = __float2bfloat16_rn(pad ? 0.f : v / total[i]);
+    if constexpr (W == 1) {
+      *o = __float2bfloat16_rn(pad ? 0.f : v[0] * inv);
+    } else {
+      uint32_t y[W / 2 > 0 ? W / 2 : 1];
+#pragma unroll
+      for (int w = 0; w < W; w += 2) y[w / 2] = pad ? 0u : pack2(v[w] * inv, v[w + 1] * inv);
+      if constexpr (W == 2) *reinterpret_cast<uint32_t*>(o) = y[0];
+      else *reinterpret_cast<uint2*>(o) = make_uint2(y[0], y[W / 2 - 1]);
+    }
+    if (!kDecode && a.lse && lane == 0 && blockIdx.y == 0)
+      a.lse[((long long)x.b * p.nh + x.h) * p.nq + x.q] = pad ? -INFINITY : mm * kLn2 + logf(total[i]);
   }
 }
 
@@ -481,24 +540,20 @@ Plan make_plan(const PrefixShape& x) {
   p.q_tiles = cdiv(p.nq, p.tq);
   p.g_tiles = cdiv(p.group, p.tg);
   p.key_tiles = cdiv(p.P, kTile);
-  // Parts: the fewest rounds over the SMs, counted in key tiles; a unit's beginning and end and the
-  // joining of its sums take about as long as three more (measured: 64 sequences, 32 heads on 8,
-  // 16384 keys).
-  const long long pairs = (long long)p.nkv * cdiv(p.row_tiles, 2);
-  long long best = -1;
-  for (int parts = 1; parts <= std::min(p.key_tiles, kMaxPrefixParts); ++parts) {
-    const long long time = ((pairs * parts + 151) / 152) * (cdiv(p.key_tiles, parts) + 3);
-    if (best < 0 || time < best) {
-      best = time;
-      p.parts = parts;
-    }
-  }
+  const int pairs = cdiv(p.row_tiles, 2);
+  p.steps = (long long)p.nkv * pairs * p.key_tiles;
+  // a CTA for each SM, but not for less than two key tiles
+  p.ctas = (int)std::min<long long>(kPrefixCtas, (p.steps + 1) / 2);
+  int most = 1;  // pieces of a unit: all units are alike but for where they begin
+  for (int u = 0; u < std::min(p.nkv * pairs, 2 * kPrefixCtas); ++u) most = std::max(most, p.pieces(u));
+  if (p.nkv * pairs > 2 * kPrefixCtas) most = std::max(most, 2);
+  p.slots = p.row_tiles % 2 ? 2 * most : most;
   return p;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-size_t sums_bytes(const Plan& p, int d) { return (size_t)p.nkv * p.row_tiles * p.slots() * kTile * d * 4; }
-size_t stats_bytes(const Plan& p) { return (size_t)p.nkv * p.row_tiles * p.slots() * kTile * 8; }
+size_t sums_bytes(const Plan& p, int d) { return (size_t)p.nkv * p.row_tiles * p.slots * kTile * d * 4; }
+size_t stats_bytes(const Plan& p) { return (size_t)p.nkv * p.row_tiles * p.slots * kTile * 8; }
 
 template <int D>
 cudaError_t prefix_part(const PrefixArgs& x, const Plan& p, cudaStream_t st) {
@@ -508,8 +563,6 @@ cudaError_t prefix_part(const PrefixArgs& x, const Plan& p, cudaStream_t st) {
   a.sums = static_cast<float4*>(x.ws);
   a.stats = reinterpret_cast<float2*>(static_cast<char*>(x.ws) + sums_bytes(p, D));
   a.sl2 = x.scale * kLog2;
-  a.units = p.nkv * ((p.row_tiles + 1) / 2) * p.parts;
-  a.slots = p.slots();
   CUtensorMap mq, mk, mv;
   if (!map_view_box(&mq, x.q.p, x.q.sb, x.q.sh, x.q.sn, p.B, p.nh, p.nq, D, p.tq, p.tg, p.tb) ||
       !map_view(&mk, x.kp.p, x.kp.sb, x.kp.sh, x.kp.sn, 1, p.nkv, p.P, D) ||
@@ -518,7 +571,7 @@ cudaError_t prefix_part(const PrefixArgs& x, const Plan& p, cudaStream_t st) {
   auto kern = prefix_tc_kernel<D>;
   const cudaError_t e = set_max_dynamic_smem((const void*)kern, C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(std::min(a.units, device_sm_count())), dim3(C::kThreads), C::SMEM, st, mq, mk, mv, a);
+  return launch_pdl(kern, dim3(p.ctas), dim3(C::kThreads), C::SMEM, st, mq, mk, mv, a);
 }
 
 template <int D>
@@ -532,7 +585,6 @@ cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
   j.p = p;
   j.sums = reinterpret_cast<const float4*>(ws);
   j.stats = reinterpret_cast<const float2*>(ws + sums_bytes(p, D));
-  j.slots = p.slots();
   j.o = x.o;
   j.lens = x.lens;
   j.nk = x.s.nk;
@@ -562,8 +614,13 @@ cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
     j.lse = x.lse;
   }
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.nkv * p.row_tiles * (kTile / kJoinRows), D / kJoinChannels);
-  return launch_pdl(decode ? prefix_join_kernel<D, true> : prefix_join_kernel<D, false>, grid, dim3(kJoinThreads), 0, st, j);
+  // Rows are few when decoding: their channels go to several CTAs then (each reads the statistics).
+  const int groups = p.nkv * p.row_tiles * (kTile / kJoinRows), smem = p.slots * kJoinRows * (int)sizeof(float2);
+  auto kern = groups >= 304 ? (decode ? prefix_join_kernel<D, D, true> : prefix_join_kernel<D, D, false>)
+                            : (decode ? prefix_join_kernel<D, 32, true> : prefix_join_kernel<D, 32, false>);
+  e = set_max_dynamic_smem((const void*)kern, 2 * kPrefixCtas * kJoinRows * (int)sizeof(float2));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(groups, groups >= 304 ? 1 : D / 32), dim3(kJoinThreads), smem, st, j);
 }
 
 }  // namespace

@@ -7,11 +7,11 @@
 // second cache; a step that evicts one row moves at most one.
 //
 // The selection is a radix select: a CTA for each list (sequence and key/value head) makes
-// sortable integers of the weights in shared memory, counts their first 11 bits, gathers those
-// that share the bits of the keep-th largest, and goes on with 11 and 10 bits among these.  What
-// stays is then one bit per row: ranks, gaps and the rows that fill them are sums over words of
-// 32 rows.  Instructions bound it (one CTA works on a list), so rows are gone through four times
-// at most.  The moves are a copy bound by memory: a second kernel over all lists, or, where a list
+// sortable integers of the weights in shared memory, counts their first 13 bits (sign, exponent, 4
+// bits of the mantissa: fewer would meet in the same counters), gathers those that share the bits
+// of the keep-th largest, and compares these with one another.  What stays is then one bit per
+// row: ranks, gaps and the rows that fill them are sums over words of 32 rows.  Latencies and
+// instructions of the one CTA bound it.  The moves are a copy bound by memory: a second kernel over all lists, or, where a list
 // can have no more than kFewMoves, the same one.
 #include <algorithm>
 
@@ -21,9 +21,9 @@
 namespace psa {
 namespace {
 
-constexpr int kBins = 2048;
-constexpr int kKeysInShared = 45 * 1024;  // longer lists are read again in every pass
-constexpr int kGathered = 1024;           // more that share their first bits are counted where they are
+constexpr int kBits = 13, kBins = 1 << kBits;  // of a key's first digit: 4 bits of the mantissa
+constexpr int kKeysInShared = 40 * 1024;       // longer lists are read again in every pass
+constexpr int kGathered = 1024;                // more that share their first digit are counted where they are
 constexpr int kFewMoves = 32;
 constexpr int kMoveThreads = 256, kMoveUnroll = 8;
 constexpr uint32_t kSafe = 0xffffffffu;
@@ -45,23 +45,22 @@ struct Shared {
 // Sum of x over the threads in front of this one; total: over all.
 __device__ __forceinline__ unsigned long long in_front(Shared& sh, unsigned long long x, unsigned long long& total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  unsigned long long upto = x;
+  auto scan = [&](unsigned long long v) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const unsigned long long y = __shfl_up_sync(kAll, upto, d);
-    if (lane >= d) upto += y;
-  }
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned long long y = __shfl_up_sync(kAll, v, d);
+      if (lane >= d) v += y;
+    }
+    return v;
+  };
+  const unsigned long long upto = scan(x);
   __syncthreads();  // of the use before
   if (lane == 31) sh.warp[warp] = upto;
   __syncthreads();
-  unsigned long long before = 0;
-  total = 0;
-  for (int w = 0; w < warps; ++w) {
-    const unsigned long long y = sh.warp[w];
-    if (w < warp) before += y;
-    total += y;
-  }
-  return before + upto - x;
+  const unsigned long long w = scan(lane < warps ? sh.warp[lane] : 0);
+  total = __shfl_sync(kAll, w, 31);
+  const unsigned long long before = __shfl_sync(kAll, w, max(warp - 1, 0));
+  return (warp > 0 ? before : 0) + upto - x;
 }
 
 // The bin that holds the need-th largest, from counts that are complete; what is above it is
@@ -69,7 +68,10 @@ __device__ __forceinline__ unsigned long long in_front(Shared& sh, unsigned long
 __device__ __forceinline__ uint32_t find_bin(Shared& sh, uint32_t& need) {
   const int tid = threadIdx.x, per = kBins / blockDim.x, hi = kBins - 1 - tid * per;
   uint32_t mine = 0;
-  for (int i = 0; i < per; ++i) mine += sh.hist[hi - i];
+  for (int i = 0; i < per; i += 4) {
+    const uint4 c = *reinterpret_cast<const uint4*>(&sh.hist[hi - i - 3]);
+    mine += c.x + c.y + c.z + c.w;
+  }
   unsigned long long total;
   uint32_t above = (uint32_t)in_front(sh, mine, total);
   if (above < need && need <= above + mine) {
@@ -83,14 +85,18 @@ __device__ __forceinline__ uint32_t find_bin(Shared& sh, uint32_t& need) {
   return sh.digit;
 }
 
+// kCached: the list's keys, and two bits for each, lie in shared memory.
+template <bool kCached>
 __global__ void __launch_bounds__(1024)
     evict_select_kernel(const EvictArgs a, const int cap, const int row16, const bool move) {
   extern __shared__ uint32_t dynamic[];
-  __shared__ Shared sh;
+  __shared__ __align__(16) Shared sh;
   pdl_launch_dependents();
-  pdl_wait();
   const int list = blockIdx.x, b = list / a.nkv, h = list % a.nkv;
   const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < kBins / 4; i += threads) reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) sh.gathered = 0;
+  pdl_wait();
   const int len = max(0, min(a.lens[b], a.max_len)), count = min(len, a.keep);
   const float* w = a.weights + (long long)list * a.max_len;
   const int* pos = a.positions + (long long)list * a.max_len;
@@ -107,70 +113,96 @@ __global__ void __launch_bounds__(1024)
     }
     return;
   }
-  for (int i = tid; i < kBins; i += threads) sh.hist[i] = 0;
-  if (tid == 0) sh.gathered = 0;
   // ---- which rows are kept whatever their weight
+  uint32_t* keys = dynamic;  // (positions at first)
   long long safe_from = 1LL << 40;
-  if (a.recent > 0) {
+  if (kCached || a.recent > 0) {
     int newest = INT_MIN;
-#pragma unroll 4
-    for (int r = tid; r < len; r += threads) newest = max(newest, pos[r]);
+#pragma unroll 8
+    for (int r = tid; r < len; r += threads) {
+      const int p = pos[r];
+      if (kCached) keys[r] = p;
+      newest = max(newest, p);
+    }
     newest = __reduce_max_sync(kAll, newest);
     if (lane == 0) sh.warp[warp] = (uint32_t)newest;
     __syncthreads();
     newest = __reduce_max_sync(kAll, lane < threads / 32 ? (int)(uint32_t)sh.warp[lane] : INT_MIN);
-    safe_from = (long long)newest - a.recent + 1;
+    if (a.recent > 0) safe_from = (long long)newest - a.recent + 1;
   }
-  __syncthreads();
-  // ---- keys, and how many have the same first 11 bits; what stays in its place already
-  const bool cached = len <= kKeysInShared, apart = w_out != w, apart_pos = pos_out != pos;
-  uint32_t* keys = dynamic;
+  // ---- keys, and how many have the same first digit; what stays in its place already
+  const bool apart = w_out != w, apart_pos = pos_out != pos;
   auto to_key = [&](float x, int p) { return p < a.sinks || p >= safe_from ? kSafe : sortable(x); };
-#pragma unroll 4
+  __syncthreads();
+#pragma unroll 8
   for (int r = tid; r < len; r += threads) {
     const float x = w[r];
-    const int p = pos[r];
+    const int p = kCached ? (int)keys[r] : pos[r];
     const uint32_t k = to_key(x, p);
-    if (cached) keys[r] = k;
-    atomicAdd(&sh.hist[k >> 21], 1u);
+    if (kCached) keys[r] = k;
+    atomicAdd(&sh.hist[k >> (32 - kBits)], 1u);
     if (r < count) {  // (gaps are written again below)
       if (apart) w_out[r] = x;
       if (apart_pos) pos_out[r] = p;
     }
   }
-  auto key = [&](int r) { return cached ? keys[r] : to_key(w[r], pos[r]); };
+  auto key = [&](int r) {
+    if constexpr (kCached) return keys[r];
+    else return to_key(w[r], pos[r]);
+  };
   __syncthreads();
   uint32_t need = count, top = find_bin(sh, need);
 
   // ---- the count-th largest key, and how many of its equals are kept
   const uint32_t shared_by = sh.hist[top];
-  const bool few = shared_by <= kGathered;
-  if (few) {
+  if (shared_by <= kGathered) {
+#pragma unroll 4
     for (int r = tid; r < len; r += threads) {
       const uint32_t k = key(r);
-      if (k >> 21 == top) sh.some[atomicAdd(&sh.gathered, 1u)] = k;
+      if (k >> (32 - kBits) == top) sh.some[atomicAdd(&sh.gathered, 1u)] = k;
     }
-  }
+    __syncthreads();
+    for (uint32_t i = tid; i < shared_by; i += threads) {
+      const uint32_t k = sh.some[i];
+      uint32_t above = 0, equal = 0;
+#pragma unroll 8
+      for (uint32_t x = 0; x < shared_by; ++x) {
+        above += sh.some[x] > k;
+        equal += sh.some[x] == k;
+      }
+      if (above < need && need <= above + equal) {  // (its equals say the same)
+        sh.digit = k;
+        sh.need = need - above;
+      }
+    }
+    __syncthreads();
+    top = sh.digit;
+    need = sh.need;
+  } else {
 #pragma unroll 1
-  for (int pass = 1; pass < 3; ++pass) {
-    const int shift = pass == 1 ? 10 : 0, bits = pass == 1 ? 11 : 10;
-    __syncthreads();  // gathered, and the counts read
-    for (int i = tid; i < kBins; i += threads) sh.hist[i] = 0;
-    __syncthreads();
-    const int n = few ? (int)shared_by : len;
-    for (int i = tid; i < n; i += threads) {
-      const uint32_t k = few ? sh.some[i] : key(i);
-      if (k >> (shift + bits) == top) atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+    for (int shift = 32 - kBits; shift > 0;) {
+      const int bits = min(shift, kBits), at = shift - bits;
+      __syncthreads();  // the counts are read
+      for (int i = tid; i < kBins; i += threads) sh.hist[i] = 0;
+      __syncthreads();
+      for (int r = tid; r < len; r += threads) {
+        const uint32_t k = key(r);
+        if (k >> shift == top) atomicAdd(&sh.hist[(k >> at) & ((1u << bits) - 1u)], 1u);
+      }
+      __syncthreads();
+      const uint32_t digit = find_bin(sh, need);
+      top = top << bits | digit;
+      shift = at;
     }
-    __syncthreads();
-    const uint32_t digit = find_bin(sh, need);
-    top = top << bits | digit;
   }
 
   // ---- one bit per row: larger than that key, or equal to it
   const int words = (len + 31) / 32;
-  uint32_t* larger = cached ? keys + (len + 3) / 4 * 4 : a.words + (long long)list * 2 * ((a.max_len + 31) / 32);
+  uint32_t* larger;
+  if constexpr (kCached) larger = keys + (len + 3) / 4 * 4;
+  else larger = a.words + (long long)list * 2 * ((a.max_len + 31) / 32);
   uint32_t* equal = larger + words;
+#pragma unroll 4
   for (int x = warp; x < words; x += threads / 32) {
     const int r = x * 32 + lane;
     const uint32_t k = r < len ? key(r) : 0u;
@@ -201,16 +233,26 @@ __global__ void __launch_bounds__(1024)
     larger[x] = kept;
     n += (unsigned long long)__popc(~kept & here) << 32 | __popc(kept & ~here);
   }
-  const unsigned long long at = in_front(sh, n, total);
-  uint32_t gap_at = (uint32_t)(at >> 32), mover_at = (uint32_t)at;
+  unsigned long long at = in_front(sh, n, total);
   const uint32_t moves = (uint32_t)total;
   for (int x = from; x < to; ++x) {
+    // where the word's gaps are listed, or the rows that fill some (of the word that has both, the
+    // latter are the first of their list)
     const uint32_t kept = larger[x], here = in_place(x);
-    for (uint32_t g = ~kept & here; g; g &= g - 1) dst[gap_at++] = x * 32 + __ffs(g) - 1;
-    for (uint32_t m = kept & ~here; m; m &= m - 1) src[mover_at++] = x * 32 + __ffs(m) - 1;
+    equal[x] = here ? (uint32_t)(at >> 32) : (uint32_t)at;
+    at += (unsigned long long)__popc(~kept & here) << 32 | __popc(kept & ~here);
   }
   if (tid == 0) a.counts[list] = moves;
   __syncthreads();
+#pragma unroll 4
+  for (int x = warp; x < words; x += threads / 32) {
+    const uint32_t kept = larger[x], here = in_place(x), first = equal[x];
+    const uint32_t gaps = ~kept & here, movers = kept & ~here, bit = 1u << lane, below = bit - 1u;
+    if (gaps & bit) dst[first + __popc(gaps & below)] = x * 32 + lane;
+    if (movers & bit) src[(here ? 0u : first) + __popc(movers & below)] = x * 32 + lane;
+  }
+  __syncthreads();
+#pragma unroll 4
   for (uint32_t i = tid; i < moves; i += threads) {
     const int s = src[i], d = dst[i];
     const float x = w[s];
@@ -282,13 +324,16 @@ cudaError_t launch_kv_evict(EvictArgs a, int row16, void* ws, cudaStream_t st) {
   a.counts = static_cast<int*>(ws);
   a.moves = reinterpret_cast<int*>(static_cast<char*>(ws) + ((size_t)lists * 4 + 15) / 16 * 16);
   a.words = reinterpret_cast<uint32_t*>(a.moves + (size_t)lists * 2 * cap);
-  const cudaError_t e = set_max_dynamic_smem((const void*)evict_select_kernel, shared_bytes(kKeysInShared));
-  if (e != cudaSuccess) return e;
-  const bool fused = cap <= kFewMoves;
+  const bool fused = cap <= kFewMoves, cached = a.max_len <= kKeysInShared;
   // (a power of two that divides the bins)
   const int threads = a.max_len > 8192 ? 1024 : a.max_len > 1024 ? 512 : 256;
-  const int smem = shared_bytes(std::min(a.max_len, kKeysInShared));
-  const cudaError_t s = launch_pdl(evict_select_kernel, dim3(lists), dim3(threads), smem, st, a, cap, row16, fused);
+  const int smem = cached ? shared_bytes(a.max_len) : 0;
+  auto select = cached ? evict_select_kernel<true> : evict_select_kernel<false>;
+  if (cached) {
+    const cudaError_t e = set_max_dynamic_smem((const void*)select, shared_bytes(kKeysInShared));
+    if (e != cudaSuccess) return e;
+  }
+  const cudaError_t s = launch_pdl(select, dim3(lists), dim3(threads), smem, st, a, cap, row16, fused);
   if (s != cudaSuccess || fused) return s;
   const long long units = (long long)cap * 2 * row16, per = kMoveThreads * kMoveUnroll;
   const dim3 grid((unsigned)((units + per - 1) / per), lists);

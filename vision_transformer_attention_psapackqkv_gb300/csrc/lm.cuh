@@ -201,6 +201,8 @@ struct DecodeArgs {
   const void *kcodes, *kscales, *vcodes, *vscales;  // 4-bit cache
   float* ws;
   float scale;
+  // partial results: blocks of 16 keys of a run, runs that there is room for in ws
+  int run, parts;
   // along with weights for each key: [B, nkv, n_k], the scores' place in the workspace, and how many
   // keys of a list have one
   float *weights, *scores;
@@ -212,10 +214,14 @@ size_t decode_ws_bytes(const Window& w, int d);
 cudaError_t launch_window_decode(const DecodeArgs& a, int d, bool kv4, cudaStream_t st);
 size_t decode_weights_ws_bytes(const Window& w, int d);
 cudaError_t launch_window_decode_weights(const DecodeArgs& a, int d, cudaStream_t st);
-// The parts' results alone, [B, nh, decode_splits][d + 2]: outputs relative to the maximum (log2
-// units), the maximum, the sum.
+// Partial results of runs of blocks of 16 keys alone, [B, nh, parts][d + 4]: outputs relative to the
+// maximum (log2 units), the maximum, the sum.  A sequence has as many as it has runs.
+struct DecodeRuns {
+  int run, parts;
+};
+DecodeRuns decode_runs(const Window& w);
 size_t decode_parts_ws_bytes(const Window& w, int d);
-cudaError_t launch_window_decode_parts(const DecodeArgs& a, int d, cudaStream_t st);
+cudaError_t launch_window_decode_parts(DecodeArgs a, int d, cudaStream_t st);
 
 // ---------------------------------------------------------------- behind a shared prefix
 struct PrefixShape {

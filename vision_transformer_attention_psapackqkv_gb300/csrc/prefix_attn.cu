@@ -361,10 +361,10 @@ struct JoinArgs {
   View<__nv_bfloat16> o;
   const int* lens;
   int nk;
-  // own keys, decoding: partial sums [B, nh, splits][D + 2]; prompts: log-sum-exp [B, nh, nq] (with
+  // own keys, decoding: partial sums [B, nh, parts][D + 4] of runs of blocks of 16 keys; prompts: log-sum-exp [B, nh, nq] (with
   // the output in o), and where the whole rows' goes to
   const float* own;
-  int splits;
+  int run, parts;
   const float* own_lse;
   float* lse;
 };
@@ -406,29 +406,32 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const JoinArg
   const int mine = p.pieces(hk * pairs + rt / 2) * (alone ? 2 : 1);  // sums of a row
   const long long at = ((long long)hk * p.row_tiles + rt) * p.slots;
   for (int s = warp; s < mine; s += kJoinWarps) stats[s * 32 + lane] = a.stats[(at + s) * kTile + r0 + lane];
+  auto own_parts = [&](int b) { return ((max(0, min(a.lens[b], a.nk)) + 15) / 16 + a.run - 1) / a.run; };
   // the own keys' maximum and sum
   if constexpr (kDecode) {
-    for (int i = warp; i < kJoinRows; i += kJoinWarps) {
-      const Row x = row_of(r0 + i);
-      float m = -INFINITY, l = 0.f;
-      if (x.valid) {
-        const float* src = a.own + ((long long)x.b * p.nh + x.h) * a.splits * (D + 2) + D;
-        for (int s = lane; s < a.splits; s += 32) {
-          const float n = fmaxf(m, src[s * (D + 2)]), f = src[s * (D + 2)] == -INFINITY ? 0.f : fast_exp2(src[s * (D + 2)] - n);
-          l = l * (m == -INFINITY ? 0.f : fast_exp2(m - n)) + src[s * (D + 2) + 1] * f;
-          m = n;
-        }
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, d), l2 = __shfl_xor_sync(0xffffffffu, l, d), n = fmaxf(m, m2);
-        l = l * (m == -INFINITY ? 0.f : fast_exp2(m - n)) + l2 * (m2 == -INFINITY ? 0.f : fast_exp2(m2 - n));
+    // (eight lanes for each of a warp's four rows: one latency for all of them)
+    const int i = warp * 4 + lane / 8;
+    const Row x = row_of(r0 + i);
+    float m = -INFINITY, l = 0.f;
+    if (x.valid) {
+      const float* src = a.own + ((long long)x.b * p.nh + x.h) * a.parts * (D + 4) + D;
+      const int own = own_parts(x.b);
+      for (int s = lane % 8; s < own; s += 8) {
+        const float2 y = *reinterpret_cast<const float2*>(src + s * (D + 4));
+        const float n = fmaxf(m, y.x);
+        l = l * (m == -INFINITY ? 0.f : fast_exp2(m - n)) + y.y * (y.x == -INFINITY ? 0.f : fast_exp2(y.x - n));
         m = n;
       }
-      if (lane == 0) {
-        own_m[i] = m;
-        own_l[i] = l;
-      }
+    }
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, d), l2 = __shfl_xor_sync(0xffffffffu, l, d), n = fmaxf(m, m2);
+      l = l * (m == -INFINITY ? 0.f : fast_exp2(m - n)) + l2 * (m2 == -INFINITY ? 0.f : fast_exp2(m2 - n));
+      m = n;
+    }
+    if (lane % 8 == 0) {
+      own_m[i] = m;
+      own_l[i] = l;
     }
   } else if (warp == 0) {
     const Row x = row_of(r0 + lane);
@@ -477,42 +480,42 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const JoinArg
     total[lane] = l + own_l[lane] * f;
   }
   __syncthreads();
-  constexpr int W = CH / 32;  // neighbouring channels of a lane
-  for (int i = warp; i < kJoinRows; i += kJoinWarps) {
+  // lanes are fours of channels now, and rows (CH 32) or parts of the own keys side by side
+  constexpr int F = CH / 4, R = 32 / F;
+  const int c4 = lane % F, sub = lane / F;
+#pragma unroll 2
+  for (int i0 = warp * R; i0 < kJoinRows; i0 += kJoinWarps * R) {
+    const int i = i0 + sub;
     const Row x = row_of(r0 + i);
     if (!x.valid) continue;
     // padding: a slot of the batch that is not in use, or a row behind its sequence
     const int n = a.lens ? a.lens[x.b] : a.nk;
     const bool pad = kDecode ? n < 0 : x.q + a.nk - p.nq >= min(n, a.nk);
     const float mm = top[i], inv = 1.f / total[i];
-    float v[W];
-#pragma unroll
-    for (int w = 0; w < W; ++w) v[w] = sum[i][lane * W + w];
-    __nv_bfloat16* o = a.o.row(x.b, x.h, x.q) + c0 + lane * W;
+    float4 v = *reinterpret_cast<const float4*>(&sum[i][4 * c4]);
+    auto add = [&](const float4& y, float f) {
+      v.x += y.x * f;
+      v.y += y.y * f;
+      v.z += y.z * f;
+      v.w += y.w * f;
+    };
+    uint2* o = reinterpret_cast<uint2*>(a.o.row(x.b, x.h, x.q) + c0 + 4 * c4);
     if constexpr (kDecode) {
-      const float* src = a.own + ((long long)x.b * p.nh + x.h) * a.splits * (D + 2);
-      for (int s = 0; s < a.splits; ++s) {
-        const float y = src[s * (D + 2) + D];
-        if (y == -INFINITY) continue;
-        const float f = fast_exp2(y - mm);
-#pragma unroll
-        for (int w = 0; w < W; ++w) v[w] += src[s * (D + 2) + c0 + lane * W + w] * f;
+      const float* src = a.own + ((long long)x.b * p.nh + x.h) * a.parts * (D + 4);
+      const int own = own_parts(x.b);
+#pragma unroll 8
+      for (int s = 0; s < own; ++s) {
+        const float y = src[s * (D + 4) + D], f = y == -INFINITY ? 0.f : fast_exp2(y - mm);
+        add(*reinterpret_cast<const float4*>(src + s * (D + 4) + c0 + 4 * c4), f);
       }
     } else if (own_m[i] != -INFINITY) {
-      const float f = fast_exp2(own_m[i] - mm);
-#pragma unroll
-      for (int w = 0; w < W; ++w) v[w] += __bfloat162float(o[w]) * f;
+      const uint2 y = *o;
+      add(make_float4(__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u), __uint_as_float(y.y << 16),
+                      __uint_as_float(y.y & 0xffff0000u)),
+          fast_exp2(own_m[i] - mm));
     }
-    if constexpr (W == 1) {
-      *o = __float2bfloat16_rn(pad ? 0.f : v[0] * inv);
-    } else {
-      uint32_t y[W / 2 > 0 ? W / 2 : 1];
-#pragma unroll
-      for (int w = 0; w < W; w += 2) y[w / 2] = pad ? 0u : pack2(v[w] * inv, v[w + 1] * inv);
-      if constexpr (W == 2) *reinterpret_cast<uint32_t*>(o) = y[0];
-      else *reinterpret_cast<uint2*>(o) = make_uint2(y[0], y[W / 2 - 1]);
-    }
-    if (!kDecode && a.lse && lane == 0 && blockIdx.y == 0)
+    *o = pad ? make_uint2(0, 0) : make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
+    if (!kDecode && a.lse && c4 == 0 && blockIdx.y == 0)
       a.lse[((long long)x.b * p.nh + x.h) * p.nq + x.q] = pad ? -INFINITY : mm * kLn2 + logf(total[i]);
   }
 }
@@ -598,8 +601,10 @@ cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
     d.ws = own;
     d.scale = x.scale;
     e = launch_window_decode_parts(d, D, st);
+    const DecodeRuns r = decode_runs(w);
     j.own = own;
-    j.splits = decode_splits(w);
+    j.run = r.run;
+    j.parts = r.parts;
   } else {
     WindowArgs<__nv_bfloat16> f{};
     f.w = w;

@@ -51,7 +51,7 @@ namespace {
 
 constexpr int kWarps = 4;        // per CTA
 constexpr int kThreads = 32 * kWarps;
-constexpr int kWeightThreads = 256;
+constexpr int kWeightThreads = 256, kWeightKeys = 4;
 constexpr int kLongBlock = 32;   // most keys that a warp takes at a time
 constexpr float kLog2eD = 1.4426950408889634074f;
 
@@ -438,16 +438,20 @@ struct Cache<D, HT, true, kShort> {
   }
 };
 
-// kPart: a partial result is left even where a sequence has one part only.
-// kScores: so are the scores of the visible keys (log2 units), for window_weights_kernel: those of a
-// key's query heads side by side, keys in the order of the blocks.
-template <int D, int HT, bool kKv4, bool kShort, bool kPart, bool kScores>
+// kWhole: the attention itself.  The others leave partial results of fixed runs of blocks, for a
+// kernel of their own to join, and every warp has a run to itself: no barriers, and runs are
+// equally long whatever the sequences' lengths (64 sequences of up to 1024 keys 44 -> 31 us).
+// kScores leaves the scores of the visible keys too (log2 units), for window_weights_kernel:
+// those of a key's query heads side by side, keys in the order of the blocks.
+enum Mode { kWhole, kParts, kScores };
+template <int D, int HT, bool kKv4, bool kShort, Mode kMode>
 __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 : 4)
     window_decode_kernel(const DecodeArgs a) {
   using C = Cache<D, HT, kKv4, kShort>;
   constexpr int MT = D / 16, kHeads = 8 * HT, U = C::U, kBlock = 16 * U;
+  constexpr bool kPart = kMode != kWhole;
   __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
-  __shared__ float sm_o[kHeads][D + 4];
+  __shared__ __align__(16) float sm_o[kPart ? kWarps * kHeads : kHeads][D + 4];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3, r = lane >> 2;
@@ -455,11 +459,18 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 
   const int b = blockIdx.z, h = blockIdx.y / tiles, g0 = (blockIdx.y % tiles) * kHeads;
   const int heads = min(kHeads, group - g0), h0 = h * group + g0;
   const Blocks<kBlock> bl(a.w, b);
-  const int from = (int)((long long)bl.count * blockIdx.x / gridDim.x);
-  const int to = (int)((long long)bl.count * (blockIdx.x + 1) / gridDim.x);
+  int blk, to;  // this warp's blocks: blk, blk + step, ... below to
+  constexpr int step = kPart ? 1 : kWarps;
+  if constexpr (kPart) {
+    blk = (blockIdx.x * kWarps + warp) * a.run;
+    to = min(bl.count, blk + a.run);
+    if (blk >= to) return;
+  } else {
+    blk = (int)((long long)bl.count * blockIdx.x / gridDim.x) + warp;
+    to = (int)((long long)bl.count * (blockIdx.x + 1) / gridDim.x);
+  }
 
   C c(a, b, h, lane);
-  int blk = from + warp;
   // where a block's 16 rows are read from: the cache's last block reaches back into the one
   // before it (whose keys are hidden there)
   const int top = max(0, a.w.nk - kBlock);
@@ -474,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 
     C::load_q(8 * ht + r < heads ? a.q.row(b, h0 + 8 * ht + r, 0) : nullptr, t, q[ht]);
   __shared__ typename C::Shared sh;
   c.prepare(q, lane, sh);
-  __syncthreads();
+  if constexpr (!kPart) __syncthreads();
   const float sl2 = a.scale * kLog2eD;
   float o[HT][MT][4];
   float m[HT][2], l[HT][2];  // heads 8 ht + 2 t, + 1; maxima in log2 units
@@ -485,11 +496,11 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[ht][i][0] = o[ht][i][1] = o[ht][i][2] = o[ht][i][3] = 0.f;
   }
-  for (; blk < to; blk += kWarps) {
+  for (; blk < to; blk += step) {
     const int first = bl.block(blk) * kBlock, j0 = min(first, top);
     float s[U][HT][4];
     c.scores(s);
-    const int next = blk + kWarps < to ? start(blk + kWarps) : -1;
+    const int next = blk + step < to ? start(blk + step) : -1;
     if (next >= 0) c.load_k(next, lane);
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -514,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 
         c.drop_scales(u, mine);
       }
     }
-    if constexpr (kScores) {
+    if constexpr (kMode == kScores) {
       // (-infinity is a hidden key: the value is not read again)
       float* dst = a.scores + (((long long)b * a.w.nkv + h) * a.slots + (long long)blk * kBlock + j0 - first) * group + g0;
 #pragma unroll
@@ -585,6 +596,25 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 
         sm_l[warp][8 * ht + 2 * t + e] = l[ht][e];
       }
     }
+  if constexpr (kPart) {
+    // each row of D outputs relative to the maximum, the maximum and the sum (16-byte aligned)
+    float(*mine)[D + 4] = sm_o + warp * kHeads;
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mine[8 * ht + 2 * t + (e & 1)][C::channel(i, r, e >> 1)] = o[ht][i][e];
+    __syncwarp();
+    const int part = blockIdx.x * kWarps + warp;
+    for (int x = lane; x < heads * (D / 4 + 1); x += 32) {
+      const int row = x / (D / 4 + 1), c4 = x % (D / 4 + 1);
+      float* dst = a.ws + (((long long)b * a.w.nh + h0 + row) * a.parts + part) * (D + 4) + 4 * c4;
+      *reinterpret_cast<float4*>(dst) = c4 < D / 4 ? *reinterpret_cast<const float4*>(&mine[row][4 * c4])
+                                                   : make_float4(sm_m[warp][row], sm_l[warp][row], 0.f, 0.f);
+    }
+    return;
+  }
   __syncthreads();
   float f[HT][2];
 #pragma unroll
@@ -620,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
       sum += sm_l[w][row] * (sm_m[w][row] == -INFINITY ? 0.f : fast_exp2(sm_m[w][row] - n));
-    if (!kPart && gridDim.x == 1) {
+    if (gridDim.x == 1) {
       a.o.row(b, h0 + row, 0)[ch] = __float2bfloat16_rn(sum != 0.f ? sm_o[row][ch] / sum : 0.f);
     } else {
       // partial result: D outputs relative to the maximum n, then n and the sum
@@ -653,112 +683,154 @@ __global__ void __launch_bounds__(D) window_join_kernel(const DecodeArgs a, int 
   a.o.row(b, h, 0)[threadIdx.x] = __float2bfloat16_rn(l != 0.f ? o / l : 0.f);
 }
 
-// Joins the partial results of a key/value head's query heads (blockIdx.x 0), and adds what its
-// keys got from them to their weights: p = 2^(s - m) / l, summed over the heads in order.
+// Joins the partial results of a key/value head's query heads (the first `joins` CTAs of a row of
+// the grid), and adds what its keys got from them to their weights: p = 2^(s - m) / l, summed over
+// the heads in order.
 template <int D>
-__global__ void __launch_bounds__(kWeightThreads) window_weights_kernel(const DecodeArgs a, int splits) {
+__global__ void __launch_bounds__(kWeightThreads, 4) window_weights_kernel(const DecodeArgs a, int joins) {
   extern __shared__ float2 stats[];  // maximum and 1 / sum of each head of the group
   pdl_launch_dependents();
   pdl_wait();
   const int h = blockIdx.y, b = blockIdx.z, group = a.w.nh / a.w.nkv, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float* src = a.ws + ((long long)b * a.w.nh + (long long)h * group) * splits * (D + 2);
-  for (int g = warp; g < group; g += kWeightThreads / 32) {
-    const float* part = src + (long long)g * splits * (D + 2) + D;
-    float n = -INFINITY, l = 0.f;
-    for (int s = lane; s < splits; s += 32) n = fmaxf(n, part[s * (D + 2)]);
+  const bool join = (int)blockIdx.x < joins;
+  const Blocks<16> bl(a.w, b);
+  const int parts = (bl.count + a.run - 1) / a.run, slots = bl.count * 16;
+  const float* src = a.ws + ((long long)b * a.w.nh + (long long)h * group) * a.parts * (D + 4);
+  const long long list = (long long)b * a.w.nkv + h;
+  // this thread's first keys: their scores and weights are on their way before the statistics are known
+  const int chunk = kWeightKeys * kWeightThreads;
+  int i = ((int)blockIdx.x - joins) * chunk + threadIdx.x;
+  if (!join && i - (int)threadIdx.x >= slots) return;
+  const bool fours = group % 4 == 0;  // then a key's scores are 16-byte aligned
+  const float* scores = a.scores + list * a.slots * group;
+  float* out = a.weights + list * a.w.nk;
+  int j[kWeightKeys];  // -1: not visible
+  float4 first[kWeightKeys];
+  float old[kWeightKeys];
+  auto fetch = [&]() {
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, x));
-    for (int s = lane; s < splits; s += 32) {
-      const float m = part[s * (D + 2)];
-      l += part[s * (D + 2) + 1] * (m == -INFINITY ? 0.f : fast_exp2(m - n));
+    for (int x = 0; x < kWeightKeys; ++x) {
+      const int n = i + x * kWeightThreads;
+      j[x] = n < slots ? bl.block(n / 16) * 16 + n % 16 : -1;
+      if (j[x] >= bl.len || (j[x] < bl.lo && j[x] >= a.w.sinks)) j[x] = -1;
+      first[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      old[x] = 0.f;
+      if (j[x] < 0) continue;
+      if (fours) first[x] = *reinterpret_cast<const float4*>(scores + (long long)n * group);
+      old[x] = out[j[x]];
+    }
+  };
+  if (!join) fetch();
+  for (int g = warp; g < group; g += kWeightThreads / 32) {
+    const float* part = src + (long long)g * a.parts * (D + 4) + D;
+    float n = -INFINITY, l = 0.f;
+    for (int s = lane; s < parts; s += 32) {
+      const float2 x = *reinterpret_cast<const float2*>(part + (long long)s * (D + 4));
+      const float m = fmaxf(n, x.x);
+      l = l * (n == -INFINITY ? 0.f : fast_exp2(n - m)) + x.y * (x.x == -INFINITY ? 0.f : fast_exp2(x.x - m));
+      n = m;
     }
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    for (int d = 16; d > 0; d >>= 1) {
+      const float n2 = __shfl_xor_sync(0xffffffffu, n, d), l2 = __shfl_xor_sync(0xffffffffu, l, d), m = fmaxf(n, n2);
+      l = l * (n == -INFINITY ? 0.f : fast_exp2(n - m)) + l2 * (n2 == -INFINITY ? 0.f : fast_exp2(n2 - m));
+      n = m;
+    }
     if (lane == 0) stats[g] = make_float2(n, l != 0.f ? 1.f / l : 0.f);
   }
   __syncthreads();
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < group * D; i += kWeightThreads) {
-      const int g = i / D, ch = i % D;
-      const float* part = src + (long long)g * splits * (D + 2);
+  if (join) {
+    for (int x = blockIdx.x * kWeightThreads + threadIdx.x; x < group * D; x += joins * kWeightThreads) {
+      const int g = x / D, ch = x % D;
+      const float* part = src + (long long)g * a.parts * (D + 4);
       const float n = stats[g].x;
       float o = 0.f;
-      for (int s = 0; s < splits; ++s) {
-        const float m = part[s * (D + 2) + D];
-        o += part[s * (D + 2) + ch] * (m == -INFINITY ? 0.f : fast_exp2(m - n));
+#pragma unroll 8
+      for (int s = 0; s < parts; ++s) {
+        const float m = part[s * (D + 4) + D];
+        o += part[s * (D + 4) + ch] * (m == -INFINITY ? 0.f : fast_exp2(m - n));
       }
       a.o.row(b, h * group + g, 0)[ch] = __float2bfloat16_rn(o * stats[g].y);
     }
     return;
   }
-  const Blocks<16> bl(a.w, b);
-  const long long list = (long long)b * a.w.nkv + h;
-  float* out = a.weights + list * a.w.nk;
-  const int slots = bl.count * 16;
-  for (int i = (blockIdx.x - 1) * kWeightThreads + threadIdx.x; i < slots; i += (gridDim.x - 1) * kWeightThreads) {
-    const int j = bl.block(i / 16) * 16 + i % 16;
-    if (j >= bl.len || (j < bl.lo && j >= a.w.sinks)) continue;
-    const float* s = a.scores + (list * a.slots + i) * group;
-    float sum = 0.f;
-    auto add = [&](float x, int g) { sum += fast_exp2(x - stats[g].x) * stats[g].y; };
-    if (group % 4 == 0) {  // then a key's scores are 16-byte aligned
-      for (int g = 0; g < group; g += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(s + g);
-        add(x.x, g);
-        add(x.y, g + 1);
-        add(x.z, g + 2);
-        add(x.w, g + 3);
+  for (; i - (int)threadIdx.x < slots; i += (gridDim.x - joins) * chunk) {
+    if (i >= chunk * (int)(gridDim.x - joins)) fetch();
+#pragma unroll
+    for (int x = 0; x < kWeightKeys; ++x) {
+      if (j[x] < 0) continue;
+      const float* s = scores + (long long)(i + x * kWeightThreads) * group;
+      float sum = 0.f;
+      auto add = [&](float y, int g) { sum += fast_exp2(y - stats[g].x) * stats[g].y; };
+      if (fours) {
+        for (int g = 0; g < group; g += 4) {
+          const float4 y = g == 0 ? first[x] : *reinterpret_cast<const float4*>(s + g);
+          add(y.x, g);
+          add(y.y, g + 1);
+          add(y.z, g + 2);
+          add(y.w, g + 3);
+        }
+      } else {
+        for (int g = 0; g < group; ++g) add(s[g], g);
       }
-    } else {
-      for (int g = 0; g < group; ++g) add(s[g], g);
+      out[j[x]] = old[x] + sum;
     }
-    out[j] += sum;
   }
 }
 
 // Query heads of a tile: eight where a group has no more (half the registers), else sixteen.
 int head_tile(const Window& w) { return w.nh / w.nkv <= 8 ? 8 : 16; }
 
-template <int D, bool kKv4, bool kPart, bool kScores>
-cudaError_t parts(const DecodeArgs& a, int splits, cudaStream_t st) {
+template <int D, bool kKv4, Mode kMode>
+cudaError_t attend(const DecodeArgs& a, int gx, cudaStream_t st) {
   const int group = a.w.nh / a.w.nkv, tile = head_tile(a.w), tiles = (group + tile - 1) / tile;
-  auto kern = a.w.nk < kLongBlock ? (tile == 8 ? window_decode_kernel<D, 1, kKv4, true, kPart, kScores>
-                                               : window_decode_kernel<D, 2, kKv4, true, kPart, kScores>)
-                                  : (tile == 8 ? window_decode_kernel<D, 1, kKv4, false, kPart, kScores>
-                                               : window_decode_kernel<D, 2, kKv4, false, kPart, kScores>);
-  return launch_pdl(kern, dim3(splits, a.w.nkv * tiles, a.w.B), dim3(kThreads), 0, st, a);
+  auto kern = a.w.nk < kLongBlock ? (tile == 8 ? window_decode_kernel<D, 1, kKv4, true, kMode>
+                                               : window_decode_kernel<D, 2, kKv4, true, kMode>)
+                                  : (tile == 8 ? window_decode_kernel<D, 1, kKv4, false, kMode>
+                                               : window_decode_kernel<D, 2, kKv4, false, kMode>);
+  return launch_pdl(kern, dim3(gx, a.w.nkv * tiles, a.w.B), dim3(kThreads), 0, st, a);
 }
 
 template <int D, bool kKv4>
 cudaError_t decode(const DecodeArgs& a, cudaStream_t st) {
   const int splits = decode_splits(a.w);
-  const cudaError_t e = parts<D, kKv4, false, false>(a, splits, st);
+  const cudaError_t e = attend<D, kKv4, kWhole>(a, splits, st);
   if (e != cudaSuccess || splits == 1) return e;
   return launch_pdl(window_join_kernel<D>, dim3(a.w.nh, a.w.B), dim3(D), 0, st, a, splits);
 }
 
-// Rows of scores that a sequence's visible blocks of 16 keys take up at most.
-long long score_slots(const Window& w) {
+// Blocks of 16 keys that a sequence sees at most.
+long long most_blocks(const Window& w) {
   const long long rows = std::min<long long>(w.nk, (long long)w.left + 1 + w.sinks);
-  return std::min<long long>((w.nk + 15) / 16, (rows + 15) / 16 + 2) * 16;
+  return std::min<long long>((w.nk + 15) / 16, (rows + 15) / 16 + 2);
+}
+
+template <int D, Mode kMode>
+cudaError_t attend_parts(DecodeArgs& a, cudaStream_t st) {
+  const DecodeRuns r = decode_runs(a.w);
+  a.run = r.run;
+  a.parts = r.parts;
+  return attend<D, false, kMode>(a, (r.parts + kWarps - 1) / kWarps, st);
 }
 
 size_t partial_bytes(const Window& w, int d) {
-  return ((size_t)w.B * w.nh * decode_splits(w) * (d + 2) * 4 + 255) / 256 * 256;
+  return ((size_t)w.B * w.nh * decode_runs(w).parts * (d + 4) * 4 + 255) / 256 * 256;
 }
 
 template <int D>
 cudaError_t decode_weights(DecodeArgs a, cudaStream_t st) {
-  const int splits = decode_splits(a.w), group = a.w.nh / a.w.nkv;
-  a.slots = score_slots(a.w);
+  const int group = a.w.nh / a.w.nkv;
+  a.slots = most_blocks(a.w) * 16;
   a.scores = a.ws + partial_bytes(a.w, D) / 4;
-  const cudaError_t e = parts<D, false, true, true>(a, splits, st);
+  const cudaError_t e = attend_parts<D, kScores>(a, st);
   if (e != cudaSuccess) return e;
-  // two keys per thread, as long as that is more than a few CTAs per SM
-  const long long lists = (long long)a.w.B * a.w.nkv, chunks = (a.slots + 2 * kWeightThreads - 1) / (2 * kWeightThreads);
-  const int gx = (int)std::min<long long>(chunks, std::max<long long>(1, 16LL * 152 / lists));
-  return launch_pdl(window_weights_kernel<D>, dim3(1 + gx, a.w.nkv, a.w.B), dim3(kWeightThreads), group * sizeof(float2),
-                    st, a, splits);
+  // a thread goes through its keys once, as long as that is not more than a few CTAs per SM
+  const long long lists = (long long)a.w.B * a.w.nkv;
+  const long long chunks = (a.slots + kWeightKeys * kWeightThreads - 1) / (kWeightKeys * kWeightThreads);
+  const int gx = (int)std::min<long long>(chunks, std::max<long long>(1, 24LL * 152 / lists));
+  const int joins = std::min(16, (group * D + kWeightThreads - 1) / kWeightThreads);
+  return launch_pdl(window_weights_kernel<D>, dim3(joins + gx, a.w.nkv, a.w.B), dim3(kWeightThreads),
+                    group * sizeof(float2), st, a, joins);
 }
 
 }  // namespace
@@ -779,15 +851,26 @@ size_t decode_ws_bytes(const Window& w, int d) {
   return s == 1 ? 256 : ((size_t)w.B * w.nh * s * (d + 2) * 4 + 255) / 256 * 256;
 }
 
+// Runs of 8 to 32 blocks of 16 keys: about two for each warp that the device holds (12 per SM), as
+// shorter ones make more partial results to join than they even out (128 runs of 4 blocks instead
+// of 32 of 16 for 8192 keys: 80 us instead of 70).
+DecodeRuns decode_runs(const Window& w) {
+  const int group = w.nh / w.nkv, tiles = (group + head_tile(w) - 1) / head_tile(w);
+  const long long blocks = most_blocks(w), all = blocks * w.B * w.nkv * tiles;
+  DecodeRuns r;
+  r.run = (int)std::max<long long>({8, std::min<long long>(32, all / (2 * 152 * 12)), (blocks + 255) / 256});
+  r.parts = (int)((blocks + r.run - 1) / r.run);
+  return r;
+}
+
 size_t decode_parts_ws_bytes(const Window& w, int d) { return partial_bytes(w, d); }
 
-cudaError_t launch_window_decode_parts(const DecodeArgs& a, int d, cudaStream_t st) {
-  const int splits = decode_splits(a.w);
-  return d == 64 ? parts<64, false, true, false>(a, splits, st) : parts<128, false, true, false>(a, splits, st);
+cudaError_t launch_window_decode_parts(DecodeArgs a, int d, cudaStream_t st) {
+  return d == 64 ? attend_parts<64, kParts>(a, st) : attend_parts<128, kParts>(a, st);
 }
 
 size_t decode_weights_ws_bytes(const Window& w, int d) {
-  return partial_bytes(w, d) + ((size_t)w.B * w.nh * score_slots(w) * 4 + 255) / 256 * 256;
+  return partial_bytes(w, d) + ((size_t)w.B * w.nh * most_blocks(w) * 64 + 255) / 256 * 256;
 }
 
 cudaError_t launch_window_decode_weights(const DecodeArgs& a, int d, cudaStream_t st) {

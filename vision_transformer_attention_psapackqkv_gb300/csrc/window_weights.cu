@@ -102,6 +102,19 @@ struct Run {
   }
 };
 
+// A place in a ring of N, and how often it has been there (its parity).
+template <int N>
+struct Place {
+  int at = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 // A step of a unit: a tile of heads, a tile of queries.
 struct Step {
   int qt, ht;
@@ -299,28 +312,29 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint64_t dQ0 = desc_rows_by_channels(sbase), dK0 = desc_rows_by_channels(sbase + C::OFF_K);
     const uint32_t id = idesc_bf16_f32(128, (a.tq * a.tg + 15) / 16 * 16, false, false);
     bool ok = true;
-    int kn[kTiles] = {}, sn[kTiles] = {}, qn = 0;
+    uint32_t k_parity[kTiles] = {}, s_parity[kTiles] = {};
+    Place<C::QST> q;
     while (ok && run.next(a)) {
       const Unit u(a, run.unit);
       const KeyTile tile[kTiles] = {KeyTile(a, u, 0), KeyTile(a, u, 1), KeyTile(a, u, 2), KeyTile(a, u, 3)};
       Step t(u, run.s);
-      for (int i = 0; ok && i < run.n; ++i, ++qn, t.next(u)) {
-        const int qs = qn % C::QST;
-        if (!mbar_wait(&bar.q_full[qs], (qn / C::QST) & 1, abort)) {
+      for (int i = 0; ok && i < run.n; ++i, t.next(u)) {
+        if (!mbar_wait(&bar.q_full[q.at], q.parity, abort)) {
           ok = false;
           break;
         }
-        const uint64_t dQ = dQ0 + (uint64_t)(qs * C::TILE >> 4);
+        const uint64_t dQ = dQ0 + (uint64_t)(q.at * C::TILE >> 4);
 #pragma unroll
         for (int w = 0; w < kTiles; ++w) {
           if (!ok || !tile[w].any()) continue;
           // (every key tile that was loaded is waited for, whether this piece's steps need it or not)
-          if (i == 0 && !mbar_wait(&bar.k_full[w], kn[w] & 1, abort)) {
+          if (i == 0 && !mbar_wait(&bar.k_full[w], k_parity[w], abort)) {
             ok = false;
             continue;
           }
           if (!tile[w].takes(t.qt)) continue;
-          if (sn[w] > 0 && !mbar_wait(&bar.s_empty[w], (sn[w] - 1) & 1, abort)) {
+          // (the first use waits for nothing: its barrier's phase before the first is over)
+          if (!mbar_wait(&bar.s_empty[w], s_parity[w] ^ 1, abort)) {
             ok = false;
             continue;
           }
@@ -330,15 +344,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           for (int kk = 0; kk < D / 16; ++kk)
             mma_bf16_warp(tmem + 128 * w, dK + kstep_channels(kk), dQ + kstep_channels(kk), id, kk > 0 ? 1u : 0u);
           mma_commit_warp(&bar.s_full[w]);
-          ++sn[w];
+          s_parity[w] ^= 1;
         }
-        if (ok) mma_commit_warp(&bar.q_empty[qs]);
+        if (ok) mma_commit_warp(&bar.q_empty[q.at]);
+        q.next();
       }
 #pragma unroll
       for (int w = 0; w < kTiles; ++w)
         if (ok && tile[w].any()) {
           mma_commit_warp(&bar.k_empty[w]);
-          ++kn[w];
+          k_parity[w] ^= 1;
         }
     }
     mma_commit_warp(&bar.done);
@@ -356,9 +371,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     for (int x = 0; x < 4; ++x) {
       my_g[x] = (lane + 32 * x) / a.tq;
       my_i[x] = lane + 32 * x - my_g[x] * a.tq;
+      if (lane + 32 * x >= rows) my_g[x] = 1 << 20;  // none
     }
     const float2 sl = make_float2(a.sl2, a.sl2);
-    int used = 0;
+    uint32_t parity = 0, flip = 0;
     bool ok = true;
     while (ok && run.next(a)) {
       const Unit u(a, run.unit);
@@ -367,15 +383,22 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       // queries that see this thread's key
       const int lo = max(max(j - w.right, 0) - off, 0);
       const int hi = min((j < w.sinks ? u.len - 1 : min(u.len - 1, j + w.left)) - off, w.nq - 1);
+      // query tiles that every key of the tile sees whole: first_whole .. last_whole
+      int first_whole = 1, last_whole = 0;
+      if (rows == kTile) {
+        const int from = max(max(0, k1 - w.right) - off, 0);
+        const int to = min(min(k1 < w.sinks ? u.len - 1 : k0 + w.left, u.len - 1) - off, w.nq - 1);
+        first_whole = a.tq < kTile ? from > 0 : (from + kTile - 1) / kTile;
+        last_whole = a.tq < kTile ? (to >= w.nq - 1 ? 0 : -1) : ((to + 1) >> 7) - 1;
+      }
       // the lane's columns of a step: lse, or (the product below is then -infinity) infinity
       float lse[4] = {0.f, 0.f, 0.f, 0.f};
+      const float* list_lse = a.lse + ((long long)u.b * w.nh + u.hk * group) * w.nq;
       auto fetch = [&](const Step& t) {
-        const float* at = a.lse + ((long long)u.b * w.nh + u.hk * group) * w.nq;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int q = t.qt * a.tq + my_i[x], g = t.ht * a.tg + my_g[x];
-          const bool there = lane + 32 * x < rows && g < group && q < w.nq;
-          lse[x] = there ? __ldg(at + (long long)g * w.nq + q) : INFINITY;
+          lse[x] = g < group && q < w.nq ? __ldg(list_lse + (long long)g * w.nq + q) : INFINITY;
         }
       };
       float sum = 0.f;
@@ -391,22 +414,22 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       seek();
       if (i < run.n) fetch(t);
       while (i < run.n) {
-        const uint32_t l = stats + (used & 1) * kTile * 4;
+        const uint32_t l = stats + flip;
+        flip ^= kTile * 4;
 #pragma unroll
         for (int x = 0; x < 4; ++x) st_shared_f32(l + 4 * (lane + 32 * x), -kLog2 * lse[x]);
         __syncwarp();
-        const int q0 = t.qt * a.tq, heads = min(a.tg, group - t.ht * a.tg), p0 = q0 + off, p1 = p0 + a.tq - 1;
-        const bool whole = rows == kTile && heads == a.tg && q0 + a.tq <= w.nq && p0 >= 0 && p1 < u.len &&
-                           p0 >= k1 - w.right && (p1 <= k0 + w.left || k1 < w.sinks);
+        const Step now = t;
+        const bool whole = t.qt >= first_whole && t.qt <= last_whole && (t.ht + 1) * a.tg <= group;
         ++i;
         t.next(u);
         seek();
         if (i < run.n) fetch(t);  // on its way during this step
-        if (!mbar_wait(&bar.s_full[wg], used & 1, abort)) {
+        if (!mbar_wait(&bar.s_full[wg], parity, abort)) {
           ok = false;
           break;
         }
-        ++used;
+        parity ^= 1;
         tc_fence_after();
         float2 s01 = make_float2(0.f, 0.f), s23 = s01;
         if (whole) {
@@ -428,6 +451,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             add16(x + 16, l0, sl, s01, s23);
           }
         } else {
+          const int q0 = now.qt * a.tq, heads = min(a.tg, group - now.ht * a.tg);
           const int from = max(0, lo - q0), to = min(a.tq - 1, hi - q0);
 #pragma unroll 1
           for (int c = 0; c < rows; c += 32) {

@@ -25,7 +25,7 @@ constexpr int kBits = 13, kBins = 1 << kBits;  // of a key's first digit: 4 bits
 constexpr int kKeysInShared = 40 * 1024;       // longer lists are read again in every pass
 constexpr int kGathered = 1024;                // more that share their first digit are counted where they are
 constexpr int kFewMoves = 32;
-constexpr int kMoveThreads = 256, kMoveUnroll = 8;
+constexpr int kMoveThreads = 256, kMoveUnroll = 4;
 constexpr uint32_t kSafe = 0xffffffffu;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -274,37 +274,47 @@ __global__ void __launch_bounds__(1024)
   for (int r = count + tid; r < len; r += threads) w_out[r] = 0.f;
 }
 
-// 16 bytes per thread: K's row, then V's, of each move of a list.
+// 16 bytes per thread: K's row, then V's, of a list's moves, kMoveUnroll at a time; the next ones'
+// places are fetched while these rows are on their way.
 template <int ROW16>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, const int cap) {
   pdl_launch_dependents();
   pdl_wait();
+  constexpr int PER = kMoveThreads / (2 * ROW16);  // moves of a CTA's threads
   const int list = blockIdx.y, b = list / a.nkv, h = list % a.nkv;
-  const int n = a.counts[list], first = blockIdx.x * kMoveThreads * kMoveUnroll + threadIdx.x;
+  const int n = a.counts[list], c = threadIdx.x % (2 * ROW16), stride = gridDim.x * PER * kMoveUnroll;
   const int* src = a.moves + (long long)list * 2 * cap;
   const int* dst = src + cap;
-  // (a stride of kMoveThreads is a whole number of rows: a thread's column stays)
-  const int c = first % (2 * ROW16);
   uint4* base = c < ROW16 ? a.k.row(b, h, 0) + c : a.v.row(b, h, 0) + c - ROW16;
   const long long step = c < ROW16 ? a.k.sn : a.v.sn;
-  const int m0 = first / (2 * ROW16);
-  uint4 x[kMoveUnroll];
-  int s[kMoveUnroll], d[kMoveUnroll];
+  int from[kMoveUnroll], to[kMoveUnroll];
+  auto fetch = [&](int m) {
 #pragma unroll
-  for (int i = 0; i < kMoveUnroll; ++i) {
-    const int m = m0 + i * (kMoveThreads / (2 * ROW16));
-    d[i] = -1;
-    if (m < n) {
-      s[i] = src[m];
-      d[i] = dst[m];
+    for (int i = 0; i < kMoveUnroll; ++i) {
+      to[i] = -1;
+      if (m + i * PER < n) {
+        from[i] = src[m + i * PER];
+        to[i] = dst[m + i * PER];
+      }
     }
+  };
+  int m = blockIdx.x * PER * kMoveUnroll + threadIdx.x / (2 * ROW16);
+  fetch(m);
+  for (; m < n; m += stride) {
+    uint4 x[kMoveUnroll];
+    uint4* at[kMoveUnroll];
+#pragma unroll
+    for (int i = 0; i < kMoveUnroll; ++i) {
+      at[i] = nullptr;
+      if (to[i] < 0) continue;
+      x[i] = base[from[i] * step];
+      at[i] = base + to[i] * step;
+    }
+    fetch(m + stride);
+#pragma unroll
+    for (int i = 0; i < kMoveUnroll; ++i)
+      if (at[i]) *at[i] = x[i];
   }
-#pragma unroll
-  for (int i = 0; i < kMoveUnroll; ++i)
-    if (d[i] >= 0) x[i] = base[s[i] * step];
-#pragma unroll
-  for (int i = 0; i < kMoveUnroll; ++i)
-    if (d[i] >= 0) base[d[i] * step] = x[i];
 }
 
 // Keys, and two bits, of a list.
@@ -335,8 +345,9 @@ cudaError_t launch_kv_evict(EvictArgs a, int row16, void* ws, cudaStream_t st) {
   }
   const cudaError_t s = launch_pdl(select, dim3(lists), dim3(threads), smem, st, a, cap, row16, fused);
   if (s != cudaSuccess || fused) return s;
-  const long long units = (long long)cap * 2 * row16, per = kMoveThreads * kMoveUnroll;
-  const dim3 grid((unsigned)((units + per - 1) / per), lists);
+  // eight CTAs per SM between the lists, if they have that many moves
+  const int per = kMoveThreads / (2 * row16) * kMoveUnroll;
+  const dim3 grid(std::min((cap + per - 1) / per, std::max(1, 8 * 152 / lists)), lists);
   auto kern = row16 == 8 ? evict_move_kernel<8> : row16 == 16 ? evict_move_kernel<16> : evict_move_kernel<32>;
   return launch_pdl(kern, grid, dim3(kMoveThreads), 0, st, a, cap);
 }

@@ -396,8 +396,7 @@ typedef struct {
  * tokens, and query row i also sees the own keys j <= i + n_k - n_q.  lens, int32 [B] on the
  * device (NULL: n_k): own tokens from lens[b] on are padding, whose queries get output 0 and
  * log-sum-exp -infinity, and which are seen by none, whatever they hold.  Every row of o is
- * written, and lse, fp32 [B, num_heads, n_q] (NULL: not wanted).  The attention over a sequence's own
- * keys is rounded to bf16 before it is joined with the prefix'.  workspace: 16-byte aligned, at least
+ * written, and lse, fp32 [B, num_heads, n_q] (NULL: not wanted).  workspace: 16-byte aligned, at least
  * psa_prefix_attn_workspace_size(p) bytes. */
 psa_status_t psa_prefix_attn_fwd(psa_rows_t q, psa_rows_t k_prefix, psa_rows_t v_prefix,
                                  psa_rows_t k, psa_rows_t v, const int *lens, psa_rows_t o,

@@ -150,6 +150,8 @@ struct WindowArgs {
 };
 // Tensor cores (window_fwd.cu, window_bwd.cu); delta points at the backward's workspace.
 cudaError_t launch_window_fwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cudaStream_t st);
+// The rows that see something in fp32, [B, nh, n_q, d], and lse alone.
+cudaError_t launch_window_fwd_raw(const WindowArgs<__nv_bfloat16>& a, float* raw, int d, cudaStream_t st);
 cudaError_t launch_window_bwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cudaStream_t st);
 size_t window_bwd_tc_ws_bytes(const Window& w, int d);
 // CUDA cores (window_simt.cu).

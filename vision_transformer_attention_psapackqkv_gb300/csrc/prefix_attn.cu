@@ -17,9 +17,8 @@
 // row's sums come in pieces (fp32, relative to the piece's maximum).  They lie in the workspace with a row's
 // neighbours in the tile side by side, four channels each: what 32 lanes write, and read again, is
 // contiguous.
-// Own keys: the single-token kernel's partial sums (decoding), or the window kernel's output and
-// log-sum-exp (prompts; that output is rounded to bf16 once more than the result has to be, 2^-9 of
-// its own share).  A last kernel joins all of a row's sums.
+// Own keys: the single-token kernel's partial sums (decoding), or the window kernel's output in fp32
+// and log-sum-exp (prompts).  A last kernel joins all of a row's sums and rounds once.
 #include <algorithm>
 
 #include "softmax_tc.cuh"
@@ -361,8 +360,8 @@ struct JoinArgs {
   View<__nv_bfloat16> o;
   const int* lens;
   int nk;
-  // own keys, decoding: partial sums [B, nh, parts][D + 4] of runs of blocks of 16 keys; prompts: log-sum-exp [B, nh, nq] (with
-  // the output in o), and where the whole rows' goes to
+  // own keys, decoding: partial sums [B, nh, parts][D + 4] of runs of blocks of 16 keys; prompts:
+  // outputs [B, nh, nq, D] and log-sum-exp [B, nh, nq], and where the whole rows' goes to
   const float* own;
   int run, parts;
   const float* own_lse;
@@ -509,10 +508,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const JoinArg
         add(*reinterpret_cast<const float4*>(src + s * (D + 4) + c0 + 4 * c4), f);
       }
     } else if (own_m[i] != -INFINITY) {
-      const uint2 y = *o;
-      add(make_float4(__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u), __uint_as_float(y.y << 16),
-                      __uint_as_float(y.y & 0xffff0000u)),
-          fast_exp2(own_m[i] - mm));
+      const long long row = ((long long)x.b * p.nh + x.h) * p.nq + x.q;
+      add(*reinterpret_cast<const float4*>(a.own + row * D + c0 + 4 * c4), fast_exp2(own_m[i] - mm));
     }
     *o = pad ? make_uint2(0, 0) : make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
     if (!kDecode && a.lse && c4 == 0 && blockIdx.y == 0)
@@ -611,11 +608,11 @@ cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
     f.q = x.q;
     f.k = x.k;
     f.v = x.v;
-    f.out = x.o;
-    f.lse = own;
+    f.lse = own + (size_t)p.B * p.nh * p.nq * D;
     f.scale = x.scale;
-    e = launch_window_fwd_tc(f, D, st);
-    j.own_lse = own;
+    e = launch_window_fwd_raw(f, own, D, st);
+    j.own = own;
+    j.own_lse = f.lse;
     j.lse = x.lse;
   }
   if (e != cudaSuccess) return e;
@@ -634,7 +631,7 @@ size_t prefix_ws_bytes(const PrefixShape& x, int d) {
   const Plan p = make_plan(x);
   const Window w{x.B, x.nh, x.nkv, x.nq, x.nk, x.nk, 0, 0, nullptr};
   const size_t own = x.nq == 1 ? decode_parts_ws_bytes(w, d) : 0;
-  return round256(sums_bytes(p, d) + stats_bytes(p) + std::max(own, (size_t)x.B * x.nh * x.nq * 4));
+  return round256(sums_bytes(p, d) + stats_bytes(p) + std::max(own, (size_t)x.B * x.nh * x.nq * (d + 1) * 4));
 }
 
 cudaError_t launch_prefix_attn(const PrefixArgs& a, int d, bool decode, cudaStream_t st) {

@@ -68,7 +68,7 @@ struct Bars {
 
 struct FwdParams {
   Window w;
-  float* lse;
+  float *lse, *raw;  // raw: [B, nh, n_q, D]
   float sl2;       // scale * log2(e)
   int units, row_tiles;
   bool head_pairs;  // the slots are two heads (else two row tiles of one head)
@@ -151,7 +151,8 @@ __device__ __forceinline__ int unit_of(int i) {
   return i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
-template <int D>
+// kRaw: the rows that see something go to a.raw in fp32, for a kernel that joins them with others.
+template <int D, bool kRaw>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     window_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       drain_wait(&bar.done, 0);
     } else if (warp == C::kStore) {
       // ------------------------------------------------------------ finished rows to memory
-      if (lane == 0) {
+      if (lane == 0 && !kRaw) {
         int n = 0;
         bool ok = true;
         for (int i = 0; ok && unit_of(i) < a.units; ++i) {
@@ -442,6 +443,25 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       if (q - r >= a.w.nq) continue;
       const bool sees = jhi >= 0;
       const float inv = 1.f / l;
+      if constexpr (kRaw) {
+        const long long row = ((long long)b * a.w.nh + h) * a.w.nq + q;
+        if (some) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_load32(tO + c, o);
+            if (sees) {
+              float4* to = reinterpret_cast<float4*>(a.raw + row * D + c);
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                to[k / 4] = make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
+            }
+          }
+          tc_fence_before();
+        }
+        if (q < a.w.nq) a.lse[row] = sees ? m * kLn2 + logf(l) : -INFINITY;
+        continue;
+      }
       // the staging tile is this slot's once the use before it has been read
       if (s || uses > 0) {
         if (!mbar_wait(&bar.stored[s], (s ? uses : uses - 1) & 1, abort)) break;
@@ -480,12 +500,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   }
 }
 
-template <int D>
-cudaError_t fwd(const WindowArgs<__nv_bfloat16>& x, cudaStream_t st) {
+template <int D, bool kRaw>
+cudaError_t fwd(const WindowArgs<__nv_bfloat16>& x, float* raw, cudaStream_t st) {
   using C = Cfg<D>;
   const Window& w = x.w;
-  CUtensorMap mq, mk, mv, mo;
-  if (!map_view(&mo, x.out.p, x.out.sb, x.out.sh, x.out.sn, w.B, w.nh, w.nq, D) ||
+  CUtensorMap mq, mk, mv, mo{};
+  if ((!kRaw && !map_view(&mo, x.out.p, x.out.sb, x.out.sh, x.out.sn, w.B, w.nh, w.nq, D)) ||
       !map_view(&mq, x.q.p, x.q.sb, x.q.sh, x.q.sn, w.B, w.nh, w.nq, D) ||
       !map_view(&mk, x.k.p, x.k.sb, x.k.sh, x.k.sn, w.B, w.nkv, w.nk, D) ||
       !map_view(&mv, x.v.p, x.v.sb, x.v.sh, x.v.sn, w.B, w.nkv, w.nk, D))
@@ -493,11 +513,12 @@ cudaError_t fwd(const WindowArgs<__nv_bfloat16>& x, cudaStream_t st) {
   FwdParams a{};
   a.w = w;
   a.lse = x.lse;
+  a.raw = raw;
   a.sl2 = x.scale * kLog2;
   a.row_tiles = (w.nq + kTile - 1) / kTile;
   a.head_pairs = (w.nh / w.nkv) % 2 == 0;
   a.units = a.head_pairs ? w.B * w.nh / 2 * a.row_tiles : w.B * w.nh * ((a.row_tiles + 1) / 2);
-  auto kern = window_fwd_tc_kernel<D>;
+  auto kern = window_fwd_tc_kernel<D, kRaw>;
   const cudaError_t e = set_max_dynamic_smem((const void*)kern, C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(std::min(a.units, device_sm_count())), dim3(C::kThreads), C::SMEM, st,
@@ -507,7 +528,10 @@ cudaError_t fwd(const WindowArgs<__nv_bfloat16>& x, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_window_fwd_tc(const WindowArgs<__nv_bfloat16>& a, int d, cudaStream_t st) {
-  return d == 64 ? fwd<64>(a, st) : fwd<128>(a, st);
+  return d == 64 ? fwd<64, false>(a, nullptr, st) : fwd<128, false>(a, nullptr, st);
+}
+cudaError_t launch_window_fwd_raw(const WindowArgs<__nv_bfloat16>& a, float* raw, int d, cudaStream_t st) {
+  return d == 64 ? fwd<64, true>(a, raw, st) : fwd<128, true>(a, raw, st);
 }
 
 }  // namespace psa

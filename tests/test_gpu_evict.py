@@ -200,6 +200,12 @@ def test_evict(lens, rows, keep, sinks, recent, d, dtype, kind):
         _check(c, keep, sinks, recent, _evict(c, keep, sinks, recent, in_place), in_place)
 
 
+@pytest.mark.parametrize("rows", [1024, 1025, 8192, 8193, 40960, 40961])
+def test_lists_at_the_lengths_where_threads_and_places_change(rows):
+    c = _case([rows, rows - 5], rows, 1, 64, BF16, 18, "ties" if rows % 2 else "spread")
+    _check(c, rows // 3, 2, rows // 9, _evict(c, rows // 3, 2, rows // 9, True), True)
+
+
 def test_lists_longer_than_shared_memory():
     c = _case([100001, 60000, 49153], 100001, 1, 64, BF16, 11)
     _check(c, 30000, 4, 1000, _evict(c, 30000, 4, 1000), False)

@@ -98,7 +98,7 @@ def test_a_prompt_in_chunks_adds_up_to_the_whole():
 
 def test_many_lists_and_long_parts():
     """More units than CTAs several times over, and key tiles whose queries are cut into parts."""
-    for Bn, nh, nkv, nq, nk, left, sinks in ((40, 4, 4, 200, 200, -1, 0), (1, 16, 1, 3100, 3100, 63, 16), (1, 2, 1, 6000, 6000, -1, 0)):
+    for Bn, nh, nkv, nq, nk, left, sinks in ((40, 4, 4, 200, 200, -1, 0), (64, 12, 12, 40, 200, -1, 0), (1, 16, 1, 3100, 3100, 63, 16), (1, 2, 1, 6000, 6000, -1, 0)):
         q, k = _randn(6, Bn, nh, nq, 64).to(BF16), _randn(7, Bn, nkv, nk, 64).to(BF16)
         win, lse = B.window_of(q, k, left, 0, sinks), torch.empty(Bn, nh, nq, device="cuda")
         B.psa_window_attn_fwd(q, k, k, None, torch.empty_like(q), lse, win, 0.2)

@@ -11,8 +11,12 @@
 // bits of the mantissa: fewer would meet in the same counters), gathers those that share the bits
 // of the keep-th largest, and compares these with one another.  What stays is then one bit per
 // row: ranks, gaps and the rows that fill them are sums over words of 32 rows.  Latencies and
-// instructions of the one CTA bound it.  The moves are a copy bound by memory: a second kernel over all lists, or, where a list
-// can have no more than kFewMoves, the same one.
+// instructions of the one CTA bound it (the counters' atomics are a third).  The moves are a copy
+// bound by memory: a second kernel over all lists, or, where a list can have no more than
+// kFewMoves, the same one.
+// Measured, 8 sequences of up to 16384 rows of 8 heads of 128 in bf16 cut to 8192: 50 us, of which
+// the selection takes 28 and the moves 21 (126 MB read and written at 5.9 TB/s, 0.87 of the copy
+// bandwidth); one row of 2049 out of 256 lists: 10 us.
 #include <algorithm>
 
 #include "lm.cuh"

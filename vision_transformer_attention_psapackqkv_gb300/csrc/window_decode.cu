@@ -36,7 +36,8 @@
 // rounded to bf16.
 //
 // Measured: bf16, 32 sequences of up to 8192 keys, 4096 visible, 32 heads of 128 on 8: 85 us (5.9
-// TB/s, 0.88 of the copy bandwidth); 4 bits, 16 sequences of up to 32768 keys: 113 us (3.4 TB/s,
+// TB/s, 0.88 of the copy bandwidth); with weights for each key, 16 sequences of up to 8192 keys: 69
+// us (343 MB; the scores and their second pass are 12 of them); 4 bits, 16 sequences of up to 32768 keys: 113 us (3.4 TB/s,
 // 0.51; the integer pipe is busy 62 % of the time, tensor instructions 18 %).  One sequence of
 // 1024 visible keys: 5.5 us with the join.
 #include <algorithm>
@@ -440,7 +441,7 @@ struct Cache<D, HT, true, kShort> {
 
 // kWhole: the attention itself.  The others leave partial results of fixed runs of blocks, for a
 // kernel of their own to join, and every warp has a run to itself: no barriers, and runs are
-// equally long whatever the sequences' lengths (64 sequences of up to 1024 keys 44 -> 31 us).
+// equally long whatever the sequences' lengths (64 sequences of up to 1024 keys 44 -> 34 us).
 // kScores leaves the scores of the visible keys too (log2 units), for window_weights_kernel:
 // those of a key's query heads side by side, keys in the order of the blocks.
 enum Mode { kWhole, kParts, kScores };
@@ -851,9 +852,10 @@ size_t decode_ws_bytes(const Window& w, int d) {
   return s == 1 ? 256 : ((size_t)w.B * w.nh * s * (d + 2) * 4 + 255) / 256 * 256;
 }
 
-// Runs of 8 to 32 blocks of 16 keys: about two for each warp that the device holds (12 per SM), as
-// shorter ones make more partial results to join than they even out (128 runs of 4 blocks instead
-// of 32 of 16 for 8192 keys: 80 us instead of 70).
+// Runs of 8 to 32 blocks of 16 keys: about two for each warp that the device holds (12 per SM).
+// Shorter ones make more partial results to join, longer ones leave warps idle (64 sequences of up to
+// 1024 keys behind a prefix, runs of 4, 8, 16, 32 blocks: 80, 79, 91, 98 us; 16 of up to 8192 with
+// weights: 71, 68, 68, 63).
 DecodeRuns decode_runs(const Window& w) {
   const int group = w.nh / w.nkv, tiles = (group + head_tile(w) - 1) / head_tile(w);
   const long long blocks = most_blocks(w), all = blocks * w.B * w.nkv * tiles;

@@ -13,10 +13,11 @@
 // units; a warp that goes through 128 scores spends most of its time on latencies.  So four key
 // tiles, each with four warps and a score tile, share the query tiles that stream by: four warps a
 // scheduler fill one another's gaps, and a query tile is read from the L2 once for four products.
-// Measured, 2 x 4096 causal, 16 heads of 128 on 4, on the device: MEASURED us.  Two key tiles with
-// their operand in tensor memory and a ring of score tiles 86 us (two warps a scheduler);
-// barriers that every thread arrives at, four times as many arrivals as work, 85 with four tiles
-// and 100 with two.
+// Measured, 2 x 4096 causal, 16 heads of 128 on 4, on the device: 75 us (0.92 PFLOP/s of visible
+// pairs, 0.48 of cuBLAS's bf16 rate; tensor pipe and multi-function units busy 46 % each, a step's
+// four products and the waits between them are what is left).  Two key tiles with their operand in
+// tensor memory and a ring of three score tiles: 86 us with four warps a tile, 79 with eight, and
+// more barriers; with barriers that every thread arrives at instead of one lane a warp 85 us.
 //   warps 0-15       sums, four warps for each key tile: one thread per key
 //   warp 16          TMA producer: key tiles, a ring of query tiles
 //   warp 17          issuer of the products (converged), tensor memory

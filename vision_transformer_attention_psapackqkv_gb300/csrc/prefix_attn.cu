@@ -150,8 +150,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
+  // The kernel before this one is the own keys', which shares nothing with it and lets it start only
+  // once all that came before has completed: this one runs beside its end, and waits for it before
+  // its own, so that the joining kernel finds both done.
   pdl_launch_dependents();
-  pdl_wait();
   const long long begin = p.from(blockIdx.x), end = p.from(blockIdx.x + 1);
 
   if (warp == C::kProducer) {
@@ -355,6 +357,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
+  pdl_wait();
 }
 
 // ---------------------------------------------------------------- a row's sums, joined
@@ -586,8 +589,7 @@ cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
   const Plan p = make_plan(x.s);
   char* ws = static_cast<char*>(x.ws);
   float* own = reinterpret_cast<float*>(ws + sums_bytes(p, D) + stats_bytes(p));
-  cudaError_t e = prefix_part<D>(x, p, st);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   JoinArgs j{};
   j.p = p;
   j.sums = reinterpret_cast<const float4*>(ws);
@@ -622,6 +624,8 @@ cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
     j.own_lse = f.lse;
     j.lse = x.lse;
   }
+  if (e != cudaSuccess) return e;
+  e = prefix_part<D>(x, p, st);
   if (e != cudaSuccess) return e;
   // Rows are few when decoding: their channels go to several CTAs then, each of which reads the
   // statistics.  Where rows fill the SMs that costs more than it gives (16 prompts of 77 tokens:

@@ -453,8 +453,10 @@ __global__ void __launch_bounds__(kThreads, HT == 2 ? 2 : D == 128 && !kKv4 ? 3 
   constexpr bool kPart = kMode != kWhole;
   __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
   __shared__ __align__(16) float sm_o[kPart ? kWarps * kHeads : kHeads][D + 4];
-  pdl_launch_dependents();
+  // (what follows partial results may start before they are there, but not before what this waits for)
+  if constexpr (!kPart) pdl_launch_dependents();
   pdl_wait();
+  if constexpr (kPart) pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3, r = lane >> 2;
   const int group = a.w.nh / a.w.nkv, tiles = (group + kHeads - 1) / kHeads;
   const int b = blockIdx.z, h = blockIdx.y / tiles, g0 = (blockIdx.y % tiles) * kHeads;

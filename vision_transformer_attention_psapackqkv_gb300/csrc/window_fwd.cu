@@ -198,8 +198,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
-  pdl_launch_dependents();
+  // (what follows raw rows may start before they are there, but not before what this waits for)
+  if constexpr (!kRaw) pdl_launch_dependents();
   pdl_wait();
+  if constexpr (kRaw) pdl_launch_dependents();
 
   if (warp >= 8) {
     if (warp == C::kProducer) {

@@ -13,6 +13,8 @@ import functools
 import math
 import os
 
+import torch
+
 from . import _build
 
 PSA_OK = 0
@@ -168,8 +170,6 @@ def _ptr(t):
 
 
 def _stream(stream):
-    import torch
-
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
@@ -180,14 +180,14 @@ def _check(fn: str, status: int):
         raise PsaError(fn, status, load().psa_status_string(status).decode())
 
 
-def dtype_code(t) -> int:
-    import torch
+_codes = {torch.bfloat16: PSA_DTYPE_BF16, torch.float32: PSA_DTYPE_F32}
 
-    if t.dtype == torch.bfloat16:
-        return PSA_DTYPE_BF16
-    if t.dtype == torch.float32:
-        return PSA_DTYPE_F32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+
+def dtype_code(t) -> int:
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def shape_of(qkv, num_heads: int, key_dim: int) -> PsaShape:
@@ -334,8 +334,6 @@ def _type_of(p, t):
 
 def _on_device(fn: str, tensors, stream, *args):
     """Calls entry point `fn` with its arguments on the tensors' one CUDA device."""
-    import torch
-
     index = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != index:
@@ -371,8 +369,6 @@ def norm_rope_of(q, k, cos, eps: float = 1e-6, interleaved: bool = False) -> Psa
 
 
 def _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p, axes=()):
-    import torch
-
     B, N, d, f32, t = p.B, p.N, p.head_dim, torch.float32, _type_of(p, q)
     table, by_q, by_k = (p.max_pos, p.rotary_dim // 2), (B, p.num_heads, N, d), (B, p.num_kv_heads, N, d)
     return by_q, by_k, (_rows(q, by_q, t, "q"), _rows(k, by_k, t, "k"), _dense(q_weight, (d,), f32, "q_weight"),
@@ -393,8 +389,6 @@ def psa_qk_norm_rope_bwd_workspace_size(p: PsaNormRope) -> int:
 
 def psa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk, dq_weight,
                          dk_weight, workspace, p: PsaNormRope, stream=None):
-    import torch
-
     by_q, by_k, args = _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p)
     t, d = q.dtype, (p.head_dim,)
     _on_device("psa_qk_norm_rope_bwd",
@@ -448,8 +442,6 @@ def psa_qk_norm_rope_axes_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_o
 def psa_qk_norm_rope_axes_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk, dq_weight,
                               dk_weight, workspace, p: PsaRopeAxes, stream=None):
     """workspace: psa_qk_norm_rope_bwd_workspace_size(p.rope) bytes."""
-    import torch
-
     by_q, by_k, args = _norm_rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, p.rope, (p.axes,))
     t, d = q.dtype, (p.rope.head_dim,)
     _on_device("psa_qk_norm_rope_axes_bwd",
@@ -466,7 +458,9 @@ def window_of(q, k, window_left: int = -1, window_right: int = 0, sinks: int = 0
     B, nh, n_q, d = q.shape
     n_k = k.shape[2]
     # nothing is past n_k, and all that is negative is alike; a C int would drop the upper bits
-    left, right, sinks = (max(-1, min(int(w), n_k)) for w in (window_left, window_right, sinks))
+    left = -1 if window_left < 0 else int(min(window_left, n_k))
+    right = -1 if window_right < 0 else int(min(window_right, n_k))
+    sinks = -1 if sinks < 0 else int(min(sinks, n_k))
     return PsaWindow(B, nh, k.shape[1], n_q, n_k, d, dtype_code(q), left, right, sinks)
 
 
@@ -477,14 +471,10 @@ def _window_shapes(win: PsaWindow):
 
 
 def _lens(lens, win: PsaWindow):
-    import torch
-
     return _dense(lens, (win.B,), torch.int32, "lens")
 
 
 def psa_window_attn_fwd(q, k, v, lens, o, lse, win: PsaWindow, scale: float, stream=None):
-    import torch
-
     by_q, by_k = _window_shapes(win)
     t = _type_of(win, q)
     _on_device("psa_window_attn_fwd", (q, k, v, lens, o, lse), stream, _rows(q, by_q, t, "q"), _rows(k, by_k, t, "k"),
@@ -498,8 +488,6 @@ def psa_window_attn_bwd_workspace_size(win: PsaWindow) -> int:
 
 def psa_window_attn_bwd(q, k, v, o, do, lse, lens, dq, dk, dv, workspace, win: PsaWindow, scale: float,
                         stream=None):
-    import torch
-
     by_q, by_k = _window_shapes(win)
     t = _type_of(win, q)
     _on_device("psa_window_attn_bwd", (q, k, v, o, do, lse, lens, dq, dk, dv, workspace), stream,
@@ -528,14 +516,10 @@ def cache_of(k, max_len: int) -> PsaCache:
 
 
 def _cache_rows(starts, counts, p: PsaCache):
-    import torch
-
     return (_dense(starts, (p.B,), torch.int32, "starts"), _dense(counts, (p.B,), torch.int32, "counts"))
 
 
 def _kv4(k_codes, k_scales, v_codes, v_scales, B, nkv, max_len, d):
-    import torch
-
     codes, scales = (B, nkv, max_len, d // 2), (B, nkv, max_len, d // 32)
     return (_dense(k_codes, codes, torch.uint8, "k_codes"), _dense(k_scales, scales, torch.bfloat16, "k_scales"),
             _dense(v_codes, codes, torch.uint8, "v_codes"), _dense(v_scales, scales, torch.bfloat16, "v_scales"))
@@ -587,8 +571,6 @@ def psa_prefix_attn_workspace_size(p: PsaPrefix) -> int:
 
 
 def _prefix_inputs(q, k_prefix, v_prefix, k, v, lens, o, p):
-    import torch
-
     t, nkv, d = _type_of(p, q), p.num_kv_heads, p.head_dim
     by_q, shared, by_k = (p.B, p.num_heads, p.n_q, d), (1, nkv, p.n_prefix, d), (p.B, nkv, p.n_k, d)
     return (_rows(q, by_q, t, "q"), _rows(k_prefix, shared, t, "k_prefix"), _rows(v_prefix, shared, t, "v_prefix"),
@@ -597,8 +579,6 @@ def _prefix_inputs(q, k_prefix, v_prefix, k, v, lens, o, p):
 
 def psa_prefix_attn_fwd(q, k_prefix, v_prefix, k, v, lens, o, lse, workspace, p: PsaPrefix, scale: float,
                         stream=None):
-    import torch
-
     _on_device("psa_prefix_attn_fwd", (q, k_prefix, v_prefix, k, v, lens, o, lse, workspace), stream,
                *_prefix_inputs(q, k_prefix, v_prefix, k, v, lens, o, p),
                _dense(lse, (p.B, p.num_heads, p.n_q), torch.float32, "lse"),
@@ -613,8 +593,6 @@ def psa_prefix_attn_decode(q, k_prefix, v_prefix, k_cache, v_cache, lens, o, wor
 
 
 def _weights(t, by_k, what: str = "weights"):
-    import torch
-
     if t is None:
         raise ValueError(f"{what} are required")
     return _dense(t, by_k[:3], torch.float32, what)
@@ -625,8 +603,6 @@ def psa_window_attn_weights_workspace_size(win: PsaWindow) -> int:
 
 
 def psa_window_attn_weights(q, k, lens, lse, weights, workspace, win: PsaWindow, scale: float, stream=None):
-    import torch
-
     by_q, by_k = _window_shapes(win)
     t = _type_of(win, q)
     _on_device("psa_window_attn_weights", (q, k, lens, lse, weights, workspace), stream, _rows(q, by_q, t, "q"),
@@ -662,8 +638,6 @@ def psa_kv_evict_workspace_size(p: PsaEvict) -> int:
 
 def psa_kv_evict(weights, positions, lens, k_cache, v_cache, weights_out, positions_out, lens_out, workspace,
                  p: PsaEvict, stream=None):
-    import torch
-
     cache, t, i32 = (p.B, p.num_kv_heads, p.max_len, p.head_dim), _type_of(p, k_cache), torch.int32
     _on_device("psa_kv_evict", (k_cache, v_cache, weights, positions, lens, weights_out, positions_out, lens_out,
                                 workspace), stream, _weights(weights, cache), _dense(positions, cache[:3], i32, "positions"),

@@ -554,9 +554,8 @@ Plan make_plan(const PrefixShape& x) {
   p.steps = (long long)p.nkv * pairs * p.key_tiles;
   // a CTA for each SM, but not for less than two key tiles
   p.ctas = (int)std::min<long long>(kPrefixCtas, (p.steps + 1) / 2);
-  int most = 1;  // pieces of a unit: all units are alike but for where they begin
-  for (int u = 0; u < std::min(p.nkv * pairs, 2 * kPrefixCtas); ++u) most = std::max(most, p.pieces(u));
-  if (p.nkv * pairs > 2 * kPrefixCtas) most = std::max(most, 2);
+  // pieces of a unit at most: the runs that its steps fill, and one that begins or ends in it
+  const int most = (int)std::min<long long>(p.ctas, (p.key_tiles * (long long)p.ctas + p.steps - 1) / p.steps + 1);
   p.slots = p.row_tiles % 2 ? 2 * most : most;
   return p;
 }

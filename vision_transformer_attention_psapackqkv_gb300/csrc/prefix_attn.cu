@@ -21,8 +21,8 @@
 // and log-sum-exp (prompts).  A last kernel joins all of a row's sums and rounds once.
 //
 // Measured, 32 heads of 128 on 8, on the device.  64 tokens behind 16384 shared and up to 1024 own
-// keys: 79 us (prefix 24, own keys 34: 5.1 TB/s, joining 14; 242 MB in all, 36 us at the copy
-// bandwidth).  16 prompts of up to 77 tokens behind 8192 keys: 162 us (prefix 123: 1.35 PFLOP/s of
+// keys: 77 us (prefix 24, own keys 34: 5.1 TB/s, joining 14; 242 MB in all, 36 us at the copy
+// bandwidth).  16 prompts of up to 77 tokens behind 8192 keys: 159 us (prefix 123: 1.35 PFLOP/s of
 // its rows, of which box edges and padding are a fifth; own keys 19, joining 24).  A step of two row
 // tiles takes 1.5 us where its products take 1.07: two warps a scheduler for the softmax, as in the
 // window attention.
@@ -628,7 +628,7 @@ cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // Rows are few when decoding: their channels go to several CTAs then, each of which reads the
   // statistics.  Where rows fill the SMs that costs more than it gives (16 prompts of 77 tokens:
-  // 196 us in all instead of 162).
+  // 196 us in all instead of 162, then).
   const int groups = p.nkv * p.row_tiles * (kTile / kJoinRows), smem = p.slots * kJoinRows * (int)sizeof(float2);
   auto kern = groups >= 304 ? (decode ? prefix_join_kernel<D, D, true> : prefix_join_kernel<D, D, false>)
                             : (decode ? prefix_join_kernel<D, 32, true> : prefix_join_kernel<D, 32, false>);

@@ -87,6 +87,23 @@ def test_prompts(Bn, nq, P, nk, lens, nh, nkv, d):
     assert none is None and torch.equal(o, again)
 
 
+@pytest.mark.parametrize("nh,nkv", [(4, 2), (1, 1), (6, 1), (32, 8)])
+@pytest.mark.parametrize("lens", [[300, 1, 0, 37, 300, 128, 129, 5, 0], [0] * 9, [-1] * 8 + [1], [0, 300] * 4 + [16], [1] * 9])
+def test_row_tiles_of_padding_are_left_out(lens, nh, nkv):
+    """Whatever the lengths leave of the row tiles: the same as without lengths, where there is something."""
+    c, scale = _case(9, nh, nkv, 300, 2300, 300, 64, 21), 0.125
+    whole, whole_lse = _prompts(c, None, scale)
+    _pad(c, lens, 0)
+    o, lse = _prompts(c, lens, scale)
+    assert torch.equal(o, _prompts(c, lens, scale)[0])
+    for b, n in enumerate(lens):
+        n = max(0, n)
+        assert (o[b, :, n:] == 0).all() and (lse[b, :, n:] == -math.inf).all()
+        # the prefix' pieces fall differently: sums in another order, P and the result rounded alike
+        assert ((o[b, :, :n].float() - whole[b, :, :n].float()).abs() <= 2.0 ** -7 * whole[b, :, :n].float().abs() + 2.0 ** -9).all()
+        assert ((lse[b, :, :n] - whole_lse[b, :, :n]).abs() <= 1e-5).all()
+
+
 # B, P, rows, lens
 STEPS = [(1, 1, 1, [1]), (2, 40, 9, [0, 9]), (4, 128, 30, [30, 1, 0, -1]), (7, 129, 200, [200, 0, 17, 16, -3, 15, 300]),
          (33, 1000, 50, [50, 49, 3] * 11), (3, 4500, 700, [700, 350, 1]), (130, 300, 20, [20, -1, 7, 0, 11] * 26), (1, 9000, 5, [5])]

@@ -13,7 +13,8 @@
 //   warps 0-3, 4-7   softmax of slot 0, 1: one thread per row
 //   warp 8           TMA producer: Q of both slots, a ring of K tiles and one of V tiles
 //   warp 9           issuer of the products, tensor memory
-// All SMs get an equal run of key tiles, whatever the rows; where a run ends inside the prefix a
+// Row tiles of padding alone are left out (counted on the device).  All SMs get an equal run of key
+// tiles, whatever the rows; where a run ends inside the prefix a
 // row's sums come in pieces (fp32, relative to the piece's maximum).  They lie in the workspace with a row's
 // neighbours in the tile side by side, four channels each: what 32 lanes write, and read again, is
 // contiguous.
@@ -21,11 +22,10 @@
 // and log-sum-exp (prompts).  A last kernel joins all of a row's sums and rounds once.
 //
 // Measured, 32 heads of 128 on 8, on the device.  64 tokens behind 16384 shared and up to 1024 own
-// keys: 77 us (prefix 24, own keys 34: 5.1 TB/s, joining 14; 242 MB in all, 36 us at the copy
-// bandwidth).  16 prompts of up to 77 tokens behind 8192 keys: 159 us (prefix 123: 1.35 PFLOP/s of
-// its rows, of which box edges and padding are a fifth; own keys 19, joining 24).  A step of two row
-// tiles takes 1.5 us where its products take 1.07: two warps a scheduler for the softmax, as in the
-// window attention.
+// keys: 78 us (prefix 24, own keys 34: 5.1 TB/s, joining 14; 242 MB in all, 36 us at the copy
+// bandwidth).  16 prompts of 20 to 77 tokens behind 8192 keys: 142 us (prefix 104: a third of its
+// rows hold no query; own keys 19, joining 25).  A step of two row tiles takes 1.6 us where its
+// products take 1.07: two warps a scheduler for the softmax, as in the window attention.
 #include <algorithm>
 
 #include "softmax_tc.cuh"
@@ -49,50 +49,64 @@ struct Bars {
   uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
 };
 
-// The rows' tiles, and how the work is dealt: units (a key/value head's pair of row tiles) of
-// key_tiles steps lie one behind another, and CTA c of `ctas` takes an equal run of all steps.  A
-// unit that several CTAs share leaves a piece of every row's sums from each.
+// The rows' tiles.
 struct Plan {
-  int B, nh, nkv, group, nq, P;
+  int B, nh, nkv, group, nq, P, nk;
   int tq, tg, tb;  // a row tile's box
   int q_tiles, g_tiles, row_tiles;
-  int key_tiles, ctas;
+  int key_tiles;
+};
+
+// How the work is dealt: units (a key/value head's pair of the row tiles in use) of key_tiles
+// steps lie one behind another, and CTA c of `ctas` takes an equal run of all steps.  What it
+// leaves of a unit is a piece, and lies at place unit + c: of neighbouring pieces one of the two is
+// larger.
+struct Deal {
+  int tiles, pairs, key_tiles, ctas;
   long long steps;
-  int slots;  // places for a row's sums
-  __host__ __device__ __forceinline__ long long from(int cta) const { return steps * cta / ctas; }
+  __host__ __device__ __forceinline__ Deal(const Plan& p, int tiles_in_use) {
+    tiles = tiles_in_use;
+    pairs = (tiles + 1) / 2;
+    key_tiles = p.key_tiles;
+    steps = (long long)p.nkv * pairs * key_tiles;
+    // a CTA for each SM, but not for less than two key tiles
+    const long long c = (steps + 1) / 2;
+    ctas = c < kPrefixCtas ? (int)c : kPrefixCtas;
+  }
+  __host__ __device__ __forceinline__ long long from(int cta) const { return cta < ctas ? steps * cta / ctas : steps; }
   __host__ __device__ __forceinline__ int cta_of(long long step) const { return (int)(((step + 1) * ctas - 1) / steps); }
   __host__ __device__ __forceinline__ int first_cta(int unit) const { return cta_of((long long)unit * key_tiles); }
-  __host__ __device__ __forceinline__ int pieces(int unit) const {
-    return cta_of((long long)(unit + 1) * key_tiles - 1) - first_cta(unit) + 1;
-  }
+  __host__ __device__ __forceinline__ int last_cta(int unit) const { return cta_of((long long)(unit + 1) * key_tiles - 1); }
 };
 
 struct Params {
   Plan p;
-  float4* sums;   // [nkv * row_tiles][slots][D / 4][128]
-  float2* stats;  // [nkv * row_tiles][slots][128]: maximum (log2 units), sum
+  float4* sums;   // [units + ctas][2 slots][D / 4][128]
+  float2* stats;  // [units + ctas][2 slots][128]: maximum (log2 units), sum
+  // Prompts with lengths: row tiles of padding alone are left out.  tile_of [row_tiles]: those in
+  // use; place [row_tiles + 1]: a tile's index among them or -1, then their number.
+  const int* lens;
+  int *tile_of, *place;
   float sl2;      // scale * log2(e)
 };
 
 // What a CTA does of a unit: it begins at step `pos` of all.
 struct Piece {
-  int hk, index, t0, n;  // key tiles t0 .. t0 + n - 1
-  int rt;                // slot 0's row tile
-  bool alone;            // slot 1 has the same one, and every second key tile
-  __device__ __forceinline__ Piece(const Params& a, long long pos, long long end) {
-    const int pairs = (a.p.row_tiles + 1) / 2, unit = (int)(pos / a.p.key_tiles);
-    t0 = (int)(pos - (long long)unit * a.p.key_tiles);
-    n = (int)min((long long)(a.p.key_tiles - t0), end - pos);
-    index = blockIdx.x - a.p.first_cta(unit);
-    hk = unit / pairs;
-    rt = 2 * (unit - hk * pairs);
-    alone = rt + 1 >= a.p.row_tiles;
+  int hk, t0, n;   // key tiles t0 .. t0 + n - 1
+  int unit, tile;  // slot 0's row tile, counted among those in use
+  bool alone;      // slot 1 has the same one, and every second key tile
+  __device__ __forceinline__ Piece(const Deal& d, long long pos, long long end) {
+    unit = (int)(pos / d.key_tiles);
+    t0 = (int)(pos - (long long)unit * d.key_tiles);
+    n = (int)min((long long)(d.key_tiles - t0), end - pos);
+    hk = unit / d.pairs;
+    tile = 2 * (unit - hk * d.pairs);
+    alone = tile + 1 >= d.tiles;
   }
   __device__ __forceinline__ bool takes(int slot, int e) const { return !alone || (e & 1) == slot; }
   __device__ __forceinline__ int first(int slot) const { return alone ? slot : 0; }
   __device__ __forceinline__ bool some(int slot) const { return first(slot) < n; }
   __device__ __forceinline__ int last(int slot) const { return alone ? n - 1 - ((n - 1 - slot) & 1) : n - 1; }
-  __device__ __forceinline__ int row_tile(int slot) const { return alone ? rt : rt + slot; }
 };
 
 // Where a row tile's box begins.
@@ -103,6 +117,12 @@ struct Box {
     rt /= p.q_tiles;
     g = rt % p.g_tiles * p.tg;
     b = rt / p.g_tiles * p.tb;
+  }
+  // whether some row is not padding
+  __device__ __forceinline__ bool in_use(const Plan& p, const int* lens) const {
+    for (int i = b; i < min(b + p.tb, p.B); ++i)
+      if (q + p.nk - p.nq < min(lens[i], p.nk)) return true;
+    return false;
   }
 };
 
@@ -121,6 +141,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Plan& p = a.p;
   const int rows = p.tq * p.tg * p.tb;
+  __shared__ int before[C::kThreads / 32];
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -146,15 +167,47 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     tmem_alloc(tmem_at, C::TM_COLS);
     tmem_relinquish();
   }
+  // The row tiles in use.  Every CTA writes the same list, of which it reads its own entries after the
+  // barrier below.
+  int tiles = p.row_tiles;
+  if (a.lens) {
+    const int per = (p.row_tiles + C::kThreads - 1) / C::kThreads;
+    const int from = min(p.row_tiles, (int)threadIdx.x * per), to = min(p.row_tiles, from + per);
+    int mine = 0;
+    for (int rt = from; rt < to; ++rt) mine += Box(p, rt).in_use(p, a.lens);
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
+    }
+    if (lane == 31) before[warp] = upto;
+    __syncthreads();
+    tiles = 0;
+#pragma unroll
+    for (int i = 0; i < C::kThreads / 32; ++i) {
+      upto += i < warp ? before[i] : 0;
+      tiles += before[i];
+    }
+    int at = upto - mine;
+    for (int rt = from; rt < to; ++rt) {
+      const bool used = Box(p, rt).in_use(p, a.lens);
+      if (used) a.tile_of[at] = rt;
+      if (blockIdx.x == 0) a.place[rt] = used ? at : -1;
+      at += used;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.place[p.row_tiles] = tiles;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
+  const Deal deal(p, tiles);
   // The kernel before this one is the own keys', which shares nothing with it and lets it start only
   // once all that came before has completed: this one runs beside its end, and waits for it before
   // its own, so that the joining kernel finds both done.
   pdl_launch_dependents();
-  const long long begin = p.from(blockIdx.x), end = p.from(blockIdx.x + 1);
+  const long long begin = deal.from(blockIdx.x), end = deal.from(blockIdx.x + 1);
 
   if (warp == C::kProducer) {
     // ------------------------------------------------------------ TMA producer
@@ -165,7 +218,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       bool ok = true;
       int q_count[2] = {0, 0}, kv = 0;
       for (long long pos = begin; ok && pos < end;) {
-        const Piece u(a, pos, end);
+        const Piece u(deal, pos, end);
         pos += u.n;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -176,7 +229,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             continue;
           }
           mbar_arrive_expect_tx(&bar.q_full[s], (uint32_t)(rows * D * 2));
-          const Box box(p, u.row_tile(s));
+          const int tile = u.alone ? u.tile : u.tile + s;
+          const Box box(p, a.lens ? a.tile_of[tile] : tile);
           load_tile<D>(smem + s * C::TILE, &tmQ, &bar.q_full[s], box.q, u.hk * p.group + box.g, box.b);
           q_count[s] = n + 1;
         }
@@ -215,7 +269,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     bool ok = true;
     int kv0 = 0, q_count[2] = {0, 0}, steps[2] = {0, 0};  // kv0: ring index of the unit's first tile
     for (long long pos = begin; ok && pos < end;) {
-      const Piece u(a, pos, end);
+      const Piece u(deal, pos, end);
       pos += u.n;
       auto cols = [&](int e) { return min(kTile, (p.P - (u.t0 + e) * kTile + 15) & ~15); };
       bool first[2] = {true, true};
@@ -304,7 +358,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     for (long long pos = begin; ok && pos < end;) {
       int n, e0, step, valid;  // what the loop needs (the piece again behind it: registers)
       {
-        const Piece u(a, pos, end);
+        const Piece u(deal, pos, end);
         n = u.n;
         e0 = u.first(s);
         step = u.alone ? 2 : 1;
@@ -327,9 +381,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       }
       if (!ok) break;
       // ---- the rows' sums
-      const Piece u(a, pos, end);
+      const Piece u(deal, pos, end);
       pos += n;
-      const long long at = ((long long)u.hk * p.row_tiles + u.row_tile(s)) * p.slots + (u.alone ? 2 * u.index + s : u.index);
+      const long long at = 2LL * (u.unit + blockIdx.x) + s;
       if (u.some(s)) {
         if (!mbar_wait(&bar.o_full[s], outs & 1, abort)) break;
         ++outs;
@@ -367,6 +421,7 @@ struct JoinArgs {
   Plan p;
   const float4* sums;
   const float2* stats;
+  const int* place;  // or null: all row tiles are in use
   View<__nv_bfloat16> o;
   const int* lens;
   int nk;
@@ -410,11 +465,19 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const JoinArg
     x.h += hk * p.group;
     return x;
   };
-  const int pairs = (p.row_tiles + 1) / 2;
-  const bool alone = rt == p.row_tiles - 1 && p.row_tiles % 2;
-  const int mine = p.pieces(hk * pairs + rt / 2) * (alone ? 2 : 1);  // sums of a row
-  const long long at = ((long long)hk * p.row_tiles + rt) * p.slots;
-  for (int s = warp; s < mine; s += kJoinWarps) stats[s * 32 + lane] = a.stats[(at + s) * kTile + r0 + lane];
+  // this tile's sums: `mine` of them, `step` places apart
+  const Deal d(p, a.place ? a.place[p.row_tiles] : p.row_tiles);
+  const int at_use = a.place ? a.place[rt] : rt, unit = hk * d.pairs + at_use / 2;
+  const bool alone = at_use + 1 == d.tiles && d.tiles % 2;
+  const int step = alone ? 1 : 2;
+  int mine = 0;
+  long long at = 0;
+  if (at_use >= 0) {
+    const int c = d.first_cta(unit);
+    mine = (d.last_cta(unit) - c + 1) * (alone ? 2 : 1);
+    at = 2LL * (unit + c) + (alone ? 0 : at_use & 1);
+  }
+  for (int s = warp; s < mine; s += kJoinWarps) stats[s * 32 + lane] = a.stats[(at + s * step) * kTile + r0 + lane];
   auto own_parts = [&](int b) { return ((max(0, min(a.lens[b], a.nk)) + 15) / 16 + a.run - 1) / a.run; };
   // the own keys' maximum and sum
   if constexpr (kDecode) {
@@ -467,7 +530,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const JoinArg
         l += st.y * f[x];
 #pragma unroll
         for (int c = 0; c < Q; ++c)  // (a piece that had no tile for the slot has left nothing)
-          v[x][c] = st.y != 0.f ? src[((long long)(s0 + x) * (D / 4) + c) * kTile] : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[x][c] = st.y != 0.f ? src[((long long)(s0 + x) * step * (D / 4) + c) * kTile] : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
       for (int x = 0; x < U; ++x)
@@ -527,8 +590,12 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const JoinArg
   }
 }
 
-// The box of a row tile that needs the fewest tiles, and of those the one with most queries.
-Plan make_plan(const PrefixShape& x) {
+// The box of a row tile that needs the fewest tiles, and of those the one with most queries.  With
+// lengths, tiles of padding alone cost nothing, and a tile of several sequences is in use up to the
+// longest of them: for lengths anywhere below n_q that is tb / (tb + 1) of their tiles, and half a
+// tile (16 prompts of 20 to 77 tokens, 32 heads on 8: boxes of 32 queries, 4 heads, one sequence instead
+// of 2, 4, 16: 142 us instead of 162).
+Plan make_plan(const PrefixShape& x, bool lengths) {
   Plan p{};
   p.B = x.B;
   p.nh = x.nh;
@@ -536,41 +603,54 @@ Plan make_plan(const PrefixShape& x) {
   p.group = x.nh / x.nkv;
   p.nq = x.nq;
   p.P = x.P;
+  p.nk = x.nk;
   auto cdiv = [](int a, int b) { return (a + b - 1) / b; };
+  double least = 0;
   for (int tq = 1; tq <= std::min(p.nq, kTile); ++tq) {
     const int tg = std::min(p.group, kTile / tq), tb = std::min(p.B, kTile / (tq * tg));
-    const int tiles = cdiv(p.nq, tq) * cdiv(p.group, tg) * cdiv(p.B, tb);
-    if (tq == 1 || tiles <= p.row_tiles) {
+    const double across = (double)cdiv(p.group, tg) * cdiv(p.B, tb);
+    const double tiles = across * (lengths ? (double)p.nq / tq * tb / (tb + 1) + 0.5 : cdiv(p.nq, tq));
+    if (tq == 1 || tiles <= least) {
+      least = tiles;
       p.tq = tq;
       p.tg = tg;
       p.tb = tb;
-      p.row_tiles = tiles;
     }
   }
   p.q_tiles = cdiv(p.nq, p.tq);
   p.g_tiles = cdiv(p.group, p.tg);
+  p.row_tiles = p.q_tiles * p.g_tiles * cdiv(p.B, p.tb);
   p.key_tiles = cdiv(p.P, kTile);
-  const int pairs = cdiv(p.row_tiles, 2);
-  p.steps = (long long)p.nkv * pairs * p.key_tiles;
-  // a CTA for each SM, but not for less than two key tiles
-  p.ctas = (int)std::min<long long>(kPrefixCtas, (p.steps + 1) / 2);
-  // pieces of a unit at most: the runs that its steps fill, and one that begins or ends in it
-  const int most = (int)std::min<long long>(p.ctas, (p.key_tiles * (long long)p.ctas + p.steps - 1) / p.steps + 1);
-  p.slots = p.row_tiles % 2 ? 2 * most : most;
   return p;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-size_t sums_bytes(const Plan& p, int d) { return (size_t)p.nkv * p.row_tiles * p.slots * kTile * d * 4; }
-size_t stats_bytes(const Plan& p) { return (size_t)p.nkv * p.row_tiles * p.slots * kTile * 8; }
+size_t pieces_at_most(const Plan& p) {
+  const Deal d(p, p.row_tiles);
+  return (size_t)p.nkv * d.pairs + d.ctas;
+}
+size_t sums_bytes(const Plan& p, int d) { return pieces_at_most(p) * 2 * kTile * d * 4; }
+size_t stats_bytes(const Plan& p) { return pieces_at_most(p) * 2 * kTile * 8; }
+size_t tiles_bytes(const Plan& p) { return round256((2 * (size_t)p.row_tiles + 1) * 4); }
+
+// A row's sums at most: the runs that a unit's steps fill, and one that begins or ends in it; with
+// row tiles left out there may be one unit for each key/value head, and one tile alone.
+int sums_at_most(const Plan& p, bool all_in_use) {
+  const int units = p.nkv * (all_in_use ? Deal(p, p.row_tiles).pairs : 1);
+  const int most = std::min(kPrefixCtas, (kPrefixCtas + units - 1) / units + 1);
+  return all_in_use && p.row_tiles % 2 == 0 ? most : 2 * most;
+}
 
 template <int D>
-cudaError_t prefix_part(const PrefixArgs& x, const Plan& p, cudaStream_t st) {
+cudaError_t prefix_part(const PrefixArgs& x, const Plan& p, bool decode, cudaStream_t st) {
   using C = Cfg<D>;
   Params a{};
   a.p = p;
   a.sums = static_cast<float4*>(x.ws);
   a.stats = reinterpret_cast<float2*>(static_cast<char*>(x.ws) + sums_bytes(p, D));
+  a.lens = decode ? nullptr : x.lens;
+  a.tile_of = reinterpret_cast<int*>(static_cast<char*>(x.ws) + sums_bytes(p, D) + stats_bytes(p));
+  a.place = a.tile_of + p.row_tiles;
   a.sl2 = x.scale * kLog2;
   CUtensorMap mq, mk, mv;
   if (!map_view_box(&mq, x.q.p, x.q.sb, x.q.sh, x.q.sn, p.B, p.nh, p.nq, D, p.tq, p.tg, p.tb) ||
@@ -580,19 +660,21 @@ cudaError_t prefix_part(const PrefixArgs& x, const Plan& p, cudaStream_t st) {
   auto kern = prefix_tc_kernel<D>;
   const cudaError_t e = set_max_dynamic_smem((const void*)kern, C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(p.ctas), dim3(C::kThreads), C::SMEM, st, mq, mk, mv, a);
+  return launch_pdl(kern, dim3(Deal(p, p.row_tiles).ctas), dim3(C::kThreads), C::SMEM, st, mq, mk, mv, a);
 }
 
 template <int D>
 cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
-  const Plan p = make_plan(x.s);
+  const Plan p = make_plan(x.s, !decode && x.lens);
   char* ws = static_cast<char*>(x.ws);
-  float* own = reinterpret_cast<float*>(ws + sums_bytes(p, D) + stats_bytes(p));
+  const int* tiles = reinterpret_cast<const int*>(ws + sums_bytes(p, D) + stats_bytes(p));
+  float* own = reinterpret_cast<float*>(ws + sums_bytes(p, D) + stats_bytes(p) + tiles_bytes(p));
   cudaError_t e;
   JoinArgs j{};
   j.p = p;
   j.sums = reinterpret_cast<const float4*>(ws);
   j.stats = reinterpret_cast<const float2*>(ws + sums_bytes(p, D));
+  j.place = !decode && x.lens ? tiles + p.row_tiles : nullptr;
   j.o = x.o;
   j.lens = x.lens;
   j.nk = x.s.nk;
@@ -624,12 +706,12 @@ cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
     j.lse = x.lse;
   }
   if (e != cudaSuccess) return e;
-  e = prefix_part<D>(x, p, st);
+  e = prefix_part<D>(x, p, decode, st);
   if (e != cudaSuccess) return e;
   // Rows are few when decoding: their channels go to several CTAs then, each of which reads the
   // statistics.  Where rows fill the SMs that costs more than it gives (16 prompts of 77 tokens:
   // 196 us in all instead of 162, then).
-  const int groups = p.nkv * p.row_tiles * (kTile / kJoinRows), smem = p.slots * kJoinRows * (int)sizeof(float2);
+  const int groups = p.nkv * p.row_tiles * (kTile / kJoinRows), smem = sums_at_most(p, !j.place) * kJoinRows * (int)sizeof(float2);
   auto kern = groups >= 304 ? (decode ? prefix_join_kernel<D, D, true> : prefix_join_kernel<D, D, false>)
                             : (decode ? prefix_join_kernel<D, 32, true> : prefix_join_kernel<D, 32, false>);
   e = set_max_dynamic_smem((const void*)kern, 2 * kPrefixCtas * kJoinRows * (int)sizeof(float2));
@@ -640,10 +722,14 @@ cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
 }  // namespace
 
 size_t prefix_ws_bytes(const PrefixShape& x, int d) {
-  const Plan p = make_plan(x);
+  size_t sums = 0;
+  for (bool lengths : {false, true}) {
+    const Plan p = make_plan(x, lengths);
+    sums = std::max(sums, sums_bytes(p, d) + stats_bytes(p) + tiles_bytes(p));
+  }
   const Window w{x.B, x.nh, x.nkv, x.nq, x.nk, x.nk, 0, 0, nullptr};
   const size_t own = x.nq == 1 ? decode_parts_ws_bytes(w, d) : 0;
-  return round256(sums_bytes(p, d) + stats_bytes(p) + std::max(own, (size_t)x.B * x.nh * x.nq * (d + 1) * 4));
+  return round256(sums + std::max(own, (size_t)x.B * x.nh * x.nq * (d + 1) * 4));
 }
 
 cudaError_t launch_prefix_attn(const PrefixArgs& a, int d, bool decode, cudaStream_t st) {

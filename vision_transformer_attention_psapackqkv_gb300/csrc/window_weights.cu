@@ -95,8 +95,9 @@ struct Run {
     unit += n > 0;
     s = n > 0 ? 0 : s;
     if (left <= 0) return false;
-    int steps;
-    while ((steps = Unit(a, unit).steps) == 0) ++unit;
+    int steps = 0;
+    while (unit < a.units && (steps = Unit(a, unit).steps) == 0) ++unit;
+    if (unit >= a.units) return false;  // (lengths that changed since they were counted)
     n = (int)min((long long)(steps - s), left);
     left -= n;
     return true;

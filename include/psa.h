@@ -37,7 +37,8 @@
  *     serialization: their CTAs may start their set-up while the previous
  *     kernel of the stream is finishing, but they read and write no global
  *     memory before that kernel has completed, so results are exactly those of
- *     plain stream order.
+ *     plain stream order.  (Between the kernels of one call: those that share
+ *     nothing may run beside one another.)
  */
 #ifndef PSA_GB300_H
 #define PSA_GB300_H

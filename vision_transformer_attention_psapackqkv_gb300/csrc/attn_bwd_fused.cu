@@ -566,8 +566,8 @@ __global__ void __launch_bounds__(896, 1)
           uint4 ov[8], dv[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            ov[c] = __ldg(reinterpret_cast<const uint4*>(args.o + base + (long long)c * N));
-            dv[c] = __ldg(reinterpret_cast<const uint4*>(args.dO + base + (long long)c * N));
+            ov[c] = ld_global16(args.o + base + (long long)c * N);
+            dv[c] = ld_global16(args.dO + base + (long long)c * N);
           }
 #pragma unroll
           for (int c = 0; c < 8; ++c) {

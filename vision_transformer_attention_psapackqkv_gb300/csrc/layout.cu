@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 4) channels_to_rows_vec_kernel(const
       for (int h = 0; h < 2; ++h) {
         const int d = d0 + i * kWarps, c = ln + 32 * h;
         if (d < a.KD && c < cvalid)
-          v[i][h] = __ldg(reinterpret_cast<const uint4*>(src + (long long)d * a.N + 8 * c));
+          v[i][h] = *reinterpret_cast<const uint4*>(src + (long long)d * a.N + 8 * c);
       }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_to_channels_vec_kernel(const
     const int c = pow2 ? idx >> lg : idx / dvec, g = idx - c * dvec;
     uint4 in[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) in[j] = __ldg(src + (long long)(8 * c + j) * dvec + g);
+    for (int j = 0; j < 8; ++j) in[j] = src[(long long)(8 * c + j) * dvec + g];
 #pragma unroll
     for (int i = 0; i < 8; ++i) tile[vec_chunk(8 * g + i, c)] = transpose8x8_row(in, i);
   }
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_to_channels_vec_kernel(const
 // Copies `slabs` contiguous slabs of slab_vec 16-byte vectors from src (slab
 // stride src_stride_vec) to dst (slab stride dst_stride_vec).
 __global__ void __launch_bounds__(kThreads)
-    strided_slab_copy_kernel(const uint4* __restrict__ src, uint4* __restrict__ dst,
+    strided_slab_copy_kernel(const uint4* src, uint4* __restrict__ dst,
                              long long slabs, long long slab_vec, long long src_stride_vec,
                              long long dst_stride_vec) {
   pdl_launch_dependents();  // (programmatic dependent launch)

@@ -155,6 +155,15 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// 16 bytes that an earlier kernel may have written, read where the call stands: volatile, so that
+// it stays behind pdl_wait (loads of the read-only path, __ldg, promise memory that nobody writes
+// during the kernel, and nothing keeps them there).
+__device__ __forceinline__ uint4 ld_global16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // Makes this thread's generic-proxy shared-memory writes visible to the async
 // proxy (tcgen05.mma operand reads, TMA).
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int q = t.qt * a.tq + my_i[x], g = t.ht * a.tg + my_g[x];
-          lse[x] = g < group && q < w.nq ? __ldg(list_lse + (long long)g * w.nq + q) : INFINITY;
+          lse[x] = g < group && q < w.nq ? list_lse[(long long)g * w.nq + q] : INFINITY;
         }
       };
       float sum = 0.f;

@@ -24,3 +24,13 @@ def test_no_read_only_loads_while_an_earlier_kernel_may_write(path):
     for kernel in code.split("__global__")[1:]:
         if "pdl_wait()" in kernel:
             assert not re.search(r"const\s+\w+\s*\*\s*__restrict__", kernel.split("{")[0])
+
+
+def test_what_the_prefix_kernel_reads_before_its_wait():
+    """The kernel over a shared prefix runs beside the end of the one before it, whose own wait covers all
+    that came earlier: the lengths are read past L1 then, where an older copy of them could lie."""
+    code = _code(os.path.join(CSRC, "prefix_attn.cu"))
+    kernel = code.split("prefix_tc_kernel(")[1].split("prefix_join_kernel(")[0]
+    assert kernel.rstrip().count("pdl_wait()") == 1 and "a.lens[" not in kernel
+    in_use = code.split("bool in_use(")[1].split("};")[0]
+    assert "ld_global_l2(lens +" in in_use and "lens[" not in in_use

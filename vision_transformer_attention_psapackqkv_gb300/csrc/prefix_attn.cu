@@ -118,10 +118,10 @@ struct Box {
     g = rt % p.g_tiles * p.tg;
     b = rt / p.g_tiles * p.tb;
   }
-  // whether some row is not padding
+  // whether some row is not padding (asked before pdl_wait: the lengths come from L2)
   __device__ __forceinline__ bool in_use(const Plan& p, const int* lens) const {
     for (int i = b; i < min(b + p.tb, p.B); ++i)
-      if (q + p.nk - p.nq < min(lens[i], p.nk)) return true;
+      if (q + p.nk - p.nq < min(ld_global_l2(lens + i), p.nk)) return true;
     return false;
   }
 };

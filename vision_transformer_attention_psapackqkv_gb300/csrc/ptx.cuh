@@ -163,6 +163,13 @@ __device__ __forceinline__ uint4 ld_global16(const void* p) {
   asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
+// Read from L2, where everything that has completed is, whatever L1 holds: for a kernel that
+// runs ahead of its pdl_wait because the kernel before it has waited for all that it reads.
+__device__ __forceinline__ int ld_global_l2(const int* p) {
+  int v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 
 // Makes this thread's generic-proxy shared-memory writes visible to the async
 // proxy (tcgen05.mma operand reads, TMA).

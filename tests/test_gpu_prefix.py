@@ -104,6 +104,31 @@ def test_row_tiles_of_padding_are_left_out(lens, nh, nkv):
         assert ((lse[b, :, :n] - whole_lse[b, :, :n]).abs() <= 1e-5).all()
 
 
+@pytest.mark.parametrize("Bn,nq,nh,nkv,P,d", [(16, 77, 32, 8, 1000, 128), (8, 200, 32, 8, 700, 64), (16, 48, 32, 8, 1500, 128),
+                                              (3, 33, 24, 3, 2000, 64), (5, 1, 8, 2, 300, 64), (16, 400, 8, 1, 260, 64)])
+def test_lengths_that_are_all_full(Bn, nq, nh, nkv, P, d):
+    """The rows are cut as without lengths then, and the work is dealt alike: the same bits."""
+    c = _case(Bn, nh, nkv, nq, P, nq, d, 51)
+    o, lse = _prompts(c, [nq] * Bn, 0.1)
+    whole, whole_lse = _prompts(c, None, 0.1)
+    assert torch.equal(o, whole) and torch.equal(lse, whole_lse)
+
+
+@pytest.mark.parametrize("lens", [[400, 1, 0, 37] * 4, [400] * 15 + [399], [64] * 16, [130, 250] * 8, [0] * 15 + [400], list(range(10, 394, 24))])
+def test_hundreds_of_row_tiles(lens):
+    """More row tiles than the threads that count those in use, whichever way the rows are cut."""
+    Bn, nh, nkv, nq, P, d, scale = 16, 8, 1, 400, 260, 64, 0.125
+    c = _case(Bn, nh, nkv, nq, P, nq, d, 61)
+    r = _reference(c, lens, scale)
+    _pad(c, lens, 0)
+    o, lse = _prompts(c, lens, scale)
+    for b, n in enumerate(lens):
+        within(o[b, :, :n], r["o"][b, :, :n], r["o_tol"][b, :, :n], "o")
+        want = r["lse"][b, :, :n]
+        within(lse[b, :, :n], want, r["lse_tol"][b, :, :n] + 8 * U * (1 + want.abs()), "lse")
+        assert (o[b, :, n:] == 0).all() and (lse[b, :, n:] == -math.inf).all()
+
+
 # B, P, rows, lens
 STEPS = [(1, 1, 1, [1]), (2, 40, 9, [0, 9]), (4, 128, 30, [30, 1, 0, -1]), (7, 129, 200, [200, 0, 17, 16, -3, 15, 300]),
          (33, 1000, 50, [50, 49, 3] * 11), (3, 4500, 700, [700, 350, 1]), (130, 300, 20, [20, -1, 7, 0, 11] * 26), (1, 9000, 5, [5])]

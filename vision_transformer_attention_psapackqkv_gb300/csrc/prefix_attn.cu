@@ -4,7 +4,8 @@
 //
 // The prefix is read once for all sequences: the queries of one key/value head, of all sequences
 // and of the heads that share it, are the rows of one product with its keys.  A tile of 128 rows
-// is a box of tq queries, tg heads and tb sequences, those extents that need the fewest tiles.
+// is a box of tq queries, tg heads and tb sequences, those extents that need the fewest tiles (with
+// lengths: one of two boxes, chosen on the device).
 // The prefix part is an online softmax without masks (but for the last tile's columns), as the
 // window attention's forward: two slots of 128 rows whose softmax steps run while the other
 // slot's products do, P in S's columns of tensor memory, products issued in order by one
@@ -44,17 +45,31 @@ struct Cfg {
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
 };
 
+constexpr int kStagedLens = 256;  // lengths that are read once, into shared memory
+
 struct Bars {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], done;
   uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
 };
 
-// The rows' tiles.
+// How the rows are cut into tiles: the box of one, and how many there are.
+struct Boxes {
+  int tq, tg, tb;  // queries, heads of a group, sequences
+  int q_tiles, g_tiles, row_tiles;
+  __host__ __device__ __forceinline__ int rows() const { return tq * tg * tb; }
+};
+// With lengths there are two ways to cut (Plan's `ways`), and the device takes the one that needs
+// fewer tiles.
 struct Plan {
   int B, nh, nkv, group, nq, P, nk;
-  int tq, tg, tb;  // a row tile's box
-  int q_tiles, g_tiles, row_tiles;
+  int ways;
+  Boxes way[2];
   int key_tiles;
+  // (not indexed: it lies with the kernel's parameters)
+  __host__ __device__ __forceinline__ Boxes boxes(int i) const { return i ? way[1] : way[0]; }
+  __host__ __device__ __forceinline__ int most_tiles() const {
+    return ways > 1 && way[1].row_tiles > way[0].row_tiles ? way[1].row_tiles : way[0].row_tiles;
+  }
 };
 
 // How the work is dealt: units (a key/value head's pair of the row tiles in use) of key_tiles
@@ -83,8 +98,9 @@ struct Params {
   Plan p;
   float4* sums;   // [units + ctas][2 slots][D / 4][128]
   float2* stats;  // [units + ctas][2 slots][128]: maximum (log2 units), sum
-  // Prompts with lengths: row tiles of padding alone are left out.  tile_of [row_tiles]: those in
-  // use; place [row_tiles + 1]: a tile's index among them or -1, then their number.
+  // Prompts with lengths: row tiles of padding alone are left out.  tile_of [most_tiles]: those in
+  // use; place [most_tiles + 2]: their number, which way the rows are cut, then each tile's index among
+  // them or -1.
   const int* lens;
   int *tile_of, *place;
   float sl2;      // scale * log2(e)
@@ -112,24 +128,30 @@ struct Piece {
 // Where a row tile's box begins.
 struct Box {
   int q, g, b;
-  __host__ __device__ __forceinline__ Box(const Plan& p, int rt) {
-    q = rt % p.q_tiles * p.tq;
-    rt /= p.q_tiles;
-    g = rt % p.g_tiles * p.tg;
-    b = rt / p.g_tiles * p.tb;
+  __device__ __forceinline__ Box(const Boxes& x, int rt) {
+    q = rt % x.q_tiles * x.tq;
+    rt /= x.q_tiles;
+    g = rt % x.g_tiles * x.tg;
+    b = rt / x.g_tiles * x.tb;
   }
-  // whether some row is not padding (asked before pdl_wait: the lengths come from L2)
-  __device__ __forceinline__ bool in_use(const Plan& p, const int* lens) const {
-    for (int i = b; i < min(b + p.tb, p.B); ++i)
-      if (q + p.nk - p.nq < min(ld_global_l2(lens + i), p.nk)) return true;
-    return false;
+  // whether some row is not padding (asked before pdl_wait: the lengths come from L2, the first of them
+  // by way of shared memory).  No way out of the loop: its reads do not wait for one another.
+  __device__ __forceinline__ bool in_use(const Plan& p, int tb, const int* lens, const int* staged) const {
+    const int end = min(b + tb, p.B);
+    int longest = 0;
+#pragma unroll 4
+    for (int i = b; i < min(end, kStagedLens); ++i) longest = max(longest, staged[i]);
+#pragma unroll 4
+    for (int i = max(b, kStagedLens); i < end; ++i) longest = max(longest, ld_global_l2(lens + i));
+    return q + p.nk - p.nq < min(longest, p.nk);
   }
 };
 
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
-    prefix_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const Params a) {
+    prefix_tc_kernel(const __grid_constant__ CUtensorMap tmQ0, const __grid_constant__ CUtensorMap tmQ1,
+                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const Params a) {
   using C = Cfg<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = align1024(smem_raw);
@@ -140,8 +162,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   static_assert(sizeof(Bars) + 16 <= 512, "barriers");
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Plan& p = a.p;
-  const int rows = p.tq * p.tg * p.tb;
-  __shared__ int before[C::kThreads / 32];
+  __shared__ int2 before[C::kThreads / 32];
+  __shared__ int staged[kStagedLens], chosen_rows;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -161,43 +183,62 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     *abort = 0;
     fence_mbar_init();
   }
-  // rows that no box fills are zeros (their scores must not move a warp's maxima)
-  if (warp < 2) zero_rows<D>(smem + warp * C::TILE, rows, kTile, lane);
   if (warp == C::kIssuer) {
     tmem_alloc(tmem_at, C::TM_COLS);
     tmem_relinquish();
   }
-  // The row tiles in use.  Every CTA writes the same list, of which it reads its own entries after the
-  // barrier below.
-  int tiles = p.row_tiles;
+  // The row tiles in use, each thread a run of them: passes 0 and 1 count them for the two ways to cut
+  // the rows, pass 2 writes the list of the one that needs fewer.  Every CTA writes the same list, of
+  // which it reads its own entries after the barrier below.  (One loop: these instructions run once, and
+  // fetching them is most of what they cost.)
+  int tiles = p.way[0].row_tiles, which = 0;
   if (a.lens) {
-    const int per = (p.row_tiles + C::kThreads - 1) / C::kThreads;
-    const int from = min(p.row_tiles, (int)threadIdx.x * per), to = min(p.row_tiles, from + per);
-    int mine = 0;
-    for (int rt = from; rt < to; ++rt) mine += Box(p, rt).in_use(p, a.lens);
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += y;
-    }
-    if (lane == 31) before[warp] = upto;
+    for (int i = threadIdx.x; i < min(p.B, kStagedLens); i += C::kThreads) staged[i] = ld_global_l2(a.lens + i);
     __syncthreads();
-    tiles = 0;
-#pragma unroll
-    for (int i = 0; i < C::kThreads / 32; ++i) {
-      upto += i < warp ? before[i] : 0;
-      tiles += before[i];
+    int mine[2] = {0, 0}, at = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const Boxes x = p.boxes(pass < 2 ? pass : which);
+      const int per = pass < p.ways || pass == 2 ? (x.row_tiles + C::kThreads - 1) / C::kThreads : 0;
+      const int from = min(x.row_tiles, (int)threadIdx.x * per), to = min(x.row_tiles, from + per);
+      int n = 0;
+#pragma unroll 1
+      for (int rt = from; rt < to; ++rt) {
+        const bool used = Box(x, rt).in_use(p, x.tb, a.lens, staged);
+        if (pass == 2) {
+          if (used) a.tile_of[at + n] = rt;
+          if (blockIdx.x == 0) a.place[2 + rt] = used ? at + n : -1;
+        }
+        n += used;
+      }
+      if (pass == 0) mine[0] = n;
+      if (pass != 1) continue;
+      mine[1] = n;
+      const int all0 = __reduce_add_sync(0xffffffffu, mine[0]), all1 = __reduce_add_sync(0xffffffffu, mine[1]);
+      if (lane == 0) before[warp] = make_int2(all0, all1);
+      __syncthreads();
+      const int2 others = lane < C::kThreads / 32 ? before[lane] : make_int2(0, 0);
+      const int2 all = make_int2(__reduce_add_sync(0xffffffffu, others.x), __reduce_add_sync(0xffffffffu, others.y));
+      which = p.ways > 1 && all.y < all.x;
+      tiles = which ? all.y : all.x;
+      const int upto = which ? mine[1] : mine[0];
+      at = __reduce_add_sync(0xffffffffu, lane >= warp ? 0 : which ? others.y : others.x) - upto;
+      int sum = upto;
+#pragma unroll 1
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += y;
+      }
+      at += sum;
     }
-    int at = upto - mine;
-    for (int rt = from; rt < to; ++rt) {
-      const bool used = Box(p, rt).in_use(p, a.lens);
-      if (used) a.tile_of[at] = rt;
-      if (blockIdx.x == 0) a.place[rt] = used ? at : -1;
-      at += used;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      a.place[0] = tiles;
+      a.place[1] = which;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.place[p.row_tiles] = tiles;
   }
+  // rows that no box fills are zeros (their scores must not move a warp's maxima)
+  if (warp < 2) zero_rows<D>(smem + warp * C::TILE, p.boxes(which).rows(), kTile, lane);
+  if (threadIdx.x == 0) chosen_rows = p.boxes(which).rows();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -212,7 +253,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   if (warp == C::kProducer) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
+      const Boxes cut = p.boxes(which);
+      const CUtensorMap* tmQ = which ? &tmQ1 : &tmQ0;
+      tma_prefetch_desc(tmQ);
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
       bool ok = true;
@@ -228,10 +271,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             ok = false;
             continue;
           }
-          mbar_arrive_expect_tx(&bar.q_full[s], (uint32_t)(rows * D * 2));
+          mbar_arrive_expect_tx(&bar.q_full[s], (uint32_t)(cut.rows() * D * 2));
           const int tile = u.alone ? u.tile : u.tile + s;
-          const Box box(p, a.lens ? a.tile_of[tile] : tile);
-          load_tile<D>(smem + s * C::TILE, &tmQ, &bar.q_full[s], box.q, u.hk * p.group + box.g, box.b);
+          const Box box(cut, a.lens ? a.tile_of[tile] : tile);
+          load_tile<D>(smem + s * C::TILE, tmQ, &bar.q_full[s], box.q, u.hk * p.group + box.g, box.b);
           q_count[s] = n + 1;
         }
         for (int e = 0; ok && e < u.n; ++e) {
@@ -383,6 +426,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       // ---- the rows' sums
       const Piece u(deal, pos, end);
       pos += n;
+      const bool valid_row = r < *(volatile int*)&chosen_rows;
       const long long at = 2LL * (u.unit + blockIdx.x) + s;
       if (u.some(s)) {
         if (!mbar_wait(&bar.o_full[s], outs & 1, abort)) break;
@@ -393,7 +437,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         for (int c = 0; c < D; c += 32) {
           float o[32];
           tmem_load32(tO + c, o);
-          if (r < rows) {
+          if (valid_row) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
               dst[(c + k) / 4 * kTile] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
@@ -401,7 +445,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         tc_fence_before();
       }
-      if (r < rows) a.stats[at * kTile + r] = make_float2(m, l);
+      if (valid_row) a.stats[at * kTile + r] = make_float2(m, l);
     }
   }
 
@@ -421,7 +465,7 @@ struct JoinArgs {
   Plan p;
   const float4* sums;
   const float2* stats;
-  const int* place;  // or null: all row tiles are in use
+  const int* place;  // or null: cut the first way, all row tiles in use
   View<__nv_bfloat16> o;
   const int* lens;
   int nk;
@@ -445,29 +489,31 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const JoinArg
   pdl_wait();
   const Plan& p = a.p;
   constexpr int groups = kTile / kJoinRows;
-  const int tile = blockIdx.x / groups, hk = tile / p.row_tiles, rt = tile - hk * p.row_tiles;
+  const int hk = blockIdx.z, rt = blockIdx.x / groups;
+  const int tiles = a.place ? a.place[0] : p.way[0].row_tiles, at_use = a.place ? a.place[2 + rt] : rt;
+  const Boxes cut = p.boxes(a.place ? a.place[1] : 0);
   const int r0 = blockIdx.x % groups * kJoinRows, c0 = blockIdx.y * CH;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rows = p.tq * p.tg * p.tb;
-  if (r0 >= rows) return;
-  const Box box(p, rt);
+  const int rows = cut.rows();
+  if (rt >= cut.row_tiles || r0 >= rows) return;  // (there are CTAs for the way that has more tiles)
+  const Box box(cut, rt);
   struct Row {
     int b, h, q;
     bool valid;
   };
   auto row_of = [&](int r) {
     Row x;
-    const int g = r / p.tq, bb = g / p.tg;
+    const int g = r / cut.tq, bb = g / cut.tg;
     x.b = box.b + bb;
-    x.h = box.g + g - bb * p.tg;
-    x.q = box.q + r - g * p.tq;
+    x.h = box.g + g - bb * cut.tg;
+    x.q = box.q + r - g * cut.tq;
     x.valid = r < rows && x.b < p.B && x.h < p.group && x.q < p.nq;
     x.h += hk * p.group;
     return x;
   };
   // this tile's sums: `mine` of them, `step` places apart
-  const Deal d(p, a.place ? a.place[p.row_tiles] : p.row_tiles);
-  const int at_use = a.place ? a.place[rt] : rt, unit = hk * d.pairs + at_use / 2;
+  const Deal d(p, tiles);
+  const int unit = hk * d.pairs + at_use / 2;
   const bool alone = at_use + 1 == d.tiles && d.tiles % 2;
   const int step = alone ? 1 : 2;
   int mine = 0;
@@ -592,9 +638,33 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const JoinArg
 
 // The box of a row tile that needs the fewest tiles, and of those the one with most queries.  With
 // lengths, tiles of padding alone cost nothing, and a tile of several sequences is in use up to the
-// longest of them: for lengths anywhere below n_q that is tb / (tb + 1) of their tiles, and half a
-// tile (16 prompts of 20 to 77 tokens, 32 heads on 8: boxes of 32 queries, 4 heads, one sequence instead
-// of 2, 4, 16: 142 us instead of 162).
+// longest of them: for lengths anywhere below n_q (`spread`) that is tb / (tb + 1) of their tiles, and half
+// a tile.
+Boxes best_boxes(const Plan& p, bool spread) {
+  auto cdiv = [](int a, int b) { return (a + b - 1) / b; };
+  Boxes x{};
+  double least = 0;
+  for (int tq = 1; tq <= std::min(p.nq, kTile); ++tq) {
+    const int tg = std::min(p.group, kTile / tq), tb = std::min(p.B, kTile / (tq * tg));
+    const double across = (double)cdiv(p.group, tg) * cdiv(p.B, tb);
+    const double tiles = across * (spread ? (double)p.nq / tq * tb / (tb + 1) + 0.5 : cdiv(p.nq, tq));
+    if (tq == 1 || tiles <= least) {
+      least = tiles;
+      x.tq = tq;
+      x.tg = tg;
+      x.tb = tb;
+    }
+  }
+  x.q_tiles = cdiv(p.nq, x.tq);
+  x.g_tiles = cdiv(p.group, x.tg);
+  x.row_tiles = x.q_tiles * x.g_tiles * cdiv(p.B, x.tb);
+  return x;
+}
+
+// Two ways where there are lengths, because which of them needs fewer tiles is known on the device only.
+// Measured, 16 prompts behind 8192 keys, 32 heads on 8, boxes of 2 queries, 4 heads, 16 sequences against
+// 32, 4, 1: lengths of 20 to 77 162 and 143 us, all 77 170 and 196, all 38 107 and 141.  Counting both ways
+// costs 0.5 to 4 us of that.
 Plan make_plan(const PrefixShape& x, bool lengths) {
   Plan p{};
   p.B = x.B;
@@ -604,41 +674,29 @@ Plan make_plan(const PrefixShape& x, bool lengths) {
   p.nq = x.nq;
   p.P = x.P;
   p.nk = x.nk;
-  auto cdiv = [](int a, int b) { return (a + b - 1) / b; };
-  double least = 0;
-  for (int tq = 1; tq <= std::min(p.nq, kTile); ++tq) {
-    const int tg = std::min(p.group, kTile / tq), tb = std::min(p.B, kTile / (tq * tg));
-    const double across = (double)cdiv(p.group, tg) * cdiv(p.B, tb);
-    const double tiles = across * (lengths ? (double)p.nq / tq * tb / (tb + 1) + 0.5 : cdiv(p.nq, tq));
-    if (tq == 1 || tiles <= least) {
-      least = tiles;
-      p.tq = tq;
-      p.tg = tg;
-      p.tb = tb;
-    }
-  }
-  p.q_tiles = cdiv(p.nq, p.tq);
-  p.g_tiles = cdiv(p.group, p.tg);
-  p.row_tiles = p.q_tiles * p.g_tiles * cdiv(p.B, p.tb);
-  p.key_tiles = cdiv(p.P, kTile);
+  p.key_tiles = (p.P + kTile - 1) / kTile;
+  p.way[0] = best_boxes(p, false);
+  p.way[1] = best_boxes(p, lengths);
+  const Boxes &a = p.way[0], &b = p.way[1];
+  p.ways = a.tq == b.tq && a.tg == b.tg && a.tb == b.tb ? 1 : 2;
   return p;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 size_t pieces_at_most(const Plan& p) {
-  const Deal d(p, p.row_tiles);
+  const Deal d(p, p.most_tiles());
   return (size_t)p.nkv * d.pairs + d.ctas;
 }
 size_t sums_bytes(const Plan& p, int d) { return pieces_at_most(p) * 2 * kTile * d * 4; }
 size_t stats_bytes(const Plan& p) { return pieces_at_most(p) * 2 * kTile * 8; }
-size_t tiles_bytes(const Plan& p) { return round256((2 * (size_t)p.row_tiles + 1) * 4); }
+size_t tiles_bytes(const Plan& p) { return round256((2 * (size_t)p.most_tiles() + 2) * 4); }
 
 // A row's sums at most: the runs that a unit's steps fill, and one that begins or ends in it; with
 // row tiles left out there may be one unit for each key/value head, and one tile alone.
 int sums_at_most(const Plan& p, bool all_in_use) {
-  const int units = p.nkv * (all_in_use ? Deal(p, p.row_tiles).pairs : 1);
+  const int units = p.nkv * (all_in_use ? Deal(p, p.way[0].row_tiles).pairs : 1);
   const int most = std::min(kPrefixCtas, (kPrefixCtas + units - 1) / units + 1);
-  return all_in_use && p.row_tiles % 2 == 0 ? most : 2 * most;
+  return all_in_use && p.way[0].row_tiles % 2 == 0 ? most : 2 * most;
 }
 
 template <int D>
@@ -650,17 +708,21 @@ cudaError_t prefix_part(const PrefixArgs& x, const Plan& p, bool decode, cudaStr
   a.stats = reinterpret_cast<float2*>(static_cast<char*>(x.ws) + sums_bytes(p, D));
   a.lens = decode ? nullptr : x.lens;
   a.tile_of = reinterpret_cast<int*>(static_cast<char*>(x.ws) + sums_bytes(p, D) + stats_bytes(p));
-  a.place = a.tile_of + p.row_tiles;
+  a.place = a.tile_of + p.most_tiles();
   a.sl2 = x.scale * kLog2;
-  CUtensorMap mq, mk, mv;
-  if (!map_view_box(&mq, x.q.p, x.q.sb, x.q.sh, x.q.sn, p.B, p.nh, p.nq, D, p.tq, p.tg, p.tb) ||
-      !map_view(&mk, x.kp.p, x.kp.sb, x.kp.sh, x.kp.sn, 1, p.nkv, p.P, D) ||
+  CUtensorMap mq[2], mk, mv;
+  for (int w = 0; w < 2; ++w) {
+    const Boxes c = p.boxes(w);
+    if (!map_view_box(&mq[w], x.q.p, x.q.sb, x.q.sh, x.q.sn, p.B, p.nh, p.nq, D, c.tq, c.tg, c.tb))
+      return cudaErrorInvalidValue;
+  }
+  if (!map_view(&mk, x.kp.p, x.kp.sb, x.kp.sh, x.kp.sn, 1, p.nkv, p.P, D) ||
       !map_view(&mv, x.vp.p, x.vp.sb, x.vp.sh, x.vp.sn, 1, p.nkv, p.P, D))
     return cudaErrorInvalidValue;
   auto kern = prefix_tc_kernel<D>;
   const cudaError_t e = set_max_dynamic_smem((const void*)kern, C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(Deal(p, p.row_tiles).ctas), dim3(C::kThreads), C::SMEM, st, mq, mk, mv, a);
+  return launch_pdl(kern, dim3(Deal(p, p.most_tiles()).ctas), dim3(C::kThreads), C::SMEM, st, mq[0], mq[1], mk, mv, a);
 }
 
 template <int D>
@@ -674,7 +736,7 @@ cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
   j.p = p;
   j.sums = reinterpret_cast<const float4*>(ws);
   j.stats = reinterpret_cast<const float2*>(ws + sums_bytes(p, D));
-  j.place = !decode && x.lens ? tiles + p.row_tiles : nullptr;
+  j.place = !decode && x.lens ? tiles + p.most_tiles() : nullptr;
   j.o = x.o;
   j.lens = x.lens;
   j.nk = x.s.nk;
@@ -711,22 +773,19 @@ cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
   // Rows are few when decoding: their channels go to several CTAs then, each of which reads the
   // statistics.  Where rows fill the SMs that costs more than it gives (16 prompts of 77 tokens:
   // 196 us in all instead of 162, then).
-  const int groups = p.nkv * p.row_tiles * (kTile / kJoinRows), smem = sums_at_most(p, !j.place) * kJoinRows * (int)sizeof(float2);
+  const int groups = p.nkv * p.most_tiles() * (kTile / kJoinRows), smem = sums_at_most(p, !j.place) * kJoinRows * (int)sizeof(float2);
   auto kern = groups >= 304 ? (decode ? prefix_join_kernel<D, D, true> : prefix_join_kernel<D, D, false>)
                             : (decode ? prefix_join_kernel<D, 32, true> : prefix_join_kernel<D, 32, false>);
   e = set_max_dynamic_smem((const void*)kern, 2 * kPrefixCtas * kJoinRows * (int)sizeof(float2));
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(groups, groups >= 304 ? 1 : D / 32), dim3(kJoinThreads), smem, st, j);
+  return launch_pdl(kern, dim3(groups / p.nkv, groups >= 304 ? 1 : D / 32, p.nkv), dim3(kJoinThreads), smem, st, j);
 }
 
 }  // namespace
 
 size_t prefix_ws_bytes(const PrefixShape& x, int d) {
-  size_t sums = 0;
-  for (bool lengths : {false, true}) {
-    const Plan p = make_plan(x, lengths);
-    sums = std::max(sums, sums_bytes(p, d) + stats_bytes(p) + tiles_bytes(p));
-  }
+  const Plan p = make_plan(x, true);  // (its tiles are no fewer than those without lengths)
+  const size_t sums = sums_bytes(p, d) + stats_bytes(p) + tiles_bytes(p);
   const Window w{x.B, x.nh, x.nkv, x.nq, x.nk, x.nk, 0, 0, nullptr};
   const size_t own = x.nq == 1 ? decode_parts_ws_bytes(w, d) : 0;
   return round256(sums + std::max(own, (size_t)x.B * x.nh * x.nq * (d + 1) * 4));

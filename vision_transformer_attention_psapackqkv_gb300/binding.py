@@ -13,7 +13,12 @@ import functools
 import math
 import os
 
-import torch
+try:
+    import torch  # (once, here: an import in every call costs small calls some of their time)
+except ModuleNotFoundError as e:
+    if e.name != "torch":
+        raise
+    torch = None  # the package loads, and the library builds, without it: only calls need it
 
 from . import _build
 
@@ -180,7 +185,7 @@ def _check(fn: str, status: int):
         raise PsaError(fn, status, load().psa_status_string(status).decode())
 
 
-_codes = {torch.bfloat16: PSA_DTYPE_BF16, torch.float32: PSA_DTYPE_F32}
+_codes = {torch.bfloat16: PSA_DTYPE_BF16, torch.float32: PSA_DTYPE_F32} if torch else {}
 
 
 def dtype_code(t) -> int:

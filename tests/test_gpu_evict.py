@@ -251,6 +251,40 @@ def test_caches_beyond_32_bit_offsets():
     assert (k[:8] == 0).all()
 
 
+def test_which_rows_of_a_long_cache_stay():
+    """Lists of 2^20 rows behind 32-bit offsets, with weights that are equal here and there: every output
+    against a stable sort."""
+    rows, nkv, b, sinks, recent = 1 << 20, 2, 8, 4, 32
+    n, keep = rows - 3, rows - 103
+    w = torch.rand(9, nkv, rows, generator=_gen(25), device="cuda")
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda").expand(9, nkv, -1).contiguous()
+    pos[b, 1] = pos[b, 1].flip(0) - 3  # (the newest tokens in the first rows)
+    k = torch.zeros(9, nkv, rows, 64, dtype=BF16, device="cuda")
+    v = torch.zeros_like(k)
+    k[b], v[b] = _randn(26, nkv, rows, 64).to(BF16), _randn(27, nkv, rows, 64).to(BF16)
+    assert k[b, 1].storage_offset() + k[b, 1].numel() > 2 ** 30 and k.numel() * 2 > 2 ** 31
+    old = k[b].clone(), v[b].clone()
+    lens, lens_out = _i32([5] * 8 + [n]), _i32([7] * 9)
+    p = B.evict_of(k, keep, sinks, recent)
+    ws = torch.full((B.psa_kv_evict_workspace_size(p),), 0xFF, dtype=torch.uint8, device="cuda")
+    w_out, pos_out = torch.full_like(w, 7.0), torch.full_like(pos, 7)
+    B.psa_kv_evict(w, pos, lens, k, v, w_out, pos_out, lens_out, ws, p)
+    assert lens_out.tolist() == [5] * 8 + [keep]
+    assert torch.equal(w_out[:b, :, :5], w[:b, :, :5]) and (w_out[:b, :, 5:] == 7).all() and (k[:b] == 0).all()
+    for h in range(nkv):
+        safe = (pos[b, h, :n] < sinks) | (pos[b, h, :n] > pos[b, h, :n].max() - recent)
+        order = torch.where(safe, math.inf, w[b, h, :n]).sort(descending=True, stable=True).indices
+        stays = torch.zeros(n, dtype=torch.bool, device="cuda")
+        stays[order[:keep]] = True
+        place = torch.arange(keep, device="cuda")
+        place[~stays[:keep]] = keep + stays[keep:].nonzero()[:, 0]
+        assert torch.equal(pos_out[b, h, :keep], pos[b, h, place]) and (pos_out[b, h, keep:] == 7).all()
+        assert torch.equal(w_out[b, h, :keep], w[b, h, place])
+        assert (w_out[b, h, keep:n] == 0).all() and (w_out[b, h, n:] == 7).all()
+        for x, was in ((k, old[0]), (v, old[1])):
+            assert torch.equal(x[b, h, :keep], was[h, place]) and torch.equal(x[b, h, keep:], was[h, keep:])
+
+
 def test_on_another_stream_and_replayed():
     c = _case([900, 700], 900, 4, 128, BF16, 16)
     want = _evict(c, 400, 4, 50)

@@ -129,6 +129,22 @@ def test_hundreds_of_row_tiles(lens):
         assert (o[b, :, n:] == 0).all() and (lse[b, :, n:] == -math.inf).all()
 
 
+@pytest.mark.parametrize("nh,nkv", [(4, 2), (1, 1)])
+@pytest.mark.parametrize("Bn,nq,nk", [(257, 3, 5), (700, 7, 7)])
+def test_many_prompts(Bn, nq, nk, nh, nkv):
+    """More sequences than the lengths that the kernel keeps at hand; a length in ten is of padding alone."""
+    c, scale = _case(Bn, nh, nkv, nq, 300, nk, 64, 71), 0.125
+    lens = [(b * 7919) % (nk + 1) if b % 10 else -b for b in range(Bn)]
+    r = _reference(c, lens, scale)
+    valid = (torch.arange(nq, device="cuda") + nk - nq)[None] < _i32(lens)[:, None]
+    _pad(c, lens, nk - nq)
+    o, lse = _prompts(c, lens, scale)
+    rows = valid[:, None, :].expand(-1, nh, -1)
+    within(o[rows], r["o"][rows], r["o_tol"][rows], "o")
+    within(lse[rows], r["lse"][rows], r["lse_tol"][rows] + 8 * U * (1 + r["lse"][rows].abs()), "lse")
+    assert (o[~rows] == 0).all() and (lse[~rows] == -math.inf).all()
+
+
 # B, P, rows, lens
 STEPS = [(1, 1, 1, [1]), (2, 40, 9, [0, 9]), (4, 128, 30, [30, 1, 0, -1]), (7, 129, 200, [200, 0, 17, 16, -3, 15, 300]),
          (33, 1000, 50, [50, 49, 3] * 11), (3, 4500, 700, [700, 350, 1]), (130, 300, 20, [20, -1, 7, 0, 11] * 26), (1, 9000, 5, [5])]

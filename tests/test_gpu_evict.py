@@ -98,6 +98,26 @@ def test_decode_weights_of_a_strided_cache_and_sums_to_the_heads():
     assert ((w.sum(-1) - 3 * nh / nkv).abs() < 1e-4).all()
 
 
+@pytest.mark.parametrize("rows", [15, 16, 17, 20, 31, 32])
+@pytest.mark.parametrize("left,sinks", [(-1, 0), (5, 3)])
+def test_decode_weights_over_short_caches(rows, left, sinks):
+    """A last block that reaches back into the one before it, in caches that end inside their second block."""
+    nh, nkv, d, scale, lens = 6, 2, 64, 0.125, [rows, rows - 1, 1, 16, 17]
+    q, k = _randn(31, 5, nh, 1, d).to(BF16), _randn(32, 5, nkv, rows, d).to(BF16)
+    v = _randn(33, 5, nkv, rows, d).to(BF16)
+    want, tol = _probabilities(q, k, lens, left, sinks, scale)
+    win = B.window_of(q, k, left, 0, sinks)
+    ws = torch.full((B.psa_window_attn_decode_weights_workspace_size(win),), 0xFF, dtype=torch.uint8, device="cuda")
+    w, o = torch.zeros(5, nkv, rows, device="cuda"), torch.full_like(q, 7.0)
+    B.psa_window_attn_decode_weights(q, k, v, _i32(lens), o, w, ws, win, scale)
+    within(w, want, tol + U * want, "weights")
+    for b, n in enumerate(lens):
+        n = min(n, rows)
+        r = window_attention(q[b:b + 1], k[b:b + 1, :, :n], v[b:b + 1, :, :n], None, left, 0, sinks, scale)
+        within(o[b:b + 1], r["o"], r["o_tol"], "o")
+        assert (w[b, :, n:] == 0).all()
+
+
 def test_a_nan_among_the_scores_shows_in_the_weights():
     q, k, v = _randn(7, 2, 4, 1, 64).to(BF16), _randn(8, 2, 2, 90, 64).to(BF16), _randn(9, 2, 2, 90, 64).to(BF16)
     k[0, 1, 40, 3] = math.nan
@@ -181,6 +201,24 @@ def _check(c, keep, sinks, recent, got, in_place):
             assert torch.equal(bits(w[b, h, n:]), bits(was_w[b, h, n:])) and torch.equal(pos[b, h, count:], was_pos[b, h, count:])
             for x, old in ((k, c["k"]), (v, c["v"])):
                 assert torch.equal(x[b, h, :count], old[b, h, place]) and torch.equal(x[b, h, count:], old[b, h, count:])
+
+
+@pytest.mark.parametrize("rows,keep", [(700, 300), (700, 690), (50000, 20000)])
+@pytest.mark.parametrize("same", ["weights", "positions"])
+def test_one_of_the_lists_in_place(rows, keep, same):
+    """Weights written where they were read and positions elsewhere, or the other way round."""
+    c = _case([rows, rows - 300], rows, 2, 64, BF16, 19, "ties")
+    want = _evict(c, keep, 4, 32)
+    k, v, w, pos = (c[n].clone() for n in ("k", "v", "w", "pos"))
+    w_out = w if same == "weights" else torch.full_like(w, 7.0)
+    pos_out = pos if same == "positions" else torch.full_like(pos, 7)
+    p, lens_out = B.evict_of(k, keep, 4, 32), torch.full_like(c["lens"], 7)
+    ws = torch.full((B.psa_kv_evict_workspace_size(p),), 0xFF, dtype=torch.uint8, device="cuda")
+    B.psa_kv_evict(w, pos, c["lens"], k, v, w_out, pos_out, lens_out, ws, p)
+    for b, n in enumerate(c["lens"].tolist()):
+        count = min(n, keep)
+        assert torch.equal(w_out[b, :, :n], want[2][b, :, :n]) and torch.equal(pos_out[b, :, :count], want[3][b, :, :count])
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1]) and torch.equal(lens_out, want[4])
 
 
 # lens, rows, keep, sinks, recent: one kernel and two, threads by length, lists that end anywhere

@@ -175,6 +175,16 @@ def test_single_tokens(Bn, P, rows, lens, nh, nkv, d):
     assert torch.equal(o, _decode(c, lens, scale))
 
 
+@pytest.mark.parametrize("rows", [15, 16, 17, 20, 31, 32])
+def test_single_tokens_over_short_caches(rows):
+    c, lens, scale = _case(5, 6, 2, 1, 130, rows, 64, 81), [rows, rows - 1, 1, 16, 17], 0.125
+    o = _decode(c, lens, scale)
+    for b, n in enumerate(lens):
+        k, v = (torch.cat([c[a], c[x][b:b + 1, :, :min(n, rows)]], 2) for a, x in (("kp", "k"), ("vp", "v")))
+        r = window_attention(c["q"][b:b + 1], k, v, None, -1, 0, 0, scale)
+        within(o[b:b + 1], r["o"], r["o_tol"], b)
+
+
 def test_strided_views_and_two_calls_at_once():
     """A packed projection's queries, a prefix in the first rows of a longer cache, two streams with a
     workspace each."""

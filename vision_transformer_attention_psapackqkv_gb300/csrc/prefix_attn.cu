@@ -147,7 +147,9 @@ struct Box {
   }
 };
 
-template <int D>
+// kLengths: a.lens is there (a kernel of its own: decoding and prompts without lengths are 1 % faster
+// without what counts the tiles).
+template <int D, bool kLengths>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tmQ0, const __grid_constant__ CUtensorMap tmQ1,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   // which it reads its own entries after the barrier below.  (One loop: these instructions run once, and
   // fetching them is most of what they cost.)
   int tiles = p.way[0].row_tiles, which = 0;
-  if (a.lens) {
+  if constexpr (kLengths) {
     for (int i = threadIdx.x; i < min(p.B, kStagedLens); i += C::kThreads) staged[i] = ld_global_l2(a.lens + i);
     __syncthreads();
     int mine[2] = {0, 0}, at = 0;
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   }
   // rows that no box fills are zeros (their scores must not move a warp's maxima)
   if (warp < 2) zero_rows<D>(smem + warp * C::TILE, p.boxes(which).rows(), kTile, lane);
-  if (threadIdx.x == 0) chosen_rows = p.boxes(which).rows();
+  if (kLengths && threadIdx.x == 0) chosen_rows = p.boxes(which).rows();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           }
           mbar_arrive_expect_tx(&bar.q_full[s], (uint32_t)(cut.rows() * D * 2));
           const int tile = u.alone ? u.tile : u.tile + s;
-          const Box box(cut, a.lens ? a.tile_of[tile] : tile);
+          const Box box(cut, kLengths ? a.tile_of[tile] : tile);
           load_tile<D>(smem + s * C::TILE, tmQ, &bar.q_full[s], box.q, u.hk * p.group + box.g, box.b);
           q_count[s] = n + 1;
         }
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       // ---- the rows' sums
       const Piece u(deal, pos, end);
       pos += n;
-      const bool valid_row = r < *(volatile int*)&chosen_rows;
+      const bool valid_row = r < (kLengths ? *(volatile int*)&chosen_rows : p.way[0].rows());
       const long long at = 2LL * (u.unit + blockIdx.x) + s;
       if (u.some(s)) {
         if (!mbar_wait(&bar.o_full[s], outs & 1, abort)) break;
@@ -719,7 +721,7 @@ cudaError_t prefix_part(const PrefixArgs& x, const Plan& p, bool decode, cudaStr
   if (!map_view(&mk, x.kp.p, x.kp.sb, x.kp.sh, x.kp.sn, 1, p.nkv, p.P, D) ||
       !map_view(&mv, x.vp.p, x.vp.sb, x.vp.sh, x.vp.sn, 1, p.nkv, p.P, D))
     return cudaErrorInvalidValue;
-  auto kern = prefix_tc_kernel<D>;
+  auto kern = a.lens ? prefix_tc_kernel<D, true> : prefix_tc_kernel<D, false>;
   const cudaError_t e = set_max_dynamic_smem((const void*)kern, C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(Deal(p, p.most_tiles()).ctas), dim3(C::kThreads), C::SMEM, st, mq[0], mq[1], mk, mv, a);

@@ -299,7 +299,7 @@ typedef struct {
     psa_norm_rope_t rope; /* max_pos: rows of the tables, which all axes index */
     int axes;             /* 1 .. 4 */
     int grid[4];          /* extents of the axes where positions is NULL, the last one innermost */
-    int normalize;        /* 1: norms as above; 0: y = R(pos) (w o x), eps plays no part */
+    int normalize;        /* 1: norms as above; 0: y = R(pos) (w o x), eps plays no part (finite, not negative) */
     unsigned char axis_of_pair[64]; /* below axes, for each of rope.rotary_dim / 2 pairs */
 } psa_rope_axes_t;
 
@@ -387,7 +387,9 @@ size_t psa_window_attn_decode_workspace_size(psa_window_t p);
  * once: k_prefix, v_prefix [1, num_kv_heads, n_prefix, d].  Behind it each sequence has keys of its
  * own, k and v [B, num_kv_heads, n_k, d]; query head h reads key/value head h / (num_heads /
  * num_kv_heads).  Every query sees the whole prefix.  bf16 (fp32: PSA_ERR_UNSUPPORTED), rounded as
- * in psa_window_attn_fwd, head_dim 64 or 128, n_q <= n_k, B * num_heads * n_q up to 2^28. */
+ * in psa_window_attn_fwd, head_dim 64 or 128, n_q <= n_k, B * num_heads up to 65535 and B *
+ * num_heads * n_q up to 2^28.  Rows of bf16 alone: a cache in 4 bits is neither read here nor, below,
+ * accounted for or cut. */
 typedef struct {
     int B, num_heads, num_kv_heads, n_q, n_prefix, n_k, head_dim;
     psa_dtype_t dtype;
@@ -397,8 +399,11 @@ typedef struct {
  * tokens, and query row i also sees the own keys j <= i + n_k - n_q.  lens, int32 [B] on the
  * device (NULL: n_k): own tokens from lens[b] on are padding, whose queries get output 0 and
  * log-sum-exp -infinity, and which are seen by none, whatever they hold.  Every row of o is
- * written, and lse, fp32 [B, num_heads, n_q] (NULL: not wanted).  workspace: 16-byte aligned, at least
- * psa_prefix_attn_workspace_size(p) bytes. */
+ * written, and lse, fp32 [B, num_heads, n_q] (NULL: not wanted).  How the work over the prefix is cut
+ * goes by the sizes and the lengths: a row's last bits may differ between batches of other lengths;
+ * lengths that are all n_k give the bits of a call without them.  workspace: 16-byte aligned, at least
+ * psa_prefix_attn_workspace_size(p) bytes, which hold sums in fp32 (8 to 9 * head_dim bytes for each of
+ * many rows of q, and up to 20 MB besides). */
 psa_status_t psa_prefix_attn_fwd(psa_rows_t q, psa_rows_t k_prefix, psa_rows_t v_prefix,
                                  psa_rows_t k, psa_rows_t v, const int *lens, psa_rows_t o,
                                  float *lse, void *workspace, size_t ws_bytes, psa_prefix_t p,
@@ -504,9 +509,10 @@ size_t psa_window_attn_decode_weights_workspace_size(psa_window_t p);
  * weights_out, positions_out: the same for the rows that stay; in front of the old length and
  * behind them weights_out is set to 0, so that rows appended later start from nothing, and
  * positions_out is left as it was.  They may be the same arrays as weights and positions.  lens_out
- * [B]: min(lens, keep) (0 for a negative one), not the same array as lens.  All outputs are written for the sequences that
- * have no more than keep rows too.  max_len up to 2^24 (PSA_ERR_UNSUPPORTED); head_dim 64 or 128;
- * bf16 or fp32. */
+ * [B]: min(lens, max_len, keep) (0 for a negative one), not the same array as lens; lens above max_len
+ * count as max_len.  All outputs are written for the sequences that have no more than keep rows too.
+ * max_len up to 2^24, B * num_kv_heads up to 65535 (PSA_ERR_UNSUPPORTED); head_dim 64 or 128; bf16 or
+ * fp32. */
 typedef struct {
     int B, num_kv_heads, max_len, head_dim;
     psa_dtype_t dtype;

@@ -238,7 +238,9 @@ struct PrefixArgs {
   void* ws;
   float scale;
 };
-constexpr int kPrefixCtas = 152;  // of the kernel over the prefix, at most
+// Runs of the kernel over the prefix, at most: one for each SM.  On a part with fewer of them what is left
+// over makes a second wave; the cuts, and the results' bits, stay the same.
+constexpr int kPrefixCtas = 152;
 size_t prefix_ws_bytes(const PrefixShape& s, int d);
 cudaError_t launch_prefix_attn(const PrefixArgs& a, int d, bool decode, cudaStream_t st);
 

@@ -14,19 +14,21 @@
 //   warps 0-3, 4-7   softmax of slot 0, 1: one thread per row
 //   warp 8           TMA producer: Q of both slots, a ring of K tiles and one of V tiles
 //   warp 9           issuer of the products, tensor memory
-// Row tiles of padding alone are left out (counted on the device).  All SMs get an equal run of key
-// tiles, whatever the rows; where a run ends inside the prefix a
-// row's sums come in pieces (fp32, relative to the piece's maximum).  They lie in the workspace with a row's
-// neighbours in the tile side by side, four channels each: what 32 lanes write, and read again, is
-// contiguous.
+// Row tiles of padding alone are left out (counted on the device).  All SMs get an equal run of steps, a
+// step being a key tile of a pair of row tiles, or of one that has no partner (half the products, so that
+// of few row tiles an odd one costs what two would).  Where a run ends
+// inside the prefix a row's sums come in pieces (fp32, relative to the piece's maximum).  They lie in the
+// workspace with a row's neighbours in the tile side by side, four channels each: what 32 lanes write,
+// and read again, is contiguous.
 // Own keys: the single-token kernel's partial sums (decoding), or the window kernel's output in fp32
 // and log-sum-exp (prompts).  A last kernel joins all of a row's sums and rounds once.
 //
 // Measured, 32 heads of 128 on 8, on the device.  64 tokens behind 16384 shared and up to 1024 own
 // keys: 78 us (prefix 24, own keys 34: 5.1 TB/s, joining 14; 242 MB in all, 36 us at the copy
-// bandwidth).  16 prompts of 20 to 77 tokens behind 8192 keys: 142 us (prefix 104: a third of its
-// rows hold no query; own keys 19, joining 25).  A step of two row tiles takes 1.6 us where its
-// products take 1.07: two warps a scheduler for the softmax, as in the window attention.
+// bandwidth).  16 prompts of 20 to 77 tokens behind 8192 keys: 143 us (prefix 105: a third of its
+// rows hold no query; own keys 20, joining 26).  A step of two row tiles takes 1.6 us where its
+// products take 1.07 (tensor pipe busy 56 % of the time, no other unit above a third): two warps a
+// scheduler for the softmax, as in the window attention.
 #include <algorithm>
 
 #include "softmax_tc.cuh"
@@ -773,8 +775,9 @@ cudaError_t run(const PrefixArgs& x, bool decode, cudaStream_t st) {
   e = prefix_part<D>(x, p, decode, st);
   if (e != cudaSuccess) return e;
   // Rows are few when decoding: their channels go to several CTAs then, each of which reads the
-  // statistics.  Where rows fill the SMs that costs more than it gives (16 prompts of 77 tokens:
-  // 196 us in all instead of 162, then).
+  // statistics (64 tokens behind 16384 keys, own caches of 1024: 91 us in all, 106 with whole rows).  Where
+  // rows fill the SMs that costs more than it gives (16 prompts of 39 to 77 tokens behind 8192 keys: 175
+  // us instead of 151).
   const int groups = p.nkv * p.most_tiles() * (kTile / kJoinRows), smem = sums_at_most(p, !j.place) * kJoinRows * (int)sizeof(float2);
   auto kern = groups >= 304 ? (decode ? prefix_join_kernel<D, D, true> : prefix_join_kernel<D, D, false>)
                             : (decode ? prefix_join_kernel<D, 32, true> : prefix_join_kernel<D, 32, false>);

@@ -854,10 +854,12 @@ size_t decode_ws_bytes(const Window& w, int d) {
   return s == 1 ? 256 : ((size_t)w.B * w.nh * s * (d + 2) * 4 + 255) / 256 * 256;
 }
 
-// Runs of 8 to 32 blocks of 16 keys: about two for each warp that the device holds (12 per SM).
-// Shorter ones make more partial results to join, longer ones leave warps idle (64 sequences of up to
-// 1024 keys behind a prefix, runs of 4, 8, 16, 32 blocks: 80, 79, 91, 98 us; 16 of up to 8192 with
-// weights: 71, 68, 68, 63).
+// Runs of 8 to 32 blocks of 16 keys: about two for each warp that the device holds (12 per SM);
+// longer ones where there would be more than 256 of them (from 131072 visible keys on).  Shorter ones
+// make more partial results to join, longer ones leave warps idle.  64 sequences of up to 1024 keys
+// behind a prefix, runs of 4, 8, 16, 32 blocks: 80, 79, 91, 98 us.  The step with weights goes by the same
+// rule, though its long caches would have longer runs: 16 sequences of up to 8192 keys take 71, 68, 68, 63 us,
+// and the rule gives 17 there.
 DecodeRuns decode_runs(const Window& w) {
   const int group = w.nh / w.nkv, tiles = (group + head_tile(w) - 1) / head_tile(w);
   const long long blocks = most_blocks(w), all = blocks * w.B * w.nkv * tiles;

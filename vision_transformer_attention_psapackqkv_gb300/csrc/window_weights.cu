@@ -13,8 +13,8 @@
 // units; a warp that goes through 128 scores spends most of its time on latencies.  So four key
 // tiles, each with four warps and a score tile, share the query tiles that stream by: four warps a
 // scheduler fill one another's gaps, and a query tile is read from the L2 once for four products.
-// Measured, 2 x 4096 causal, 16 heads of 128 on 4, on the device: 75 us (0.92 PFLOP/s of visible
-// pairs, 0.48 of cuBLAS's bf16 rate; tensor pipe and multi-function units busy 46 % each, a step's
+// Measured, 2 x 4096 causal, 16 heads of 128 on 4, on the device: 76 us (0.91 PFLOP/s of visible
+// pairs, 0.47 of cuBLAS's bf16 rate; tensor pipe and multi-function units busy 46 % each, a step's
 // four products and the waits between them are what is left).  Two key tiles with their operand in
 // tensor memory and a ring of three score tiles: 86 us with four warps a tile, 79 with eight, and
 // more barriers; with barriers that every thread arrives at instead of one lane a warp 85 us.
@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kTiles = 4;  // key tiles of a unit
 constexpr int kUnitKeys = kTiles * kTile;
-constexpr int kWeightCtas = 152;
+constexpr int kWeightCtas = 152;  // a run for each SM; the same on a part with fewer of them, so that bits are too
 
 template <int D>
 struct Cfg {
